@@ -108,6 +108,7 @@ def load() -> ctypes.CDLL:
     lib.indexer_bwd_last_device_status.restype = i
     lib.indexer_bwd_status_string.argtypes = [i]
     lib.indexer_bwd_status_string.restype = ctypes.c_char_p
+    train.declare(lib)
     _lib = lib
     return lib
 
@@ -399,3 +400,12 @@ def indexer_backward(q, k, w, index_score, attn_score, topk_idx=None, grad_scale
         indexer_bwd(q, k, w, index_score, attn_score, topk_idx, dq, dw, dk, grad_scale, dk_mode, workspace,
                     stream)
     return dq, dw, dk
+
+
+# ---------------------------------------------------- training operators ---
+
+from . import train  # noqa: E402  (it uses the helpers above)
+from .train import (distill_bwd, distill_fwd, distill_grad, layer_norm_bwd,  # noqa: E402,F401
+                    layer_norm_bwd_workspace_size, layer_norm_fwd, token_logprobs_bwd, token_logprobs_fwd)
+
+EXPORTS += train.EXPORTS

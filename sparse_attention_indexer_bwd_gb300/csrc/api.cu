@@ -4,6 +4,7 @@
 
 #include "indexer_bwd.h"
 #include "internal.h"
+#include "train.h"
 
 namespace {
 
@@ -56,15 +57,7 @@ int device_info(DeviceInfo** out) {
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Non-null, 16-byte aligned and addressable by the device.
-bool dev_ptr_ok(const void* p) {
-  if (!aligned16(p)) return false;
-  cudaPointerAttributes at{};
-  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
-}
+bool dev_ptr_ok(const void* p) { return ibwd::device_pointer_ok(p, 16); }
 
 bool shape_ok(int B, int S_q, int S_k, int H, int D, int L) {
   if (B < 1 || S_q < 1 || S_k < 1 || L < 1) return false;
@@ -202,6 +195,27 @@ int gemm_common(const uint16_t* q, const uint16_t* k, const float* w, const floa
 }
 
 }  // namespace
+
+namespace ibwd {
+
+int current_device(int* num_sms) {
+  DeviceInfo* dv = nullptr;
+  const int rc = device_info(&dv);
+  if (!rc) *num_sms = dv->num_sms;
+  return rc;
+}
+
+bool device_pointer_ok(const void* p, size_t align) {
+  if (!p || (reinterpret_cast<uintptr_t>(p) & (align - 1))) return false;
+  cudaPointerAttributes at{};
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
+}
+
+}  // namespace ibwd
 
 // The forward: index_score from q, k, w (and topk_idx unless dense).
 int fwd_common(const uint16_t* q, const uint16_t* k, const float* w, const int32_t* idx, bool need_idx, float* out,

@@ -1,0 +1,651 @@
+// Operators over rows of logits on sm_103a: log probabilities, entropy and
+// top alternatives, their gradient, and the distillation loss from a
+// teacher's top logits with its gradient.
+//
+// A row x of V logits has, with c = log2(e) / temperature,
+//   m = max x,  d_v = (x_v - m) c,  s = sum 2^d_v,  u = sum 2^d_v d_v
+//   lse = m / temperature + ln 2 log2 s,  log2 p_v = d_v - log2 s,
+//   entropy = ln 2 (log2 s - u / s)
+// and every function of the row follows from (m, s, u) and single logits.
+// (m, s, u) of disjoint parts join exactly like running ones: both are scaled
+// to the larger maximum.
+//
+// A cluster of C thread blocks takes a row, each block a contiguous part; the
+// parts' statistics are exchanged through distributed shared memory and
+// joined in the blocks' order, so few rows still fill the machine and every
+// result is bitwise reproducible.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "train.h"
+
+namespace cg = cooperative_groups;
+
+namespace ibwd {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxTop = 128;
+constexpr int kMaxKept = 1024;
+constexpr int kCand = 1024;      // candidates a block ranks for the top alternatives
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
+#define NEG_INF (-INFINITY)
+
+struct Stat {
+  float m, s, u;
+};
+
+// The reference point of the exponents: the maximum, or 0 while there is none
+// (every term is then 2^-inf = 0; x - m of two infinities never occurs).
+__device__ __forceinline__ float finite_max(float m) { return m == NEG_INF ? 0.f : m; }
+
+template <bool U>
+__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
+  const float m = fmaxf(a.m, b.m), mr = finite_max(m);
+  // a part without terms has s = u = 0; its difference is kept finite for u
+  const float da = fmaxf((a.m - mr) * c, -1.0e30f), db = fmaxf((b.m - mr) * c, -1.0e30f);
+  const float fa = ex2(da), fb = ex2(db);
+  Stat r;
+  r.m = m;
+  r.s = a.s * fa + b.s * fb;
+  r.u = 0.f;
+  if (U) r.u = fa * (a.u + a.s * da) + fb * (b.u + b.s * db);
+  return r;
+}
+
+// Adds N logits to a running statistic.
+template <bool U, int N>
+__device__ __forceinline__ void add(Stat& t, const float (&x)[N], float c) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+  if (m > t.m) {
+    const float d = fmaxf((t.m - m) * c, -1.0e30f), f = ex2(d);
+    if (U) t.u = f * (t.u + t.s * d);
+    t.s *= f;
+    t.m = m;
+  }
+  const float mr = finite_max(t.m);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = (x[i] - mr) * c;
+    const float e = ex2(d);
+    t.s += e;
+    if (U) t.u = fmaf(e, fmaxf(d, -1.0e30f), t.u);  // 0 for a masked logit
+  }
+}
+
+// The part [lo, hi) of a row as this block reads it: single elements up to a
+// 16-byte boundary, whole 16-byte vectors, single elements.
+template <typename T>
+struct Part {
+  const T* head;
+  int nhead, nvec, ntail;
+  __device__ Part(const T* row, int lo, int hi) {
+    head = row + lo;
+    const int n = hi - lo;
+    const int mis = (int)((16 - (reinterpret_cast<uintptr_t>(head) & 15)) & 15) / (int)sizeof(T);
+    nhead = min(n, mis);
+    nvec = (n - nhead) / kVec<T>;
+    ntail = n - nhead - nvec * kVec<T>;
+  }
+  __device__ const T* vec(int i) const { return head + nhead + (long long)i * kVec<T>; }
+  __device__ const T* tail() const { return vec(nvec); }
+  // single elements are numbered 0 .. nhead + ntail - 1
+  __device__ int singles() const { return nhead + ntail; }
+  __device__ int single_at(int i) const { return i < nhead ? i : i + nvec * kVec<T>; }  // offset from head
+};
+
+template <typename T, bool U>
+__device__ __forceinline__ Stat part_stat(const Part<T>& p, float c) {
+  Stat t{NEG_INF, 0.f, 0.f};
+  constexpr int UNR = 4;
+  int i = threadIdx.x;
+  for (; i + (UNR - 1) * kThreads < p.nvec; i += UNR * kThreads) {
+    uint4 r[UNR];
+#pragma unroll
+    for (int k = 0; k < UNR; ++k) r[k] = ld_stream(p.vec(i + k * kThreads));
+#pragma unroll
+    for (int k = 0; k < UNR; ++k) {
+      float v[kVec<T>];
+      unpack(r[k], v, T{});
+      add<U>(t, v, c);
+    }
+  }
+  for (; i < p.nvec; i += kThreads) {
+    float v[kVec<T>];
+    unpack(ld_stream(p.vec(i)), v, T{});
+    add<U>(t, v, c);
+  }
+  if ((int)threadIdx.x < p.singles()) {
+    const float v[1] = {to_f32(p.head[p.single_at(threadIdx.x)])};
+    add<U>(t, v, c);
+  }
+  return t;
+}
+
+// Statistic of the whole block, in thread 0 .. kThreads - 1 alike.
+template <bool U>
+__device__ __forceinline__ Stat block_stat(Stat t, float c, Stat* stage) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Stat b;
+    b.m = __shfl_xor_sync(0xffffffffu, t.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, t.s, o);
+    b.u = U ? __shfl_xor_sync(0xffffffffu, t.u, o) : 0.f;
+    // the lower lane's part first, so that both lanes get the same bits
+    t = (threadIdx.x & o) ? join<U>(b, t, c) : join<U>(t, b, c);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) stage[threadIdx.x >> 5] = t;
+  __syncthreads();
+  t = stage[0];
+  for (int w = 1; w < kThreads / 32; ++w) t = join<U>(t, stage[w], c);
+  return t;
+}
+
+__device__ __forceinline__ float block_sum(float v, float* stage) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) stage[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < kThreads / 32; ++w) v += stage[w];
+  return v;
+}
+__device__ __forceinline__ float block_max(float v, float* stage) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) stage[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = stage[0];
+  for (int w = 1; w < kThreads / 32; ++w) v = fmaxf(v, stage[w]);
+  return v;
+}
+
+// The statistic of the row from its blocks', joined in the blocks' order.
+template <bool U>
+__device__ __forceinline__ Stat cluster_stat(Stat t, float c, Stat* all, int C) {
+  if (C == 1) return t;
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();  // every block has started
+  if ((int)threadIdx.x < C) *cl.map_shared_rank(all + cl.block_rank(), threadIdx.x) = t;
+  cl.sync();
+  t = all[0];
+  for (int i = 1; i < C; ++i) t = join<U>(t, all[i], c);
+  return t;
+}
+
+// ------------------------------------------------------- top alternatives --
+// Order of the candidates: larger logit first, then lower index, as one
+// unsigned 64-bit key (-0 counts as +0).
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+__device__ __forceinline__ unsigned long long order_key(float x, int v) {
+  return ((unsigned long long)order_bits(x) << 32) | (uint32_t)~v;
+}
+
+struct TopShared {
+  float segmax[kThreads];
+  unsigned long long cand[kCand];
+  unsigned long long merge[kMaxTop * kMaxCluster];
+  int merge_n[kMaxCluster];
+  int hot[kThreads];
+  int nhot, ncand;
+  float bound;
+  int warp_n[kThreads / 32];
+};
+
+// Calls f(x, v) for every element of this block's part, in any order.
+template <typename T, typename F>
+__device__ __forceinline__ void for_each(const Part<T>& p, int lo, F f) {
+  for (int i = threadIdx.x; i < p.nvec; i += kThreads) {
+    float v[kVec<T>];
+    unpack(ld_stream(p.vec(i)), v, T{});
+#pragma unroll
+    for (int k = 0; k < kVec<T>; ++k) f(v[k], lo + p.nhead + i * kVec<T> + k);
+  }
+  if ((int)threadIdx.x < p.singles()) {
+    const int o = p.single_at(threadIdx.x);
+    f(to_f32(p.head[o]), lo + o);
+  }
+}
+
+__device__ __forceinline__ int block_count(int n, float* stage) {
+  return (int)block_sum((float)n, stage);  // exact: counts stay below 2^24
+}
+
+// The rare case of more than kCand entries at or above the bound (many equal
+// logits, or logits whose order follows the threads): the exact value of the
+// n-th largest by bisection over the order of fp32, then everything above it
+// and the equal ones of lowest index.
+template <typename T>
+__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, float bound, float most,
+                                       TopShared& sh) {
+  auto above = [&](float cut) {  // entries of the part above `cut`
+    int k = 0;
+    for_each(p, lo, [&](float x, int) { k += (x > cut) ? 1 : 0; });
+    __syncthreads();
+    if (threadIdx.x == 0) sh.ncand = 0;
+    __syncthreads();
+    if (k) atomicAdd(&sh.ncand, k);
+    __syncthreads();
+    return sh.ncand;
+  };
+  uint32_t a = order_bits(bound), b = order_bits(most);
+  int count = above(bound);
+  bool equal = count < n;  // the cut is the n-th largest value itself
+  // entries above a: `count`, at least n; entries above b: fewer than n
+  while (!equal && count > kCand) {
+    if (b - a == 1) {  // more than kCand entries are equal to b's value
+      a = b;
+      equal = true;
+      break;
+    }
+    const uint32_t mid = a + (b - a) / 2;
+    const int k = above(order_value(mid));
+    if (k >= n) {
+      a = mid;
+      count = k;
+    } else {
+      b = mid;
+    }
+  }
+  const float cut = order_value(a);
+  __syncthreads();
+  if (threadIdx.x == 0) sh.ncand = 0;
+  __syncthreads();
+  for_each(p, lo, [&](float x, int v) {
+    if (x > cut) sh.cand[atomicAdd(&sh.ncand, 1)] = order_key(x, v);
+  });
+  __syncthreads();
+  if (!equal) return;
+  // the lowest indices among the equal ones, in order
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int have = sh.ncand;
+  for (int v0 = lo; v0 < hi && have < n; v0 += kThreads) {
+    const int v = v0 + threadIdx.x;
+    const bool eq = v < hi && to_f32(p.head[v - lo]) == cut;
+    const unsigned mask = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) sh.warp_n[warp] = __popc(mask);
+    __syncthreads();
+    int at = have + __popc(mask & ((1u << lane) - 1u)), total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += sh.warp_n[w];
+      total += sh.warp_n[w];
+    }
+    if (eq && at < n) sh.cand[at] = order_key(cut, v);
+    have += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) sh.ncand = min(have, n);
+  __syncthreads();
+}
+
+// The n largest entries of this block's part, as sorted keys in
+// out[0 .. return value), from the threads' own maxima: the n-th largest of
+// those bounds the n-th largest entry from below (they are maxima of disjoint
+// sets), and only threads whose maximum reaches the bound can hold an entry
+// that does, so the second look reads a few of them.
+template <typename T>
+__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, TopShared& sh,
+                                        float* stage, unsigned long long* out) {
+  const int t = threadIdx.x;
+  sh.segmax[t] = my_max;
+  if (t == 0) {
+    sh.nhot = sh.ncand = 0;
+    sh.bound = NEG_INF;
+  }
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < kThreads; i += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(&sh.segmax[i]);
+    rank += (o.x > my_max || (o.x == my_max && i < t)) + (o.y > my_max || (o.y == my_max && i + 1 < t)) +
+            (o.z > my_max || (o.z == my_max && i + 2 < t)) + (o.w > my_max || (o.w == my_max && i + 3 < t));
+  }
+  if (rank == n - 1) sh.bound = my_max;
+  __syncthreads();
+  const float bound = sh.bound;
+  if (my_max >= bound && my_max > NEG_INF) sh.hot[atomicAdd(&sh.nhot, 1)] = t;
+  __syncthreads();
+  const int warp = t >> 5, lane = t & 31;
+  auto offer = [&](float x, int v) {
+    if (x >= bound && x > NEG_INF) {
+      const int at = atomicAdd(&sh.ncand, 1);
+      if (at < kCand) sh.cand[at] = order_key(x, v);
+    }
+  };
+  for (int h = warp; h < sh.nhot; h += kThreads / 32)
+    for (int i = sh.hot[h] + lane * kThreads; i < p.nvec; i += 32 * kThreads) {
+      float v[kVec<T>];
+      unpack(ld_stream(p.vec(i)), v, T{});
+#pragma unroll
+      for (int k = 0; k < kVec<T>; ++k) offer(v[k], lo + p.nhead + i * kVec<T> + k);
+    }
+  if (t < p.singles()) {
+    const int o = p.single_at(t);
+    offer(to_f32(p.head[o]), lo + o);
+  }
+  __syncthreads();
+  if (sh.ncand > kCand) {  // uniform
+    const float most = block_max(my_max, stage);
+    top_exact(p, lo, hi, n, bound, most, sh);
+  }
+  const int count = sh.ncand;
+  for (int i = t; i < count; i += kThreads) {
+    const unsigned long long key = sh.cand[i];
+    int r = 0;
+    for (int k = 0; k < count; ++k) r += sh.cand[k] > key;
+    if (r < n) out[r] = key;
+  }
+  return min(count, n);
+}
+
+// ------------------------------------------------------------ distillation --
+struct KeptShared {
+  int id[kMaxKept];       // kept token, or -1
+  float p[kMaxKept];      // 2^((teacher - max) c), then the probability
+  float x[kMaxKept];      // the student's logit of it
+};
+
+// Writes the gradient of this block's part, f(x) for each logit: by vectors
+// where logits and gradient lie alike in their 16-byte blocks.
+template <typename T, typename F>
+__device__ __forceinline__ void map_part(const Part<T>& p, T* dst, F f) {
+  // dst: the gradient of p.head[0]
+  const bool alike = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(p.head)) & 15) == 0;
+  if (alike) {
+    constexpr int UNR = 2;
+    int i = threadIdx.x;
+    T* dv = dst + p.nhead;
+    for (; i + (UNR - 1) * kThreads < p.nvec; i += UNR * kThreads) {
+      uint4 r[UNR];
+#pragma unroll
+      for (int k = 0; k < UNR; ++k) r[k] = ld_stream(p.vec(i + k * kThreads));
+#pragma unroll
+      for (int k = 0; k < UNR; ++k) {
+        float v[kVec<T>];
+        unpack(r[k], v, T{});
+#pragma unroll
+        for (int j = 0; j < kVec<T>; ++j) v[j] = f(v[j]);
+        st_stream(dv + (long long)(i + k * kThreads) * kVec<T>, pack(v, T{}));
+      }
+    }
+    for (; i < p.nvec; i += kThreads) {
+      float v[kVec<T>];
+      unpack(ld_stream(p.vec(i)), v, T{});
+#pragma unroll
+      for (int j = 0; j < kVec<T>; ++j) v[j] = f(v[j]);
+      st_stream(dv + (long long)i * kVec<T>, pack(v, T{}));
+    }
+    if ((int)threadIdx.x < p.singles()) {
+      const int o = p.single_at(threadIdx.x);
+      dst[o] = from_f32<T>(f(to_f32(p.head[o])));
+    }
+  } else {
+    const int n = p.singles() + p.nvec * kVec<T>;
+    for (int i = threadIdx.x; i < n; i += kThreads) dst[i] = from_f32<T>(f(to_f32(p.head[i])));
+  }
+}
+
+template <typename T, RowOp OP, bool TOP>
+__global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
+  constexpr bool kLogp = OP == RowOp::kLogpFwd || OP == RowOp::kLogpBwd;
+  constexpr bool kDistill = !kLogp;
+  constexpr bool kStat = OP == RowOp::kLogpFwd || OP == RowOp::kDistillFwd || OP == RowOp::kDistillGrad;
+  constexpr bool kGrad = OP == RowOp::kLogpBwd || OP == RowOp::kDistillBwd || OP == RowOp::kDistillGrad;
+  constexpr bool kEntropy = OP == RowOp::kLogpFwd;
+  __shared__ Stat stage[kThreads / 32], all[kMaxCluster];
+  __shared__ float fstage[kThreads / 32];
+  __shared__ __align__(16) unsigned char raw[TOP ? sizeof(TopShared) : kDistill ? sizeof(KeptShared) : 16];
+  TopShared& top = *reinterpret_cast<TopShared*>(raw);
+  KeptShared& kept = *reinterpret_cast<KeptShared*>(raw);
+
+  const int rank = C == 1 ? 0 : (int)(blockIdx.x % C);
+  const long long row = blockIdx.x / C;
+  const int t = threadIdx.x;
+  // parts are whole multiples of 64 logits, so that aligned rows stay aligned
+  const int len = (((a.V + C - 1) / C) + 63) & ~63;
+  const int lo = (int)min((long long)a.V, (long long)rank * len), hi = (int)min((long long)a.V, (long long)lo + len);
+  const T* xr = static_cast<const T*>(a.x) + row * a.x_stride;
+  const Part<T> part(xr, lo, hi);
+  const float inv_t = 1.f / a.temperature, c = kLog2e / a.temperature;
+
+  // the teacher's slots: ids and, from the whole row, the student's logits
+  float tmax = NEG_INF;
+  if (kDistill) {
+    for (int j = t; j < a.K; j += kThreads) {
+      const int id = a.ids[row * a.K + j];
+      const float tv = a.teacher[row * a.K + j];
+      const bool ok = id >= 0 && id < a.V;
+      kept.id[j] = ok ? id : -1;
+      kept.p[j] = ok ? tv : NEG_INF;
+      kept.x[j] = ok ? to_f32(xr[id]) : 0.f;
+      if (ok) tmax = fmaxf(tmax, tv);
+    }
+    tmax = block_max(tmax, fstage);
+  }
+
+  Stat st{0.f, 1.f, 0.f};
+  float my_max = NEG_INF;
+  if (kStat) {
+    const Stat mine = part_stat<T, kEntropy>(part, c);
+    my_max = mine.m;
+    st = cluster_stat<kEntropy>(block_stat<kEntropy>(mine, c, stage), c, all, C);
+  }
+  // log2 p_v = (x_v - ref) c - l2s
+  float ref, l2s;
+  bool empty;  // every logit masked
+  if (kStat) {
+    empty = st.m == NEG_INF && st.s == 0.f;  // (s is NaN when the row holds a NaN)
+    ref = finite_max(st.m);
+    l2s = log2f(st.s);
+  } else {
+    const float lse = a.lse[row];
+    empty = lse == NEG_INF;
+    ref = 0.f;
+    l2s = lse * kLog2e;
+  }
+
+  if (OP == RowOp::kLogpFwd) {
+    if (rank == 0 && t == 0) {
+      if (a.lse) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
+      if (a.entropy) a.entropy[row] = empty ? 0.f : kLn2 * (l2s - st.u / st.s);
+      if (a.tokens) {
+        const int id = a.tokens[row];
+        float lp = 0.f;
+        if (id >= 0 && id < a.V) lp = empty ? NEG_INF : (to_f32(xr[id]) - ref) * inv_t - kLn2 * l2s;
+        a.logprob[row] = lp;
+      }
+    }
+    if (TOP) {
+      const int n = a.top_n;
+      int count = 0;
+      const unsigned long long* keys = top.merge;
+      int total;
+      if (C == 1) {
+        total = part_top(part, lo, hi, n, my_max, top, fstage, top.merge);
+        __syncthreads();
+        for (int i = t; i < n; i += kThreads) {
+          const long long o = row * n + i;
+          if (i < total) {
+            const unsigned long long key = keys[i];
+            a.top_ids[o] = (int)~(uint32_t)key;
+            a.top_logprobs[o] = (order_value((uint32_t)(key >> 32)) - ref) * inv_t - kLn2 * l2s;
+          } else {
+            a.top_ids[o] = -1;
+            a.top_logprobs[o] = isnan(l2s) ? l2s : NEG_INF;
+          }
+        }
+      } else {
+        cg::cluster_group cl = cg::this_cluster();
+        count = part_top(part, lo, hi, n, my_max, top, fstage, cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
+        if (t == 0) *(cl.map_shared_rank(top.merge_n, 0) + rank) = count;
+        cl.sync();
+        if (rank == 0) {
+          total = 0;
+          for (int i = 0; i < C; ++i) total += top.merge_n[i];
+          // place of an entry: its own place plus, in every other sorted
+          // list, the number of larger keys
+          for (int e = t; e < C * kMaxTop; e += kThreads) {
+            const int l = e / kMaxTop, i = e % kMaxTop;
+            if (i >= top.merge_n[l]) continue;
+            const unsigned long long key = top.merge[e];
+            int r = i;
+            for (int k = 0; k < C; ++k) {
+              if (k == l) continue;
+              int x0 = 0, x1 = top.merge_n[k];
+              while (x0 < x1) {
+                const int mid = (x0 + x1) >> 1;
+                if (top.merge[k * kMaxTop + mid] > key)
+                  x0 = mid + 1;
+                else
+                  x1 = mid;
+              }
+              r += x0;
+            }
+            if (r < n) {
+              a.top_ids[row * n + r] = (int)~(uint32_t)key;
+              a.top_logprobs[row * n + r] = (order_value((uint32_t)(key >> 32)) - ref) * inv_t - kLn2 * l2s;
+            }
+          }
+          for (int i = total + t; i < n; i += kThreads) {
+            a.top_ids[row * n + i] = -1;
+            a.top_logprobs[row * n + i] = isnan(l2s) ? l2s : NEG_INF;
+          }
+        }
+      }
+    }
+    return;
+  }
+
+  if (OP == RowOp::kLogpBwd) {
+    const int id = a.tokens ? a.tokens[row] : -1;
+    const bool tok = id >= 0 && id < a.V && a.dlogprob != nullptr;
+    const float g = tok ? a.dlogprob[row] * inv_t : 0.f;
+    const float b = a.dentropy ? a.dentropy[row] * inv_t : 0.f;
+    const float h = a.dentropy ? a.entropy[row] : 0.f;
+    const float xt = tok ? to_f32(xr[id]) : 0.f;
+    __syncthreads();  // the logit is read before its place may be overwritten
+    auto grad = [&](float x) {
+      if (empty) return 0.f;
+      const float d = x * c - l2s;
+      const float p = ex2(d);
+      return -p * (g + b * (kLn2 * fmaxf(d, -1.0e30f) + h));
+    };
+    T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
+    map_part(part, dst, grad);
+    __syncthreads();
+    if (t == 0 && tok && id >= lo && id < hi) dst[id - lo] = from_f32<T>(empty ? 0.f : g + grad(xt));
+    return;
+  }
+
+  if (kDistill) {
+    // p_j = w_j / z with w_j = 2^((teacher_j - tmax) c)
+    const bool none = tmax == NEG_INF;
+    const float tref = finite_max(tmax);
+    float z = 0.f, gap = 0.f;
+    for (int j = t; j < a.K; j += kThreads) {
+      const float d = kept.p[j] - tref;
+      const float w = ex2(d * c);
+      z += w;
+      // in natural units: a lowest-value mask stays finite there
+      if (w > 0.f) gap += w * (d * inv_t - (kept.x[j] - ref) * inv_t);
+      kept.p[j] = w;
+    }
+    z = block_sum(z, fstage);
+    if (OP != RowOp::kDistillBwd && a.loss != nullptr) {
+      gap = block_sum(gap, fstage);
+      if (rank == 0 && t == 0)
+        a.loss[row] = none || empty ? 0.f : a.temperature * a.temperature * (gap / z + kLn2 * (l2s - log2f(z)));
+    }
+    if (OP == RowOp::kDistillFwd) {
+      if (rank == 0 && t == 0) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
+      return;
+    }
+    __syncthreads();
+    float g = a.dloss ? a.dloss[row] * a.temperature : a.temperature;
+    if (OP == RowOp::kDistillGrad) g *= a.grad_scale;
+    const bool zero = none || empty;
+    const float iz = 1.f / z;
+    T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
+    auto grad = [&](float x) {
+      if (zero) return 0.f;
+      return g * ex2((x - ref) * c - l2s);
+    };
+    // every block has read its logits of kept tokens before any is overwritten
+    // (with statistics, they have met since)
+    if (!kStat && C > 1) cg::this_cluster().sync();
+    map_part(part, dst, grad);
+    __syncthreads();
+    for (int j = t; j < a.K; j += kThreads) {
+      const int id = kept.id[j];
+      if (id < lo || id >= hi || zero) continue;
+      float p = 0.f;
+      bool first = true;
+      for (int k = 0; k < a.K; ++k)
+        if (kept.id[k] == id) {
+          if (k < j) first = false;
+          p += kept.p[k];
+        }
+      if (first) dst[id - lo] = from_f32<T>(g * (ex2((kept.x[j] - ref) * c - l2s) - p * iz));
+    }
+  }
+}
+
+template <typename T, RowOp OP, bool TOP>
+cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.rows * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP>, a, C);
+}
+
+template <typename T>
+cudaError_t launch_typed(RowOp op, const RowArgs& a, int C, cudaStream_t st) {
+  switch (op) {
+    case RowOp::kLogpFwd:
+      return a.top_n ? launch_rows_t<T, RowOp::kLogpFwd, true>(a, C, st)
+                     : launch_rows_t<T, RowOp::kLogpFwd, false>(a, C, st);
+    case RowOp::kLogpBwd: return launch_rows_t<T, RowOp::kLogpBwd, false>(a, C, st);
+    case RowOp::kDistillFwd: return launch_rows_t<T, RowOp::kDistillFwd, false>(a, C, st);
+    case RowOp::kDistillBwd: return launch_rows_t<T, RowOp::kDistillBwd, false>(a, C, st);
+    default: return launch_rows_t<T, RowOp::kDistillGrad, false>(a, C, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rows(RowOp op, const RowArgs& a, cudaStream_t st) {
+  if (!a.rows) return cudaSuccess;
+  // blocks a row: as many as make two a SM, while a part
+  // keeps at least two vectors a thread
+  const int vec = a.type == 0 ? 4 : 8;
+  int C = 1;
+  while (C < kMaxCluster && a.rows * 2 * C <= 2LL * a.num_sms && (long long)a.V >= 4LL * C * kThreads * vec) C *= 2;
+  switch (a.type) {
+    case 0: return launch_typed<float>(op, a, C, st);
+    case 1: return launch_typed<__nv_bfloat16>(op, a, C, st);
+    default: return launch_typed<__half>(op, a, C, st);
+  }
+}
+
+}  // namespace ibwd

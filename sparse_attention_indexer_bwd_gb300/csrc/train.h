@@ -1,0 +1,77 @@
+// Launchers of the training operators (layer norm, token log probabilities,
+// distillation), shared by train_api.cu and their kernels' files.  Each
+// returns a cudaError_t from its launches.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace ibwd {
+
+// The current device: IBWD_OK with its SM count, or the status that refuses it.
+int current_device(int* num_sms);
+// Non-null, aligned to `align` bytes and addressable by the device.
+bool device_pointer_ok(const void* p, size_t align);
+
+struct NormFwdArgs {
+  const void* x;
+  const void* gamma;  // [N] or nullptr
+  const void* beta;
+  void* y;
+  float* mean;  // [rows] or nullptr
+  float* rstd;
+  long long rows, x_stride, y_stride;
+  int N, x_type, y_type, w_type;
+  float eps;
+  int num_sms;
+};
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t st);
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* x;
+  const void* gamma;  // [N] or nullptr
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  float* dgamma;  // [N] or nullptr
+  float* dbeta;
+  float* part;  // workspace: [groups][2][N] column sums
+  long long rows, dy_stride, x_stride, dx_stride;
+  int N, x_type, dy_type, w_type;
+  int num_sms;
+};
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st);
+size_t norm_bwd_workspace(long long rows, int N);
+
+// Which function of a row of logits a launch computes.
+enum class RowOp { kLogpFwd, kLogpBwd, kDistillFwd, kDistillBwd, kDistillGrad };
+
+struct RowArgs {
+  const void* x;  // logits [rows, V]
+  void* dx;       // their gradient, may be x
+  long long rows, x_stride, dx_stride;
+  int V, type;
+  float temperature;
+  // log probabilities
+  const int32_t* tokens;
+  const float* dlogprob;
+  const float* dentropy;
+  float* logprob;
+  float* entropy;  // written forward, read backward
+  int32_t* top_ids;
+  float* top_logprobs;
+  int top_n;
+  // distillation
+  const int32_t* ids;
+  const float* teacher;
+  int K;
+  const float* dloss;  // row weight of the gradient, or nullptr for 1
+  float grad_scale;
+  float* loss;
+  float* lse;  // written forward, read backward
+  int num_sms;
+};
+cudaError_t launch_rows(RowOp op, const RowArgs& a, cudaStream_t st);
+
+}  // namespace ibwd
