@@ -11,12 +11,11 @@ to that stream, and the arguments are recorded on it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
-from . import _check, _stream, load
+from . import _check, load
 
 _F32, _I32 = torch.float32, torch.int32
 _CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -92,18 +91,19 @@ def _like(t, name, shape, dtype, device):
 
 
 def _weights(x, width, gamma, beta):
-    """Type code of gamma and beta (float32 or the type of x)."""
-    code = 0
-    for name, w, other in (("gamma", gamma, beta), ("beta", beta, gamma)):
-        if w is None:
-            continue
-        if not isinstance(w, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if w.dtype not in (_F32, x.dtype) or (other is not None and w.dtype != other.dtype):
-            raise ValueError(f"{name}: expected float32 or {x.dtype} (gamma and beta alike), got {w.dtype}")
-        _like(w, name, (width,), w.dtype, x.device)
-        code = _CODE[w.dtype]
-    return code
+    """Type code of gamma and beta (float32 or the type of x, both alike) and their addresses."""
+    dtype = _F32
+    for w in (gamma, beta):
+        if w is not None:
+            if not isinstance(w, torch.Tensor):
+                raise TypeError("gamma and beta must be torch.Tensors")
+            dtype = w.dtype
+            break
+    if dtype != _F32 and dtype != x.dtype:
+        raise ValueError(f"gamma and beta: expected float32 or {x.dtype}, got {dtype}")
+    shape, device = (width,), x.device
+    return (_CODE[dtype], None if gamma is None else _like(gamma, "gamma", shape, dtype, device),
+            None if beta is None else _like(beta, "beta", shape, dtype, device))
 
 
 def _matrix_out(out, like, dtype, name):
@@ -121,29 +121,19 @@ def _matrix_out(out, like, dtype, name):
     return out, _rows(out, name)[2]
 
 
-class _On:
-    """Runs a call on `stream`: its allocations belong to it, its arguments are recorded on it."""
-
-    def __init__(self, stream, *args):
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
-        self.context, self.stream, self.args = torch.cuda.stream(stream), stream, args
-
-    def __enter__(self):
-        self.context.__enter__()
-
-    def __exit__(self, *exc):
-        for t in self.args:
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(self.stream)
-        return self.context.__exit__(*exc)
+def _on(stream, call, *args, **kwargs):
+    """call(...) with `stream` as the current one, its arguments recorded on it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    with torch.cuda.stream(stream):
+        result = call(*args, **kwargs)
+    for t in (*args, *kwargs.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return result
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(stream, *args):
-    return _HERE if stream is None else _On(stream, *args)
+_current_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: building a Stream object takes 3 us
 
 
 def _p(t):
@@ -159,18 +149,19 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, out_dtype=None, 
     gamma and beta are float32 or of x's type; out_dtype (default: x's type)
     may be any type for a float32 x.  `out` may supply y, x itself among it.
     Returns (y, mean, rstd), the statistics float32 or None without `stats`."""
+    if stream is not None:
+        return _on(stream, layer_norm_fwd, x, gamma, beta, eps, out_dtype, out, stats)
     rows, width, xs = _rows(x, "x")
-    wt = _weights(x, width, gamma, beta)
-    with _on(stream, x, gamma, beta, out):
-        dtype = out_dtype or (x.dtype if out is None else out.dtype)
-        if dtype not in _CODE:
-            raise ValueError(f"out_dtype: expected float32, bfloat16 or float16, got {dtype}")
-        y, ys = _matrix_out(out, x, dtype, "out")
-        mean = torch.empty(x.shape[:-1], dtype=_F32, device=x.device) if stats else None
-        rstd = torch.empty_like(mean) if stats else None
-        rc = load().ibwd_layer_norm_fwd(x.data_ptr(), _CODE[x.dtype], xs, _p(gamma), _p(beta), wt, y.data_ptr(),
-                                        _CODE[dtype], xs if ys is None else ys, _p(mean), _p(rstd), rows, width, eps,
-                                        _stream(None))
+    wt, pg, pb = _weights(x, width, gamma, beta)
+    dtype = out_dtype or (x.dtype if out is None else out.dtype)
+    if dtype not in _CODE:
+        raise ValueError(f"out_dtype: expected float32, bfloat16 or float16, got {dtype}")
+    y, ys = _matrix_out(out, x, dtype, "out")
+    mean = torch.empty(x.shape[:-1], dtype=_F32, device=x.device) if stats else None
+    rstd = torch.empty_like(mean) if stats else None
+    rc = load().ibwd_layer_norm_fwd(x.data_ptr(), _CODE[x.dtype], xs, pg, pb, wt, y.data_ptr(),
+                                    _CODE[dtype], xs if ys is None else ys, _p(mean), _p(rstd), rows, width, eps,
+                                    _current_stream(x.device.index))
     _check(rc, "ibwd_layer_norm_fwd")
     return y, mean, rstd
 
@@ -185,29 +176,30 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, weight_grads: bool =
 
     dy has x's type or float32 (any type for a float32 x).  `out` may supply
     dx: x, or dy where the types agree, among it."""
+    if stream is not None:
+        return _on(stream, layer_norm_bwd, dy, x, mean, rstd, gamma, out, weight_grads, workspace)
     rows, width, xs = _rows(x, "x")
     dyr, dyw, dys = _rows(dy, "dy")
     if dy.shape != x.shape or dy.device != x.device:
         raise ValueError(f"dy: expected {tuple(x.shape)} on {x.device}, got {tuple(dy.shape)} on {dy.device}")
-    wt = _weights(x, width, gamma, None)
+    wt, pg, _ = _weights(x, width, gamma, None)
     lead = x.shape[:-1]
     pm = _like(mean, "mean", lead, _F32, x.device)
     pr = _like(rstd, "rstd", lead, _F32, x.device)
     lib = load()
-    with _on(stream, dy, x, mean, rstd, gamma, out, workspace):
-        dx, dxs = _matrix_out(out, x, x.dtype, "out")
-        dgamma = dbeta = None
-        if weight_grads:
-            dgamma = torch.empty(width, dtype=_F32, device=x.device)
-            dbeta = torch.empty_like(dgamma)
-            if workspace is None:
-                workspace = torch.empty(lib.ibwd_layer_norm_bwd_workspace_size(rows, width), dtype=torch.uint8,
-                                        device=x.device)
-        rc = lib.ibwd_layer_norm_bwd(dy.data_ptr(), _CODE[dy.dtype], dys, x.data_ptr(), _CODE[x.dtype], xs, _p(gamma),
-                                     wt, pm, pr, dx.data_ptr(), xs if dxs is None else dxs, _p(dgamma), _p(dbeta),
-                                     rows, width, _p(workspace),
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                     _stream(None))
+    dx, dxs = _matrix_out(out, x, x.dtype, "out")
+    dgamma = dbeta = None
+    if weight_grads:
+        dgamma = torch.empty(width, dtype=_F32, device=x.device)
+        dbeta = torch.empty_like(dgamma)
+        if workspace is None:
+            workspace = torch.empty(lib.ibwd_layer_norm_bwd_workspace_size(rows, width), dtype=torch.uint8,
+                                    device=x.device)
+    rc = lib.ibwd_layer_norm_bwd(dy.data_ptr(), _CODE[dy.dtype], dys, x.data_ptr(), _CODE[x.dtype], xs, pg,
+                                 wt, pm, pr, dx.data_ptr(), xs if dxs is None else dxs, _p(dgamma), _p(dbeta),
+                                 rows, width, _p(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 _current_stream(x.device.index))
     _check(rc, "ibwd_layer_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -221,20 +213,21 @@ def token_logprobs_fwd(logits, tokens=None, top_n: int = 0, temperature: float =
 
     Returns (logprob, entropy, lse, top_ids, top_logprobs); logprob is None
     without tokens, the last two without top_n."""
+    if stream is not None:
+        return _on(stream, token_logprobs_fwd, logits, tokens, top_n, temperature)
     rows, vocab, step = _rows(logits, "logits")
     lead, dev = logits.shape[:-1], logits.device
     pt = None if tokens is None else _like(tokens, "tokens", lead, _I32, dev)
-    with _on(stream, logits, tokens):
-        entropy = torch.empty(lead, dtype=_F32, device=dev)
-        lse = torch.empty_like(entropy)
-        logprob = None if tokens is None else torch.empty_like(entropy)
-        top_ids = top_logprobs = None
-        if top_n:
-            top_logprobs = torch.empty((*lead, max(0, top_n)), dtype=_F32, device=dev)
-            top_ids = torch.empty_like(top_logprobs, dtype=_I32)
-        rc = load().ibwd_token_logprobs_fwd(logits.data_ptr(), _CODE[logits.dtype], step, pt, temperature,
-                                            _p(logprob), entropy.data_ptr(), lse.data_ptr(), _p(top_ids),
-                                            _p(top_logprobs), top_n, rows, vocab, _stream(None))
+    entropy = torch.empty(lead, dtype=_F32, device=dev)
+    lse = torch.empty_like(entropy)
+    logprob = None if tokens is None else torch.empty_like(entropy)
+    top_ids = top_logprobs = None
+    if top_n:
+        top_logprobs = torch.empty((*lead, max(0, top_n)), dtype=_F32, device=dev)
+        top_ids = torch.empty_like(top_logprobs, dtype=_I32)
+    rc = load().ibwd_token_logprobs_fwd(logits.data_ptr(), _CODE[logits.dtype], step, pt, temperature,
+                                        _p(logprob), entropy.data_ptr(), lse.data_ptr(), _p(top_ids),
+                                        _p(top_logprobs), top_n, rows, vocab, _current_stream(logits.device.index))
     _check(rc, "ibwd_token_logprobs_fwd")
     return logprob, entropy, lse, top_ids, top_logprobs
 
@@ -244,6 +237,8 @@ def token_logprobs_bwd(logits, tokens, lse, entropy=None, dlogprob=None, dentrop
     """Gradient of the log probabilities (dlogprob) and the entropies
     (dentropy, which needs entropy) with respect to the logits; `out` may
     supply it, the logits themselves among it."""
+    if stream is not None:
+        return _on(stream, token_logprobs_bwd, logits, tokens, lse, entropy, dlogprob, dentropy, temperature, out)
     rows, vocab, step = _rows(logits, "logits")
     lead, dev = logits.shape[:-1], logits.device
     if dlogprob is None:
@@ -253,11 +248,10 @@ def token_logprobs_bwd(logits, tokens, lse, entropy=None, dlogprob=None, dentrop
     pe = None if entropy is None else _like(entropy, "entropy", lead, _F32, dev)
     pd = None if dlogprob is None else _like(dlogprob, "dlogprob", lead, _F32, dev)
     ph = None if dentropy is None else _like(dentropy, "dentropy", lead, _F32, dev)
-    with _on(stream, logits, tokens, lse, entropy, dlogprob, dentropy, out):
-        dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
-        rc = load().ibwd_token_logprobs_bwd(logits.data_ptr(), _CODE[logits.dtype], step, pt, temperature, pl, pe, pd,
-                                            ph, dx.data_ptr(), step if dxs is None else dxs, rows, vocab,
-                                            _stream(None))
+    dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
+    rc = load().ibwd_token_logprobs_bwd(logits.data_ptr(), _CODE[logits.dtype], step, pt, temperature, pl, pe, pd,
+                                        ph, dx.data_ptr(), step if dxs is None else dxs, rows, vocab,
+                                        _current_stream(logits.device.index))
     _check(rc, "ibwd_token_logprobs_bwd")
     return dx
 
@@ -280,13 +274,14 @@ def distill_fwd(logits, ids, teacher, temperature: float = 1.0, stream=None):
     probabilities `teacher` (float32).  With p the softmax of teacher / T over
     the kept slots and q that of logits / T over the vocabulary,
     loss = T^2 sum p (log p - log q).  Returns (loss, lse)."""
+    if stream is not None:
+        return _on(stream, distill_fwd, logits, ids, teacher, temperature)
     rows, vocab, step = _rows(logits, "logits")
     pi, pt, k = _kept(logits, ids, teacher)
-    with _on(stream, logits, ids, teacher):
-        loss = torch.empty(logits.shape[:-1], dtype=_F32, device=logits.device)
-        lse = torch.empty_like(loss)
-        rc = load().ibwd_distill_fwd(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature,
-                                     loss.data_ptr(), lse.data_ptr(), rows, vocab, _stream(None))
+    loss = torch.empty(logits.shape[:-1], dtype=_F32, device=logits.device)
+    lse = torch.empty_like(loss)
+    rc = load().ibwd_distill_fwd(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature,
+                                 loss.data_ptr(), lse.data_ptr(), rows, vocab, _current_stream(logits.device.index))
     _check(rc, "ibwd_distill_fwd")
     return loss, lse
 
@@ -294,15 +289,16 @@ def distill_fwd(logits, ids, teacher, temperature: float = 1.0, stream=None):
 def distill_bwd(logits, ids, teacher, lse, dloss, temperature: float = 1.0, out=None, stream=None):
     """Gradient of distill_fwd's losses with respect to the logits, given the
     losses' own gradient dloss; `out` may supply it, the logits among it."""
+    if stream is not None:
+        return _on(stream, distill_bwd, logits, ids, teacher, lse, dloss, temperature, out)
     rows, vocab, step = _rows(logits, "logits")
     pi, pt, k = _kept(logits, ids, teacher)
     lead = logits.shape[:-1]
     pl = _like(lse, "lse", lead, _F32, logits.device)
     pd = _like(dloss, "dloss", lead, _F32, logits.device)
-    with _on(stream, logits, ids, teacher, lse, dloss, out):
-        dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
-        rc = load().ibwd_distill_bwd(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature, pl, pd,
-                                     dx.data_ptr(), step if dxs is None else dxs, rows, vocab, _stream(None))
+    dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
+    rc = load().ibwd_distill_bwd(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature, pl, pd,
+                                 dx.data_ptr(), step if dxs is None else dxs, rows, vocab, _current_stream(logits.device.index))
     _check(rc, "ibwd_distill_bwd")
     return dx
 
@@ -312,15 +308,16 @@ def distill_grad(logits, ids, teacher, row_weight=None, grad_scale: float = 1.0,
     """Loss and gradient in one call: (loss, dlogits) with dlogits the
     gradient of grad_scale * sum row_weight * loss (row_weight float32, one a
     row; None for 1).  `out` may supply dlogits, the logits among it."""
+    if stream is not None:
+        return _on(stream, distill_grad, logits, ids, teacher, row_weight, grad_scale, temperature, out)
     rows, vocab, step = _rows(logits, "logits")
     pi, pt, k = _kept(logits, ids, teacher)
     lead = logits.shape[:-1]
     pw = None if row_weight is None else _like(row_weight, "row_weight", lead, _F32, logits.device)
-    with _on(stream, logits, ids, teacher, row_weight, out):
-        loss = torch.empty(lead, dtype=_F32, device=logits.device)
-        dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
-        rc = load().ibwd_distill_grad(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature, pw,
-                                      grad_scale, loss.data_ptr(), dx.data_ptr(), step if dxs is None else dxs, rows,
-                                      vocab, _stream(None))
+    loss = torch.empty(lead, dtype=_F32, device=logits.device)
+    dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
+    rc = load().ibwd_distill_grad(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature, pw,
+                                  grad_scale, loss.data_ptr(), dx.data_ptr(), step if dxs is None else dxs, rows,
+                                  vocab, _current_stream(logits.device.index))
     _check(rc, "ibwd_distill_grad")
     return loss, dx
