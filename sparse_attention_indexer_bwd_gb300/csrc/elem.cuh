@@ -23,6 +23,22 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
+// A pair of 16-bit elements, the lower half first.
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2_of(float2 v, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2_of(float2 v, __half) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ void unpack(uint4 r, float (&v)[4], float) {
   v[0] = __uint_as_float(r.x);
   v[1] = __uint_as_float(r.y);

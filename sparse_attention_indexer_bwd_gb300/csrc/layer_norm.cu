@@ -7,10 +7,11 @@
 //
 // A team of threads holds a row in registers (16 elements a thread at most),
 // so every element is read once: 8 to 32 lanes of a warp for short rows, a
-// thread block for longer ones.  Teams stay resident and walk the rows, the
-// next row's loads in flight while the current one is reduced; gamma and beta
-// stay in registers, and so do the backward pass's column sums of the team's
-// rows.  Those meet in a fixed order: a block's teams in shared memory, the
+// thread block for longer ones.  Teams stay resident and walk the rows; each
+// thread copies its own elements of the next rows into its own slots of a
+// shared-memory ring (cp.async), so several rows are in flight without
+// registers or barriers.  gamma and beta stay in registers, and so do the
+// backward pass's column sums of the team's rows.  Those meet in a fixed order: a block's teams in shared memory, the
 // blocks of a cluster through distributed shared memory, the clusters in a
 // second small kernel.  Rows too wide for a block take several passes.
 #include <cooperative_groups.h>
@@ -30,6 +31,10 @@ constexpr int kThreads = 256;     // block of several teams, and of the kernels 
 constexpr int kMaxTeam = 512;     // threads of a block that is one team
 constexpr int kCluster = 8;       // blocks whose column sums meet before they are written
 constexpr int kElems = 16;        // elements of a row a thread holds at most
+// Rows of a team in flight or in work: four, or three where a row of 8192
+// elements of x and dy takes 64 KB (227 KB of shared memory a block).
+template <typename TX, typename TD>
+constexpr int kStagesOf = sizeof(TX) + sizeof(TD) > 6 ? 3 : 4;
 constexpr int kMaxTeamWidth = kMaxTeam * kElems;
 
 // VEC consecutive elements as they lie in memory.
@@ -44,6 +49,8 @@ struct Chunk {
         reinterpret_cast<uint4*>(e)[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
     } else if constexpr (kBytes == 8) {
       *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) e[i] = p[i];
@@ -56,9 +63,55 @@ struct Chunk {
         st_stream(reinterpret_cast<uint4*>(p) + i, reinterpret_cast<const uint4*>(e)[i]);
     } else if constexpr (kBytes == 8) {
       *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(e);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) p[i] = e[i];
+    }
+  }
+};
+
+// A thread's slots in a ring of rows in shared memory: K chunks a row, each in
+// pieces of at most 16 bytes that lie side by side for neighbouring threads.
+// The thread that copies a chunk is the only one that reads it.  A copy takes
+// 4, 8 or 16 bytes; single 16-bit elements have none.
+template <typename T, int VEC, int K>
+struct Ring {
+  static constexpr int kBytes = VEC * (int)sizeof(T);
+  static constexpr bool kAsync = kBytes >= 4;
+  static constexpr int kPiece = kBytes < 16 ? kBytes : 16;
+  static constexpr int kRow = K * kBytes;  // bytes of a thread and row
+  uint32_t base;                           // of this thread
+  uint32_t pitch;                          // bytes between the pieces of a thread
+  __device__ Ring(unsigned char* smem, int t, int threads)
+      : base(smem_u32(smem) + t * kPiece), pitch(threads * kPiece) {}
+  __device__ __forceinline__ void copy(int stage, int k, const T* src) const {
+#pragma unroll
+    for (int i = 0; i < kBytes / kPiece; ++i) {
+      const uint32_t dst = base + ((stage * K + k) * (kBytes / kPiece) + i) * pitch;
+      const char* from = reinterpret_cast<const char*>(src) + i * kPiece;
+      if constexpr (kPiece == 16)
+        cp_async16(dst, from, 16);
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(kPiece) : "memory");
+    }
+  }
+  __device__ __forceinline__ void read(int stage, int k, Chunk<T, VEC>& c) const {
+#pragma unroll
+    for (int i = 0; i < kBytes / kPiece; ++i) {
+      const uint32_t src = base + ((stage * K + k) * (kBytes / kPiece) + i) * pitch;
+      if constexpr (kPiece == 16) {
+        reinterpret_cast<uint4*>(c.e)[i] = ld_shared_v4(src);
+      } else if constexpr (kPiece == 8) {
+        uint2 v;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(src));
+        *reinterpret_cast<uint2*>(c.e) = v;
+      } else {
+        uint32_t v;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(src));
+        *reinterpret_cast<uint32_t*>(c.e) = v;
+      }
     }
   }
 };
@@ -70,9 +123,59 @@ __device__ __forceinline__ float weight(const void* w, int n, bool f32, float no
   return f32 ? static_cast<const float*>(w)[n] : to_f32(static_cast<const T*>(w)[n]);
 }
 
+// Packed pairs of fp32 (one instruction for two elements: the kernels below
+// are bound by instruction issue as soon as they are not by HBM).
+__device__ __forceinline__ uint64_t bits2(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  const uint64_t d = mul_f32x2(bits2(a), bits2(b));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  const uint64_t d = fma_f32x2(bits2(a), bits2(b), bits2(c));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Elements 2i and 2i + 1 of a chunk list as fp32, and back.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ float2 pair_of(const Chunk<T, VEC> (&c)[K], int i) {
+  if constexpr (VEC == 1) {
+    return make_float2(to_f32(c[2 * i].e[0]), to_f32(c[2 * i + 1].e[0]));
+  } else {
+    const T* e = &c[2 * i / VEC].e[2 * i % VEC];
+    if constexpr (sizeof(T) == 4) {
+      return make_float2(to_f32(e[0]), to_f32(e[1]));
+    } else {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(e);
+      return unpack2(w, T{});
+    }
+  }
+}
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void set_pair(Chunk<T, VEC> (&c)[K], int i, float2 v) {
+  if constexpr (VEC == 1) {
+    c[2 * i].e[0] = from_f32<T>(v.x);
+    c[2 * i + 1].e[0] = from_f32<T>(v.y);
+  } else {
+    T* e = &c[2 * i / VEC].e[2 * i % VEC];
+    if constexpr (sizeof(T) == 4) {
+      e[0] = v.x;
+      e[1] = v.y;
+    } else {
+      *reinterpret_cast<uint32_t*>(e) = pack2_of(v, T{});
+    }
+  }
+}
+
 // Sums of K values over a team, the same bits in each of its threads.  TEAM
-// lanes of a warp, or 0 for the block: then `stage` holds 2 * 32 * K floats,
-// used in turn (`turn` flips), so one barrier a call is enough.
+// lanes of a warp, or 0 for the block: then `stage` holds 2 * K * 32 floats,
+// zero beyond the block's warps and used in turn (`turn` flips), so one
+// barrier a call is enough.
 template <int TEAM, int K>
 __device__ __forceinline__ void team_sums(float (&v)[K], float* stage, int& turn) {
 #pragma unroll
@@ -80,92 +183,138 @@ __device__ __forceinline__ void team_sums(float (&v)[K], float* stage, int& turn
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if constexpr (TEAM == 0) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     float* s = stage + turn * 32 * K;
     turn ^= 1;
-    if (lane == 0)
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int k = 0; k < K; ++k) s[warp * K + k] = v[k];
+      for (int k = 0; k < K; ++k) s[k * 32 + (threadIdx.x >> 5)] = v[k];
     __syncthreads();
+    float4 f[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.f;
-    for (int w = 0; w < nw; ++w)
+    for (int k = 0; k < K; ++k) f[k] = *reinterpret_cast<const float4*>(s + k * 32);
+    for (int w = 4; w < (int)(blockDim.x >> 5); w += 4)
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += s[w * K + k];
+      for (int k = 0; k < K; ++k) {
+        const float4 o = *reinterpret_cast<const float4*>(s + k * 32 + w);
+        f[k].x += o.x;
+        f[k].y += o.y;
+        f[k].z += o.z;
+        f[k].w += o.w;
+      }
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = (f[k].x + f[k].y) + (f[k].z + f[k].w);
   }
+}
+
+// s / n given 1 / n, to the last bit but one (a constant row gets its value):
+// the remainder of the product is added back.
+__device__ __forceinline__ float over_n(float s, float n, float inv_n) {
+  const float q = s * inv_n;
+  return fmaf(fmaf(-q, n, s), inv_n, q);
 }
 
 template <typename TX, typename TY, int VEC, int K, int TEAM>
 __global__ void __launch_bounds__(TEAM ? kThreads : kMaxTeam) norm_fwd_team(NormFwdArgs a) {
-  __shared__ float stage[64];
+  constexpr int kStages = 4;
+  extern __shared__ __align__(16) unsigned char smem[];  // the ring
+  __shared__ __align__(16) float stage[64];
   constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
+  constexpr int P = K * VEC / 2;  // pairs a thread
   const int team = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0;
   const int t = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x, T = TEAM ? TEAM : blockDim.x;
   const int nvec = a.N / VEC;
   const float inv_n = 1.f / a.N;
-  float g[K][VEC], b[K][VEC];
+  if (TEAM == 0 && threadIdx.x < 64) stage[threadIdx.x] = 0.f;
+  if (TEAM == 0) __syncthreads();
+  float2 g[P], b[P];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int i = 0; i < P; ++i) {
+    float w[4];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int j = t + k * T, n = j * VEC + i;
-      g[k][i] = j < nvec ? weight<TX>(a.gamma, n, a.w_type == 0, 1.f) : 0.f;
-      b[k][i] = j < nvec ? weight<TX>(a.beta, n, a.w_type == 0, 0.f) : 0.f;
+    for (int h = 0; h < 2; ++h) {
+      const int e = 2 * i + h, j = t + e / VEC * T, n = j * VEC + e % VEC;
+      w[h] = j < nvec ? weight<TX>(a.gamma, n, a.w_type == 0, 1.f) : 0.f;
+      w[2 + h] = j < nvec ? weight<TX>(a.beta, n, a.w_type == 0, 0.f) : 0.f;
     }
-  Chunk<TX, VEC> cur[K], nxt[K];
-  auto load = [&](Chunk<TX, VEC>(&c)[K], long long r) {
-    const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (r < a.rows && t + k * T < nvec) c[k].load(x + (t + k * T) * VEC);
-  };
-  int turn = 0;
+    g[i] = make_float2(w[0], w[1]);
+    b[i] = make_float2(w[2], w[3]);
+  }
+  using XRing = Ring<TX, VEC, K>;
+  const XRing ring(smem, threadIdx.x, blockDim.x);
+  Chunk<TX, VEC> cur[K] = {};  // (zero where a thread has no element)
   const long long step = (long long)gridDim.x * TPB;
-  long long base = (long long)blockIdx.x * TPB;
-  load(cur, base + team);
-  for (; base < a.rows; base += step) {
-    const long long r = base + team;
-    load(nxt, r + step);
-    float v[K][VEC];
-    float s[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        v[k][i] = t + k * T < nvec ? to_f32(cur[k].e[i]) : 0.f;
-        s[0] += v[k][i];
-      }
-    team_sums<TEAM>(s, stage, turn);
-    const float mean = s[0] / a.N;  // (a constant row has its mean exactly)
-    float q[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (t + k * T < nvec)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          v[k][i] -= mean;
-          q[0] = fmaf(v[k][i], v[k][i], q[0]);
-        }
-    team_sums<TEAM>(q, stage, turn);
-    const float rstd = 1.f / sqrtf(fmaf(q[0], inv_n, a.eps));
-    if (r < a.rows) {
-      TY* y = static_cast<TY*>(a.y) + r * a.y_stride;
+  const long long first = (long long)blockIdx.x * TPB + team;
+  const TX* xr = static_cast<const TX*>(a.x) + first * a.x_stride + t * VEC;  // of the row to fetch
+  const long long x_step = step * a.x_stride, y_step = step * a.y_stride;
+  TY* yr = static_cast<TY*>(a.y) + first * a.y_stride + t * VEC;
+  auto fetch = [&](int slot, bool on) {
+    if (XRing::kAsync && on)
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec) {
-          Chunk<TY, VEC> o;
+        if (t + k * T < nvec) ring.copy(slot, k, xr + k * T * VEC);
+    xr += x_step;
+    cp_async_commit();
+  };
+  int turn = 0, slot = 0;
+  if (XRing::kAsync)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o.e[i] = from_f32<TY>(fmaf(v[k][i] * rstd, g[k][i], b[k][i]));
-          o.store(y + (t + k * T) * VEC);
-        }
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * step < a.rows);
+  // (a block's teams leave together: their rows differ by less than a step)
+  for (long long r = first; r - team < a.rows; r += step) {
+    const bool on = r < a.rows;
+    if (XRing::kAsync) {
+      fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
+      cp_async_wait<kStages - 1>();
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (on && t + k * T < nvec) {
+        if constexpr (XRing::kAsync)
+          ring.read(slot, k, cur[k]);
+        else
+          cur[k].load(xr + k * T * VEC);
+      }
+    if (!XRing::kAsync) xr += x_step;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    float2 v[P], sum = both(0.f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      v[i] = pair_of(cur, i);
+      sum = add2(sum, v[i]);
+    }
+    float s[1] = {sum.x + sum.y};
+    team_sums<TEAM>(s, stage, turn);
+    const float mean = over_n(s[0], (float)a.N, inv_n);
+    sum = both(0.f);
+    // elements the thread does not have are left out of the squares
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      v[i] = add2(v[i], both(-mean));
+      if constexpr (VEC > 1) {
+        if (t + 2 * i / VEC * T < nvec) sum = fma2(v[i], v[i], sum);
+      } else {
+        if (t + 2 * i * T < nvec) sum.x = fmaf(v[i].x, v[i].x, sum.x);
+        if (t + (2 * i + 1) * T < nvec) sum.y = fmaf(v[i].y, v[i].y, sum.y);
+      }
+    }
+    float q[1] = {sum.x + sum.y};
+    team_sums<TEAM>(q, stage, turn);
+    const float rstd = rsqrtf(fmaf(q[0], inv_n, a.eps));
+    if (on) {
+      Chunk<TY, VEC> o[K];
+#pragma unroll
+      for (int i = 0; i < P; ++i) set_pair(o, i, fma2(mul2(v[i], both(rstd)), g[i], b[i]));
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (t + k * T < nvec) o[k].store(yr + k * T * VEC);
       if (t == 0) {
         if (a.mean) a.mean[r] = mean;
         if (a.rstd) a.rstd[r] = rstd;
       }
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) cur[k] = nxt[k];
+    yr += y_step;
   }
+  cp_async_wait_all();
 }
 
 // Column sums of a block, [2][N] in shared memory in the order of the
@@ -202,103 +351,139 @@ __device__ __forceinline__ void write_sums(const NormBwdArgs& a, const float* su
 
 template <typename TX, typename TD, int VEC, int K, int TEAM>
 __global__ void __launch_bounds__(TEAM ? kThreads : kMaxTeam) norm_bwd_team(NormBwdArgs a, int cluster) {
-  extern __shared__ float sums[];  // [2][N]
-  __shared__ float stage[128];
+  constexpr int kStages = kStagesOf<TX, TD>;
+  extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end [2][N] column sums
+  float* sums = reinterpret_cast<float*>(smem);
+  __shared__ __align__(16) float stage[128];
   constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
-  // single elements take a register each: 16 of two rows would spill
-  constexpr bool kAhead = VEC > 1;
+  constexpr int P = K * VEC / 2;  // pairs a thread
   const int team = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0;
   const int t = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x, T = TEAM ? TEAM : blockDim.x;
   const int nvec = a.N / VEC;
   const float inv_n = 1.f / a.N;
-  float g[K][VEC], dg[K][VEC], db[K][VEC];
+  if (TEAM == 0)
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) stage[i] = 0.f;
+  if (TEAM == 0) __syncthreads();
+  float2 g[P], dg[P], db[P];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int i = 0; i < P; ++i) {
+    float w[2];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int j = t + k * T;
-      g[k][i] = j < nvec ? weight<TX>(a.gamma, j * VEC + i, a.w_type == 0, 1.f) : 0.f;
-      dg[k][i] = db[k][i] = 0.f;
+    for (int h = 0; h < 2; ++h) {
+      const int e = 2 * i + h, j = t + e / VEC * T;
+      w[h] = j < nvec ? weight<TX>(a.gamma, j * VEC + e % VEC, a.w_type == 0, 1.f) : 0.f;
     }
-  Chunk<TX, VEC> cx[K], nx[K];
-  Chunk<TD, VEC> cd[K], nd[K];
-  float cm = 0.f, cr = 0.f, nm = 0.f, nr = 0.f;
-  auto load = [&](Chunk<TX, VEC>(&x)[K], Chunk<TD, VEC>(&d)[K], float& mean, float& rstd, long long r) {
-    if (r >= a.rows) return;
-    const TX* px = static_cast<const TX*>(a.x) + r * a.x_stride;
-    const TD* pd = static_cast<const TD*>(a.dy) + r * a.dy_stride;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (t + k * T < nvec) {
-        x[k].load(px + (t + k * T) * VEC);
-        d[k].load(pd + (t + k * T) * VEC);
-      }
-    mean = a.mean[r];
-    rstd = a.rstd[r];
-  };
-  int turn = 0;
+    g[i] = make_float2(w[0], w[1]);
+    dg[i] = db[i] = both(0.f);
+  }
+  using XRing = Ring<TX, VEC, K>;
+  using DRing = Ring<TD, VEC, K>;
+  constexpr bool kAsync = XRing::kAsync && DRing::kAsync;
+  const XRing xring(smem, threadIdx.x, blockDim.x);
+  const DRing dring(smem + kStages * XRing::kRow * blockDim.x, threadIdx.x, blockDim.x);
+  // zero where a thread has no element: dy = 0 adds nothing to any sum
+  Chunk<TX, VEC> cx[K] = {};
+  Chunk<TD, VEC> cd[K] = {};
   const long long step = (long long)gridDim.x * TPB;
-  long long base = (long long)blockIdx.x * TPB;
-  if (kAhead) load(cx, cd, cm, cr, base + team);
-  for (; base < a.rows; base += step) {
-    const long long r = base + team;
-    const bool on = r < a.rows;
-    if (kAhead)
-      load(nx, nd, nm, nr, r + step);
-    else
-      load(cx, cd, cm, cr, r);
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (on && t + k * T < nvec)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float xh = (to_f32(cx[k].e[i]) - cm) * cr, dy = to_f32(cd[k].e[i]);
-          const float d = dy * g[k][i];
-          dg[k][i] = fmaf(dy, xh, dg[k][i]);
-          db[k][i] += dy;
-          s[0] += d;
-          s[1] = fmaf(d, xh, s[1]);
-        }
-    team_sums<TEAM>(s, stage, turn);
-    if (on) {
-      const float ma = s[0] * inv_n, mb = s[1] * inv_n;
-      TX* dx = static_cast<TX*>(a.dx) + r * a.dx_stride;
+  const long long first = (long long)blockIdx.x * TPB + team;
+  const TX* xr = static_cast<const TX*>(a.x) + first * a.x_stride + t * VEC;  // of the row to fetch
+  const TD* dr = static_cast<const TD*>(a.dy) + first * a.dy_stride + t * VEC;
+  TX* or_ = static_cast<TX*>(a.dx) + first * a.dx_stride + t * VEC;
+  const long long x_step = step * a.x_stride, d_step = step * a.dy_stride, o_step = step * a.dx_stride;
+  auto fetch = [&](int slot, bool on) {
+    if (kAsync && on)
 #pragma unroll
       for (int k = 0; k < K; ++k)
         if (t + k * T < nvec) {
-          Chunk<TX, VEC> o;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float xh = (to_f32(cx[k].e[i]) - cm) * cr;
-            o.e[i] = from_f32<TX>(cr * (fmaf(to_f32(cd[k].e[i]), g[k][i], -ma) - xh * mb));
-          }
-          o.store(dx + (t + k * T) * VEC);
+          xring.copy(slot, k, xr + k * T * VEC);
+          dring.copy(slot, k, dr + k * T * VEC);
         }
-    }
-    if (kAhead) {
+    xr += x_step;
+    dr += d_step;
+    cp_async_commit();
+  };
+  int turn = 0, slot = 0;
+  if (kAsync)
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        cx[k] = nx[k];
-        cd[k] = nd[k];
-      }
-      cm = nm;
-      cr = nr;
-    }
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * step < a.rows);
+  float nm = 0.f, nr = 0.f;  // the next row's statistics
+  if (first < a.rows) {
+    nm = a.mean[first];
+    nr = a.rstd[first];
   }
+  for (long long r = first; r - team < a.rows; r += step) {
+    const bool on = r < a.rows;
+    const float cm = nm, cr = nr;
+    if (r + step < a.rows) {
+      nm = a.mean[r + step];
+      nr = a.rstd[r + step];
+    }
+    if (kAsync) {
+      fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
+      cp_async_wait<kStages - 1>();
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (on && t + k * T < nvec) {
+        if constexpr (kAsync) {
+          xring.read(slot, k, cx[k]);
+          dring.read(slot, k, cd[k]);
+        } else {
+          cx[k].load(xr + k * T * VEC);
+          cd[k].load(dr + k * T * VEC);
+        }
+      }
+    if (!kAsync) {
+      xr += x_step;
+      dr += d_step;
+    }
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    float s[2] = {0.f, 0.f};
+    if (on) {
+      float2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 xh = mul2(add2(pair_of(cx, i), both(-cm)), both(cr)), dy = pair_of(cd, i);
+        const float2 d = mul2(dy, g[i]);
+        dg[i] = fma2(dy, xh, dg[i]);
+        db[i] = add2(db[i], dy);
+        s0 = add2(s0, d);
+        s1 = fma2(d, xh, s1);
+      }
+      s[0] = s0.x + s0.y;
+      s[1] = s1.x + s1.y;
+    }
+    team_sums<TEAM>(s, stage, turn);
+    if (on) {
+      const float ma = s[0] * inv_n, mb = s[1] * inv_n;
+      Chunk<TX, VEC> o[K];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 xh = mul2(add2(pair_of(cx, i), both(-cm)), both(cr));
+        const float2 d = fma2(pair_of(cd, i), g[i], both(-ma));
+        set_pair(o, i, mul2(fma2(xh, both(-mb), d), both(cr)));
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (t + k * T < nvec) o[k].store(or_ + k * T * VEC);
+    }
+    or_ += o_step;
+  }
+  cp_async_wait_all();
   if (!a.dgamma && !a.dbeta) return;
+  __syncthreads();  // the rings are done with
   // the teams' sums, in the teams' order
   for (int w = 0; w < TPB; ++w) {
     if (w == team)
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const int c = (t + k * T) * VEC + i;
-            sums[c] = w ? sums[c] + dg[k][i] : dg[k][i];
-            sums[a.N + c] = w ? sums[a.N + c] + db[k][i] : db[k][i];
-          }
+      for (int e = 0; e < 2 * P; ++e) {
+        const int j = t + e / VEC * T, c = j * VEC + e % VEC;
+        if (j < nvec) {
+          const float vg = e & 1 ? dg[e / 2].y : dg[e / 2].x, vb = e & 1 ? db[e / 2].y : db[e / 2].x;
+          sums[c] = w ? sums[c] + vg : vg;
+          sums[a.N + c] = w ? sums[a.N + c] + vb : vb;
+        }
+      }
     if (TPB > 1) __syncthreads();
   }
   griddep_launch_dependents();
@@ -335,7 +520,9 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_join(const float* part, int
 
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kThreads) norm_fwd_wide(NormFwdArgs a) {
-  __shared__ float stage[64];
+  __shared__ __align__(16) float stage[64];
+  if (threadIdx.x < 64) stage[threadIdx.x] = 0.f;
+  __syncthreads();
   int turn = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
@@ -363,7 +550,9 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_wide(NormFwdArgs a) {
 
 template <typename TX, typename TD>
 __global__ void __launch_bounds__(kThreads) norm_bwd_wide(NormBwdArgs a) {
-  __shared__ float stage[128];
+  __shared__ __align__(16) float stage[128];
+  if (threadIdx.x < 128) stage[threadIdx.x] = 0.f;
+  __syncthreads();
   int turn = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
@@ -451,7 +640,7 @@ TeamShape team_shape(long long rows, int N, int elems, int teams_per_block, int 
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), const TeamShape& s, size_t smem, cudaStream_t st, Args... args) {
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {  // beyond 48 KB with the static part
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
@@ -479,7 +668,9 @@ template <typename TX, typename TY, int VEC, int K, int TEAM>
 cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
   const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, kFwdPerSm, a.num_sms,
                                  false);
-  return launch_cluster(norm_fwd_team<TX, TY, VEC, K, TEAM>, s, 0, st, a);
+  using XRing = Ring<TX, VEC, K>;
+  const size_t smem = XRing::kAsync ? (size_t)4 * XRing::kRow * s.threads : 0;
+  return launch_cluster(norm_fwd_team<TX, TY, VEC, K, TEAM>, s, smem, st, a);
 }
 
 template <typename TX, typename TY>
@@ -498,6 +689,12 @@ cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t st) {
     if (a.N <= 32 * kElems) return fwd_team<TX, TY, V, kElems / V, 32>(a, st);
     return fwd_team<TX, TY, V, kElems / V, 0>(a, st);
   }
+  // else 4 bytes of x
+  constexpr int W = V / 4;
+  if (W > 1 && a.N % W == 0 && aligned(a.x, a.x_stride, sizeof(TX), 4) && aligned(a.y, a.y_stride, ysize, W * ysize)) {
+    if (a.N <= 32 * kElems) return fwd_team<TX, TY, W, kElems / W, 32>(a, st);
+    return fwd_team<TX, TY, W, kElems / W, 0>(a, st);
+  }
   if (a.N <= 128) return fwd_team<TX, TY, 1, 4, 32>(a, st);
   if (a.N <= 32 * kElems) return fwd_team<TX, TY, 1, kElems, 32>(a, st);
   return fwd_team<TX, TY, 1, kElems, 0>(a, st);
@@ -513,8 +710,11 @@ cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
   const bool sums = a.dgamma || a.dbeta;
   const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, kBwdPerSm, a.num_sms,
                                  sums);
-  cudaError_t e = launch_cluster(norm_bwd_team<TX, TD, VEC, K, TEAM>, s, sums ? 2 * a.N * sizeof(float) : 0, st, a,
-                                 s.cluster);
+  using XRing = Ring<TX, VEC, K>;
+  using DRing = Ring<TD, VEC, K>;
+  const size_t rings = (size_t)kStagesOf<TX, TD> * (XRing::kRow + DRing::kRow) * s.threads;
+  const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, sums ? 2 * a.N * sizeof(float) : 0);
+  cudaError_t e = launch_cluster(norm_bwd_team<TX, TD, VEC, K, TEAM>, s, smem, st, a, s.cluster);
   const int groups = s.blocks / s.cluster;
   if (e == cudaSuccess && sums && groups > 1) e = join_sums(a, groups, st);
   return e;
@@ -549,6 +749,12 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
     if (a.N <= 32 * V) return bwd_team<TX, TD, V, 1, 32>(a, st);
     if (a.N <= 32 * kElems) return bwd_team<TX, TD, V, kElems / V, 32>(a, st);
     return bwd_team<TX, TD, V, kElems / V, 0>(a, st);
+  }
+  constexpr int W = V / 4;
+  if (W > 1 && a.N % W == 0 && aligned(a.x, a.x_stride, sizeof(TX), 4) && aligned(a.dx, a.dx_stride, sizeof(TX), 4) &&
+      aligned(a.dy, a.dy_stride, dsize, W * dsize)) {
+    if (a.N <= 32 * kElems) return bwd_team<TX, TD, W, kElems / W, 32>(a, st);
+    return bwd_team<TX, TD, W, kElems / W, 0>(a, st);
   }
   if (a.N <= 128) return bwd_team<TX, TD, 1, 4, 32>(a, st);
   if (a.N <= 32 * kElems) return bwd_team<TX, TD, 1, kElems, 32>(a, st);
