@@ -20,6 +20,7 @@
 
 #include "elem.cuh"
 #include "kcommon.cuh"
+#include "packed.cuh"
 #include "train.h"
 
 namespace cg = cooperative_groups;
@@ -122,24 +123,6 @@ __device__ __forceinline__ float weight(const void* w, int n, bool f32, float no
   if (w == nullptr) return none;
   return f32 ? static_cast<const float*>(w)[n] : to_f32(static_cast<const T*>(w)[n]);
 }
-
-// Packed pairs of fp32 (one instruction for two elements: the kernels below
-// are bound by instruction issue as soon as they are not by HBM).
-__device__ __forceinline__ uint64_t bits2(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  const uint64_t d = mul_f32x2(bits2(a), bits2(b));
-  return *reinterpret_cast<const float2*>(&d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  const uint64_t d = fma_f32x2(bits2(a), bits2(b), bits2(c));
-  return *reinterpret_cast<const float2*>(&d);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Elements 2i and 2i + 1 of a chunk list as fp32, and back.
 template <typename T, int VEC, int K>

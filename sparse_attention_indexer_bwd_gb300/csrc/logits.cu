@@ -14,12 +14,19 @@
 // parts' statistics are exchanged through distributed shared memory and
 // joined in the blocks' order, so few rows still fill the machine and every
 // result is bitwise reproducible.
+//
+// Bound by HBM when an element costs few enough instructions: unpacking, the
+// maximum, two packed operations for d, one exponential and one or two packed
+// sums.  Where the loss and the gradient come from one call the row's part
+// stays in shared memory between its two passes, so it is read once.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 
 #include "elem.cuh"
 #include "internal.h"
+#include "packed.cuh"
+#include "ptx.cuh"
 #include "train.h"
 
 namespace cg = cooperative_groups;
@@ -27,13 +34,14 @@ namespace cg = cooperative_groups;
 namespace ibwd {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = 128;
-constexpr int kMaxKept = 1024;
 constexpr int kCand = 1024;      // candidates a block ranks for the top alternatives
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
+// An exponent whose power of two is 0, kept finite so that 0 times it is 0.
+constexpr float kLeast = -1e20f;
 #define NEG_INF (-INFINITY)
 
 struct Stat {
@@ -48,7 +56,7 @@ template <bool U>
 __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
   const float m = fmaxf(a.m, b.m), mr = finite_max(m);
   // a part without terms has s = u = 0; its difference is kept finite for u
-  const float da = fmaxf((a.m - mr) * c, -1.0e30f), db = fmaxf((b.m - mr) * c, -1.0e30f);
+  const float da = fmaxf((a.m - mr) * c, kLeast), db = fmaxf((b.m - mr) * c, kLeast);
   const float fa = ex2(da), fb = ex2(db);
   Stat r;
   r.m = m;
@@ -65,7 +73,7 @@ __device__ __forceinline__ void add(Stat& t, const float (&x)[N], float c) {
 #pragma unroll
   for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
   if (m > t.m) {
-    const float d = fmaxf((t.m - m) * c, -1.0e30f), f = ex2(d);
+    const float d = fmaxf((t.m - m) * c, kLeast), f = ex2(d);
     if (U) t.u = f * (t.u + t.s * d);
     t.s *= f;
     t.m = m;
@@ -76,7 +84,7 @@ __device__ __forceinline__ void add(Stat& t, const float (&x)[N], float c) {
     const float d = (x[i] - mr) * c;
     const float e = ex2(d);
     t.s += e;
-    if (U) t.u = fmaf(e, fmaxf(d, -1.0e30f), t.u);  // 0 for a masked logit
+    if (U) t.u = fmaf(e, fmaxf(d, kLeast), t.u);  // 0 for a masked logit
   }
 }
 
@@ -101,23 +109,11 @@ struct Part {
   __device__ int single_at(int i) const { return i < nhead ? i : i + nvec * kVec<T>; }  // offset from head
 };
 
+// The careful statistic: any values, one element at a time.
 template <typename T, bool U>
-__device__ __forceinline__ Stat part_stat(const Part<T>& p, float c) {
+__device__ __noinline__ Stat part_stat_any(const Part<T>& p, float c) {
   Stat t{NEG_INF, 0.f, 0.f};
-  constexpr int UNR = 4;
-  int i = threadIdx.x;
-  for (; i + (UNR - 1) * kThreads < p.nvec; i += UNR * kThreads) {
-    uint4 r[UNR];
-#pragma unroll
-    for (int k = 0; k < UNR; ++k) r[k] = ld_stream(p.vec(i + k * kThreads));
-#pragma unroll
-    for (int k = 0; k < UNR; ++k) {
-      float v[kVec<T>];
-      unpack(r[k], v, T{});
-      add<U>(t, v, c);
-    }
-  }
-  for (; i < p.nvec; i += kThreads) {
+  for (int i = threadIdx.x; i < p.nvec; i += kThreads) {
     float v[kVec<T>];
     unpack(ld_stream(p.vec(i)), v, T{});
     add<U>(t, v, c);
@@ -127,6 +123,182 @@ __device__ __forceinline__ Stat part_stat(const Part<T>& p, float c) {
     add<U>(t, v, c);
   }
   return t;
+}
+
+// The fast statistic starts from the maximum kFloor, so that x - m is always
+// finite: a logit far below it (a mask) adds 2^-huge = 0.  It does not hold
+// for rows without a logit above kFloor, nor for scales that make kFloor
+// small; those take the careful one.
+constexpr float kFloor = -9.9499216e29f;  // 0xF1490000: also a bf16
+constexpr float kLeastScale = 1e-20f, kMostScale = 1e6f;
+
+struct Run {
+  float m;
+  float2 s, u;  // two interleaved sums
+};
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// max(a, kFloor) that keeps a NaN.
+__device__ __forceinline__ float floor_nan(float a) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(kFloor));
+  return d;
+}
+
+template <typename T>
+__device__ __forceinline__ float max_of(const uint4* r, int n) {
+  if constexpr (sizeof(T) == 4) {
+    float m = kFloor;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)),
+                         fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
+    return m;
+  } else {
+    uint32_t m = max2(max2(r[0].x, r[0].y, T{}), max2(r[0].z, r[0].w, T{}), T{});
+#pragma unroll
+    for (int i = 1; i < n; ++i) m = max2(m, max2(max2(r[i].x, r[i].y, T{}), max2(r[i].z, r[i].w, T{}), T{}), T{});
+    const float2 f = unpack2(m, T{});
+    return fmaxf(f.x, f.y);
+  }
+}
+
+__device__ __forceinline__ void raise(Run& t, float m, float c, bool u) {
+  if (m > t.m) {
+    const float d = fmaxf((t.m - m) * c, kLeast), f = ex2(d);
+    if (u) {
+      t.u.x = f * fmaf(t.s.x, d, t.u.x);
+      t.u.y = f * fmaf(t.s.y, d, t.u.y);
+    }
+    t.s.x *= f;
+    t.s.y *= f;
+    t.m = m;
+  }
+}
+
+template <bool U>
+__device__ __forceinline__ void add_pair(Run& t, float2 x, float2 neg_m, float2 c2) {
+  if (U) {  // 0 * -inf is no term: masked logits are lifted to kFloor
+    x.x = floor_nan(x.x);
+    x.y = floor_nan(x.y);
+  }
+  const float2 d = mul2(add2(x, neg_m), c2);
+  const float2 e = make_float2(ex2(d.x), ex2(d.y));
+  t.s = add2(t.s, e);
+  if (U) t.u = fma2(e, d, t.u);
+}
+
+template <typename T, bool U, int N>
+__device__ __forceinline__ void add_vectors(Run& t, const uint4 (&r)[N], float c) {
+  raise(t, max_of<T>(r, N), c, U);
+  const float2 nm = both(-t.m), c2 = both(c);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      add_pair<U>(t, make_float2(__uint_as_float(r[i].x), __uint_as_float(r[i].y)), nm, c2);
+      add_pair<U>(t, make_float2(__uint_as_float(r[i].z), __uint_as_float(r[i].w)), nm, c2);
+    } else {
+      add_pair<U>(t, unpack2(r[i].x, T{}), nm, c2);
+      add_pair<U>(t, unpack2(r[i].y, T{}), nm, c2);
+      add_pair<U>(t, unpack2(r[i].z, T{}), nm, c2);
+      add_pair<U>(t, unpack2(r[i].w, T{}), nm, c2);
+    }
+  }
+}
+
+template <typename T, bool U>
+__device__ __forceinline__ Stat finish(Run& t, const Part<T>& p, float c) {
+  if ((int)threadIdx.x < p.singles()) {
+    const float x = to_f32(p.head[p.single_at(threadIdx.x)]);
+    raise(t, fmaxf(x, kFloor), c, U);
+    const float d = (floor_nan(x) - t.m) * c, e = ex2(d);
+    t.s.x += e;
+    if (U) t.u.x = fmaf(e, d, t.u.x);
+  }
+  return Stat{t.m, t.s.x + t.s.y, t.u.x + t.u.y};
+}
+
+constexpr int kUnroll = 4;
+
+// Streamed from global memory, the next vectors' loads ahead of the sums.
+template <typename T, bool U>
+__device__ __forceinline__ Stat part_stat(const Part<T>& p, float c) {
+  Run t{kFloor, {0.f, 0.f}, {0.f, 0.f}};
+  int i = threadIdx.x;
+  constexpr int kStep = kUnroll * kThreads;
+  if (i + (kUnroll - 1) * kThreads < p.nvec) {
+    uint4 r[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) r[k] = ld_stream(p.vec(i + k * kThreads));
+    for (i += kStep; i + (kUnroll - 1) * kThreads < p.nvec; i += kStep) {
+      uint4 n[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) n[k] = ld_stream(p.vec(i + k * kThreads));
+      add_vectors<T, U>(t, r, c);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) r[k] = n[k];
+    }
+    add_vectors<T, U>(t, r, c);
+  }
+  for (; i < p.nvec; i += kThreads) {
+    const uint4 r[1] = {ld_stream(p.vec(i))};
+    add_vectors<T, U>(t, r, c);
+  }
+  return finish<T, U>(t, p, c);
+}
+
+// Through shared memory, where the part stays: each thread copies the vectors
+// it reads itself, all of them at once, and takes them up as they arrive.
+constexpr int kGroups = 4;
+constexpr int kResident = kGroups * kUnroll * kThreads;  // vectors a part may have
+
+template <typename T>
+__device__ __forceinline__ void fetch_part(const Part<T>& p, uint32_t mine) {
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int i = threadIdx.x + (g * kUnroll + k) * kThreads;
+      if (i < p.nvec) cp_async16(mine + (g * kUnroll + k) * kThreads * 16, p.vec(i), 16);
+    }
+    cp_async_commit();
+  }
+}
+
+template <typename T, bool U>
+__device__ __forceinline__ Stat resident_stat(const Part<T>& p, uint32_t mine, float c) {
+  Run t{kFloor, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    if (g == 0) cp_async_wait<3>();
+    if (g == 1) cp_async_wait<2>();
+    if (g == 2) cp_async_wait<1>();
+    if (g == 3) cp_async_wait<0>();
+    const uint32_t from = mine + g * kUnroll * kThreads * 16;
+    if ((int)threadIdx.x + (g * kUnroll + kUnroll - 1) * kThreads < p.nvec) {
+      uint4 r[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) r[k] = ld_shared_v4(from + k * kThreads * 16);
+      add_vectors<T, U>(t, r, c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kUnroll - 1; ++k)
+        if ((int)threadIdx.x + (g * kUnroll + k) * kThreads < p.nvec) {
+          const uint4 r[1] = {ld_shared_v4(from + k * kThreads * 16)};
+          add_vectors<T, U>(t, r, c);
+        }
+    }
+  }
+  return finish<T, U>(t, p, c);
 }
 
 // Statistic of the whole block, in thread 0 .. kThreads - 1 alike.
@@ -197,12 +369,13 @@ __device__ __forceinline__ unsigned long long order_key(float x, int v) {
 }
 
 struct TopShared {
-  float segmax[kThreads];
+  uint32_t segmax[kThreads];
   unsigned long long cand[kCand];
   unsigned long long merge[kMaxTop * kMaxCluster];
   int merge_n[kMaxCluster];
   int hot[kThreads];
   int nhot, ncand;
+  uint32_t least, below;
   float bound;
   int warp_n[kThreads / 32];
 };
@@ -222,52 +395,71 @@ __device__ __forceinline__ void for_each(const Part<T>& p, int lo, F f) {
   }
 }
 
-__device__ __forceinline__ int block_count(int n, float* stage) {
-  return (int)block_sum((float)n, stage);  // exact: counts stay below 2^24
-}
-
 // The rare case of more than kCand entries at or above the bound (many equal
-// logits, or logits whose order follows the threads): the exact value of the
-// n-th largest by bisection over the order of fp32, then everything above it
-// and the equal ones of lowest index.
+// logits, or logits whose order follows the threads): the exact order of the
+// n-th largest by bisection, then everything above it and the equal ones of
+// lowest index.
 template <typename T>
-__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, float bound, float most,
-                                       TopShared& sh) {
-  auto above = [&](float cut) {  // entries of the part above `cut`
+__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, float bound, TopShared& sh) {
+  // masked logits and NaN are no entries
+  auto order = [](float x) { return x > NEG_INF ? order_bits(x) : 0u; };
+  // entries of the part above `cut`: their number, the least of them, and the
+  // largest at or below it
+  auto above = [&](uint32_t cut, uint32_t& least, uint32_t& below) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sh.ncand = 0;
+      sh.least = ~0u;
+      sh.below = 0;
+    }
+    __syncthreads();
     int k = 0;
-    for_each(p, lo, [&](float x, int) { k += (x > cut) ? 1 : 0; });
-    __syncthreads();
-    if (threadIdx.x == 0) sh.ncand = 0;
-    __syncthreads();
+    uint32_t l = ~0u, h = 0;
+    for_each(p, lo, [&](float x, int) {
+      const uint32_t key = order(x);
+      if (key > cut) {
+        ++k;
+        l = min(l, key);
+      } else {
+        h = max(h, key);
+      }
+    });
     if (k) atomicAdd(&sh.ncand, k);
+    atomicMin(&sh.least, l);
+    atomicMax(&sh.below, h);
     __syncthreads();
+    least = sh.least;
+    below = sh.below;
     return sh.ncand;
   };
-  uint32_t a = order_bits(bound), b = order_bits(most);
-  int count = above(bound);
-  bool equal = count < n;  // the cut is the n-th largest value itself
-  // entries above a: `count`, at least n; entries above b: fewer than n
+  // entries above a: `count`, at least n; entries above b: fewer than n.
+  // Both move to the nearest entries that occur.
+  uint32_t a = order_bits(bound), b = ~0u, least, below;
+  int count = above(a, least, below);
+  bool equal = count < n;  // a is the n-th largest itself
   while (!equal && count > kCand) {
-    if (b - a == 1) {  // more than kCand entries are equal to b's value
+    a = least - 1;
+    if (b - a == 1) {  // more than kCand entries are equal to b
       a = b;
       equal = true;
       break;
     }
     const uint32_t mid = a + (b - a) / 2;
-    const int k = above(order_value(mid));
+    uint32_t l;
+    const int k = above(mid, l, below);
     if (k >= n) {
       a = mid;
       count = k;
+      least = l;
     } else {
-      b = mid;
+      b = below;  // (some entry lies in (a, mid])
     }
   }
-  const float cut = order_value(a);
   __syncthreads();
   if (threadIdx.x == 0) sh.ncand = 0;
   __syncthreads();
   for_each(p, lo, [&](float x, int v) {
-    if (x > cut) sh.cand[atomicAdd(&sh.ncand, 1)] = order_key(x, v);
+    if (order(x) > a) sh.cand[atomicAdd(&sh.ncand, 1)] = order_key(x, v);
   });
   __syncthreads();
   if (!equal) return;
@@ -276,7 +468,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
   int have = sh.ncand;
   for (int v0 = lo; v0 < hi && have < n; v0 += kThreads) {
     const int v = v0 + threadIdx.x;
-    const bool eq = v < hi && to_f32(p.head[v - lo]) == cut;
+    const bool eq = v < hi && order(to_f32(p.head[v - lo])) == a;
     const unsigned mask = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) sh.warp_n[warp] = __popc(mask);
     __syncthreads();
@@ -285,7 +477,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
       if (w < warp) at += sh.warp_n[w];
       total += sh.warp_n[w];
     }
-    if (eq && at < n) sh.cand[at] = order_key(cut, v);
+    if (eq && at < n) sh.cand[at] = ((unsigned long long)a << 32) | (uint32_t)~v;
     have += total;
     __syncthreads();
   }
@@ -297,27 +489,33 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
 // out[0 .. return value), from the threads' own maxima: the n-th largest of
 // those bounds the n-th largest entry from below (they are maxima of disjoint
 // sets), and only threads whose maximum reaches the bound can hold an entry
-// that does, so the second look reads a few of them.
+// that does, so the second look reads a few of them.  One warp finds the
+// bound, to the upper 16 bits of its order (all of a bf16): 16 steps.
 template <typename T>
 __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, TopShared& sh,
-                                        float* stage, unsigned long long* out) {
+                                        unsigned long long* out) {
   const int t = threadIdx.x;
-  sh.segmax[t] = my_max;
-  if (t == 0) {
-    sh.nhot = sh.ncand = 0;
-    sh.bound = NEG_INF;
+  sh.segmax[t] = order_bits(my_max) >> 16;
+  if (t == 0) sh.nhot = sh.ncand = 0;
+  __syncthreads();
+  if (t < 32) {
+    uint32_t v[kThreads / 32];
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v[i] = sh.segmax[t + 32 * i];
+    uint32_t key = 0;  // largest with at least n maxima at or above it
+#pragma unroll 1
+    for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
+      unsigned k = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) k += v[i] >= (key | bit);
+      if (__reduce_add_sync(0xffffffffu, k) >= (unsigned)n) key |= bit;
+    }
+    if (t == 0) sh.bound = order_value(key << 16);
   }
   __syncthreads();
-  int rank = 0;
-  for (int i = 0; i < kThreads; i += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(&sh.segmax[i]);
-    rank += (o.x > my_max || (o.x == my_max && i < t)) + (o.y > my_max || (o.y == my_max && i + 1 < t)) +
-            (o.z > my_max || (o.z == my_max && i + 2 < t)) + (o.w > my_max || (o.w == my_max && i + 3 < t));
-  }
-  if (rank == n - 1) sh.bound = my_max;
-  __syncthreads();
-  const float bound = sh.bound;
-  if (my_max >= bound && my_max > NEG_INF) sh.hot[atomicAdd(&sh.nhot, 1)] = t;
+  // (the maxima stop at kFloor; order patterns below -inf are no values)
+  const float bound = sh.bound > kFloor ? sh.bound : NEG_INF;
+  if (my_max >= bound) sh.hot[atomicAdd(&sh.nhot, 1)] = t;
   __syncthreads();
   const int warp = t >> 5, lane = t & 31;
   auto offer = [&](float x, int v) {
@@ -326,22 +524,33 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
       if (at < kCand) sh.cand[at] = order_key(x, v);
     }
   };
-  for (int h = warp; h < sh.nhot; h += kThreads / 32)
-    for (int i = sh.hot[h] + lane * kThreads; i < p.nvec; i += 32 * kThreads) {
-      float v[kVec<T>];
-      unpack(ld_stream(p.vec(i)), v, T{});
+  // a warp takes 32 of a thread's vectors at a time, four such looks together
+  const int looks = (p.nvec + 32 * kThreads - 1) / (32 * kThreads), items = sh.nhot * looks;
+  for (int q0 = warp; q0 < items; q0 += kUnroll * (kThreads / 32)) {
+    uint4 r[kUnroll];
+    int at[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kVec<T>; ++k) offer(v[k], lo + p.nhead + i * kVec<T> + k);
+    for (int k = 0; k < kUnroll; ++k) {
+      const int q = q0 + k * (kThreads / 32);
+      at[k] = p.nvec;
+      if (q < items) at[k] = sh.hot[q / looks] + (q % looks * 32 + lane) * kThreads;
+      if (at[k] < p.nvec) r[k] = ld_stream(p.vec(at[k]));
     }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (at[k] < p.nvec && max_of<T>(&r[k], 1) >= bound) {
+        float v[kVec<T>];
+        unpack(r[k], v, T{});
+#pragma unroll
+        for (int j = 0; j < kVec<T>; ++j) offer(v[j], lo + p.nhead + at[k] * kVec<T> + j);
+      }
+  }
   if (t < p.singles()) {
     const int o = p.single_at(t);
     offer(to_f32(p.head[o]), lo + o);
   }
   __syncthreads();
-  if (sh.ncand > kCand) {  // uniform
-    const float most = block_max(my_max, stage);
-    top_exact(p, lo, hi, n, bound, most, sh);
-  }
+  if (sh.ncand > kCand) top_exact(p, lo, hi, n, bound, sh);  // uniform
   const int count = sh.ncand;
   for (int i = t; i < count; i += kThreads) {
     const unsigned long long key = sh.cand[i];
@@ -353,26 +562,27 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
 }
 
 // ------------------------------------------------------------ distillation --
-struct KeptShared {
-  int id[kMaxKept];       // kept token, or -1
-  float p[kMaxKept];      // 2^((teacher - max) c), then the probability
-  float x[kMaxKept];      // the student's logit of it
+struct Kept {  // [K] each, in shared memory
+  int* id;   // kept token, or -1
+  float* p;  // the teacher's value, then 2^((value - max) c)
+  float* x;  // the student's logit of it
 };
 
 // Writes the gradient of this block's part, f(x) for each logit: by vectors
 // where logits and gradient lie alike in their 16-byte blocks.
-template <typename T, typename F>
-__device__ __forceinline__ void map_part(const Part<T>& p, T* dst, F f) {
+template <typename T, bool RES, typename F>
+__device__ __forceinline__ void map_part(const Part<T>& p, uint32_t mine, T* dst, F f) {
   // dst: the gradient of p.head[0]
   const bool alike = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(p.head)) & 15) == 0;
   if (alike) {
-    constexpr int UNR = 2;
+    constexpr int UNR = kUnroll;
     int i = threadIdx.x;
     T* dv = dst + p.nhead;
+    auto take = [&](int i) { return RES ? ld_shared_v4(mine + (i - threadIdx.x) * 16) : ld_stream(p.vec(i)); };
     for (; i + (UNR - 1) * kThreads < p.nvec; i += UNR * kThreads) {
       uint4 r[UNR];
 #pragma unroll
-      for (int k = 0; k < UNR; ++k) r[k] = ld_stream(p.vec(i + k * kThreads));
+      for (int k = 0; k < UNR; ++k) r[k] = take(i + k * kThreads);
 #pragma unroll
       for (int k = 0; k < UNR; ++k) {
         float v[kVec<T>];
@@ -384,7 +594,7 @@ __device__ __forceinline__ void map_part(const Part<T>& p, T* dst, F f) {
     }
     for (; i < p.nvec; i += kThreads) {
       float v[kVec<T>];
-      unpack(ld_stream(p.vec(i)), v, T{});
+      unpack(take(i), v, T{});
 #pragma unroll
       for (int j = 0; j < kVec<T>; ++j) v[j] = f(v[j]);
       st_stream(dv + (long long)i * kVec<T>, pack(v, T{}));
@@ -399,18 +609,22 @@ __device__ __forceinline__ void map_part(const Part<T>& p, T* dst, F f) {
   }
 }
 
-template <typename T, RowOp OP, bool TOP>
-__global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
+// RES: the part fits in shared memory and stays there (kDistillGrad only).
+template <typename T, RowOp OP, bool TOP, bool RES>
+__global__ void __launch_bounds__(kThreads, 3) rows_kernel(RowArgs a, int C) {
   constexpr bool kLogp = OP == RowOp::kLogpFwd || OP == RowOp::kLogpBwd;
   constexpr bool kDistill = !kLogp;
   constexpr bool kStat = OP == RowOp::kLogpFwd || OP == RowOp::kDistillFwd || OP == RowOp::kDistillGrad;
-  constexpr bool kGrad = OP == RowOp::kLogpBwd || OP == RowOp::kDistillBwd || OP == RowOp::kDistillGrad;
   constexpr bool kEntropy = OP == RowOp::kLogpFwd;
   __shared__ Stat stage[kThreads / 32], all[kMaxCluster];
   __shared__ float fstage[kThreads / 32];
-  __shared__ __align__(16) unsigned char raw[TOP ? sizeof(TopShared) : kDistill ? sizeof(KeptShared) : 16];
+  extern __shared__ __align__(16) unsigned char raw[];  // TopShared, or the resident part and the kept tokens
   TopShared& top = *reinterpret_cast<TopShared*>(raw);
-  KeptShared& kept = *reinterpret_cast<KeptShared*>(raw);
+  Kept kept;
+  kept.id = reinterpret_cast<int*>(raw + (RES ? kResident * 16 : 0));
+  kept.p = reinterpret_cast<float*>(kept.id + a.K);
+  kept.x = kept.p + a.K;
+  const uint32_t mine = smem_u32(raw) + threadIdx.x * 16;
 
   const int rank = C == 1 ? 0 : (int)(blockIdx.x % C);
   const long long row = blockIdx.x / C;
@@ -421,6 +635,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
   const T* xr = static_cast<const T*>(a.x) + row * a.x_stride;
   const Part<T> part(xr, lo, hi);
   const float inv_t = 1.f / a.temperature, c = kLog2e / a.temperature;
+
+  if constexpr (RES) fetch_part(part, mine);
 
   // the teacher's slots: ids and, from the whole row, the student's logits
   float tmax = NEG_INF;
@@ -440,9 +656,15 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
   Stat st{0.f, 1.f, 0.f};
   float my_max = NEG_INF;
   if (kStat) {
-    const Stat mine = part_stat<T, kEntropy>(part, c);
-    my_max = mine.m;
-    st = cluster_stat<kEntropy>(block_stat<kEntropy>(mine, c, stage), c, all, C);
+    Stat own;
+    if constexpr (RES)
+      own = resident_stat<T, kEntropy>(part, mine, c);
+    else
+      own = part_stat<T, kEntropy>(part, c);
+    my_max = own.m;
+    st = cluster_stat<kEntropy>(block_stat<kEntropy>(own, c, stage), c, all, C);
+    if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale)  // uniform over the cluster
+      st = cluster_stat<kEntropy>(block_stat<kEntropy>(part_stat_any<T, kEntropy>(part, c), c, stage), c, all, C);
   }
   // log2 p_v = (x_v - ref) c - l2s
   float ref, l2s;
@@ -475,7 +697,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
       const unsigned long long* keys = top.merge;
       int total;
       if (C == 1) {
-        total = part_top(part, lo, hi, n, my_max, top, fstage, top.merge);
+        total = part_top(part, lo, hi, n, my_max, top, top.merge);
         __syncthreads();
         for (int i = t; i < n; i += kThreads) {
           const long long o = row * n + i;
@@ -490,7 +712,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
         }
       } else {
         cg::cluster_group cl = cg::this_cluster();
-        count = part_top(part, lo, hi, n, my_max, top, fstage, cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
+        count = part_top(part, lo, hi, n, my_max, top, cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
         if (t == 0) *(cl.map_shared_rank(top.merge_n, 0) + rank) = count;
         cl.sync();
         if (rank == 0) {
@@ -542,10 +764,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
       if (empty) return 0.f;
       const float d = x * c - l2s;
       const float p = ex2(d);
-      return -p * (g + b * (kLn2 * fmaxf(d, -1.0e30f) + h));
+      return -p * (g + b * (kLn2 * fmaxf(d, kLeast) + h));
     };
     T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
-    map_part(part, dst, grad);
+    map_part<T, RES>(part, mine, dst, grad);
     __syncthreads();
     if (t == 0 && tok && id >= lo && id < hi) dst[id - lo] = from_f32<T>(empty ? 0.f : g + grad(xt));
     return;
@@ -587,7 +809,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
     // every block has read its logits of kept tokens before any is overwritten
     // (with statistics, they have met since)
     if (!kStat && C > 1) cg::this_cluster().sync();
-    map_part(part, dst, grad);
+    map_part<T, RES>(part, mine, dst, grad);
     __syncthreads();
     for (int j = t; j < a.K; j += kThreads) {
       const int id = kept.id[j];
@@ -604,11 +826,18 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(RowArgs a, int C) {
   }
 }
 
-template <typename T, RowOp OP, bool TOP>
+template <typename T, RowOp OP, bool TOP, bool RES>
 cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
+  const size_t smem = TOP ? sizeof(TopShared) : (RES ? kResident * 16 : 0) + (size_t)a.K * 12;
+  if (smem > 40 * 1024) {  // beyond 48 KB with the static part
+    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<T, OP, TOP, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -616,35 +845,43 @@ cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP>, a, C);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP, RES>, a, C);
 }
 
+// Logits of a block's part when C blocks share a row.
+int part_len(int V, int C) { return (((V + C - 1) / C) + 63) & ~63; }
+
 template <typename T>
-cudaError_t launch_typed(RowOp op, const RowArgs& a, int C, cudaStream_t st) {
+cudaError_t launch_typed(RowOp op, const RowArgs& a, cudaStream_t st) {
+  // Blocks a row: as many as keep four an SM busy, while a part keeps two
+  // vectors a thread.
+  int C = 1;
+  while (C < kMaxCluster && a.rows * 2 * C <= 4LL * a.num_sms && (long long)a.V >= 4LL * C * kThreads * kVec<T>) C *= 2;
   switch (op) {
     case RowOp::kLogpFwd:
-      return a.top_n ? launch_rows_t<T, RowOp::kLogpFwd, true>(a, C, st)
-                     : launch_rows_t<T, RowOp::kLogpFwd, false>(a, C, st);
-    case RowOp::kLogpBwd: return launch_rows_t<T, RowOp::kLogpBwd, false>(a, C, st);
-    case RowOp::kDistillFwd: return launch_rows_t<T, RowOp::kDistillFwd, false>(a, C, st);
-    case RowOp::kDistillBwd: return launch_rows_t<T, RowOp::kDistillBwd, false>(a, C, st);
-    default: return launch_rows_t<T, RowOp::kDistillGrad, false>(a, C, st);
+      return a.top_n ? launch_rows_t<T, RowOp::kLogpFwd, true, false>(a, C, st)
+                     : launch_rows_t<T, RowOp::kLogpFwd, false, false>(a, C, st);
+    case RowOp::kLogpBwd: return launch_rows_t<T, RowOp::kLogpBwd, false, false>(a, C, st);
+    case RowOp::kDistillFwd: return launch_rows_t<T, RowOp::kDistillFwd, false, false>(a, C, st);
+    case RowOp::kDistillBwd: return launch_rows_t<T, RowOp::kDistillBwd, false, false>(a, C, st);
+    default: break;
   }
+  // loss and gradient: parts of at most 64 KB stay in shared memory, three
+  // blocks an SM
+  int R = C;
+  while (R < kMaxCluster && part_len(a.V, R) > kResident * kVec<T>) R *= 2;
+  if (part_len(a.V, R) <= kResident * kVec<T>) return launch_rows_t<T, RowOp::kDistillGrad, false, true>(a, R, st);
+  return launch_rows_t<T, RowOp::kDistillGrad, false, false>(a, C, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(RowOp op, const RowArgs& a, cudaStream_t st) {
   if (!a.rows) return cudaSuccess;
-  // blocks a row: as many as make two a SM, while a part
-  // keeps at least two vectors a thread
-  const int vec = a.type == 0 ? 4 : 8;
-  int C = 1;
-  while (C < kMaxCluster && a.rows * 2 * C <= 2LL * a.num_sms && (long long)a.V >= 4LL * C * kThreads * vec) C *= 2;
   switch (a.type) {
-    case 0: return launch_typed<float>(op, a, C, st);
-    case 1: return launch_typed<__nv_bfloat16>(op, a, C, st);
-    default: return launch_typed<__half>(op, a, C, st);
+    case 0: return launch_typed<float>(op, a, st);
+    case 1: return launch_typed<__nv_bfloat16>(op, a, st);
+    default: return launch_typed<__half>(op, a, st);
   }
 }
 
