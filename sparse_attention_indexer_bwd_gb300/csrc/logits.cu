@@ -34,10 +34,14 @@ namespace cg = cooperative_groups;
 namespace ibwd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;         // streaming kernels
+constexpr int kResidentThreads = 128;  // kernels that keep their part in shared memory
+constexpr int kMaxWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = 128;
-constexpr int kCand = 1024;      // candidates a block ranks for the top alternatives
+constexpr int kCand = 1024;  // candidates a block ranks for the top alternatives
+constexpr int kSegments = 16;  // maxima a thread keeps of its logits
+constexpr int kUnroll = 4;   // vectors a thread takes together
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 // An exponent whose power of two is 0, kept finite so that 0 times it is 0.
@@ -52,43 +56,7 @@ struct Stat {
 // (every term is then 2^-inf = 0; x - m of two infinities never occurs).
 __device__ __forceinline__ float finite_max(float m) { return m == NEG_INF ? 0.f : m; }
 
-template <bool U>
-__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
-  const float m = fmaxf(a.m, b.m), mr = finite_max(m);
-  // a part without terms has s = u = 0; its difference is kept finite for u
-  const float da = fmaxf((a.m - mr) * c, kLeast), db = fmaxf((b.m - mr) * c, kLeast);
-  const float fa = ex2(da), fb = ex2(db);
-  Stat r;
-  r.m = m;
-  r.s = a.s * fa + b.s * fb;
-  r.u = 0.f;
-  if (U) r.u = fa * (a.u + a.s * da) + fb * (b.u + b.s * db);
-  return r;
-}
-
-// Adds N logits to a running statistic.
-template <bool U, int N>
-__device__ __forceinline__ void add(Stat& t, const float (&x)[N], float c) {
-  float m = x[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
-  if (m > t.m) {
-    const float d = fmaxf((t.m - m) * c, kLeast), f = ex2(d);
-    if (U) t.u = f * (t.u + t.s * d);
-    t.s *= f;
-    t.m = m;
-  }
-  const float mr = finite_max(t.m);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float d = (x[i] - mr) * c;
-    const float e = ex2(d);
-    t.s += e;
-    if (U) t.u = fmaf(e, fmaxf(d, kLeast), t.u);  // 0 for a masked logit
-  }
-}
-
-// The part [lo, hi) of a row as this block reads it: single elements up to a
+// The part [lo, hi) of a row as a block reads it: single elements up to a
 // 16-byte boundary, whole 16-byte vectors, single elements.
 template <typename T>
 struct Part {
@@ -103,32 +71,49 @@ struct Part {
     ntail = n - nhead - nvec * kVec<T>;
   }
   __device__ const T* vec(int i) const { return head + nhead + (long long)i * kVec<T>; }
-  __device__ const T* tail() const { return vec(nvec); }
   // single elements are numbered 0 .. nhead + ntail - 1
   __device__ int singles() const { return nhead + ntail; }
   __device__ int single_at(int i) const { return i < nhead ? i : i + nvec * kVec<T>; }  // offset from head
 };
 
-// The careful statistic: any values, one element at a time.
-template <typename T, bool U>
-__device__ __noinline__ Stat part_stat_any(const Part<T>& p, float c) {
-  Stat t{NEG_INF, 0.f, 0.f};
-  for (int i = threadIdx.x; i < p.nvec; i += kThreads) {
+// Calls f(x, v) for every element of the part, which begins at index lo.
+template <int NT, typename T, typename F>
+__device__ __forceinline__ void for_each(const Part<T>& p, int lo, F f) {
+  for (int i = threadIdx.x; i < p.nvec; i += NT) {
     float v[kVec<T>];
     unpack(ld_stream(p.vec(i)), v, T{});
-    add<U>(t, v, c);
+#pragma unroll
+    for (int k = 0; k < kVec<T>; ++k) f(v[k], lo + p.nhead + i * kVec<T> + k);
   }
   if ((int)threadIdx.x < p.singles()) {
-    const float v[1] = {to_f32(p.head[p.single_at(threadIdx.x)])};
-    add<U>(t, v, c);
+    const int o = p.single_at(threadIdx.x);
+    f(to_f32(p.head[o]), lo + o);
   }
+}
+
+// -------------------------------------------------------------- statistics --
+// The careful statistic: any values, one element at a time.
+template <int NT, typename T, bool U>
+__device__ __noinline__ Stat part_stat_any(const Part<T>& p, float c) {
+  Stat t{NEG_INF, 0.f, 0.f};
+  for_each<NT>(p, 0, [&](float x, int) {
+    if (x > t.m) {
+      const float d = fmaxf((t.m - x) * c, kLeast), f = ex2(d);
+      t.u = f * (t.u + t.s * d);
+      t.s *= f;
+      t.m = x;
+    }
+    const float d = (x - finite_max(t.m)) * c, e = ex2(d);
+    t.s += e;
+    t.u = fmaf(e, fmaxf(d, kLeast), t.u);  // 0 for a masked logit
+  });
   return t;
 }
 
 // The fast statistic starts from the maximum kFloor, so that x - m is always
 // finite: a logit far below it (a mask) adds 2^-huge = 0.  It does not hold
 // for rows without a logit above kFloor, nor for scales that make kFloor
-// small; those take the careful one.
+// small or huge; those take the careful one.
 constexpr float kFloor = -9.9499216e29f;  // 0xF1490000: also a bf16
 constexpr float kLeastScale = 1e-20f, kMostScale = 1e6f;
 
@@ -154,19 +139,19 @@ __device__ __forceinline__ float floor_nan(float a) {
   return d;
 }
 
-template <typename T>
-__device__ __forceinline__ float max_of(const uint4* r, int n) {
+template <typename T, int N>
+__device__ __forceinline__ float max_of(const uint4 (&r)[N]) {
   if constexpr (sizeof(T) == 4) {
     float m = kFloor;
 #pragma unroll
-    for (int i = 0; i < n; ++i)
+    for (int i = 0; i < N; ++i)
       m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)),
                          fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
     return m;
   } else {
     uint32_t m = max2(max2(r[0].x, r[0].y, T{}), max2(r[0].z, r[0].w, T{}), T{});
 #pragma unroll
-    for (int i = 1; i < n; ++i) m = max2(m, max2(max2(r[i].x, r[i].y, T{}), max2(r[i].z, r[i].w, T{}), T{}), T{});
+    for (int i = 1; i < N; ++i) m = max2(m, max2(max2(r[i].x, r[i].y, T{}), max2(r[i].z, r[i].w, T{}), T{}), T{});
     const float2 f = unpack2(m, T{});
     return fmaxf(f.x, f.y);
   }
@@ -197,9 +182,10 @@ __device__ __forceinline__ void add_pair(Run& t, float2 x, float2 neg_m, float2 
   if (U) t.u = fma2(e, d, t.u);
 }
 
+// Adds vectors of maximum `most`.
 template <typename T, bool U, int N>
-__device__ __forceinline__ void add_vectors(Run& t, const uint4 (&r)[N], float c) {
-  raise(t, max_of<T>(r, N), c, U);
+__device__ __forceinline__ void add_vectors(Run& t, const uint4 (&r)[N], float most, float c) {
+  raise(t, most, c, U);
   const float2 nm = both(-t.m), c2 = both(c);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -227,13 +213,37 @@ __device__ __forceinline__ Stat finish(Run& t, const Part<T>& p, float c) {
   return Stat{t.m, t.s.x + t.s.y, t.u.x + t.u.y};
 }
 
-constexpr int kUnroll = 4;
+// Order of the logits as unsigned numbers (-0 counts as +0).
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// Maxima of a thread's vectors in runs of kUnroll << shift of them, at most
+// kSegments, by the upper half of their order.
+struct Segments {
+  uint16_t* at;  // [kSegments][kThreads], or nullptr
+  int shift;
+  float run;
+  template <typename T>
+  __device__ Segments(uint16_t* a, const Part<T>& p) : at(a), shift(0), run(NEG_INF) {
+    const int blocks = (p.nvec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+    while ((blocks - 1) >> shift >= kSegments) ++shift;
+  }
+  __device__ __forceinline__ void put(int block, float most) {
+    run = (block & ((1 << shift) - 1)) ? fmaxf(run, most) : most;
+    at[(block >> shift) * kThreads + threadIdx.x] = (uint16_t)(order_bits(run) >> 16);
+  }
+};
 
 // Streamed from global memory, the next vectors' loads ahead of the sums.
-template <typename T, bool U>
-__device__ __forceinline__ Stat part_stat(const Part<T>& p, float c) {
+template <typename T, bool U, bool TOP>
+__device__ __forceinline__ Stat part_stat(const Part<T>& p, Segments& seg, float c) {
   Run t{kFloor, {0.f, 0.f}, {0.f, 0.f}};
-  int i = threadIdx.x;
+  int i = threadIdx.x, block = 0;
   constexpr int kStep = kUnroll * kThreads;
   if (i + (kUnroll - 1) * kThreads < p.nvec) {
     uint4 r[kUnroll];
@@ -243,164 +253,169 @@ __device__ __forceinline__ Stat part_stat(const Part<T>& p, float c) {
       uint4 n[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) n[k] = ld_stream(p.vec(i + k * kThreads));
-      add_vectors<T, U>(t, r, c);
+      const float most = max_of<T>(r);
+      if (TOP) seg.put(block++, most);
+      add_vectors<T, U>(t, r, most, c);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) r[k] = n[k];
     }
-    add_vectors<T, U>(t, r, c);
+    const float most = max_of<T>(r);
+    if (TOP) seg.put(block++, most);
+    add_vectors<T, U>(t, r, most, c);
   }
-  for (; i < p.nvec; i += kThreads) {
-    const uint4 r[1] = {ld_stream(p.vec(i))};
-    add_vectors<T, U>(t, r, c);
+  if (i < p.nvec) {
+    float all = NEG_INF;
+    for (; i < p.nvec; i += kThreads) {
+      const uint4 r[1] = {ld_stream(p.vec(i))};
+      const float most = max_of<T>(r);
+      all = fmaxf(all, most);
+      add_vectors<T, U>(t, r, most, c);
+    }
+    if (TOP) seg.put(block, all);
   }
   return finish<T, U>(t, p, c);
 }
 
 // Through shared memory, where the part stays: each thread copies the vectors
 // it reads itself, all of them at once, and takes them up as they arrive.
-constexpr int kGroups = 4;
-constexpr int kResident = kGroups * kUnroll * kThreads;  // vectors a part may have
+constexpr int kGroups = 8;
+constexpr int kResident = kGroups * kUnroll * kResidentThreads;  // vectors a part may have: 64 KB
 
 template <typename T>
 __device__ __forceinline__ void fetch_part(const Part<T>& p, uint32_t mine) {
+  const T* from = p.vec(threadIdx.x);
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int i = threadIdx.x + (g * kUnroll + k) * kThreads;
-      if (i < p.nvec) cp_async16(mine + (g * kUnroll + k) * kThreads * 16, p.vec(i), 16);
+      constexpr int NT = kResidentThreads;
+      const int o = (g * kUnroll + k) * NT;
+      if ((int)threadIdx.x + o < p.nvec) cp_async16(mine + o * 16, from + o * kVec<T>, 16);
     }
     cp_async_commit();
   }
 }
 
+template <typename T, bool U, int G>
+__device__ __forceinline__ void take_group(Run& t, const Part<T>& p, uint32_t mine, float c) {
+  constexpr int NT = kResidentThreads;
+  cp_async_wait<kGroups - 1 - G>();
+  const int first = (int)threadIdx.x + G * kUnroll * NT;
+  const uint32_t from = mine + G * kUnroll * NT * 16;
+  if (first + (kUnroll - 1) * NT < p.nvec) {
+    uint4 r[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) r[k] = ld_shared_v4(from + k * NT * 16);
+    add_vectors<T, U>(t, r, max_of<T>(r), c);
+  } else {
+#pragma unroll 1
+    for (int k = 0; first + k * NT < p.nvec; ++k) {
+      const uint4 r[1] = {ld_shared_v4(from + k * NT * 16)};
+      add_vectors<T, U>(t, r, max_of<T>(r), c);
+    }
+  }
+  if constexpr (G + 1 < kGroups) take_group<T, U, G + 1>(t, p, mine, c);
+}
+
 template <typename T, bool U>
 __device__ __forceinline__ Stat resident_stat(const Part<T>& p, uint32_t mine, float c) {
   Run t{kFloor, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    if (g == 0) cp_async_wait<3>();
-    if (g == 1) cp_async_wait<2>();
-    if (g == 2) cp_async_wait<1>();
-    if (g == 3) cp_async_wait<0>();
-    const uint32_t from = mine + g * kUnroll * kThreads * 16;
-    if ((int)threadIdx.x + (g * kUnroll + kUnroll - 1) * kThreads < p.nvec) {
-      uint4 r[kUnroll];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) r[k] = ld_shared_v4(from + k * kThreads * 16);
-      add_vectors<T, U>(t, r, c);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kUnroll - 1; ++k)
-        if ((int)threadIdx.x + (g * kUnroll + k) * kThreads < p.nvec) {
-          const uint4 r[1] = {ld_shared_v4(from + k * kThreads * 16)};
-          add_vectors<T, U>(t, r, c);
-        }
-    }
-  }
+  take_group<T, U, 0>(t, p, mine, c);
   return finish<T, U>(t, p, c);
 }
 
-// Statistic of the whole block, in thread 0 .. kThreads - 1 alike.
-template <bool U>
-__device__ __forceinline__ Stat block_stat(Stat t, float c, Stat* stage) {
+__device__ __forceinline__ float warp_max_f(float v) {
+  // as signed numbers of the same order, in one instruction
+  int b = __float_as_int(v);
+  b ^= (b >> 31) & 0x7FFFFFFF;
+  b = __reduce_max_sync(0xffffffffu, b);
+  return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF));
+}
+
+struct Stage {
+  float m[kMaxWarps], s[kMaxWarps], u[kMaxWarps];
+  Stat of_block[kMaxCluster];
+};
+
+// Terms of a part brought to the reference point of a larger set.
+__device__ __forceinline__ void rescale(Stat& t, float m, float c) {
+  const float d = fmaxf((t.m - finite_max(m)) * c, kLeast), f = ex2(d);
+  t.u = f * fmaf(t.s, d, t.u);
+  t.s *= f;
+  t.m = m;
+}
+
+// The statistic of the row in every thread of its blocks: the maximum first,
+// then sums in the order of lanes, warps and blocks.
+template <int NT, bool U>
+__device__ __forceinline__ Stat row_stat(Stat t, float c, Stage& st, int C) {
+  constexpr int NW = NT / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float wm = warp_max_f(t.m);
+  __syncthreads();
+  if (lane == 0) st.m[warp] = wm;
+  __syncthreads();
+  float m = st.m[0];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, t.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, t.s, o);
-    b.u = U ? __shfl_xor_sync(0xffffffffu, t.u, o) : 0.f;
-    // the lower lane's part first, so that both lanes get the same bits
-    t = (threadIdx.x & o) ? join<U>(b, t, c) : join<U>(t, b, c);
+  for (int w = 1; w < NW; ++w) m = fmaxf(m, st.m[w]);
+  rescale(t, m, c);
+  t.s = warp_sum(t.s);
+  if (U) t.u = warp_sum(t.u);
+  if (lane == 0) {
+    st.s[warp] = t.s;
+    if (U) st.u[warp] = t.u;
   }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) stage[threadIdx.x >> 5] = t;
-  __syncthreads();
-  t = stage[0];
-  for (int w = 1; w < kThreads / 32; ++w) t = join<U>(t, stage[w], c);
-  return t;
-}
-
-__device__ __forceinline__ float block_sum(float v, float* stage) {
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) stage[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int w = 0; w < kThreads / 32; ++w) v += stage[w];
-  return v;
-}
-__device__ __forceinline__ float block_max(float v, float* stage) {
+  t.s = t.u = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) stage[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = stage[0];
-  for (int w = 1; w < kThreads / 32; ++w) v = fmaxf(v, stage[w]);
-  return v;
-}
-
-// The statistic of the row from its blocks', joined in the blocks' order.
-template <bool U>
-__device__ __forceinline__ Stat cluster_stat(Stat t, float c, Stat* all, int C) {
+  for (int w = 0; w < NW; ++w) {
+    t.s += st.s[w];
+    if (U) t.u += st.u[w];
+  }
   if (C == 1) return t;
   cg::cluster_group cl = cg::this_cluster();
-  cl.sync();  // every block has started
-  if ((int)threadIdx.x < C) *cl.map_shared_rank(all + cl.block_rank(), threadIdx.x) = t;
+  cl.sync();  // every block has started, and is done with an earlier exchange
+  if ((int)threadIdx.x < C) *cl.map_shared_rank(&st.of_block[cl.block_rank()], threadIdx.x) = t;
   cl.sync();
-  t = all[0];
-  for (int i = 1; i < C; ++i) t = join<U>(t, all[i], c);
-  return t;
+  m = st.of_block[0].m;
+  for (int i = 1; i < C; ++i) m = fmaxf(m, st.of_block[i].m);
+  Stat r{m, 0.f, 0.f};
+  for (int i = 0; i < C; ++i) {
+    Stat o = st.of_block[i];
+    rescale(o, m, c);
+    r.s += o.s;
+    r.u += o.u;
+  }
+  return r;
 }
 
 // ------------------------------------------------------- top alternatives --
-// Order of the candidates: larger logit first, then lower index, as one
-// unsigned 64-bit key (-0 counts as +0).
-__device__ __forceinline__ uint32_t order_bits(float x) {
-  const uint32_t b = __float_as_uint(x + 0.f);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float order_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-}
+// Candidates as one unsigned key: larger logit first, then lower index.
 __device__ __forceinline__ unsigned long long order_key(float x, int v) {
   return ((unsigned long long)order_bits(x) << 32) | (uint32_t)~v;
 }
 
+constexpr int kHot = 1024;  // segments looked at again
+
 struct TopShared {
-  uint32_t segmax[kThreads];
   unsigned long long cand[kCand];
   unsigned long long merge[kMaxTop * kMaxCluster];
   int merge_n[kMaxCluster];
-  int hot[kThreads];
+  uint16_t segment[kSegments * kThreads];
+  uint16_t thread_max[kThreads];
+  int hot[kHot];
   int nhot, ncand;
   uint32_t least, below;
-  float bound;
-  int warp_n[kThreads / 32];
+  uint32_t bound;  // upper half of an order
+  int warp_n[kMaxWarps];
 };
-
-// Calls f(x, v) for every element of this block's part, in any order.
-template <typename T, typename F>
-__device__ __forceinline__ void for_each(const Part<T>& p, int lo, F f) {
-  for (int i = threadIdx.x; i < p.nvec; i += kThreads) {
-    float v[kVec<T>];
-    unpack(ld_stream(p.vec(i)), v, T{});
-#pragma unroll
-    for (int k = 0; k < kVec<T>; ++k) f(v[k], lo + p.nhead + i * kVec<T> + k);
-  }
-  if ((int)threadIdx.x < p.singles()) {
-    const int o = p.single_at(threadIdx.x);
-    f(to_f32(p.head[o]), lo + o);
-  }
-}
 
 // The rare case of more than kCand entries at or above the bound (many equal
 // logits, or logits whose order follows the threads): the exact order of the
 // n-th largest by bisection, then everything above it and the equal ones of
 // lowest index.
 template <typename T>
-__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, float bound, TopShared& sh) {
+__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, uint32_t bound, TopShared& sh) {
   // masked logits and NaN are no entries
   auto order = [](float x) { return x > NEG_INF ? order_bits(x) : 0u; };
   // entries of the part above `cut`: their number, the least of them, and the
@@ -415,7 +430,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
     __syncthreads();
     int k = 0;
     uint32_t l = ~0u, h = 0;
-    for_each(p, lo, [&](float x, int) {
+    for_each<kThreads>(p, lo, [&](float x, int) {
       const uint32_t key = order(x);
       if (key > cut) {
         ++k;
@@ -432,12 +447,12 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
     below = sh.below;
     return sh.ncand;
   };
-  // entries above a: `count`, at least n; entries above b: fewer than n.
-  // Both move to the nearest entries that occur.
-  uint32_t a = order_bits(bound), b = ~0u, least, below;
+  // entries above a: `count`, at least n of them while over kCand; entries
+  // above b: fewer than n.  Both move to the nearest entries that occur.
+  uint32_t a = bound, b = ~0u, least, below;
   int count = above(a, least, below);
-  bool equal = count < n;  // a is the n-th largest itself
-  while (!equal && count > kCand) {
+  bool equal = false;  // a is the n-th largest itself
+  while (count > kCand) {
     a = least - 1;
     if (b - a == 1) {  // more than kCand entries are equal to b
       a = b;
@@ -458,7 +473,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
   __syncthreads();
   if (threadIdx.x == 0) sh.ncand = 0;
   __syncthreads();
-  for_each(p, lo, [&](float x, int v) {
+  for_each<kThreads>(p, lo, [&](float x, int v) {
     if (order(x) > a) sh.cand[atomicAdd(&sh.ncand, 1)] = order_key(x, v);
   });
   __syncthreads();
@@ -473,7 +488,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
     if (lane == 0) sh.warp_n[warp] = __popc(mask);
     __syncthreads();
     int at = have + __popc(mask & ((1u << lane) - 1u)), total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kMaxWarps; ++w) {
       if (w < warp) at += sh.warp_n[w];
       total += sh.warp_n[w];
     }
@@ -488,136 +503,152 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
 // The n largest entries of this block's part, as sorted keys in
 // out[0 .. return value), from the threads' own maxima: the n-th largest of
 // those bounds the n-th largest entry from below (they are maxima of disjoint
-// sets), and only threads whose maximum reaches the bound can hold an entry
-// that does, so the second look reads a few of them.  One warp finds the
-// bound, to the upper 16 bits of its order (all of a bf16): 16 steps.
+// sets), and only segments whose maximum reaches the bound can hold an entry
+// that does, so the second look reads a few of them (a 131072-logit row: some
+// 80 of 4096).  One warp finds the bound, to the upper 16 bits of its order
+// (all of a bf16).
 template <typename T>
-__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, TopShared& sh,
-                                        unsigned long long* out) {
+__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, int shift,
+                                        TopShared& sh, unsigned long long* out) {
   const int t = threadIdx.x;
-  sh.segmax[t] = order_bits(my_max) >> 16;
+  const uint32_t my_key = order_bits(my_max) >> 16;
+  sh.thread_max[t] = (uint16_t)my_key;
   if (t == 0) sh.nhot = sh.ncand = 0;
   __syncthreads();
   if (t < 32) {
-    uint32_t v[kThreads / 32];
+    uint32_t v[kMaxWarps];
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v[i] = sh.segmax[t + 32 * i];
+    for (int i = 0; i < kMaxWarps; ++i) v[i] = sh.thread_max[t + 32 * i];
     uint32_t key = 0;  // largest with at least n maxima at or above it
 #pragma unroll 1
     for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
       unsigned k = 0;
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) k += v[i] >= (key | bit);
+      for (int i = 0; i < kMaxWarps; ++i) k += v[i] >= (key | bit);
       if (__reduce_add_sync(0xffffffffu, k) >= (unsigned)n) key |= bit;
     }
-    if (t == 0) sh.bound = order_value(key << 16);
+    if (t == 0) sh.bound = key;
   }
   __syncthreads();
-  // (the maxima stop at kFloor; order patterns below -inf are no values)
-  const float bound = sh.bound > kFloor ? sh.bound : NEG_INF;
-  if (my_max >= bound) sh.hot[atomicAdd(&sh.nhot, 1)] = t;
+  // (a thread without logits above kFloor stops there: no bound then)
+  const uint32_t half = sh.bound > order_bits(kFloor) >> 16 ? sh.bound : 0;
+  const uint32_t bound = max(half << 16, order_bits(NEG_INF) + 1);
+  if (my_key >= half) {
+    const int mine = p.nvec > t ? (p.nvec - t + kThreads - 1) / kThreads : 0;  // vectors of this thread
+    const int segments = (mine + (kUnroll << shift) - 1) / (kUnroll << shift);
+    for (int s = 0; s < segments; ++s)
+      if (sh.segment[s * kThreads + t] >= half) {
+        const int at = atomicAdd(&sh.nhot, 1);
+        if (at < kHot) sh.hot[at] = s * kThreads + t;
+      }
+  }
   __syncthreads();
-  const int warp = t >> 5, lane = t & 31;
   auto offer = [&](float x, int v) {
-    if (x >= bound && x > NEG_INF) {
+    if (x > NEG_INF && order_bits(x) >= bound) {
       const int at = atomicAdd(&sh.ncand, 1);
       if (at < kCand) sh.cand[at] = order_key(x, v);
     }
   };
-  // a warp takes 32 of a thread's vectors at a time, four such looks together
-  const int looks = (p.nvec + 32 * kThreads - 1) / (32 * kThreads), items = sh.nhot * looks;
-  for (int q0 = warp; q0 < items; q0 += kUnroll * (kThreads / 32)) {
-    uint4 r[kUnroll];
-    int at[kUnroll];
+  const int nhot = sh.nhot;
+  if (nhot <= kHot) {
+    const int bits = 2 + shift;  // a segment has 1 << bits vectors
+    static_assert(kUnroll == 4, "bits counts on it");
+    for (int e0 = t; e0 < nhot << bits; e0 += kUnroll * kThreads) {
+      uint4 r[kUnroll][1];
+      int at[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int q = q0 + k * (kThreads / 32);
-      at[k] = p.nvec;
-      if (q < items) at[k] = sh.hot[q / looks] + (q % looks * 32 + lane) * kThreads;
-      if (at[k] < p.nvec) r[k] = ld_stream(p.vec(at[k]));
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-      if (at[k] < p.nvec && max_of<T>(&r[k], 1) >= bound) {
-        float v[kVec<T>];
-        unpack(r[k], v, T{});
-#pragma unroll
-        for (int j = 0; j < kVec<T>; ++j) offer(v[j], lo + p.nhead + at[k] * kVec<T> + j);
+      for (int k = 0; k < kUnroll; ++k) {
+        const int e = e0 + k * kThreads;
+        at[k] = p.nvec;
+        if (e < nhot << bits) {
+          const int h = sh.hot[e >> bits];
+          at[k] = h % kThreads + (((h / kThreads) << bits) + (e & ((1 << bits) - 1))) * kThreads;
+        }
+        if (at[k] < p.nvec) r[k][0] = ld_stream(p.vec(at[k]));
       }
-  }
-  if (t < p.singles()) {
-    const int o = p.single_at(t);
-    offer(to_f32(p.head[o]), lo + o);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (at[k] < p.nvec && (half == 0 || order_bits(max_of<T>(r[k])) >= bound)) {
+          float v[kVec<T>];
+          unpack(r[k][0], v, T{});
+#pragma unroll
+          for (int j = 0; j < kVec<T>; ++j) offer(v[j], lo + p.nhead + at[k] * kVec<T> + j);
+        }
+    }
+    if (t < p.singles()) {
+      const int o = p.single_at(t);
+      offer(to_f32(p.head[o]), lo + o);
+    }
   }
   __syncthreads();
-  if (sh.ncand > kCand) top_exact(p, lo, hi, n, bound, sh);  // uniform
+  if (nhot > kHot || sh.ncand > kCand) top_exact(p, lo, hi, n, bound - 1, sh);  // uniform
   const int count = sh.ncand;
   for (int i = t; i < count; i += kThreads) {
     const unsigned long long key = sh.cand[i];
     int r = 0;
+#pragma unroll 4
     for (int k = 0; k < count; ++k) r += sh.cand[k] > key;
     if (r < n) out[r] = key;
   }
   return min(count, n);
 }
 
-// ------------------------------------------------------------ distillation --
+// --------------------------------------------------------------- gradients --
+// Writes the gradient of this block's part, f of each pair of logits: by
+// vectors where logits and gradient lie alike in their 16-byte blocks.
+// dst: the gradient of p.head[0].  RES: the vectors lie in shared memory.
+template <int NT, typename T, bool RES, typename F>
+__device__ __forceinline__ void map_part(const Part<T>& p, uint32_t mine, T* dst, F f) {
+  const bool alike = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(p.head)) & 15) == 0;
+  if (alike) {
+    T* dv = dst + p.nhead;
+    auto take = [&](int i) { return RES ? ld_shared_v4(mine + (i - threadIdx.x) * 16) : ld_stream(p.vec(i)); };
+    auto give = [&](int i, uint4 r) {
+      if constexpr (sizeof(T) == 4) {
+        const float2 a = f(make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
+        const float2 b = f(make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
+        r = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+      } else {
+        r = make_uint4(pack2_of(f(unpack2(r.x, T{})), T{}), pack2_of(f(unpack2(r.y, T{})), T{}),
+                       pack2_of(f(unpack2(r.z, T{})), T{}), pack2_of(f(unpack2(r.w, T{})), T{}));
+      }
+      st_stream(dv + (long long)i * kVec<T>, r);
+    };
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * NT < p.nvec; i += kUnroll * NT) {
+      uint4 r[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) r[k] = take(i + k * NT);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) give(i + k * NT, r[k]);
+    }
+    for (; i < p.nvec; i += NT) give(i, take(i));
+    if ((int)threadIdx.x < p.singles()) {
+      const int o = p.single_at(threadIdx.x);
+      dst[o] = from_f32<T>(f(both(to_f32(p.head[o]))).x);
+    }
+  } else {
+    const int n = p.singles() + p.nvec * kVec<T>;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += NT) dst[i] = from_f32<T>(f(both(to_f32(p.head[i]))).x);
+  }
+}
+
 struct Kept {  // [K] each, in shared memory
   int* id;   // kept token, or -1
   float* p;  // the teacher's value, then 2^((value - max) c)
   float* x;  // the student's logit of it
 };
 
-// Writes the gradient of this block's part, f(x) for each logit: by vectors
-// where logits and gradient lie alike in their 16-byte blocks.
-template <typename T, bool RES, typename F>
-__device__ __forceinline__ void map_part(const Part<T>& p, uint32_t mine, T* dst, F f) {
-  // dst: the gradient of p.head[0]
-  const bool alike = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(p.head)) & 15) == 0;
-  if (alike) {
-    constexpr int UNR = kUnroll;
-    int i = threadIdx.x;
-    T* dv = dst + p.nhead;
-    auto take = [&](int i) { return RES ? ld_shared_v4(mine + (i - threadIdx.x) * 16) : ld_stream(p.vec(i)); };
-    for (; i + (UNR - 1) * kThreads < p.nvec; i += UNR * kThreads) {
-      uint4 r[UNR];
-#pragma unroll
-      for (int k = 0; k < UNR; ++k) r[k] = take(i + k * kThreads);
-#pragma unroll
-      for (int k = 0; k < UNR; ++k) {
-        float v[kVec<T>];
-        unpack(r[k], v, T{});
-#pragma unroll
-        for (int j = 0; j < kVec<T>; ++j) v[j] = f(v[j]);
-        st_stream(dv + (long long)(i + k * kThreads) * kVec<T>, pack(v, T{}));
-      }
-    }
-    for (; i < p.nvec; i += kThreads) {
-      float v[kVec<T>];
-      unpack(take(i), v, T{});
-#pragma unroll
-      for (int j = 0; j < kVec<T>; ++j) v[j] = f(v[j]);
-      st_stream(dv + (long long)i * kVec<T>, pack(v, T{}));
-    }
-    if ((int)threadIdx.x < p.singles()) {
-      const int o = p.single_at(threadIdx.x);
-      dst[o] = from_f32<T>(f(to_f32(p.head[o])));
-    }
-  } else {
-    const int n = p.singles() + p.nvec * kVec<T>;
-    for (int i = threadIdx.x; i < n; i += kThreads) dst[i] = from_f32<T>(f(to_f32(p.head[i])));
-  }
-}
-
 // RES: the part fits in shared memory and stays there (kDistillGrad only).
 template <typename T, RowOp OP, bool TOP, bool RES>
-__global__ void __launch_bounds__(kThreads, 3) rows_kernel(RowArgs a, int C) {
-  constexpr bool kLogp = OP == RowOp::kLogpFwd || OP == RowOp::kLogpBwd;
-  constexpr bool kDistill = !kLogp;
+__global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_kernel(RowArgs a, int C) {
+  constexpr int NT = RES ? kResidentThreads : kThreads, NW = NT / 32;
+  constexpr bool kDistill = OP == RowOp::kDistillFwd || OP == RowOp::kDistillBwd || OP == RowOp::kDistillGrad;
   constexpr bool kStat = OP == RowOp::kLogpFwd || OP == RowOp::kDistillFwd || OP == RowOp::kDistillGrad;
   constexpr bool kEntropy = OP == RowOp::kLogpFwd;
-  __shared__ Stat stage[kThreads / 32], all[kMaxCluster];
-  __shared__ float fstage[kThreads / 32];
+  __shared__ Stage stage;
+  __shared__ float kept_max[kMaxWarps], kept_z[kMaxWarps], kept_gap[kMaxWarps];
   extern __shared__ __align__(16) unsigned char raw[];  // TopShared, or the resident part and the kept tokens
   TopShared& top = *reinterpret_cast<TopShared*>(raw);
   Kept kept;
@@ -628,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 3) rows_kernel(RowArgs a, int C) {
 
   const int rank = C == 1 ? 0 : (int)(blockIdx.x % C);
   const long long row = blockIdx.x / C;
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   // parts are whole multiples of 64 logits, so that aligned rows stay aligned
   const int len = (((a.V + C - 1) / C) + 63) & ~63;
   const int lo = (int)min((long long)a.V, (long long)rank * len), hi = (int)min((long long)a.V, (long long)lo + len);
@@ -639,9 +670,9 @@ __global__ void __launch_bounds__(kThreads, 3) rows_kernel(RowArgs a, int C) {
   if constexpr (RES) fetch_part(part, mine);
 
   // the teacher's slots: ids and, from the whole row, the student's logits
-  float tmax = NEG_INF;
   if (kDistill) {
-    for (int j = t; j < a.K; j += kThreads) {
+    float tmax = NEG_INF;
+    for (int j = t; j < a.K; j += NT) {
       const int id = a.ids[row * a.K + j];
       const float tv = a.teacher[row * a.K + j];
       const bool ok = id >= 0 && id < a.V;
@@ -650,21 +681,25 @@ __global__ void __launch_bounds__(kThreads, 3) rows_kernel(RowArgs a, int C) {
       kept.x[j] = ok ? to_f32(xr[id]) : 0.f;
       if (ok) tmax = fmaxf(tmax, tv);
     }
-    tmax = block_max(tmax, fstage);
+    tmax = warp_max_f(tmax);
+    if (lane == 0) kept_max[warp] = tmax;
+    // (read after the statistics' barriers, or this one)
+    if (!kStat) __syncthreads();
   }
 
   Stat st{0.f, 1.f, 0.f};
   float my_max = NEG_INF;
+  Segments segments(TOP ? top.segment : nullptr, part);
   if (kStat) {
     Stat own;
     if constexpr (RES)
       own = resident_stat<T, kEntropy>(part, mine, c);
     else
-      own = part_stat<T, kEntropy>(part, c);
+      own = part_stat<T, kEntropy, TOP>(part, segments, c);
     my_max = own.m;
-    st = cluster_stat<kEntropy>(block_stat<kEntropy>(own, c, stage), c, all, C);
+    st = row_stat<NT, kEntropy>(own, c, stage, C);
     if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale)  // uniform over the cluster
-      st = cluster_stat<kEntropy>(block_stat<kEntropy>(part_stat_any<T, kEntropy>(part, c), c, stage), c, all, C);
+      st = row_stat<NT, kEntropy>(part_stat_any<NT, T, kEntropy>(part, c), c, stage, C);
   }
   // log2 p_v = (x_v - ref) c - l2s
   float ref, l2s;
@@ -693,135 +728,150 @@ __global__ void __launch_bounds__(kThreads, 3) rows_kernel(RowArgs a, int C) {
     }
     if (TOP) {
       const int n = a.top_n;
-      int count = 0;
-      const unsigned long long* keys = top.merge;
-      int total;
+      auto put = [&](int i, unsigned long long key) {
+        a.top_ids[row * n + i] = (int)~(uint32_t)key;
+        a.top_logprobs[row * n + i] = (order_value((uint32_t)(key >> 32)) - ref) * inv_t - kLn2 * l2s;
+      };
+      int total = 0;
       if (C == 1) {
-        total = part_top(part, lo, hi, n, my_max, top, top.merge);
+        total = part_top(part, lo, hi, n, my_max, segments.shift, top, top.merge);
         __syncthreads();
-        for (int i = t; i < n; i += kThreads) {
-          const long long o = row * n + i;
-          if (i < total) {
-            const unsigned long long key = keys[i];
-            a.top_ids[o] = (int)~(uint32_t)key;
-            a.top_logprobs[o] = (order_value((uint32_t)(key >> 32)) - ref) * inv_t - kLn2 * l2s;
-          } else {
-            a.top_ids[o] = -1;
-            a.top_logprobs[o] = isnan(l2s) ? l2s : NEG_INF;
-          }
-        }
+        for (int i = t; i < total; i += NT) put(i, top.merge[i]);
       } else {
         cg::cluster_group cl = cg::this_cluster();
-        count = part_top(part, lo, hi, n, my_max, top, cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
+        const int count = part_top(part, lo, hi, n, my_max, segments.shift, top,
+                                   cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
         if (t == 0) *(cl.map_shared_rank(top.merge_n, 0) + rank) = count;
         cl.sync();
-        if (rank == 0) {
-          total = 0;
-          for (int i = 0; i < C; ++i) total += top.merge_n[i];
-          // place of an entry: its own place plus, in every other sorted
-          // list, the number of larger keys
-          for (int e = t; e < C * kMaxTop; e += kThreads) {
-            const int l = e / kMaxTop, i = e % kMaxTop;
-            if (i >= top.merge_n[l]) continue;
-            const unsigned long long key = top.merge[e];
-            int r = i;
-            for (int k = 0; k < C; ++k) {
-              if (k == l) continue;
-              int x0 = 0, x1 = top.merge_n[k];
-              while (x0 < x1) {
-                const int mid = (x0 + x1) >> 1;
-                if (top.merge[k * kMaxTop + mid] > key)
-                  x0 = mid + 1;
-                else
-                  x1 = mid;
-              }
-              r += x0;
+        if (rank != 0) return;
+        for (int i = 0; i < C; ++i) total += top.merge_n[i];
+        // place of an entry: its own place plus, in every other sorted list,
+        // the number of larger keys
+        for (int e = t; e < C * kMaxTop; e += NT) {
+          const int l = e / kMaxTop, i = e % kMaxTop;
+          if (i >= top.merge_n[l]) continue;
+          const unsigned long long key = top.merge[e];
+          int r = i;
+          for (int k = 0; k < C; ++k) {
+            if (k == l) continue;
+            int x0 = 0, x1 = top.merge_n[k];
+            while (x0 < x1) {
+              const int mid = (x0 + x1) >> 1;
+              if (top.merge[k * kMaxTop + mid] > key)
+                x0 = mid + 1;
+              else
+                x1 = mid;
             }
-            if (r < n) {
-              a.top_ids[row * n + r] = (int)~(uint32_t)key;
-              a.top_logprobs[row * n + r] = (order_value((uint32_t)(key >> 32)) - ref) * inv_t - kLn2 * l2s;
-            }
+            r += x0;
           }
-          for (int i = total + t; i < n; i += kThreads) {
-            a.top_ids[row * n + i] = -1;
-            a.top_logprobs[row * n + i] = isnan(l2s) ? l2s : NEG_INF;
-          }
+          if (r < n) put(r, key);
         }
+      }
+      for (int i = total + t; i < n; i += NT) {
+        a.top_ids[row * n + i] = -1;
+        a.top_logprobs[row * n + i] = isnan(l2s) ? l2s : NEG_INF;
       }
     }
     return;
   }
 
+  T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
   if (OP == RowOp::kLogpBwd) {
     const int id = a.tokens ? a.tokens[row] : -1;
     const bool tok = id >= 0 && id < a.V && a.dlogprob != nullptr;
     const float g = tok ? a.dlogprob[row] * inv_t : 0.f;
     const float b = a.dentropy ? a.dentropy[row] * inv_t : 0.f;
     const float h = a.dentropy ? a.entropy[row] : 0.f;
-    const float xt = tok ? to_f32(xr[id]) : 0.f;
+    const bool here = tok && id >= lo && id < hi;
+    const float xt = here ? to_f32(xr[id]) : 0.f;
     __syncthreads();  // the logit is read before its place may be overwritten
-    auto grad = [&](float x) {
-      if (empty) return 0.f;
-      const float d = x * c - l2s;
-      const float p = ex2(d);
-      return -p * (g + b * (kLn2 * fmaxf(d, kLeast) + h));
+    if (empty) {
+      map_part<NT, T, RES>(part, mine, dst, [](float2) { return both(0.f); });
+      return;
+    }
+    // -p (g + b (log p + h))
+    const float2 c2 = both(c), off = both(-l2s), k0 = both(-fmaf(b, h, g)), k1 = both(-b * kLn2);
+    auto grad = [&](float2 x) {
+      float2 d = fma2(x, c2, off);
+      const float2 p = make_float2(ex2(d.x), ex2(d.y));
+      d.x = fmaxf(d.x, kLeast);
+      d.y = fmaxf(d.y, kLeast);
+      return mul2(p, fma2(d, k1, k0));
     };
-    T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
-    map_part<T, RES>(part, mine, dst, grad);
+    map_part<NT, T, RES>(part, mine, dst, grad);
     __syncthreads();
-    if (t == 0 && tok && id >= lo && id < hi) dst[id - lo] = from_f32<T>(empty ? 0.f : g + grad(xt));
+    if (t == 0 && here) dst[id - lo] = from_f32<T>(g + grad(both(xt)).x);
     return;
   }
 
   if (kDistill) {
     // p_j = w_j / z with w_j = 2^((teacher_j - tmax) c)
-    const bool none = tmax == NEG_INF;
+    float tmax = kept_max[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) tmax = fmaxf(tmax, kept_max[w]);
+    const bool zero = tmax == NEG_INF || empty;
     const float tref = finite_max(tmax);
     float z = 0.f, gap = 0.f;
-    for (int j = t; j < a.K; j += kThreads) {
-      const float d = kept.p[j] - tref;
-      const float w = ex2(d * c);
-      z += w;
-      // in natural units: a lowest-value mask stays finite there
-      if (w > 0.f) gap += w * (d * inv_t - (kept.x[j] - ref) * inv_t);
-      kept.p[j] = w;
+    if (warp * 32 < a.K) {
+      for (int j = t; j < a.K; j += NT) {
+        const float d = kept.p[j] - tref;
+        const float w = ex2(d * c);
+        z += w;
+        // in natural units: a lowest-value mask stays finite there
+        if (w > 0.f) gap += w * (d * inv_t - (kept.x[j] - ref) * inv_t);
+        kept.p[j] = w;
+      }
+      z = warp_sum(z);
+      gap = warp_sum(gap);
     }
-    z = block_sum(z, fstage);
-    if (OP != RowOp::kDistillBwd && a.loss != nullptr) {
-      gap = block_sum(gap, fstage);
-      if (rank == 0 && t == 0)
-        a.loss[row] = none || empty ? 0.f : a.temperature * a.temperature * (gap / z + kLn2 * (l2s - log2f(z)));
+    if (lane == 0) {
+      kept_z[warp] = z;
+      kept_gap[warp] = gap;
     }
-    if (OP == RowOp::kDistillFwd) {
-      if (rank == 0 && t == 0) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
-      return;
-    }
-    __syncthreads();
-    float g = a.dloss ? a.dloss[row] * a.temperature : a.temperature;
-    if (OP == RowOp::kDistillGrad) g *= a.grad_scale;
-    const bool zero = none || empty;
-    const float iz = 1.f / z;
-    T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
-    auto grad = [&](float x) {
-      if (zero) return 0.f;
-      return g * ex2((x - ref) * c - l2s);
-    };
-    // every block has read its logits of kept tokens before any is overwritten
-    // (with statistics, they have met since)
-    if (!kStat && C > 1) cg::this_cluster().sync();
-    map_part<T, RES>(part, mine, dst, grad);
-    __syncthreads();
-    for (int j = t; j < a.K; j += kThreads) {
-      const int id = kept.id[j];
-      if (id < lo || id >= hi || zero) continue;
-      float p = 0.f;
-      bool first = true;
-      for (int k = 0; k < a.K; ++k)
-        if (kept.id[k] == id) {
-          if (k < j) first = false;
-          p += kept.p[k];
+    if (OP != RowOp::kDistillFwd) {
+      // every block has read its logits of kept tokens before any is
+      // overwritten (with statistics, they have met since)
+      if (!kStat && C > 1) cg::this_cluster().sync();
+      float g = a.dloss ? a.dloss[row] * a.temperature : a.temperature;
+      if (OP == RowOp::kDistillGrad) g *= a.grad_scale;
+      const float2 c2 = both(c), nref = both(-ref), off = both(-l2s), g2 = both(g);
+      auto grad = [&](float2 x) {
+        const float2 d = fma2(add2(x, nref), c2, off);
+        return mul2(make_float2(ex2(d.x), ex2(d.y)), g2);
+      };
+      if (zero)
+        map_part<NT, T, RES>(part, mine, dst, [](float2) { return both(0.f); });
+      else
+        map_part<NT, T, RES>(part, mine, dst, grad);
+      __syncthreads();
+      z = gap = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) z += kept_z[w];
+      const float iz = 1.f / z;
+      if (!zero)
+        for (int j = t; j < a.K; j += NT) {
+          const int id = kept.id[j];
+          if (id < lo || id >= hi) continue;
+          float p = 0.f;
+          bool first = true;
+          for (int k = 0; k < a.K; ++k)
+            if (kept.id[k] == id) {
+              if (k < j) first = false;
+              p += kept.p[k];
+            }
+          if (first) dst[id - lo] = from_f32<T>(grad(both(kept.x[j])).x - g * p * iz);
         }
-      if (first) dst[id - lo] = from_f32<T>(g * (ex2((kept.x[j] - ref) * c - l2s) - p * iz));
+    } else {
+      __syncthreads();
+    }
+    if (OP != RowOp::kDistillBwd && rank == 0 && t == 0) {
+      z = gap = 0.f;
+      for (int w = 0; w < NW; ++w) {
+        z += kept_z[w];
+        gap += kept_gap[w];
+      }
+      if (a.loss) a.loss[row] = zero ? 0.f : a.temperature * a.temperature * (gap / z + kLn2 * (l2s - log2f(z)));
+      if (OP == RowOp::kDistillFwd) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
     }
   }
 }
@@ -836,7 +886,7 @@ cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(RES ? kResidentThreads : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
