@@ -398,7 +398,7 @@ __device__ __forceinline__ unsigned long long order_key(float x, int v) {
 constexpr int kHot = 1024;  // segments looked at again
 
 struct TopShared {
-  unsigned long long cand[kCand];
+  alignas(16) unsigned long long cand[kCand + 2];
   unsigned long long merge[kMaxTop * kMaxCluster];
   int merge_n[kMaxCluster];
   uint16_t segment[kSegments * kThreads];
@@ -519,9 +519,20 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
     uint32_t v[kMaxWarps];
 #pragma unroll
     for (int i = 0; i < kMaxWarps; ++i) v[i] = sh.thread_max[t + 32 * i];
-    uint32_t key = 0;  // largest with at least n maxima at or above it
+    uint32_t hi_key = v[0], lo_key = v[0];
+#pragma unroll
+    for (int i = 1; i < kMaxWarps; ++i) {
+      hi_key = max(hi_key, v[i]);
+      lo_key = min(lo_key, v[i]);
+    }
+    hi_key = __reduce_max_sync(0xffffffffu, hi_key);
+    lo_key = __reduce_min_sync(0xffffffffu, lo_key);
+    // the largest key with at least n maxima at or above it, below the bits
+    // that all of them share
+    const int bits = 32 - __clz(hi_key ^ lo_key);
+    uint32_t key = hi_key >> bits << bits;
 #pragma unroll 1
-    for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
+    for (uint32_t bit = (1u << bits) >> 1; bit; bit >>= 1) {
       unsigned k = 0;
 #pragma unroll
       for (int i = 0; i < kMaxWarps; ++i) k += v[i] >= (key | bit);
@@ -583,11 +594,19 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
   __syncthreads();
   if (nhot > kHot || sh.ncand > kCand) top_exact(p, lo, hi, n, bound - 1, sh);  // uniform
   const int count = sh.ncand;
+  if (count & 1) {
+    if (t == 0) sh.cand[count] = 0;
+    __syncthreads();
+  }
   for (int i = t; i < count; i += kThreads) {
     const unsigned long long key = sh.cand[i];
     int r = 0;
+    // (one slot past the end is read; it is below every key)
 #pragma unroll 4
-    for (int k = 0; k < count; ++k) r += sh.cand[k] > key;
+    for (int k = 0; k < count; k += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.cand[k]);
+      r += (o.x > key) + (o.y > key);
+    }
     if (r < n) out[r] = key;
   }
   return min(count, n);
@@ -640,9 +659,30 @@ struct Kept {  // [K] each, in shared memory
   float* x;  // the student's logit of it
 };
 
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Starts the next part that a block of this place will take on its way to L2
+// (its first kAhead bytes), while this one has no more loads to make: blocks
+// that began together are in their joins and selections together, and HBM
+// would idle meanwhile.
+constexpr int kAhead = 64 * 1024;
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const RowArgs& a, long long row, int C, int lo, int hi) {
+  const long long next = row + a.ahead;
+  if (threadIdx.x != 0 || a.ahead == 0 || next >= a.rows || lo >= hi) return;
+  const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + next * a.x_stride + lo);
+  const uintptr_t to = from + (uintptr_t)(hi - lo) * sizeof(T);
+  const uintptr_t p = (from + 15) & ~(uintptr_t)15;
+  if (p + 16 > to) return;
+  const uint32_t bytes = (uint32_t)min((unsigned long long)kAhead, (unsigned long long)(to - p)) & ~15u;
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // RES: the part fits in shared memory and stays there (kDistillGrad only).
 template <typename T, RowOp OP, bool TOP, bool RES>
-__global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_kernel(RowArgs a, int C) {
+__global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4) rows_kernel(RowArgs a, int C) {
   constexpr int NT = RES ? kResidentThreads : kThreads, NW = NT / 32;
   constexpr bool kDistill = OP == RowOp::kDistillFwd || OP == RowOp::kDistillBwd || OP == RowOp::kDistillGrad;
   constexpr bool kStat = OP == RowOp::kLogpFwd || OP == RowOp::kDistillFwd || OP == RowOp::kDistillGrad;
@@ -667,36 +707,58 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_ker
   const Part<T> part(xr, lo, hi);
   const float inv_t = 1.f / a.temperature, c = kLog2e / a.temperature;
 
-  if constexpr (RES) fetch_part(part, mine);
-
-  // the teacher's slots: ids and, from the whole row, the student's logits
+  // what the row needs besides its logits is on its way before them
+  int token = -1;
+  if (OP == RowOp::kLogpFwd && rank == 0 && t == 0 && a.tokens) token = a.tokens[row];
   if (kDistill) {
-    float tmax = NEG_INF;
     for (int j = t; j < a.K; j += NT) {
-      const int id = a.ids[row * a.K + j];
-      const float tv = a.teacher[row * a.K + j];
-      const bool ok = id >= 0 && id < a.V;
-      kept.id[j] = ok ? id : -1;
-      kept.p[j] = ok ? tv : NEG_INF;
-      kept.x[j] = ok ? to_f32(xr[id]) : 0.f;
-      if (ok) tmax = fmaxf(tmax, tv);
+      cp_async4(smem_u32(kept.id + j), a.ids + row * a.K + j);
+      cp_async4(smem_u32(kept.p + j), a.teacher + row * a.K + j);
     }
-    tmax = warp_max_f(tmax);
-    if (lane == 0) kept_max[warp] = tmax;
-    // (read after the statistics' barriers, or this one)
-    if (!kStat) __syncthreads();
+    cp_async_commit();
   }
+  if constexpr (RES) fetch_part(part, mine);
 
   Stat st{0.f, 1.f, 0.f};
   float my_max = NEG_INF;
   Segments segments(TOP ? top.segment : nullptr, part);
+  Stat own{NEG_INF, 0.f, 0.f};
   if (kStat) {
-    Stat own;
     if constexpr (RES)
       own = resident_stat<T, kEntropy>(part, mine, c);
     else
       own = part_stat<T, kEntropy, TOP>(part, segments, c);
     my_max = own.m;
+  }
+  if (!RES) prefetch_row<T>(a, row, C, lo, hi);
+  // The student's logits of the teacher's slots; the first one of a thread is
+  // used after the row's statistic and comes in meanwhile.
+  float x_first = 0.f;
+  if (kDistill) {
+    cp_async_wait_all();
+    float tmax = NEG_INF;
+    for (int j = t; j < a.K; j += NT) {
+      const int id = kept.id[j];
+      const bool ok = id >= 0 && id < a.V;
+      const float x = ok ? to_f32(xr[id]) : 0.f;
+      if (ok)
+        tmax = fmaxf(tmax, kept.p[j]);
+      else {
+        kept.id[j] = -1;
+        kept.p[j] = NEG_INF;
+      }
+      if (j == t)
+        x_first = x;
+      else
+        kept.x[j] = x;
+    }
+    tmax = warp_max_f(tmax);
+    if (lane == 0) kept_max[warp] = tmax;
+    if (!kStat) __syncthreads();  // (the statistic has barriers of its own)
+  }
+  float x_token = 0.f;
+  if (OP == RowOp::kLogpFwd && token >= 0 && token < a.V) x_token = to_f32(xr[token]);
+  if (kStat) {
     st = row_stat<NT, kEntropy>(own, c, stage, C);
     if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale)  // uniform over the cluster
       st = row_stat<NT, kEntropy>(part_stat_any<NT, T, kEntropy>(part, c), c, stage, C);
@@ -720,9 +782,8 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_ker
       if (a.lse) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
       if (a.entropy) a.entropy[row] = empty ? 0.f : kLn2 * (l2s - st.u / st.s);
       if (a.tokens) {
-        const int id = a.tokens[row];
         float lp = 0.f;
-        if (id >= 0 && id < a.V) lp = empty ? NEG_INF : (to_f32(xr[id]) - ref) * inv_t - kLn2 * l2s;
+        if (token >= 0 && token < a.V) lp = empty ? NEG_INF : (x_token - ref) * inv_t - kLn2 * l2s;
         a.logprob[row] = lp;
       }
     }
@@ -818,7 +879,8 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_ker
         const float w = ex2(d * c);
         z += w;
         // in natural units: a lowest-value mask stays finite there
-        if (w > 0.f) gap += w * (d * inv_t - (kept.x[j] - ref) * inv_t);
+        const float x = j == t ? x_first : kept.x[j];
+        if (w > 0.f) gap += w * (d * inv_t - (x - ref) * inv_t);
         kept.p[j] = w;
       }
       z = warp_sum(z);
@@ -859,7 +921,7 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_ker
               if (k < j) first = false;
               p += kept.p[k];
             }
-          if (first) dst[id - lo] = from_f32<T>(grad(both(kept.x[j])).x - g * p * iz);
+          if (first) dst[id - lo] = from_f32<T>(grad(both(j == t ? x_first : kept.x[j])).x - g * p * iz);
         }
     } else {
       __syncthreads();
@@ -877,7 +939,7 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, 3) rows_ker
 }
 
 template <typename T, RowOp OP, bool TOP, bool RES>
-cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
+cudaError_t launch_rows_t(RowArgs a, int C, cudaStream_t st) {
   const size_t smem = TOP ? sizeof(TopShared) : (RES ? kResident * 16 : 0) + (size_t)a.K * 12;
   if (smem > 40 * 1024) {  // beyond 48 KB with the static part
     const cudaError_t e = cudaFuncSetAttribute(rows_kernel<T, OP, TOP, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -885,6 +947,7 @@ cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
+  a.ahead = std::max(1, 4 * a.num_sms / C);
   cfg.gridDim = dim3((unsigned)(a.rows * C));
   cfg.blockDim = dim3(RES ? kResidentThreads : kThreads);
   cfg.dynamicSmemBytes = smem;

@@ -71,6 +71,7 @@ struct RowArgs {
   float* loss;
   float* lse;  // written forward, read backward
   int num_sms;
+  int ahead;  // set by the launch: rows between a block's row and the next one in its place
 };
 cudaError_t launch_rows(RowOp op, const RowArgs& a, cudaStream_t st);
 
