@@ -17,201 +17,25 @@
 //
 // Bound by HBM when an element costs few enough instructions: unpacking, the
 // maximum, two packed operations for d, one exponential and one or two packed
-// sums.  Where the loss and the gradient come from one call the row's part
-// stays in shared memory between its two passes, so it is read once.
+// sums.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 
-#include "elem.cuh"
-#include "internal.h"
-#include "packed.cuh"
-#include "ptx.cuh"
-#include "train.h"
+#include "logits.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace ibwd {
 namespace {
 
-constexpr int kThreads = 256;         // streaming kernels
-constexpr int kResidentThreads = 128;  // kernels that keep their part in shared memory
+constexpr int kThreads = 256;
 constexpr int kMaxWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = 128;
-constexpr int kCand = 1024;  // candidates a block ranks for the top alternatives
+constexpr int kBlocks = 4;     // of an SM
+constexpr int kAhead = 64 * 1024;  // bytes of the next row
+constexpr int kCand = 1024;    // candidates a block ranks for the top alternatives
 constexpr int kSegments = 16;  // maxima a thread keeps of its logits
-constexpr int kUnroll = 4;   // vectors a thread takes together
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
-// An exponent whose power of two is 0, kept finite so that 0 times it is 0.
-constexpr float kLeast = -1e20f;
-#define NEG_INF (-INFINITY)
-
-struct Stat {
-  float m, s, u;
-};
-
-// The reference point of the exponents: the maximum, or 0 while there is none
-// (every term is then 2^-inf = 0; x - m of two infinities never occurs).
-__device__ __forceinline__ float finite_max(float m) { return m == NEG_INF ? 0.f : m; }
-
-// The part [lo, hi) of a row as a block reads it: single elements up to a
-// 16-byte boundary, whole 16-byte vectors, single elements.
-template <typename T>
-struct Part {
-  const T* head;
-  int nhead, nvec, ntail;
-  __device__ Part(const T* row, int lo, int hi) {
-    head = row + lo;
-    const int n = hi - lo;
-    const int mis = (int)((16 - (reinterpret_cast<uintptr_t>(head) & 15)) & 15) / (int)sizeof(T);
-    nhead = min(n, mis);
-    nvec = (n - nhead) / kVec<T>;
-    ntail = n - nhead - nvec * kVec<T>;
-  }
-  __device__ const T* vec(int i) const { return head + nhead + (long long)i * kVec<T>; }
-  // single elements are numbered 0 .. nhead + ntail - 1
-  __device__ int singles() const { return nhead + ntail; }
-  __device__ int single_at(int i) const { return i < nhead ? i : i + nvec * kVec<T>; }  // offset from head
-};
-
-// Calls f(x, v) for every element of the part, which begins at index lo.
-template <int NT, typename T, typename F>
-__device__ __forceinline__ void for_each(const Part<T>& p, int lo, F f) {
-  for (int i = threadIdx.x; i < p.nvec; i += NT) {
-    float v[kVec<T>];
-    unpack(ld_stream(p.vec(i)), v, T{});
-#pragma unroll
-    for (int k = 0; k < kVec<T>; ++k) f(v[k], lo + p.nhead + i * kVec<T> + k);
-  }
-  if ((int)threadIdx.x < p.singles()) {
-    const int o = p.single_at(threadIdx.x);
-    f(to_f32(p.head[o]), lo + o);
-  }
-}
-
-// -------------------------------------------------------------- statistics --
-// The careful statistic: any values, one element at a time.
-template <int NT, typename T, bool U>
-__device__ __noinline__ Stat part_stat_any(const Part<T>& p, float c) {
-  Stat t{NEG_INF, 0.f, 0.f};
-  for_each<NT>(p, 0, [&](float x, int) {
-    if (x > t.m) {
-      const float d = fmaxf((t.m - x) * c, kLeast), f = ex2(d);
-      t.u = f * (t.u + t.s * d);
-      t.s *= f;
-      t.m = x;
-    }
-    const float d = (x - finite_max(t.m)) * c, e = ex2(d);
-    t.s += e;
-    t.u = fmaf(e, fmaxf(d, kLeast), t.u);  // 0 for a masked logit
-  });
-  return t;
-}
-
-// The fast statistic starts from the maximum kFloor, so that x - m is always
-// finite: a logit far below it (a mask) adds 2^-huge = 0.  It does not hold
-// for rows without a logit above kFloor, nor for scales that make kFloor
-// small or huge; those take the careful one.
-constexpr float kFloor = -9.9499216e29f;  // 0xF1490000: also a bf16
-constexpr float kLeastScale = 1e-20f, kMostScale = 1e6f;
-
-struct Run {
-  float m;
-  float2 s, u;  // two interleaved sums
-};
-
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __nv_bfloat16) {
-  uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half) {
-  uint32_t d;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// max(a, kFloor) that keeps a NaN.
-__device__ __forceinline__ float floor_nan(float a) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(kFloor));
-  return d;
-}
-
-template <typename T, int N>
-__device__ __forceinline__ float max_of(const uint4 (&r)[N]) {
-  if constexpr (sizeof(T) == 4) {
-    float m = kFloor;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(r[i].x), __uint_as_float(r[i].y)),
-                         fmaxf(__uint_as_float(r[i].z), __uint_as_float(r[i].w))));
-    return m;
-  } else {
-    uint32_t m = max2(max2(r[0].x, r[0].y, T{}), max2(r[0].z, r[0].w, T{}), T{});
-#pragma unroll
-    for (int i = 1; i < N; ++i) m = max2(m, max2(max2(r[i].x, r[i].y, T{}), max2(r[i].z, r[i].w, T{}), T{}), T{});
-    const float2 f = unpack2(m, T{});
-    return fmaxf(f.x, f.y);
-  }
-}
-
-__device__ __forceinline__ void raise(Run& t, float m, float c, bool u) {
-  if (m > t.m) {
-    const float d = fmaxf((t.m - m) * c, kLeast), f = ex2(d);
-    if (u) {
-      t.u.x = f * fmaf(t.s.x, d, t.u.x);
-      t.u.y = f * fmaf(t.s.y, d, t.u.y);
-    }
-    t.s.x *= f;
-    t.s.y *= f;
-    t.m = m;
-  }
-}
-
-template <bool U>
-__device__ __forceinline__ void add_pair(Run& t, float2 x, float2 neg_m, float2 c2) {
-  if (U) {  // 0 * -inf is no term: masked logits are lifted to kFloor
-    x.x = floor_nan(x.x);
-    x.y = floor_nan(x.y);
-  }
-  const float2 d = mul2(add2(x, neg_m), c2);
-  const float2 e = make_float2(ex2(d.x), ex2(d.y));
-  t.s = add2(t.s, e);
-  if (U) t.u = fma2(e, d, t.u);
-}
-
-// Adds vectors of maximum `most`.
-template <typename T, bool U, int N>
-__device__ __forceinline__ void add_vectors(Run& t, const uint4 (&r)[N], float most, float c) {
-  raise(t, most, c, U);
-  const float2 nm = both(-t.m), c2 = both(c);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      add_pair<U>(t, make_float2(__uint_as_float(r[i].x), __uint_as_float(r[i].y)), nm, c2);
-      add_pair<U>(t, make_float2(__uint_as_float(r[i].z), __uint_as_float(r[i].w)), nm, c2);
-    } else {
-      add_pair<U>(t, unpack2(r[i].x, T{}), nm, c2);
-      add_pair<U>(t, unpack2(r[i].y, T{}), nm, c2);
-      add_pair<U>(t, unpack2(r[i].z, T{}), nm, c2);
-      add_pair<U>(t, unpack2(r[i].w, T{}), nm, c2);
-    }
-  }
-}
-
-template <typename T, bool U>
-__device__ __forceinline__ Stat finish(Run& t, const Part<T>& p, float c) {
-  if ((int)threadIdx.x < p.singles()) {
-    const float x = to_f32(p.head[p.single_at(threadIdx.x)]);
-    raise(t, fmaxf(x, kFloor), c, U);
-    const float d = (floor_nan(x) - t.m) * c, e = ex2(d);
-    t.s.x += e;
-    if (U) t.u.x = fmaf(e, d, t.u.x);
-  }
-  return Stat{t.m, t.s.x + t.s.y, t.u.x + t.u.y};
-}
 
 // Order of the logits as unsigned numbers (-0 counts as +0).
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -276,79 +100,16 @@ __device__ __forceinline__ Stat part_stat(const Part<T>& p, Segments& seg, float
   return finish<T, U>(t, p, c);
 }
 
-// Through shared memory, where the part stays: each thread copies the vectors
-// it reads itself, all of them at once, and takes them up as they arrive.
-constexpr int kGroups = 8;
-constexpr int kResident = kGroups * kUnroll * kResidentThreads;  // vectors a part may have: 64 KB
-
-template <typename T>
-__device__ __forceinline__ void fetch_part(const Part<T>& p, uint32_t mine) {
-  const T* from = p.vec(threadIdx.x);
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      constexpr int NT = kResidentThreads;
-      const int o = (g * kUnroll + k) * NT;
-      if ((int)threadIdx.x + o < p.nvec) cp_async16(mine + o * 16, from + o * kVec<T>, 16);
-    }
-    cp_async_commit();
-  }
-}
-
-template <typename T, bool U, int G>
-__device__ __forceinline__ void take_group(Run& t, const Part<T>& p, uint32_t mine, float c) {
-  constexpr int NT = kResidentThreads;
-  cp_async_wait<kGroups - 1 - G>();
-  const int first = (int)threadIdx.x + G * kUnroll * NT;
-  const uint32_t from = mine + G * kUnroll * NT * 16;
-  if (first + (kUnroll - 1) * NT < p.nvec) {
-    uint4 r[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) r[k] = ld_shared_v4(from + k * NT * 16);
-    add_vectors<T, U>(t, r, max_of<T>(r), c);
-  } else {
-#pragma unroll 1
-    for (int k = 0; first + k * NT < p.nvec; ++k) {
-      const uint4 r[1] = {ld_shared_v4(from + k * NT * 16)};
-      add_vectors<T, U>(t, r, max_of<T>(r), c);
-    }
-  }
-  if constexpr (G + 1 < kGroups) take_group<T, U, G + 1>(t, p, mine, c);
-}
-
-template <typename T, bool U>
-__device__ __forceinline__ Stat resident_stat(const Part<T>& p, uint32_t mine, float c) {
-  Run t{kFloor, {0.f, 0.f}, {0.f, 0.f}};
-  take_group<T, U, 0>(t, p, mine, c);
-  return finish<T, U>(t, p, c);
-}
-
-__device__ __forceinline__ float warp_max_f(float v) {
-  // as signed numbers of the same order, in one instruction
-  int b = __float_as_int(v);
-  b ^= (b >> 31) & 0x7FFFFFFF;
-  b = __reduce_max_sync(0xffffffffu, b);
-  return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF));
-}
-
 struct Stage {
   float m[kMaxWarps], s[kMaxWarps], u[kMaxWarps];
   Stat of_block[kMaxCluster];
 };
 
-// Terms of a part brought to the reference point of a larger set.
-__device__ __forceinline__ void rescale(Stat& t, float m, float c) {
-  const float d = fmaxf((t.m - finite_max(m)) * c, kLeast), f = ex2(d);
-  t.u = f * fmaf(t.s, d, t.u);
-  t.s *= f;
-  t.m = m;
-}
-
 // The statistic of the row in every thread of its blocks: the maximum first,
-// then sums in the order of lanes, warps and blocks.
+// then sums in the order of lanes, warps and blocks.  most: the maximum of
+// this block's part.
 template <int NT, bool U>
-__device__ __forceinline__ Stat row_stat(Stat t, float c, Stage& st, int C) {
+__device__ __forceinline__ Stat row_stat(Stat t, float c, Stage& st, int C, float& most) {
   constexpr int NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float wm = warp_max_f(t.m);
@@ -358,6 +119,7 @@ __device__ __forceinline__ Stat row_stat(Stat t, float c, Stage& st, int C) {
   float m = st.m[0];
 #pragma unroll
   for (int w = 1; w < NW; ++w) m = fmaxf(m, st.m[w]);
+  most = m;
   rescale(t, m, c);
   t.s = warp_sum(t.s);
   if (U) t.u = warp_sum(t.u);
@@ -402,7 +164,7 @@ struct TopShared {
   unsigned long long merge[kMaxTop * kMaxCluster];
   int merge_n[kMaxCluster];
   uint16_t segment[kSegments * kThreads];
-  uint16_t thread_max[kThreads];
+  int count_at[kThreads];  // threads by the distance of their maximum from the largest one
   int hot[kHot];
   int nhot, ncand;
   uint32_t least, below;
@@ -488,7 +250,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
     if (lane == 0) sh.warp_n[warp] = __popc(mask);
     __syncthreads();
     int at = have + __popc(mask & ((1u << lane) - 1u)), total = 0;
-    for (int w = 0; w < kMaxWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) at += sh.warp_n[w];
       total += sh.warp_n[w];
     }
@@ -505,42 +267,55 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
 // those bounds the n-th largest entry from below (they are maxima of disjoint
 // sets), and only segments whose maximum reaches the bound can hold an entry
 // that does, so the second look reads a few of them (a 131072-logit row: some
-// 80 of 4096).  One warp finds the bound, to the upper 16 bits of its order
-// (all of a bf16).
+// 80 of 4096).  The bound is found to the upper 16 bits of its order (all of
+// a bf16) by counting the maxima at each distance from the largest, or by
+// bisection where it is further away than that.
+// sh.count_at is zero and sh.nhot, sh.ncand are 0 on entry.
 template <typename T>
-__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, int shift,
+__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, float most, int shift,
                                         TopShared& sh, unsigned long long* out) {
-  const int t = threadIdx.x;
-  const uint32_t my_key = order_bits(my_max) >> 16;
-  sh.thread_max[t] = (uint16_t)my_key;
-  if (t == 0) sh.nhot = sh.ncand = 0;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const uint32_t my_key = order_bits(my_max) >> 16, top_key = order_bits(most) >> 16;
+  const bool near = top_key - my_key < kThreads;
+  if (near) atomicAdd(&sh.count_at[top_key - my_key], 1);
   __syncthreads();
   if (t < 32) {
-    uint32_t v[kMaxWarps];
+    // lane i has distances 8 i .. 8 i + 7
+    constexpr int PER = kThreads / 32;
+    int c[PER], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxWarps; ++i) v[i] = sh.thread_max[t + 32 * i];
-    uint32_t hi_key = v[0], lo_key = v[0];
-#pragma unroll
-    for (int i = 1; i < kMaxWarps; ++i) {
-      hi_key = max(hi_key, v[i]);
-      lo_key = min(lo_key, v[i]);
+    for (int i = 0; i < PER; ++i) {
+      c[i] = sh.count_at[lane * PER + i];
+      sum += c[i];
     }
-    hi_key = __reduce_max_sync(0xffffffffu, hi_key);
-    lo_key = __reduce_min_sync(0xffffffffu, lo_key);
-    // the largest key with at least n maxima at or above it, below the bits
-    // that all of them share
-    const int bits = 32 - __clz(hi_key ^ lo_key);
-    uint32_t key = hi_key >> bits << bits;
-#pragma unroll 1
-    for (uint32_t bit = (1u << bits) >> 1; bit; bit >>= 1) {
-      unsigned k = 0;
+    int upto = sum;  // maxima at the distances of this lane and those before it
 #pragma unroll
-      for (int i = 0; i < kMaxWarps; ++i) k += v[i] >= (key | bit);
-      if (__reduce_add_sync(0xffffffffu, k) >= (unsigned)n) key |= bit;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    if (t == 0) sh.bound = key;
+    const unsigned reach = __ballot_sync(0xffffffffu, upto >= n);
+    if (reach == 0) {
+      if (lane == 0) sh.bound = ~0u;
+    } else if (lane == __ffs(reach) - 1) {
+      int have = upto - sum, d = lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (have < n) {
+          have += c[i];
+          d = lane * PER + i;
+        }
+      sh.bound = top_key - d;
+    }
   }
   __syncthreads();
+  if (sh.bound == ~0u) {  // uniform: bisection over all 16 bits
+    uint32_t key = 0;
+    for (uint32_t bit = 1u << 15; bit; bit >>= 1)
+      if (__syncthreads_count(my_key >= (key | bit)) >= n) key |= bit;
+    if (t == 0) sh.bound = key;
+    __syncthreads();
+  }
   // (a thread without logits above kFloor stops there: no bound then)
   const uint32_t half = sh.bound > order_bits(kFloor) >> 16 ? sh.bound : 0;
   const uint32_t bound = max(half << 16, order_bits(NEG_INF) + 1);
@@ -554,41 +329,68 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
       }
   }
   __syncthreads();
-  auto offer = [&](float x, int v) {
-    if (x > NEG_INF && order_bits(x) >= bound) {
-      const int at = atomicAdd(&sh.ncand, 1);
-      if (at < kCand) sh.cand[at] = order_key(x, v);
-    }
-  };
   const int nhot = sh.nhot;
-  if (nhot <= kHot) {
-    const int bits = 2 + shift;  // a segment has 1 << bits vectors
-    static_assert(kUnroll == 4, "bits counts on it");
-    for (int e0 = t; e0 < nhot << bits; e0 += kUnroll * kThreads) {
-      uint4 r[kUnroll][1];
-      int at[kUnroll];
+  const float cut = half ? order_value(bound) : NEG_INF;
+  auto wanted = [&](float x) { return half ? x >= cut : x > cut; };
+  // Appends the wanted ones of a lane's E values: one addition a warp.
+  auto append = [&](unsigned mask, auto key_of) {
+    const int mine = __popc(mask);
+    int upto = mine;
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int e = e0 + k * kThreads;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    int base = 0;
+    if (lane == 31 && upto) base = atomicAdd(&sh.ncand, upto);
+    base = __shfl_sync(0xffffffffu, base, 31) + upto - mine;
+    for (; mask; mask &= mask - 1, ++base)
+      if (base < kCand) sh.cand[base] = key_of(__ffs(mask) - 1);
+  };
+  if (nhot <= kHot) {
+    static_assert(kUnroll == 4, "a segment has 4 << shift vectors");
+    const int bits = 2 + shift, items = nhot << bits;
+    constexpr int V = kVec<T>, TAKE = kUnroll;  // vectors a lane takes together: 32 values at most
+    for (int e0 = warp * 32; e0 < items; e0 += TAKE * kThreads) {
+      uint4 r[TAKE];
+      int at[TAKE];
+#pragma unroll
+      for (int k = 0; k < TAKE; ++k) {
+        const int e = e0 + lane + k * kThreads;
         at[k] = p.nvec;
-        if (e < nhot << bits) {
+        if (e < items) {
           const int h = sh.hot[e >> bits];
           at[k] = h % kThreads + (((h / kThreads) << bits) + (e & ((1 << bits) - 1))) * kThreads;
         }
-        if (at[k] < p.nvec) r[k][0] = ld_stream(p.vec(at[k]));
+        if (at[k] < p.nvec) r[k] = ld_stream(p.vec(at[k]));
       }
+      unsigned mask = 0;
+      float v[TAKE][V];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-        if (at[k] < p.nvec && (half == 0 || order_bits(max_of<T>(r[k])) >= bound)) {
-          float v[kVec<T>];
-          unpack(r[k][0], v, T{});
+      for (int k = 0; k < TAKE; ++k)
+        if (at[k] < p.nvec) {
+          unpack(r[k], v[k], T{});
 #pragma unroll
-          for (int j = 0; j < kVec<T>; ++j) offer(v[j], lo + p.nhead + at[k] * kVec<T> + j);
+          for (int j = 0; j < V; ++j) mask |= wanted(v[k][j]) ? 1u << (k * V + j) : 0u;
         }
+      append(mask, [&](int i) {
+        float x = 0.f;
+        int index = 0;
+#pragma unroll
+        for (int k = 0; k < TAKE; ++k)
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (i == k * V + j) {
+              x = v[k][j];
+              index = lo + p.nhead + at[k] * V + j;
+            }
+        return order_key(x, index);
+      });
     }
-    if (t < p.singles()) {
-      const int o = p.single_at(t);
-      offer(to_f32(p.head[o]), lo + o);
+    if (warp == 0) {
+      const int o = lane < p.singles() ? p.single_at(lane) : 0;
+      const float x = lane < p.singles() ? to_f32(p.head[o]) : NEG_INF;
+      append(wanted(x) ? 1u : 0u, [&](int) { return order_key(x, lo + o); });
     }
   }
   __syncthreads();
@@ -615,33 +417,24 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
 // --------------------------------------------------------------- gradients --
 // Writes the gradient of this block's part, f of each pair of logits: by
 // vectors where logits and gradient lie alike in their 16-byte blocks.
-// dst: the gradient of p.head[0].  RES: the vectors lie in shared memory.
-template <int NT, typename T, bool RES, typename F>
-__device__ __forceinline__ void map_part(const Part<T>& p, uint32_t mine, T* dst, F f) {
+// dst: the gradient of p.head[0].
+template <int NT, typename T, typename F>
+__device__ __forceinline__ void map_part(const Part<T>& p, T* dst, F f) {
   const bool alike = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(p.head)) & 15) == 0;
   if (alike) {
     T* dv = dst + p.nhead;
-    auto take = [&](int i) { return RES ? ld_shared_v4(mine + (i - threadIdx.x) * 16) : ld_stream(p.vec(i)); };
     auto give = [&](int i, uint4 r) {
-      if constexpr (sizeof(T) == 4) {
-        const float2 a = f(make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
-        const float2 b = f(make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
-        r = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
-      } else {
-        r = make_uint4(pack2_of(f(unpack2(r.x, T{})), T{}), pack2_of(f(unpack2(r.y, T{})), T{}),
-                       pack2_of(f(unpack2(r.z, T{})), T{}), pack2_of(f(unpack2(r.w, T{})), T{}));
-      }
-      st_stream(dv + (long long)i * kVec<T>, r);
+      st_stream(dv + (long long)i * kVec<T>, map_vector<T>(r, f));
     };
     int i = threadIdx.x;
     for (; i + (kUnroll - 1) * NT < p.nvec; i += kUnroll * NT) {
       uint4 r[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) r[k] = take(i + k * NT);
+      for (int k = 0; k < kUnroll; ++k) r[k] = ld_stream(p.vec(i + k * NT));
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) give(i + k * NT, r[k]);
     }
-    for (; i < p.nvec; i += NT) give(i, take(i));
+    for (; i < p.nvec; i += NT) give(i, ld_stream(p.vec(i)));
     if ((int)threadIdx.x < p.singles()) {
       const int o = p.single_at(threadIdx.x);
       dst[o] = from_f32<T>(f(both(to_f32(p.head[o]))).x);
@@ -656,52 +449,28 @@ __device__ __forceinline__ void map_part(const Part<T>& p, uint32_t mine, T* dst
 struct Kept {  // [K] each, in shared memory
   int* id;   // kept token, or -1
   float* p;  // the teacher's value, then 2^((value - max) c)
-  float* x;  // the student's logit of it
+  float* x;  // the student's logit of it (read by the thread that wrote it)
 };
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// Starts the next part that a block of this place will take on its way to L2
-// (its first kAhead bytes), while this one has no more loads to make: blocks
-// that began together are in their joins and selections together, and HBM
-// would idle meanwhile.
-constexpr int kAhead = 64 * 1024;
-template <typename T>
-__device__ __forceinline__ void prefetch_row(const RowArgs& a, long long row, int C, int lo, int hi) {
-  const long long next = row + a.ahead;
-  if (threadIdx.x != 0 || a.ahead == 0 || next >= a.rows || lo >= hi) return;
-  const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + next * a.x_stride + lo);
-  const uintptr_t to = from + (uintptr_t)(hi - lo) * sizeof(T);
-  const uintptr_t p = (from + 15) & ~(uintptr_t)15;
-  if (p + 16 > to) return;
-  const uint32_t bytes = (uint32_t)min((unsigned long long)kAhead, (unsigned long long)(to - p)) & ~15u;
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
-// RES: the part fits in shared memory and stays there (kDistillGrad only).
-template <typename T, RowOp OP, bool TOP, bool RES>
-__global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4) rows_kernel(RowArgs a, int C) {
-  constexpr int NT = RES ? kResidentThreads : kThreads, NW = NT / 32;
+template <typename T, RowOp OP, bool TOP>
+__global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int C) {
+  constexpr int NT = kThreads, NW = NT / 32;
   constexpr bool kDistill = OP == RowOp::kDistillFwd || OP == RowOp::kDistillBwd || OP == RowOp::kDistillGrad;
   constexpr bool kStat = OP == RowOp::kLogpFwd || OP == RowOp::kDistillFwd || OP == RowOp::kDistillGrad;
   constexpr bool kEntropy = OP == RowOp::kLogpFwd;
   __shared__ Stage stage;
   __shared__ float kept_max[kMaxWarps], kept_z[kMaxWarps], kept_gap[kMaxWarps];
-  extern __shared__ __align__(16) unsigned char raw[];  // TopShared, or the resident part and the kept tokens
+  extern __shared__ __align__(16) unsigned char raw[];  // TopShared, or the kept tokens
   TopShared& top = *reinterpret_cast<TopShared*>(raw);
   Kept kept;
-  kept.id = reinterpret_cast<int*>(raw + (RES ? kResident * 16 : 0));
+  kept.id = reinterpret_cast<int*>(raw);
   kept.p = reinterpret_cast<float*>(kept.id + a.K);
   kept.x = kept.p + a.K;
-  const uint32_t mine = smem_u32(raw) + threadIdx.x * 16;
 
   const int rank = C == 1 ? 0 : (int)(blockIdx.x % C);
   const long long row = blockIdx.x / C;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  // parts are whole multiples of 64 logits, so that aligned rows stay aligned
-  const int len = (((a.V + C - 1) / C) + 63) & ~63;
+  const int len = part_len(a.V, C);
   const int lo = (int)min((long long)a.V, (long long)rank * len), hi = (int)min((long long)a.V, (long long)lo + len);
   const T* xr = static_cast<const T*>(a.x) + row * a.x_stride;
   const Part<T> part(xr, lo, hi);
@@ -717,20 +486,16 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
     }
     cp_async_commit();
   }
-  if constexpr (RES) fetch_part(part, mine);
 
   Stat st{0.f, 1.f, 0.f};
-  float my_max = NEG_INF;
+  float my_max = NEG_INF, most = NEG_INF;  // of the thread's and of the block's logits
   Segments segments(TOP ? top.segment : nullptr, part);
   Stat own{NEG_INF, 0.f, 0.f};
   if (kStat) {
-    if constexpr (RES)
-      own = resident_stat<T, kEntropy>(part, mine, c);
-    else
-      own = part_stat<T, kEntropy, TOP>(part, segments, c);
+    own = part_stat<T, kEntropy, TOP>(part, segments, c);
     my_max = own.m;
   }
-  if (!RES) prefetch_row<T>(a, row, C, lo, hi);
+  prefetch_part<T>(a, row, lo, hi, kAhead);
   // The student's logits of the teacher's slots; the first one of a thread is
   // used after the row's statistic and comes in meanwhile.
   float x_first = 0.f;
@@ -759,9 +524,15 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
   float x_token = 0.f;
   if (OP == RowOp::kLogpFwd && token >= 0 && token < a.V) x_token = to_f32(xr[token]);
   if (kStat) {
-    st = row_stat<NT, kEntropy>(own, c, stage, C);
-    if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale)  // uniform over the cluster
-      st = row_stat<NT, kEntropy>(part_stat_any<NT, T, kEntropy>(part, c), c, stage, C);
+    if (TOP) {  // (before the statistic's barriers)
+      top.count_at[t] = 0;
+      if (t == 0) top.nhot = top.ncand = 0;
+    }
+    st = row_stat<NT, kEntropy>(own, c, stage, C, most);
+    if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale) {  // uniform over the cluster
+      float ignored;
+      st = row_stat<NT, kEntropy>(part_stat_any<NT, T, kEntropy>(part, c), c, stage, C, ignored);
+    }
   }
   // log2 p_v = (x_v - ref) c - l2s
   float ref, l2s;
@@ -795,12 +566,12 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
       };
       int total = 0;
       if (C == 1) {
-        total = part_top(part, lo, hi, n, my_max, segments.shift, top, top.merge);
+        total = part_top(part, lo, hi, n, my_max, most, segments.shift, top, top.merge);
         __syncthreads();
         for (int i = t; i < total; i += NT) put(i, top.merge[i]);
       } else {
         cg::cluster_group cl = cg::this_cluster();
-        const int count = part_top(part, lo, hi, n, my_max, segments.shift, top,
+        const int count = part_top(part, lo, hi, n, my_max, most, segments.shift, top,
                                    cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
         if (t == 0) *(cl.map_shared_rank(top.merge_n, 0) + rank) = count;
         cl.sync();
@@ -847,7 +618,7 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
     const float xt = here ? to_f32(xr[id]) : 0.f;
     __syncthreads();  // the logit is read before its place may be overwritten
     if (empty) {
-      map_part<NT, T, RES>(part, mine, dst, [](float2) { return both(0.f); });
+      map_part<NT>(part, dst, [](float2) { return both(0.f); });
       return;
     }
     // -p (g + b (log p + h))
@@ -859,7 +630,7 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
       d.y = fmaxf(d.y, kLeast);
       return mul2(p, fma2(d, k1, k0));
     };
-    map_part<NT, T, RES>(part, mine, dst, grad);
+    map_part<NT>(part, dst, grad);
     __syncthreads();
     if (t == 0 && here) dst[id - lo] = from_f32<T>(g + grad(both(xt)).x);
     return;
@@ -902,9 +673,9 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
         return mul2(make_float2(ex2(d.x), ex2(d.y)), g2);
       };
       if (zero)
-        map_part<NT, T, RES>(part, mine, dst, [](float2) { return both(0.f); });
+        map_part<NT>(part, dst, [](float2) { return both(0.f); });
       else
-        map_part<NT, T, RES>(part, mine, dst, grad);
+        map_part<NT>(part, dst, grad);
       __syncthreads();
       z = gap = 0.f;
 #pragma unroll
@@ -916,6 +687,7 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
           if (id < lo || id >= hi) continue;
           float p = 0.f;
           bool first = true;
+#pragma unroll 4
           for (int k = 0; k < a.K; ++k)
             if (kept.id[k] == id) {
               if (k < j) first = false;
@@ -938,18 +710,13 @@ __global__ void __launch_bounds__(RES ? kResidentThreads : kThreads, RES ? 3 : 4
   }
 }
 
-template <typename T, RowOp OP, bool TOP, bool RES>
+template <typename T, RowOp OP, bool TOP>
 cudaError_t launch_rows_t(RowArgs a, int C, cudaStream_t st) {
-  const size_t smem = TOP ? sizeof(TopShared) : (RES ? kResident * 16 : 0) + (size_t)a.K * 12;
-  if (smem > 40 * 1024) {  // beyond 48 KB with the static part
-    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<T, OP, TOP, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = TOP ? sizeof(TopShared) : (size_t)a.K * 12;
   cudaLaunchConfig_t cfg{};
-  a.ahead = std::max(1, 4 * a.num_sms / C);
+  a.ahead = std::max(1, kBlocks * a.num_sms / C);
   cfg.gridDim = dim3((unsigned)(a.rows * C));
-  cfg.blockDim = dim3(RES ? kResidentThreads : kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -958,39 +725,38 @@ cudaError_t launch_rows_t(RowArgs a, int C, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP, RES>, a, C);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP>, a, C);
 }
-
-// Logits of a block's part when C blocks share a row.
-int part_len(int V, int C) { return (((V + C - 1) / C) + 63) & ~63; }
 
 template <typename T>
 cudaError_t launch_typed(RowOp op, const RowArgs& a, cudaStream_t st) {
-  // Blocks a row: as many as keep four an SM busy, while a part keeps two
-  // vectors a thread.
+  // Blocks a row.  Rows that meet in a cluster or select a top pay for each
+  // block (2-3 us of joins; a top's selection and merging more), so they
+  // share only where SMs would be idle, and parts keep some work: 8 rows of
+  // 65536 bf16 with 20 alternatives take 8.5 us in one block each, 8.8 in
+  // two, 16.6 in eight; 32 rows of 32768 with their gradient 7.6 and 6.6.
+  // The plain backward has no joins and takes as many as fill the SMs.
+  const bool top = op == RowOp::kLogpFwd && a.top_n;
+  const long long blocks = op == RowOp::kLogpBwd ? (long long)kBlocks * a.num_sms : a.num_sms;
+  const int least = (top ? 8 : 4) * kThreads * kVec<T>;
   int C = 1;
-  while (C < kMaxCluster && a.rows * 2 * C <= 4LL * a.num_sms && (long long)a.V >= 4LL * C * kThreads * kVec<T>) C *= 2;
+  while (C < kMaxCluster && a.rows * 2 * C <= blocks && a.V >= 2LL * C * least) C *= 2;
   switch (op) {
     case RowOp::kLogpFwd:
-      return a.top_n ? launch_rows_t<T, RowOp::kLogpFwd, true, false>(a, C, st)
-                     : launch_rows_t<T, RowOp::kLogpFwd, false, false>(a, C, st);
-    case RowOp::kLogpBwd: return launch_rows_t<T, RowOp::kLogpBwd, false, false>(a, C, st);
-    case RowOp::kDistillFwd: return launch_rows_t<T, RowOp::kDistillFwd, false, false>(a, C, st);
-    case RowOp::kDistillBwd: return launch_rows_t<T, RowOp::kDistillBwd, false, false>(a, C, st);
-    default: break;
+      return a.top_n ? launch_rows_t<T, RowOp::kLogpFwd, true>(a, C, st)
+                     : launch_rows_t<T, RowOp::kLogpFwd, false>(a, C, st);
+    case RowOp::kLogpBwd: return launch_rows_t<T, RowOp::kLogpBwd, false>(a, C, st);
+    case RowOp::kDistillFwd: return launch_rows_t<T, RowOp::kDistillFwd, false>(a, C, st);
+    case RowOp::kDistillBwd: return launch_rows_t<T, RowOp::kDistillBwd, false>(a, C, st);
+    default: return launch_rows_t<T, RowOp::kDistillGrad, false>(a, C, st);
   }
-  // loss and gradient: parts of at most 64 KB stay in shared memory, three
-  // blocks an SM
-  int R = C;
-  while (R < kMaxCluster && part_len(a.V, R) > kResident * kVec<T>) R *= 2;
-  if (part_len(a.V, R) <= kResident * kVec<T>) return launch_rows_t<T, RowOp::kDistillGrad, false, true>(a, R, st);
-  return launch_rows_t<T, RowOp::kDistillGrad, false, false>(a, C, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(RowOp op, const RowArgs& a, cudaStream_t st) {
   if (!a.rows) return cudaSuccess;
+  if (op == RowOp::kDistillGrad && distill_resident(a)) return launch_distill_resident(a, st);
   switch (a.type) {
     case 0: return launch_typed<float>(op, a, st);
     case 1: return launch_typed<__nv_bfloat16>(op, a, st);

@@ -74,5 +74,8 @@ struct RowArgs {
   int ahead;  // set by the launch: rows between a block's row and the next one in its place
 };
 cudaError_t launch_rows(RowOp op, const RowArgs& a, cudaStream_t st);
+// kDistillGrad with its rows resident in shared memory, where they fit.
+bool distill_resident(const RowArgs& a);
+cudaError_t launch_distill_resident(const RowArgs& a, cudaStream_t st);
 
 }  // namespace ibwd

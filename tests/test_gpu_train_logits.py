@@ -332,3 +332,21 @@ def test_offsets_past_32_bits():
     loss, dx = ibwd.distill_grad(x, ids, teacher, out=x)
     check_distill(loss[some], None, dx[some], torch.ones(len(some), device="cuda"), part, ids[some], teacher[some], 1.0,
                   "far rows")
+
+
+@pytest.mark.parametrize("rows,v,kind", [(2, 400000, "bf16"), (3, 170001, "fp32"), (700, 9000, "bf16"), (500, 18001, "fp16"),
+                                         (200, 37000, "bf16"), (170, 70001, "bf16"), (90, 150000, "bf16"),
+                                         (160, 60000, "fp32")])
+def test_loss_and_gradient_over_row_sizes(rows, v, kind):
+    """Rows that fit one, several or no blocks' shared memory, several rows a block."""
+    x = logits(rows, v, kind, seed=rows)
+    ids, teacher = kept(x, 30)
+    w = torch.rand(rows, device="cuda")
+    loss, dx = ibwd.distill_grad(x, ids, teacher, w)
+    step = max(1, (1 << 23) // v)
+    for a in range(0, rows, step):
+        r = slice(a, min(rows, a + step))
+        check_distill(loss[r], None, dx[r], w[r], x[r], ids[r], teacher[r], 1.0, f"{rows}x{v}")
+    z = x.clone()
+    l2, d2 = ibwd.distill_grad(z, ids, teacher, w, out=z)
+    assert same(l2, loss) and same(z, dx)
