@@ -30,8 +30,9 @@ namespace {
 
 constexpr int kThreads = 256;     // block of several teams, and of the kernels for wide rows
 constexpr int kMaxTeam = 512;     // threads of a block that is one team
-constexpr int kCluster = 8;       // blocks whose column sums meet before they are written
+constexpr int kCluster = 2;       // blocks whose column sums meet before they are written
 constexpr int kElems = 16;        // elements of a row a thread holds at most
+constexpr int kFwdPerSm = 768, kBwdPerSm = 512;  // threads of an SM: 80 and 128 registers each
 // Rows of a team in flight or in work: four, or three where a row of 8192
 // elements of x and dy takes 64 KB (227 KB of shared memory a block).
 template <typename TX, typename TD>
@@ -124,6 +125,35 @@ __device__ __forceinline__ float weight(const void* w, int n, bool f32, float no
   return f32 ? static_cast<const float*>(w)[n] : to_f32(static_cast<const T*>(w)[n]);
 }
 
+// gamma / beta of this thread's elements as pairs: K chunks of VEC, T chunks
+// apart, `none` without a vector and 0 beyond the row.
+template <typename TX, int VEC, int K>
+__device__ __forceinline__ void weights(float2 (&out)[K * VEC / 2], const void* w, bool f32, float none, int t, int T,
+                                        int nvec) {
+  const bool wide = VEC >= 4 && f32 && w != nullptr && (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < K * VEC / 4; ++i) {
+      const int j = t + 4 * i / VEC * T;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < nvec) v = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + j * VEC + 4 * i % VEC);
+      out[2 * i] = make_float2(v.x, v.y);
+      out[2 * i + 1] = make_float2(v.z, v.w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < K * VEC / 2; ++i) {
+    float v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = 2 * i + h, j = t + e / VEC * T;
+      v[h] = j < nvec ? weight<TX>(w, j * VEC + e % VEC, f32, none) : 0.f;
+    }
+    out[i] = make_float2(v[0], v[1]);
+  }
+}
+
 // Elements 2i and 2i + 1 of a chunk list as fp32, and back.
 template <typename T, int VEC, int K>
 __device__ __forceinline__ float2 pair_of(const Chunk<T, VEC> (&c)[K], int i) {
@@ -196,8 +226,8 @@ __device__ __forceinline__ float over_n(float s, float n, float inv_n) {
   return fmaf(fmaf(-q, n, s), inv_n, q);
 }
 
-template <typename TX, typename TY, int VEC, int K, int TEAM>
-__global__ void __launch_bounds__(TEAM ? kThreads : kMaxTeam) norm_fwd_team(NormFwdArgs a) {
+template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT>
+__global__ void __launch_bounds__(MAXT, kFwdPerSm / MAXT) norm_fwd_team(NormFwdArgs a) {
   constexpr int kStages = 4;
   extern __shared__ __align__(16) unsigned char smem[];  // the ring
   __shared__ __align__(16) float stage[64];
@@ -210,18 +240,8 @@ __global__ void __launch_bounds__(TEAM ? kThreads : kMaxTeam) norm_fwd_team(Norm
   if (TEAM == 0 && threadIdx.x < 64) stage[threadIdx.x] = 0.f;
   if (TEAM == 0) __syncthreads();
   float2 g[P], b[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    float w[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int e = 2 * i + h, j = t + e / VEC * T, n = j * VEC + e % VEC;
-      w[h] = j < nvec ? weight<TX>(a.gamma, n, a.w_type == 0, 1.f) : 0.f;
-      w[2 + h] = j < nvec ? weight<TX>(a.beta, n, a.w_type == 0, 0.f) : 0.f;
-    }
-    g[i] = make_float2(w[0], w[1]);
-    b[i] = make_float2(w[2], w[3]);
-  }
+  weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec);
+  weights<TX, VEC, K>(b, a.beta, a.w_type == 0, 0.f, t, T, nvec);
   using XRing = Ring<TX, VEC, K>;
   const XRing ring(smem, threadIdx.x, blockDim.x);
   Chunk<TX, VEC> cur[K] = {};  // (zero where a thread has no element)
@@ -332,8 +352,8 @@ __device__ __forceinline__ void write_sums(const NormBwdArgs& a, const float* su
   cl.sync();  // no block leaves while its sums are read
 }
 
-template <typename TX, typename TD, int VEC, int K, int TEAM>
-__global__ void __launch_bounds__(TEAM ? kThreads : kMaxTeam) norm_bwd_team(NormBwdArgs a, int cluster) {
+template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
+__global__ void __launch_bounds__(MAXT, kBwdPerSm / MAXT) norm_bwd_team(NormBwdArgs a, int cluster) {
   constexpr int kStages = kStagesOf<TX, TD>;
   extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end [2][N] column sums
   float* sums = reinterpret_cast<float*>(smem);
@@ -348,17 +368,9 @@ __global__ void __launch_bounds__(TEAM ? kThreads : kMaxTeam) norm_bwd_team(Norm
     for (int i = threadIdx.x; i < 128; i += blockDim.x) stage[i] = 0.f;
   if (TEAM == 0) __syncthreads();
   float2 g[P], dg[P], db[P];
+  weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec);
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    float w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int e = 2 * i + h, j = t + e / VEC * T;
-      w[h] = j < nvec ? weight<TX>(a.gamma, j * VEC + e % VEC, a.w_type == 0, 1.f) : 0.f;
-    }
-    g[i] = make_float2(w[0], w[1]);
-    dg[i] = db[i] = both(0.f);
-  }
+  for (int i = 0; i < P; ++i) dg[i] = db[i] = both(0.f);
   using XRing = Ring<TX, VEC, K>;
   using DRing = Ring<TD, VEC, K>;
   constexpr bool kAsync = XRing::kAsync && DRing::kAsync;
@@ -613,10 +625,11 @@ TeamShape team_shape(long long rows, int N, int elems, int teams_per_block, int 
   s.blocks = (int)std::min<long long>(rows, (long long)num_sms * std::max(1, per_sm / s.threads));
   s.cluster = 1;
   if (sums) {
-    // column sums meet in clusters; up to 16 rows one cluster takes them all
-    // and writes the results itself
+    // column sums meet in clusters of two (of eight, not all clusters were
+    // resident at once: 8192x4096 bf16 took 60 us, without sums 35); up to
+    // 16 rows one cluster takes them all and writes the results itself
     s.cluster = kCluster;
-    s.blocks = rows <= 2 * kCluster ? kCluster : (s.blocks + kCluster - 1) / kCluster * kCluster;
+    s.blocks = rows <= 8 * kCluster ? kCluster : (s.blocks + kCluster - 1) / kCluster * kCluster;
   }
   return s;
 }
@@ -645,15 +658,19 @@ bool aligned(const void* p, long long stride, int size, int bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0;
 }
 
-constexpr int kFwdPerSm = 768, kBwdPerSm = 512;
-
-template <typename TX, typename TY, int VEC, int K, int TEAM>
-cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
+template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT>
+cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
   const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, kFwdPerSm, a.num_sms,
                                  false);
   using XRing = Ring<TX, VEC, K>;
   const size_t smem = XRing::kAsync ? (size_t)4 * XRing::kRow * s.threads : 0;
-  return launch_cluster(norm_fwd_team<TX, TY, VEC, K, TEAM>, s, smem, st, a);
+  return launch_cluster(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT>, s, smem, st, a);
+}
+
+template <typename TX, typename TY, int VEC, int K, int TEAM>
+cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
+  if (TEAM || a.N <= kThreads * kElems) return fwd_launch<TX, TY, VEC, K, TEAM, kThreads>(a, st);
+  return fwd_launch<TX, TY, VEC, K, 0, kMaxTeam>(a, st);
 }
 
 template <typename TX, typename TY>
@@ -688,8 +705,8 @@ cudaError_t join_sums(const NormBwdArgs& a, int groups, cudaStream_t st) {
                    a.dgamma, a.dbeta);
 }
 
-template <typename TX, typename TD, int VEC, int K, int TEAM>
-cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
+template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
+cudaError_t bwd_launch(const NormBwdArgs& a, cudaStream_t st) {
   const bool sums = a.dgamma || a.dbeta;
   const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, kBwdPerSm, a.num_sms,
                                  sums);
@@ -697,10 +714,16 @@ cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
   using DRing = Ring<TD, VEC, K>;
   const size_t rings = (size_t)kStagesOf<TX, TD> * (XRing::kRow + DRing::kRow) * s.threads;
   const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, sums ? 2 * a.N * sizeof(float) : 0);
-  cudaError_t e = launch_cluster(norm_bwd_team<TX, TD, VEC, K, TEAM>, s, smem, st, a, s.cluster);
+  cudaError_t e = launch_cluster(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT>, s, smem, st, a, s.cluster);
   const int groups = s.blocks / s.cluster;
   if (e == cudaSuccess && sums && groups > 1) e = join_sums(a, groups, st);
   return e;
+}
+
+template <typename TX, typename TD, int VEC, int K, int TEAM>
+cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
+  if (TEAM || a.N <= kThreads * kElems) return bwd_launch<TX, TD, VEC, K, TEAM, kThreads>(a, st);
+  return bwd_launch<TX, TD, VEC, K, 0, kMaxTeam>(a, st);
 }
 
 template <typename TX, typename TD>
