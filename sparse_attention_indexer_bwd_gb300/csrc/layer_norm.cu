@@ -11,11 +11,9 @@
 // thread copies its own elements of the next rows into its own slots of a
 // shared-memory ring (cp.async), so several rows are in flight without
 // registers or barriers.  gamma and beta stay in registers, and so do the
-// backward pass's column sums of the team's rows.  Those meet in a fixed order: a block's teams in shared memory, the
-// blocks of a cluster through distributed shared memory, the clusters in a
-// second small kernel.  Rows too wide for a block take several passes.
-#include <cooperative_groups.h>
-
+// backward pass's column sums of the team's rows.  Those meet in a fixed
+// order: a block's teams in shared memory, the blocks in a second small
+// kernel.  Rows too wide for a block take several passes.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -23,14 +21,11 @@
 #include "packed.cuh"
 #include "train.h"
 
-namespace cg = cooperative_groups;
-
 namespace ibwd {
 namespace {
 
 constexpr int kThreads = 256;     // block of several teams, and of the kernels for wide rows
 constexpr int kMaxTeam = 512;     // threads of a block that is one team
-constexpr int kCluster = 2;       // blocks whose column sums meet before they are written
 constexpr int kElems = 16;        // elements of a row a thread holds at most
 constexpr int kFwdPerSm = 768, kBwdPerSm = 512;  // threads of an SM: 80 and 128 registers each
 // Rows of a team in flight or in work: four, or three where a row of 8192
@@ -185,6 +180,17 @@ __device__ __forceinline__ void set_pair(Chunk<T, VEC> (&c)[K], int i, float2 v)
   }
 }
 
+// Two consecutive column sums at an even column: 8 bytes where the row of
+// sums begins on an even one, too.
+__device__ __forceinline__ void put_pair(float* p, float2 v) {
+  if ((reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+    *reinterpret_cast<float2*>(p) = v;
+  } else {
+    p[0] = v.x;
+    p[1] = v.y;
+  }
+}
+
 // Sums of K values over a team, the same bits in each of its threads.  TEAM
 // lanes of a warp, or 0 for the block: then `stage` holds 2 * K * 32 floats,
 // zero beyond the block's warps and used in turn (`turn` flips), so one
@@ -320,43 +326,10 @@ __global__ void __launch_bounds__(MAXT, kFwdPerSm / MAXT) norm_fwd_team(NormFwdA
   cp_async_wait_all();
 }
 
-// Column sums of a block, [2][N] in shared memory in the order of the
-// teams, written to part[group] -- or, where there is only one group, to
-// dgamma and dbeta.  A cluster's blocks first add up: each takes a share of
-// the columns over the blocks in their order.
-__device__ __forceinline__ void write_sums(const NormBwdArgs& a, const float* sums, int cluster) {
-  const int n2 = 2 * a.N;
-  const int groups = gridDim.x / cluster, group = blockIdx.x / cluster;
-  auto put = [&](int c, float v) {
-    if (groups > 1)
-      a.part[(long long)group * n2 + c] = v;
-    else if (c < a.N) {
-      if (a.dgamma) a.dgamma[c] = v;
-    } else if (a.dbeta)
-      a.dbeta[c - a.N] = v;
-  };
-  if (cluster == 1) {
-    __syncthreads();
-    for (int c = threadIdx.x; c < n2; c += blockDim.x) put(c, sums[c]);
-    return;
-  }
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  const int rank = (int)cl.block_rank();
-  for (int c = rank * blockDim.x + threadIdx.x; c < n2; c += kCluster * blockDim.x) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kCluster; ++i) v += *cl.map_shared_rank(sums + c, i);
-    put(c, v);
-  }
-  cl.sync();  // no block leaves while its sums are read
-}
-
 template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
-__global__ void __launch_bounds__(MAXT, kBwdPerSm / MAXT) norm_bwd_team(NormBwdArgs a, int cluster) {
+__global__ void __launch_bounds__(MAXT, kBwdPerSm / MAXT) norm_bwd_team(NormBwdArgs a) {
   constexpr int kStages = kStagesOf<TX, TD>;
-  extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end [2][N] column sums
-  float* sums = reinterpret_cast<float*>(smem);
+  extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end the teams' column sums
   __shared__ __align__(16) float stage[128];
   constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
   constexpr int P = K * VEC / 2;  // pairs a thread
@@ -466,47 +439,75 @@ __global__ void __launch_bounds__(MAXT, kBwdPerSm / MAXT) norm_bwd_team(NormBwdA
   }
   cp_async_wait_all();
   if (!a.dgamma && !a.dbeta) return;
-  __syncthreads();  // the rings are done with
-  // the teams' sums, in the teams' order
-  for (int w = 0; w < TPB; ++w) {
-    if (w == team)
+  griddep_launch_dependents();  // the join's blocks come as these leave
+  // The block's column sums: a group of part[groups][2][N] -- or, where it is
+  // the only block, dgamma and dbeta.
+  float* const out_g = gridDim.x > 1 ? a.part + (long long)blockIdx.x * 2 * a.N : a.dgamma;
+  float* const out_b = gridDim.x > 1 ? out_g + a.N : a.dbeta;
+  if constexpr (TEAM == 0) {
 #pragma unroll
-      for (int e = 0; e < 2 * P; ++e) {
-        const int j = t + e / VEC * T, c = j * VEC + e % VEC;
-        if (j < nvec) {
-          const float vg = e & 1 ? dg[e / 2].y : dg[e / 2].x, vb = e & 1 ? db[e / 2].y : db[e / 2].x;
-          sums[c] = w ? sums[c] + vg : vg;
-          sums[a.N + c] = w ? sums[a.N + c] + vb : vb;
-        }
+    for (int i = 0; i < P; ++i) {
+      const int j = t + 2 * i / VEC * T, c = j * VEC + 2 * i % VEC;
+      if constexpr (VEC == 1) {
+        if (j < nvec && out_g) out_g[c] = dg[i].x;
+        if (j < nvec && out_b) out_b[c] = db[i].x;
+        if (j + T < nvec && out_g) out_g[c + T] = dg[i].y;
+        if (j + T < nvec && out_b) out_b[c + T] = db[i].y;
+      } else {
+        if (j < nvec && out_g) put_pair(out_g + c, dg[i]);
+        if (j < nvec && out_b) put_pair(out_b + c, db[i]);
       }
-    if (TPB > 1) __syncthreads();
+    }
+  } else {
+    // the teams' sums side by side in shared memory, added in the teams' order
+    float* const sums = reinterpret_cast<float*>(smem) + team * 2 * a.N;
+    __syncthreads();  // the rings are done with
+#pragma unroll
+    for (int e = 0; e < 2 * P; ++e) {
+      const int j = t + e / VEC * T, c = j * VEC + e % VEC;
+      if (j < nvec) {
+        sums[c] = e & 1 ? dg[e / 2].y : dg[e / 2].x;
+        sums[a.N + c] = e & 1 ? db[e / 2].y : db[e / 2].x;
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.N; c += kThreads) {
+      float v = 0.f;
+      for (int w = 0; w < TPB; ++w) v += reinterpret_cast<const float*>(smem)[w * 2 * a.N + c];
+      if (c < a.N) {
+        if (out_g) out_g[c] = v;
+      } else if (out_b) {
+        out_b[c - a.N] = v;
+      }
+    }
   }
-  griddep_launch_dependents();
-  write_sums(a, sums, cluster);
 }
 
 // dgamma and dbeta from the groups' column sums [groups][2][N]: 32 columns a
-// block, eight interleaved sums of groups each, joined in order.
-__global__ void __launch_bounds__(kThreads) norm_bwd_join(const float* part, int groups, int N, float* dgamma,
-                                                          float* dbeta) {
-  __shared__ float s[8][33];
+// block, 32 interleaved sums of groups each, joined in order.
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) norm_bwd_join(const float* part, int groups, int N, float* dgamma,
+                                                              float* dbeta) {
+  __shared__ float s[32][33];
   griddep_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < 2 * N) {
-#pragma unroll 4
-    for (int i = w; i < groups; i += 8) v += part[(long long)i * 2 * N + c];
+    const float* p = part + c;
+#pragma unroll 8
+    for (int i = w; i < groups; i += 32) v += p[(long long)i * 2 * N];
   }
   s[w][lane] = v;
   __syncthreads();
-  if (w == 0 && c < 2 * N) {
-    v = 0.f;
-    for (int i = 0; i < 8; ++i) v += s[i][lane];
-    if (c < N) {
-      if (dgamma) dgamma[c] = v;
+  // warp w adds up column w
+  v = warp_sum(s[lane][w]);
+  const int cw = blockIdx.x * 32 + w;
+  if (lane == 0 && cw < 2 * N) {
+    if (cw < N) {
+      if (dgamma) dgamma[cw] = v;
     } else if (dbeta)
-      dbeta[c - N] = v;
+      dbeta[cw - N] = v;
   }
 }
 
@@ -606,52 +607,32 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_wide_columns(NormBwdArgs a,
 constexpr int kMaxSms = 160;       // the workspace does not depend on the device
 constexpr int kMaxWideGroups = 64;
 
-// The shape of a team launch: threads of the block, blocks, cluster.
+// The shape of a team launch; teams_per_block 0: the block is the team.
 struct TeamShape {
-  int threads, blocks, cluster;
+  int threads, blocks;
 };
 
-// teams_per_block 0: the block is the team.  About `per_sm` threads an SM.
+// All blocks resident: `per_sm` threads an SM.  With column sums fewer blocks
+// where that leaves a team less than four rows: each block's sums are written
+// and read again (4096x128: 12.3 us by 256 blocks), and few rows go to one.
 TeamShape team_shape(long long rows, int N, int elems, int teams_per_block, int per_sm, int num_sms, bool sums) {
   TeamShape s;
-  if (teams_per_block) {
-    s.threads = kThreads;
-    s.blocks = (int)std::min<long long>((rows + teams_per_block - 1) / teams_per_block,
-                                        (long long)num_sms * (per_sm / kThreads));
-    s.cluster = 1;
-    return s;
-  }
-  s.threads = std::max(32, ((N + elems - 1) / elems + 31) / 32 * 32);
-  s.blocks = (int)std::min<long long>(rows, (long long)num_sms * std::max(1, per_sm / s.threads));
-  s.cluster = 1;
-  if (sums) {
-    // column sums meet in clusters of two (of eight, not all clusters were
-    // resident at once: 8192x4096 bf16 took 60 us, without sums 35); up to
-    // 16 rows one cluster takes them all and writes the results itself
-    s.cluster = kCluster;
-    s.blocks = rows <= 8 * kCluster ? kCluster : (s.blocks + kCluster - 1) / kCluster * kCluster;
-  }
+  s.threads = teams_per_block ? kThreads : std::max(32, ((N + elems - 1) / elems + 31) / 32 * 32);
+  const long long teams = sums ? (rows + 3) / 4 : rows;
+  const int per_block = std::max(1, teams_per_block);
+  s.blocks = (int)std::min<long long>((teams + per_block - 1) / per_block,
+                                      (long long)num_sms * std::max(1, per_sm / s.threads));
   return s;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), const TeamShape& s, size_t smem, cudaStream_t st, Args... args) {
+template <typename Args>
+cudaError_t launch_team(void (*kern)(Args), const TeamShape& s, size_t smem, cudaStream_t st, const Args& a) {
   if (smem > 40 * 1024) {  // beyond 48 KB with the static part
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(s.blocks);
-  cfg.blockDim = dim3(s.threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = s.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = s.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  kern<<<s.blocks, s.threads, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 bool aligned(const void* p, long long stride, int size, int bytes) {
@@ -664,7 +645,7 @@ cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
                                  false);
   using XRing = Ring<TX, VEC, K>;
   const size_t smem = XRing::kAsync ? (size_t)4 * XRing::kRow * s.threads : 0;
-  return launch_cluster(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT>, s, smem, st, a);
+  return launch_team(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT>, s, smem, st, a);
 }
 
 template <typename TX, typename TY, int VEC, int K, int TEAM>
@@ -701,7 +682,7 @@ cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t st) {
 }
 
 cudaError_t join_sums(const NormBwdArgs& a, int groups, cudaStream_t st) {
-  return launch_ex(norm_bwd_join, (2 * a.N + 31) / 32, kThreads, 0, st, true, (const float*)a.part, groups, a.N,
+  return launch_ex(norm_bwd_join, (2 * a.N + 31) / 32, kJoinThreads, 0, st, true, (const float*)a.part, groups, a.N,
                    a.dgamma, a.dbeta);
 }
 
@@ -713,10 +694,10 @@ cudaError_t bwd_launch(const NormBwdArgs& a, cudaStream_t st) {
   using XRing = Ring<TX, VEC, K>;
   using DRing = Ring<TD, VEC, K>;
   const size_t rings = (size_t)kStagesOf<TX, TD> * (XRing::kRow + DRing::kRow) * s.threads;
-  const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, sums ? 2 * a.N * sizeof(float) : 0);
-  cudaError_t e = launch_cluster(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT>, s, smem, st, a, s.cluster);
-  const int groups = s.blocks / s.cluster;
-  if (e == cudaSuccess && sums && groups > 1) e = join_sums(a, groups, st);
+  const size_t teams = TEAM && sums ? kThreads / (TEAM ? TEAM : 1) * 2 * a.N * sizeof(float) : 0;
+  const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, teams);
+  cudaError_t e = launch_team(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT>, s, smem, st, a);
+  if (e == cudaSuccess && sums && s.blocks > 1) e = join_sums(a, s.blocks, st);
   return e;
 }
 
@@ -769,16 +750,14 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Column sums of every group any launch for this shape makes: a block of
-// several teams is a group of its own, eight blocks of one team are one.
+// Column sums of every group that any launch for this shape makes: of the
+// blocks of team_shape with the fewest threads and the most SMs.
 size_t norm_bwd_workspace(long long rows, int N) {
   long long groups = kMaxWideGroups;
-  if (N <= 32 * kElems)
-    groups = std::min<long long>((rows + 7) / 8, (long long)kMaxSms * (kBwdPerSm / kThreads));
-  else if (N <= kMaxTeamWidth)
-    groups = (std::min<long long>(rows, (long long)kMaxSms * (kBwdPerSm / 32)) + kCluster - 1) / kCluster;
-  else
-    groups = std::min<long long>(kMaxWideGroups, (rows + 31) / 32);
+  if (N <= kMaxTeamWidth) {
+    const int threads = N <= 32 * kElems ? kThreads : std::max(32, (N + kElems - 1) / kElems);
+    groups = std::min<long long>((rows + 3) / 4, (long long)kMaxSms * (kBwdPerSm / threads));
+  }
   return (size_t)std::max<long long>(1, groups) * 2 * N * sizeof(float);
 }
 
