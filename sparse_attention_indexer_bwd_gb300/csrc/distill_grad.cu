@@ -38,10 +38,10 @@ template <int NT>
 constexpr int kRoom = kGroups * kUnroll * NT;  // vectors of a part that NT threads hold
 constexpr int kMaxWarps = 256 / 32;
 // Blocks of an SM: registers for four of 256 threads, of which three find
-// room for 64 KB, or eight of 128 with parts of at most 24 KB.
+// room for 64 KB, or eight of 128 with parts of at most 32 KB.
 template <int NT>
 constexpr int kBlocks = NT == 256 ? 4 : 8;
-constexpr int kSmallPart = 24 * 1024;
+constexpr int kSmallPart = 32 * 1024;
 
 // What the blocks of a cluster tell each other about a row: the part's
 // maximum and sum, and of the kept tokens in it the sums of w (x - m) / T and

@@ -27,7 +27,11 @@ namespace {
 constexpr int kThreads = 256;     // block of several teams, and of the kernels for wide rows
 constexpr int kMaxTeam = 512;     // threads of a block that is one team
 constexpr int kElems = 16;        // elements of a row a thread holds at most
-constexpr int kFwdPerSm = 768, kBwdPerSm = 512;  // threads of an SM: 80 and 128 registers each
+// Threads of an SM by the elements each holds (64 to 128 registers): rows of
+// up to 2048 elements take eight a thread, which leaves more warps.
+constexpr int kFewElems = 8;
+constexpr int fwd_per_sm(int elems) { return elems > kFewElems ? 768 : 1024; }
+constexpr int bwd_per_sm(int elems) { return elems > kFewElems ? 512 : 768; }
 // Rows of a team in flight or in work: four, or three where a row of 8192
 // elements of x and dy takes 64 KB (227 KB of shared memory a block).
 template <typename TX, typename TD>
@@ -233,7 +237,7 @@ __device__ __forceinline__ float over_n(float s, float n, float inv_n) {
 }
 
 template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT>
-__global__ void __launch_bounds__(MAXT, kFwdPerSm / MAXT) norm_fwd_team(NormFwdArgs a) {
+__global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K) / MAXT) norm_fwd_team(NormFwdArgs a) {
   constexpr int kStages = 4;
   extern __shared__ __align__(16) unsigned char smem[];  // the ring
   __shared__ __align__(16) float stage[64];
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(MAXT, kFwdPerSm / MAXT) norm_fwd_team(NormFwdA
 }
 
 template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
-__global__ void __launch_bounds__(MAXT, kBwdPerSm / MAXT) norm_bwd_team(NormBwdArgs a) {
+__global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_team(NormBwdArgs a) {
   constexpr int kStages = kStagesOf<TX, TD>;
   extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end the teams' column sums
   __shared__ __align__(16) float stage[128];
@@ -641,7 +645,7 @@ bool aligned(const void* p, long long stride, int size, int bytes) {
 
 template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT>
 cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
-  const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, kFwdPerSm, a.num_sms,
+  const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, fwd_per_sm(VEC * K), a.num_sms,
                                  false);
   using XRing = Ring<TX, VEC, K>;
   const size_t smem = XRing::kAsync ? (size_t)4 * XRing::kRow * s.threads : 0;
@@ -650,6 +654,7 @@ cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
 
 template <typename TX, typename TY, int VEC, int K, int TEAM>
 cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
+  if (!TEAM && a.N <= kThreads * kFewElems) return fwd_launch<TX, TY, VEC, kFewElems / VEC, 0, kThreads>(a, st);
   if (TEAM || a.N <= kThreads * kElems) return fwd_launch<TX, TY, VEC, K, TEAM, kThreads>(a, st);
   return fwd_launch<TX, TY, VEC, K, 0, kMaxTeam>(a, st);
 }
@@ -689,7 +694,7 @@ cudaError_t join_sums(const NormBwdArgs& a, int groups, cudaStream_t st) {
 template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
 cudaError_t bwd_launch(const NormBwdArgs& a, cudaStream_t st) {
   const bool sums = a.dgamma || a.dbeta;
-  const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, kBwdPerSm, a.num_sms,
+  const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, bwd_per_sm(VEC * K), a.num_sms,
                                  sums);
   using XRing = Ring<TX, VEC, K>;
   using DRing = Ring<TD, VEC, K>;
@@ -703,6 +708,7 @@ cudaError_t bwd_launch(const NormBwdArgs& a, cudaStream_t st) {
 
 template <typename TX, typename TD, int VEC, int K, int TEAM>
 cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
+  if (!TEAM && a.N <= kThreads * kFewElems) return bwd_launch<TX, TD, VEC, kFewElems / VEC, 0, kThreads>(a, st);
   if (TEAM || a.N <= kThreads * kElems) return bwd_launch<TX, TD, VEC, K, TEAM, kThreads>(a, st);
   return bwd_launch<TX, TD, VEC, K, 0, kMaxTeam>(a, st);
 }
@@ -750,13 +756,18 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Column sums of every group that any launch for this shape makes: of the
-// blocks of team_shape with the fewest threads and the most SMs.
+// Column sums of every group that any launch for this shape makes, on a
+// device of up to kMaxSms.
 size_t norm_bwd_workspace(long long rows, int N) {
   long long groups = kMaxWideGroups;
   if (N <= kMaxTeamWidth) {
-    const int threads = N <= 32 * kElems ? kThreads : std::max(32, (N + kElems - 1) / kElems);
-    groups = std::min<long long>((rows + 3) / 4, (long long)kMaxSms * (kBwdPerSm / threads));
+    int threads = kThreads, per_sm = bwd_per_sm(kFewElems);
+    if (N > 32 * kElems) {
+      const int elems = N <= kThreads * kFewElems ? kFewElems : kElems;
+      threads = (N + elems - 1) / elems;
+      per_sm = bwd_per_sm(elems);
+    }
+    groups = std::min<long long>((rows + 3) / 4, (long long)kMaxSms * std::max(1, per_sm / threads));
   }
   return (size_t)std::max<long long>(1, groups) * 2 * N * sizeof(float);
 }

@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
     own = part_stat<T, kEntropy, TOP>(part, segments, c);
     my_max = own.m;
   }
-  prefetch_part<T>(a, row, lo, hi, kAhead);
+  if (kStat) prefetch_part<T>(a, row, lo, hi, kAhead);
   // The student's logits of the teacher's slots; the first one of a thread is
   // used after the row's statistic and comes in meanwhile.
   float x_first = 0.f;

@@ -110,7 +110,7 @@ def _matrix_out(out, like, dtype, name):
     """An output with the shape of `like` and its row stride: given, or allocated with the strides of `like`."""
     if out is None:
         if like.is_contiguous():
-            out = torch.empty_like(like, dtype=dtype)
+            out = torch.empty_like(like) if dtype == like.dtype else torch.empty_like(like, dtype=dtype)
         else:
             rows, width, step = _rows(like, name)
             out = torch.empty(rows * step, dtype=dtype, device=like.device).as_strided(like.shape, like.stride())
@@ -162,7 +162,8 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, out_dtype=None, 
     rc = load().ibwd_layer_norm_fwd(x.data_ptr(), _CODE[x.dtype], xs, pg, pb, wt, y.data_ptr(),
                                     _CODE[dtype], xs if ys is None else ys, _p(mean), _p(rstd), rows, width, eps,
                                     _current_stream(x.device.index))
-    _check(rc, "ibwd_layer_norm_fwd")
+    if rc:
+        _check(rc, "ibwd_layer_norm_fwd")
     return y, mean, rstd
 
 
@@ -200,7 +201,8 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, weight_grads: bool =
                                  rows, width, _p(workspace),
                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
                                  _current_stream(x.device.index))
-    _check(rc, "ibwd_layer_norm_bwd")
+    if rc:
+        _check(rc, "ibwd_layer_norm_bwd")
     return dx, dgamma, dbeta
 
 
@@ -228,7 +230,8 @@ def token_logprobs_fwd(logits, tokens=None, top_n: int = 0, temperature: float =
     rc = load().ibwd_token_logprobs_fwd(logits.data_ptr(), _CODE[logits.dtype], step, pt, temperature,
                                         _p(logprob), entropy.data_ptr(), lse.data_ptr(), _p(top_ids),
                                         _p(top_logprobs), top_n, rows, vocab, _current_stream(logits.device.index))
-    _check(rc, "ibwd_token_logprobs_fwd")
+    if rc:
+        _check(rc, "ibwd_token_logprobs_fwd")
     return logprob, entropy, lse, top_ids, top_logprobs
 
 
@@ -252,7 +255,8 @@ def token_logprobs_bwd(logits, tokens, lse, entropy=None, dlogprob=None, dentrop
     rc = load().ibwd_token_logprobs_bwd(logits.data_ptr(), _CODE[logits.dtype], step, pt, temperature, pl, pe, pd,
                                         ph, dx.data_ptr(), step if dxs is None else dxs, rows, vocab,
                                         _current_stream(logits.device.index))
-    _check(rc, "ibwd_token_logprobs_bwd")
+    if rc:
+        _check(rc, "ibwd_token_logprobs_bwd")
     return dx
 
 
@@ -282,7 +286,8 @@ def distill_fwd(logits, ids, teacher, temperature: float = 1.0, stream=None):
     lse = torch.empty_like(loss)
     rc = load().ibwd_distill_fwd(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature,
                                  loss.data_ptr(), lse.data_ptr(), rows, vocab, _current_stream(logits.device.index))
-    _check(rc, "ibwd_distill_fwd")
+    if rc:
+        _check(rc, "ibwd_distill_fwd")
     return loss, lse
 
 
@@ -299,7 +304,8 @@ def distill_bwd(logits, ids, teacher, lse, dloss, temperature: float = 1.0, out=
     dx, dxs = _matrix_out(out, logits, logits.dtype, "out")
     rc = load().ibwd_distill_bwd(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature, pl, pd,
                                  dx.data_ptr(), step if dxs is None else dxs, rows, vocab, _current_stream(logits.device.index))
-    _check(rc, "ibwd_distill_bwd")
+    if rc:
+        _check(rc, "ibwd_distill_bwd")
     return dx
 
 
@@ -319,5 +325,6 @@ def distill_grad(logits, ids, teacher, row_weight=None, grad_scale: float = 1.0,
     rc = load().ibwd_distill_grad(logits.data_ptr(), _CODE[logits.dtype], step, pi, pt, k, temperature, pw,
                                   grad_scale, loss.data_ptr(), dx.data_ptr(), step if dxs is None else dxs, rows,
                                   vocab, _current_stream(logits.device.index))
-    _check(rc, "ibwd_distill_grad")
+    if rc:
+        _check(rc, "ibwd_distill_grad")
     return loss, dx
