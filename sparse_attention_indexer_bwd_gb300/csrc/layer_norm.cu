@@ -1,796 +1,30 @@
-// Layer norm over the rows of a matrix, forward and backward, on sm_103a:
-//   y = (x - mean) rstd gamma + beta,
-//   dx = rstd (d - sum(d)/N - xh sum(d xh)/N),  xh = (x - mean) rstd, d = dy gamma,
-//   dgamma = sum_rows dy xh,  dbeta = sum_rows dy.
-// About ten operations an element beside four to twelve bytes: bound by HBM,
-// or by the launch where rows are few.
-//
-// A team of threads holds a row in registers (16 elements a thread at most),
-// so every element is read once: 8 to 32 lanes of a warp for short rows, a
-// thread block for longer ones.  Teams stay resident and walk the rows; each
-// thread copies its own elements of the next rows into its own slots of a
-// shared-memory ring (cp.async), so several rows are in flight without
-// registers or barriers.  gamma and beta stay in registers, and so do the
-// backward pass's column sums of the team's rows.  Those meet in a fixed
-// order: a block's teams in shared memory, the blocks in a second small
-// kernel.  Rows too wide for a block take several passes.
-#include <algorithm>
-
-#include "elem.cuh"
-#include "kcommon.cuh"
-#include "packed.cuh"
-#include "train.h"
+// Layer norm: the workspace, and the choice of the type's kernels (each type of
+// x is a translation unit of its own, layer_norm_*.cu).
+#include "layer_norm.cuh"
 
 namespace ibwd {
-namespace {
-
-constexpr int kThreads = 256;     // block of several teams, and of the kernels for wide rows
-constexpr int kMaxTeam = 512;     // threads of a block that is one team
-constexpr int kElems = 16;        // elements of a row a thread holds at most
-// Threads of an SM by the elements each holds (64 to 128 registers): rows of
-// up to 2048 elements take eight a thread, which leaves more warps.
-constexpr int kFewElems = 8;
-constexpr int fwd_per_sm(int elems) { return elems > kFewElems ? 768 : 1024; }
-constexpr int bwd_per_sm(int elems) { return elems > kFewElems ? 512 : 768; }
-// Rows of a team in flight or in work: four, or three where a row of 8192
-// elements of x and dy takes 64 KB (227 KB of shared memory a block).
-template <typename TX, typename TD>
-constexpr int kStagesOf = sizeof(TX) + sizeof(TD) > 6 ? 3 : 4;
-constexpr int kMaxTeamWidth = kMaxTeam * kElems;
-
-// VEC consecutive elements as they lie in memory.
-template <typename T, int VEC>
-struct Chunk {
-  static constexpr int kBytes = VEC * (int)sizeof(T);
-  alignas(kBytes < 16 ? kBytes : 16) T e[VEC];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i)
-        reinterpret_cast<uint4*>(e)[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
-    } else if constexpr (kBytes == 8) {
-      *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
-    } else if constexpr (kBytes == 4) {
-      *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = p[i];
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i)
-        st_stream(reinterpret_cast<uint4*>(p) + i, reinterpret_cast<const uint4*>(e)[i]);
-    } else if constexpr (kBytes == 8) {
-      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
-    } else if constexpr (kBytes == 4) {
-      *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(e);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) p[i] = e[i];
-    }
-  }
-};
-
-// A thread's slots in a ring of rows in shared memory: K chunks a row, each in
-// pieces of at most 16 bytes that lie side by side for neighbouring threads.
-// The thread that copies a chunk is the only one that reads it.  A copy takes
-// 4, 8 or 16 bytes; single 16-bit elements have none.
-template <typename T, int VEC, int K>
-struct Ring {
-  static constexpr int kBytes = VEC * (int)sizeof(T);
-  static constexpr bool kAsync = kBytes >= 4;
-  static constexpr int kPiece = kBytes < 16 ? kBytes : 16;
-  static constexpr int kRow = K * kBytes;  // bytes of a thread and row
-  uint32_t base;                           // of this thread
-  uint32_t pitch;                          // bytes between the pieces of a thread
-  __device__ Ring(unsigned char* smem, int t, int threads)
-      : base(smem_u32(smem) + t * kPiece), pitch(threads * kPiece) {}
-  __device__ __forceinline__ void copy(int stage, int k, const T* src) const {
-#pragma unroll
-    for (int i = 0; i < kBytes / kPiece; ++i) {
-      const uint32_t dst = base + ((stage * K + k) * (kBytes / kPiece) + i) * pitch;
-      const char* from = reinterpret_cast<const char*>(src) + i * kPiece;
-      if constexpr (kPiece == 16)
-        cp_async16(dst, from, 16);
-      else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(kPiece) : "memory");
-    }
-  }
-  __device__ __forceinline__ void read(int stage, int k, Chunk<T, VEC>& c) const {
-#pragma unroll
-    for (int i = 0; i < kBytes / kPiece; ++i) {
-      const uint32_t src = base + ((stage * K + k) * (kBytes / kPiece) + i) * pitch;
-      if constexpr (kPiece == 16) {
-        reinterpret_cast<uint4*>(c.e)[i] = ld_shared_v4(src);
-      } else if constexpr (kPiece == 8) {
-        uint2 v;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(src));
-        *reinterpret_cast<uint2*>(c.e) = v;
-      } else {
-        uint32_t v;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(src));
-        *reinterpret_cast<uint32_t*>(c.e) = v;
-      }
-    }
-  }
-};
-
-// gamma / beta element n as fp32: fp32 or the type of x.
-template <typename T>
-__device__ __forceinline__ float weight(const void* w, int n, bool f32, float none) {
-  if (w == nullptr) return none;
-  return f32 ? static_cast<const float*>(w)[n] : to_f32(static_cast<const T*>(w)[n]);
-}
-
-// gamma / beta of this thread's elements as pairs: K chunks of VEC, T chunks
-// apart, `none` without a vector and 0 beyond the row.
-template <typename TX, int VEC, int K>
-__device__ __forceinline__ void weights(float2 (&out)[K * VEC / 2], const void* w, bool f32, float none, int t, int T,
-                                        int nvec) {
-  const bool wide = VEC >= 4 && f32 && w != nullptr && (reinterpret_cast<uintptr_t>(w) & 15) == 0;
-  if (wide) {
-#pragma unroll
-    for (int i = 0; i < K * VEC / 4; ++i) {
-      const int j = t + 4 * i / VEC * T;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j < nvec) v = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + j * VEC + 4 * i % VEC);
-      out[2 * i] = make_float2(v.x, v.y);
-      out[2 * i + 1] = make_float2(v.z, v.w);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < K * VEC / 2; ++i) {
-    float v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int e = 2 * i + h, j = t + e / VEC * T;
-      v[h] = j < nvec ? weight<TX>(w, j * VEC + e % VEC, f32, none) : 0.f;
-    }
-    out[i] = make_float2(v[0], v[1]);
-  }
-}
-
-// Elements 2i and 2i + 1 of a chunk list as fp32, and back.
-template <typename T, int VEC, int K>
-__device__ __forceinline__ float2 pair_of(const Chunk<T, VEC> (&c)[K], int i) {
-  if constexpr (VEC == 1) {
-    return make_float2(to_f32(c[2 * i].e[0]), to_f32(c[2 * i + 1].e[0]));
-  } else {
-    const T* e = &c[2 * i / VEC].e[2 * i % VEC];
-    if constexpr (sizeof(T) == 4) {
-      return make_float2(to_f32(e[0]), to_f32(e[1]));
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(e);
-      return unpack2(w, T{});
-    }
-  }
-}
-template <typename T, int VEC, int K>
-__device__ __forceinline__ void set_pair(Chunk<T, VEC> (&c)[K], int i, float2 v) {
-  if constexpr (VEC == 1) {
-    c[2 * i].e[0] = from_f32<T>(v.x);
-    c[2 * i + 1].e[0] = from_f32<T>(v.y);
-  } else {
-    T* e = &c[2 * i / VEC].e[2 * i % VEC];
-    if constexpr (sizeof(T) == 4) {
-      e[0] = v.x;
-      e[1] = v.y;
-    } else {
-      *reinterpret_cast<uint32_t*>(e) = pack2_of(v, T{});
-    }
-  }
-}
-
-// Two consecutive column sums at an even column: 8 bytes where the row of
-// sums begins on an even one, too.
-__device__ __forceinline__ void put_pair(float* p, float2 v) {
-  if ((reinterpret_cast<uintptr_t>(p) & 7) == 0) {
-    *reinterpret_cast<float2*>(p) = v;
-  } else {
-    p[0] = v.x;
-    p[1] = v.y;
-  }
-}
-
-// Sums of K values over a team, the same bits in each of its threads.  TEAM
-// lanes of a warp, or 0 for the block: then `stage` holds 2 * K * 32 floats,
-// zero beyond the block's warps and used in turn (`turn` flips), so one
-// barrier a call is enough.
-template <int TEAM, int K>
-__device__ __forceinline__ void team_sums(float (&v)[K], float* stage, int& turn) {
-#pragma unroll
-  for (int o = (TEAM ? TEAM : 32) / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if constexpr (TEAM == 0) {
-    float* s = stage + turn * 32 * K;
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-      for (int k = 0; k < K; ++k) s[k * 32 + (threadIdx.x >> 5)] = v[k];
-    __syncthreads();
-    float4 f[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) f[k] = *reinterpret_cast<const float4*>(s + k * 32);
-    for (int w = 4; w < (int)(blockDim.x >> 5); w += 4)
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float4 o = *reinterpret_cast<const float4*>(s + k * 32 + w);
-        f[k].x += o.x;
-        f[k].y += o.y;
-        f[k].z += o.z;
-        f[k].w += o.w;
-      }
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = (f[k].x + f[k].y) + (f[k].z + f[k].w);
-  }
-}
-
-// s / n given 1 / n, to the last bit but one (a constant row gets its value):
-// the remainder of the product is added back.
-__device__ __forceinline__ float over_n(float s, float n, float inv_n) {
-  const float q = s * inv_n;
-  return fmaf(fmaf(-q, n, s), inv_n, q);
-}
-
-template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT>
-__global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K) / MAXT) norm_fwd_team(NormFwdArgs a) {
-  constexpr int kStages = 4;
-  extern __shared__ __align__(16) unsigned char smem[];  // the ring
-  __shared__ __align__(16) float stage[64];
-  constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
-  constexpr int P = K * VEC / 2;  // pairs a thread
-  const int team = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0;
-  const int t = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x, T = TEAM ? TEAM : blockDim.x;
-  const int nvec = a.N / VEC;
-  const float inv_n = 1.f / a.N;
-  if (TEAM == 0 && threadIdx.x < 64) stage[threadIdx.x] = 0.f;
-  if (TEAM == 0) __syncthreads();
-  float2 g[P], b[P];
-  weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec);
-  weights<TX, VEC, K>(b, a.beta, a.w_type == 0, 0.f, t, T, nvec);
-  using XRing = Ring<TX, VEC, K>;
-  const XRing ring(smem, threadIdx.x, blockDim.x);
-  Chunk<TX, VEC> cur[K] = {};  // (zero where a thread has no element)
-  const long long step = (long long)gridDim.x * TPB;
-  const long long first = (long long)blockIdx.x * TPB + team;
-  const TX* xr = static_cast<const TX*>(a.x) + first * a.x_stride + t * VEC;  // of the row to fetch
-  const long long x_step = step * a.x_stride, y_step = step * a.y_stride;
-  TY* yr = static_cast<TY*>(a.y) + first * a.y_stride + t * VEC;
-  auto fetch = [&](int slot, bool on) {
-    if (XRing::kAsync && on)
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec) ring.copy(slot, k, xr + k * T * VEC);
-    xr += x_step;
-    cp_async_commit();
-  };
-  int turn = 0, slot = 0;
-  if (XRing::kAsync)
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * step < a.rows);
-  // (a block's teams leave together: their rows differ by less than a step)
-  for (long long r = first; r - team < a.rows; r += step) {
-    const bool on = r < a.rows;
-    if (XRing::kAsync) {
-      fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
-      cp_async_wait<kStages - 1>();
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (on && t + k * T < nvec) {
-        if constexpr (XRing::kAsync)
-          ring.read(slot, k, cur[k]);
-        else
-          cur[k].load(xr + k * T * VEC);
-      }
-    if (!XRing::kAsync) xr += x_step;
-    slot = slot == kStages - 1 ? 0 : slot + 1;
-    float2 v[P], sum = both(0.f);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      v[i] = pair_of(cur, i);
-      sum = add2(sum, v[i]);
-    }
-    float s[1] = {sum.x + sum.y};
-    team_sums<TEAM>(s, stage, turn);
-    const float mean = over_n(s[0], (float)a.N, inv_n);
-    sum = both(0.f);
-    // elements the thread does not have are left out of the squares
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      v[i] = add2(v[i], both(-mean));
-      if constexpr (VEC > 1) {
-        if (t + 2 * i / VEC * T < nvec) sum = fma2(v[i], v[i], sum);
-      } else {
-        if (t + 2 * i * T < nvec) sum.x = fmaf(v[i].x, v[i].x, sum.x);
-        if (t + (2 * i + 1) * T < nvec) sum.y = fmaf(v[i].y, v[i].y, sum.y);
-      }
-    }
-    float q[1] = {sum.x + sum.y};
-    team_sums<TEAM>(q, stage, turn);
-    const float rstd = rsqrtf(fmaf(q[0], inv_n, a.eps));
-    if (on) {
-      Chunk<TY, VEC> o[K];
-#pragma unroll
-      for (int i = 0; i < P; ++i) set_pair(o, i, fma2(mul2(v[i], both(rstd)), g[i], b[i]));
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec) o[k].store(yr + k * T * VEC);
-      if (t == 0) {
-        if (a.mean) a.mean[r] = mean;
-        if (a.rstd) a.rstd[r] = rstd;
-      }
-    }
-    yr += y_step;
-  }
-  cp_async_wait_all();
-}
-
-template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
-__global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_team(NormBwdArgs a) {
-  constexpr int kStages = kStagesOf<TX, TD>;
-  extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end the teams' column sums
-  __shared__ __align__(16) float stage[128];
-  constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
-  constexpr int P = K * VEC / 2;  // pairs a thread
-  const int team = TEAM ? threadIdx.x / (TEAM ? TEAM : 1) : 0;
-  const int t = TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x, T = TEAM ? TEAM : blockDim.x;
-  const int nvec = a.N / VEC;
-  const float inv_n = 1.f / a.N;
-  if (TEAM == 0)
-    for (int i = threadIdx.x; i < 128; i += blockDim.x) stage[i] = 0.f;
-  if (TEAM == 0) __syncthreads();
-  float2 g[P], dg[P], db[P];
-  weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec);
-#pragma unroll
-  for (int i = 0; i < P; ++i) dg[i] = db[i] = both(0.f);
-  using XRing = Ring<TX, VEC, K>;
-  using DRing = Ring<TD, VEC, K>;
-  constexpr bool kAsync = XRing::kAsync && DRing::kAsync;
-  const XRing xring(smem, threadIdx.x, blockDim.x);
-  const DRing dring(smem + kStages * XRing::kRow * blockDim.x, threadIdx.x, blockDim.x);
-  // zero where a thread has no element: dy = 0 adds nothing to any sum
-  Chunk<TX, VEC> cx[K] = {};
-  Chunk<TD, VEC> cd[K] = {};
-  const long long step = (long long)gridDim.x * TPB;
-  const long long first = (long long)blockIdx.x * TPB + team;
-  const TX* xr = static_cast<const TX*>(a.x) + first * a.x_stride + t * VEC;  // of the row to fetch
-  const TD* dr = static_cast<const TD*>(a.dy) + first * a.dy_stride + t * VEC;
-  TX* or_ = static_cast<TX*>(a.dx) + first * a.dx_stride + t * VEC;
-  const long long x_step = step * a.x_stride, d_step = step * a.dy_stride, o_step = step * a.dx_stride;
-  auto fetch = [&](int slot, bool on) {
-    if (kAsync && on)
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec) {
-          xring.copy(slot, k, xr + k * T * VEC);
-          dring.copy(slot, k, dr + k * T * VEC);
-        }
-    xr += x_step;
-    dr += d_step;
-    cp_async_commit();
-  };
-  int turn = 0, slot = 0;
-  if (kAsync)
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * step < a.rows);
-  float nm = 0.f, nr = 0.f;  // the next row's statistics
-  if (first < a.rows) {
-    nm = a.mean[first];
-    nr = a.rstd[first];
-  }
-  for (long long r = first; r - team < a.rows; r += step) {
-    const bool on = r < a.rows;
-    const float cm = nm, cr = nr;
-    if (r + step < a.rows) {
-      nm = a.mean[r + step];
-      nr = a.rstd[r + step];
-    }
-    if (kAsync) {
-      fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
-      cp_async_wait<kStages - 1>();
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (on && t + k * T < nvec) {
-        if constexpr (kAsync) {
-          xring.read(slot, k, cx[k]);
-          dring.read(slot, k, cd[k]);
-        } else {
-          cx[k].load(xr + k * T * VEC);
-          cd[k].load(dr + k * T * VEC);
-        }
-      }
-    if (!kAsync) {
-      xr += x_step;
-      dr += d_step;
-    }
-    slot = slot == kStages - 1 ? 0 : slot + 1;
-    float s[2] = {0.f, 0.f};
-    if (on) {
-      float2 s0 = both(0.f), s1 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float2 xh = mul2(add2(pair_of(cx, i), both(-cm)), both(cr)), dy = pair_of(cd, i);
-        const float2 d = mul2(dy, g[i]);
-        dg[i] = fma2(dy, xh, dg[i]);
-        db[i] = add2(db[i], dy);
-        s0 = add2(s0, d);
-        s1 = fma2(d, xh, s1);
-      }
-      s[0] = s0.x + s0.y;
-      s[1] = s1.x + s1.y;
-    }
-    team_sums<TEAM>(s, stage, turn);
-    if (on) {
-      const float ma = s[0] * inv_n, mb = s[1] * inv_n;
-      Chunk<TX, VEC> o[K];
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float2 xh = mul2(add2(pair_of(cx, i), both(-cm)), both(cr));
-        const float2 d = fma2(pair_of(cd, i), g[i], both(-ma));
-        set_pair(o, i, mul2(fma2(xh, both(-mb), d), both(cr)));
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec) o[k].store(or_ + k * T * VEC);
-    }
-    or_ += o_step;
-  }
-  cp_async_wait_all();
-  if (!a.dgamma && !a.dbeta) return;
-  griddep_launch_dependents();  // the join's blocks come as these leave
-  // The block's column sums: a group of part[groups][2][N] -- or, where it is
-  // the only block, dgamma and dbeta.
-  float* const out_g = gridDim.x > 1 ? a.part + (long long)blockIdx.x * 2 * a.N : a.dgamma;
-  float* const out_b = gridDim.x > 1 ? out_g + a.N : a.dbeta;
-  if constexpr (TEAM == 0) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int j = t + 2 * i / VEC * T, c = j * VEC + 2 * i % VEC;
-      if constexpr (VEC == 1) {
-        if (j < nvec && out_g) out_g[c] = dg[i].x;
-        if (j < nvec && out_b) out_b[c] = db[i].x;
-        if (j + T < nvec && out_g) out_g[c + T] = dg[i].y;
-        if (j + T < nvec && out_b) out_b[c + T] = db[i].y;
-      } else {
-        if (j < nvec && out_g) put_pair(out_g + c, dg[i]);
-        if (j < nvec && out_b) put_pair(out_b + c, db[i]);
-      }
-    }
-  } else {
-    // the teams' sums side by side in shared memory, added in the teams' order
-    float* const sums = reinterpret_cast<float*>(smem) + team * 2 * a.N;
-    __syncthreads();  // the rings are done with
-#pragma unroll
-    for (int e = 0; e < 2 * P; ++e) {
-      const int j = t + e / VEC * T, c = j * VEC + e % VEC;
-      if (j < nvec) {
-        sums[c] = e & 1 ? dg[e / 2].y : dg[e / 2].x;
-        sums[a.N + c] = e & 1 ? db[e / 2].y : db[e / 2].x;
-      }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.N; c += kThreads) {
-      float v = 0.f;
-      for (int w = 0; w < TPB; ++w) v += reinterpret_cast<const float*>(smem)[w * 2 * a.N + c];
-      if (c < a.N) {
-        if (out_g) out_g[c] = v;
-      } else if (out_b) {
-        out_b[c - a.N] = v;
-      }
-    }
-  }
-}
-
-// dgamma and dbeta from the groups' column sums [groups][2][N]: 32 columns a
-// block, 32 interleaved sums of groups each, joined in order.
-constexpr int kJoinThreads = 1024;
-__global__ void __launch_bounds__(kJoinThreads) norm_bwd_join(const float* part, int groups, int N, float* dgamma,
-                                                              float* dbeta) {
-  __shared__ float s[32][33];
-  griddep_wait();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < 2 * N) {
-    const float* p = part + c;
-#pragma unroll 8
-    for (int i = w; i < groups; i += 32) v += p[(long long)i * 2 * N];
-  }
-  s[w][lane] = v;
-  __syncthreads();
-  // warp w adds up column w
-  v = warp_sum(s[lane][w]);
-  const int cw = blockIdx.x * 32 + w;
-  if (lane == 0 && cw < 2 * N) {
-    if (cw < N) {
-      if (dgamma) dgamma[cw] = v;
-    } else if (dbeta)
-      dbeta[cw - N] = v;
-  }
-}
-
-// ------------------------------------------------------------- wide rows ---
-// Any width and alignment: a block takes a row in three passes (two backward).
-
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(kThreads) norm_fwd_wide(NormFwdArgs a) {
-  __shared__ __align__(16) float stage[64];
-  if (threadIdx.x < 64) stage[threadIdx.x] = 0.f;
-  __syncthreads();
-  int turn = 0;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
-    TY* y = static_cast<TY*>(a.y) + r * a.y_stride;
-    float s[1] = {0.f};
-    for (int n = threadIdx.x; n < a.N; n += kThreads) s[0] += to_f32(x[n]);
-    team_sums<0>(s, stage, turn);
-    const float mean = s[0] / a.N;
-    float q[1] = {0.f};
-    for (int n = threadIdx.x; n < a.N; n += kThreads) {
-      const float d = to_f32(x[n]) - mean;
-      q[0] += d * d;
-    }
-    team_sums<0>(q, stage, turn);
-    const float rstd = 1.f / sqrtf(q[0] / a.N + a.eps);
-    for (int n = threadIdx.x; n < a.N; n += kThreads)
-      y[n] = from_f32<TY>((to_f32(x[n]) - mean) * rstd * weight<TX>(a.gamma, n, a.w_type == 0, 1.f) +
-                          weight<TX>(a.beta, n, a.w_type == 0, 0.f));
-    if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
-    }
-  }
-}
-
-template <typename TX, typename TD>
-__global__ void __launch_bounds__(kThreads) norm_bwd_wide(NormBwdArgs a) {
-  __shared__ __align__(16) float stage[128];
-  if (threadIdx.x < 128) stage[threadIdx.x] = 0.f;
-  __syncthreads();
-  int turn = 0;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
-    const TD* dy = static_cast<const TD*>(a.dy) + r * a.dy_stride;
-    TX* dx = static_cast<TX*>(a.dx) + r * a.dx_stride;
-    const float mean = a.mean[r], rstd = a.rstd[r];
-    float s[2] = {0.f, 0.f};
-    for (int n = threadIdx.x; n < a.N; n += kThreads) {
-      const float d = to_f32(dy[n]) * weight<TX>(a.gamma, n, a.w_type == 0, 1.f);
-      s[0] += d;
-      s[1] += d * ((to_f32(x[n]) - mean) * rstd);
-    }
-    team_sums<0>(s, stage, turn);
-    const float ma = s[0] / a.N, mb = s[1] / a.N;
-    for (int n = threadIdx.x; n < a.N; n += kThreads) {
-      const float xh = (to_f32(x[n]) - mean) * rstd;
-      const float d = to_f32(dy[n]) * weight<TX>(a.gamma, n, a.w_type == 0, 1.f);
-      dx[n] = from_f32<TX>(rstd * (d - ma - xh * mb));
-    }
-  }
-}
-
-// Column sums of row group blockIdx.y for the columns of blockIdx.x: 32
-// columns by 8 interleaved rows a block, the eight joined in order.
-template <typename TX, typename TD>
-__global__ void __launch_bounds__(kThreads) norm_bwd_wide_columns(NormBwdArgs a, int group_rows) {
-  __shared__ float sg[8][33], sb[8][33];
-  const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = blockIdx.x * 32 + c;
-  const long long r0 = (long long)blockIdx.y * group_rows;
-  const long long r1 = min(a.rows, r0 + group_rows);
-  float g = 0.f, b = 0.f;
-  if (n < a.N)
-    for (long long r = r0 + w; r < r1; r += 8) {
-      const float d = to_f32(static_cast<const TD*>(a.dy)[r * a.dy_stride + n]);
-      const float xh = (to_f32(static_cast<const TX*>(a.x)[r * a.x_stride + n]) - a.mean[r]) * a.rstd[r];
-      g += d * xh;
-      b += d;
-    }
-  sg[w][c] = g;
-  sb[w][c] = b;
-  __syncthreads();
-  if (w == 0 && n < a.N) {
-    g = b = 0.f;
-    for (int i = 0; i < 8; ++i) {
-      g += sg[i][c];
-      b += sb[i][c];
-    }
-    a.part[((long long)blockIdx.y * 2) * a.N + n] = g;
-    a.part[((long long)blockIdx.y * 2 + 1) * a.N + n] = b;
-  }
-}
-
-// -------------------------------------------------------------- launches ---
-
-constexpr int kMaxSms = 160;       // the workspace does not depend on the device
-constexpr int kMaxWideGroups = 64;
-
-// The shape of a team launch; teams_per_block 0: the block is the team.
-struct TeamShape {
-  int threads, blocks;
-};
-
-// All blocks resident: `per_sm` threads an SM.  With column sums fewer blocks
-// where that leaves a team less than four rows: each block's sums are written
-// and read again (4096x128: 12.3 us by 256 blocks), and few rows go to one.
-TeamShape team_shape(long long rows, int N, int elems, int teams_per_block, int per_sm, int num_sms, bool sums) {
-  TeamShape s;
-  s.threads = teams_per_block ? kThreads : std::max(32, ((N + elems - 1) / elems + 31) / 32 * 32);
-  const long long teams = sums ? (rows + 3) / 4 : rows;
-  const int per_block = std::max(1, teams_per_block);
-  s.blocks = (int)std::min<long long>((teams + per_block - 1) / per_block,
-                                      (long long)num_sms * std::max(1, per_sm / s.threads));
-  return s;
-}
-
-template <typename Args>
-cudaError_t launch_team(void (*kern)(Args), const TeamShape& s, size_t smem, cudaStream_t st, const Args& a) {
-  if (smem > 40 * 1024) {  // beyond 48 KB with the static part
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<s.blocks, s.threads, smem, st>>>(a);
-  return cudaGetLastError();
-}
-
-bool aligned(const void* p, long long stride, int size, int bytes) {
-  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0;
-}
-
-template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT>
-cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
-  const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, fwd_per_sm(VEC * K), a.num_sms,
-                                 false);
-  using XRing = Ring<TX, VEC, K>;
-  const size_t smem = XRing::kAsync ? (size_t)4 * XRing::kRow * s.threads : 0;
-  return launch_team(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT>, s, smem, st, a);
-}
-
-template <typename TX, typename TY, int VEC, int K, int TEAM>
-cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
-  if (!TEAM && a.N <= kThreads * kFewElems) return fwd_launch<TX, TY, VEC, kFewElems / VEC, 0, kThreads>(a, st);
-  if (TEAM || a.N <= kThreads * kElems) return fwd_launch<TX, TY, VEC, K, TEAM, kThreads>(a, st);
-  return fwd_launch<TX, TY, VEC, K, 0, kMaxTeam>(a, st);
-}
-
-template <typename TX, typename TY>
-cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t st) {
-  constexpr int V = kVec<TX>;
-  const int ysize = (int)sizeof(TY);
-  if (a.N > kMaxTeamWidth) {
-    norm_fwd_wide<TX, TY><<<(int)std::min<long long>(a.rows, 8LL * a.num_sms), kThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  // whole 16-byte vectors of x where every row allows it, else elements
-  if (a.N % V == 0 && aligned(a.x, a.x_stride, sizeof(TX), 16) && aligned(a.y, a.y_stride, ysize, V * ysize)) {
-    if (a.N <= 8 * V) return fwd_team<TX, TY, V, 1, 8>(a, st);
-    if (a.N <= 16 * V) return fwd_team<TX, TY, V, 1, 16>(a, st);
-    if (a.N <= 32 * V) return fwd_team<TX, TY, V, 1, 32>(a, st);
-    if (a.N <= 32 * kElems) return fwd_team<TX, TY, V, kElems / V, 32>(a, st);
-    return fwd_team<TX, TY, V, kElems / V, 0>(a, st);
-  }
-  // else 4 bytes of x
-  constexpr int W = V / 4;
-  if (W > 1 && a.N % W == 0 && aligned(a.x, a.x_stride, sizeof(TX), 4) && aligned(a.y, a.y_stride, ysize, W * ysize)) {
-    if (a.N <= 32 * kElems) return fwd_team<TX, TY, W, kElems / W, 32>(a, st);
-    return fwd_team<TX, TY, W, kElems / W, 0>(a, st);
-  }
-  if (a.N <= 128) return fwd_team<TX, TY, 1, 4, 32>(a, st);
-  if (a.N <= 32 * kElems) return fwd_team<TX, TY, 1, kElems, 32>(a, st);
-  return fwd_team<TX, TY, 1, kElems, 0>(a, st);
-}
-
-cudaError_t join_sums(const NormBwdArgs& a, int groups, cudaStream_t st) {
-  return launch_ex(norm_bwd_join, (2 * a.N + 31) / 32, kJoinThreads, 0, st, true, (const float*)a.part, groups, a.N,
-                   a.dgamma, a.dbeta);
-}
-
-template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT>
-cudaError_t bwd_launch(const NormBwdArgs& a, cudaStream_t st) {
-  const bool sums = a.dgamma || a.dbeta;
-  const TeamShape s = team_shape(a.rows, a.N, VEC * K, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, bwd_per_sm(VEC * K), a.num_sms,
-                                 sums);
-  using XRing = Ring<TX, VEC, K>;
-  using DRing = Ring<TD, VEC, K>;
-  const size_t rings = (size_t)kStagesOf<TX, TD> * (XRing::kRow + DRing::kRow) * s.threads;
-  const size_t teams = TEAM && sums ? kThreads / (TEAM ? TEAM : 1) * 2 * a.N * sizeof(float) : 0;
-  const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, teams);
-  cudaError_t e = launch_team(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT>, s, smem, st, a);
-  if (e == cudaSuccess && sums && s.blocks > 1) e = join_sums(a, s.blocks, st);
-  return e;
-}
-
-template <typename TX, typename TD, int VEC, int K, int TEAM>
-cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
-  if (!TEAM && a.N <= kThreads * kFewElems) return bwd_launch<TX, TD, VEC, kFewElems / VEC, 0, kThreads>(a, st);
-  if (TEAM || a.N <= kThreads * kElems) return bwd_launch<TX, TD, VEC, K, TEAM, kThreads>(a, st);
-  return bwd_launch<TX, TD, VEC, K, 0, kMaxTeam>(a, st);
-}
-
-template <typename TX, typename TD>
-cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
-  constexpr int V = kVec<TX>;
-  const int dsize = (int)sizeof(TD);
-  const bool sums = a.dgamma || a.dbeta;
-  if (!a.rows) {
-    if (a.dgamma) cudaMemsetAsync(a.dgamma, 0, a.N * sizeof(float), st);
-    if (a.dbeta) cudaMemsetAsync(a.dbeta, 0, a.N * sizeof(float), st);
-    return cudaGetLastError();
-  }
-  if (a.N > kMaxTeamWidth) {
-    if (sums) {  // before the rows: dx may be x or dy
-      const int groups = (int)std::min<long long>(kMaxWideGroups, (a.rows + 31) / 32);
-      const int group_rows = (int)((a.rows + groups - 1) / groups);
-      norm_bwd_wide_columns<TX, TD><<<dim3((a.N + 31) / 32, groups), kThreads, 0, st>>>(a, group_rows);
-      cudaError_t e = cudaGetLastError();
-      if (e == cudaSuccess) e = join_sums(a, groups, st);
-      if (e != cudaSuccess) return e;
-    }
-    norm_bwd_wide<TX, TD><<<(int)std::min<long long>(a.rows, 8LL * a.num_sms), kThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  if (a.N % V == 0 && aligned(a.x, a.x_stride, sizeof(TX), 16) && aligned(a.dx, a.dx_stride, sizeof(TX), 16) &&
-      aligned(a.dy, a.dy_stride, dsize, std::min(16, V * dsize))) {
-    if (a.N <= 8 * V) return bwd_team<TX, TD, V, 1, 8>(a, st);
-    if (a.N <= 16 * V) return bwd_team<TX, TD, V, 1, 16>(a, st);
-    if (a.N <= 32 * V) return bwd_team<TX, TD, V, 1, 32>(a, st);
-    if (a.N <= 32 * kElems) return bwd_team<TX, TD, V, kElems / V, 32>(a, st);
-    return bwd_team<TX, TD, V, kElems / V, 0>(a, st);
-  }
-  constexpr int W = V / 4;
-  if (W > 1 && a.N % W == 0 && aligned(a.x, a.x_stride, sizeof(TX), 4) && aligned(a.dx, a.dx_stride, sizeof(TX), 4) &&
-      aligned(a.dy, a.dy_stride, dsize, W * dsize)) {
-    if (a.N <= 32 * kElems) return bwd_team<TX, TD, W, kElems / W, 32>(a, st);
-    return bwd_team<TX, TD, W, kElems / W, 0>(a, st);
-  }
-  if (a.N <= 128) return bwd_team<TX, TD, 1, 4, 32>(a, st);
-  if (a.N <= 32 * kElems) return bwd_team<TX, TD, 1, kElems, 32>(a, st);
-  return bwd_team<TX, TD, 1, kElems, 0>(a, st);
-}
-
-}  // namespace
 
 // Column sums of every group that any launch for this shape makes, on a
 // device of up to kMaxSms.
 size_t norm_bwd_workspace(long long rows, int N) {
   long long groups = kMaxWideGroups;
-  if (N <= kMaxTeamWidth) {
-    int threads = kThreads, per_sm = bwd_per_sm(kFewElems);
-    if (N > 32 * kElems) {
-      const int elems = N <= kThreads * kFewElems ? kFewElems : kElems;
-      threads = (N + elems - 1) / elems;
-      per_sm = bwd_per_sm(elems);
-    }
-    groups = std::min<long long>((rows + 3) / 4, (long long)kMaxSms * std::max(1, per_sm / threads));
+  if (N <= kMaxLateWidth) {
+    // blocks of several teams, or of a team of at least N / 16 threads (with 8
+    // elements each a block has more threads by more than an SM has)
+    const int per_sm = N <= 32 * kElems ? bwd_per_sm(kFewElems) / kThreads
+                                        : std::max(1, bwd_per_sm(kElems) * kElems / N);
+    groups = std::min<long long>((rows + 3) / 4 + 8, (long long)kMaxSms * per_sm);
+    groups = std::max<long long>(groups, std::min<long long>(kMaxWideGroups, (rows + 31) / 32));
   }
   return (size_t)std::max<long long>(1, groups) * 2 * N * sizeof(float);
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t st) {
-  using bf = __nv_bfloat16;
-  if (a.x_type == 0) {
-    if (a.y_type == 0) return norm_fwd<float, float>(a, st);
-    if (a.y_type == 1) return norm_fwd<float, bf>(a, st);
-    return norm_fwd<float, __half>(a, st);
-  }
-  return a.x_type == 1 ? norm_fwd<bf, bf>(a, st) : norm_fwd<__half, __half>(a, st);
+  return a.x_type == 0 ? norm_fwd_f32(a, st) : a.x_type == 1 ? norm_fwd_bf16(a, st) : norm_fwd_f16(a, st);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
-  using bf = __nv_bfloat16;
-  if (a.x_type == 0) {
-    if (a.dy_type == 0) return norm_bwd<float, float>(a, st);
-    if (a.dy_type == 1) return norm_bwd<float, bf>(a, st);
-    return norm_bwd<float, __half>(a, st);
-  }
-  if (a.x_type == 1) return a.dy_type == 0 ? norm_bwd<bf, float>(a, st) : norm_bwd<bf, bf>(a, st);
-  return a.dy_type == 0 ? norm_bwd<__half, float>(a, st) : norm_bwd<__half, __half>(a, st);
+  return a.x_type == 0 ? norm_bwd_f32(a, st) : a.x_type == 1 ? norm_bwd_bf16(a, st) : norm_bwd_f16(a, st);
 }
 
 }  // namespace ibwd

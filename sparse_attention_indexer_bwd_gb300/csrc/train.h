@@ -43,6 +43,13 @@ struct NormBwdArgs {
 };
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st);
 size_t norm_bwd_workspace(long long rows, int N);
+// The same by the type of x.
+cudaError_t norm_fwd_f32(const NormFwdArgs& a, cudaStream_t st);
+cudaError_t norm_fwd_bf16(const NormFwdArgs& a, cudaStream_t st);
+cudaError_t norm_fwd_f16(const NormFwdArgs& a, cudaStream_t st);
+cudaError_t norm_bwd_f32(const NormBwdArgs& a, cudaStream_t st);
+cudaError_t norm_bwd_bf16(const NormBwdArgs& a, cudaStream_t st);
+cudaError_t norm_bwd_f16(const NormBwdArgs& a, cudaStream_t st);
 
 // Which function of a row of logits a launch computes.
 enum class RowOp { kLogpFwd, kLogpBwd, kDistillFwd, kDistillBwd, kDistillGrad };

@@ -97,6 +97,27 @@ def test_strides_and_alignments(n, pad, offset, kind):
     check_norm_fwd(got, x, gamma, beta, 1e-5, dt, "unaligned weights")
 
 
+@pytest.mark.parametrize("rows,n,pad", [(1500, 333, 0), (1500, 333, 5), (2001, 1001, 0), (1203, 2051, 2), (1100, 4099, 0),
+                                        (640, 7001, 3), (400, 9001, 0), (333, 16383, 1), (320, 12288, 0), (40, 20001, 0),
+                                        (7, 2049, 0), (9, 2049, 0), (33, 650, 4)])
+@pytest.mark.parametrize("kind,dy_kind", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32"), ("fp32", "bf16")])
+def test_unaligned_rows(rows, n, pad, kind, dy_kind):
+    """Rows that begin anywhere in a 16-byte block, alike in all matrices or not, several of them a team."""
+    dt = DTYPES[kind]
+    x, dy = matrix(rows, n, dt, pad, seed=21), matrix(rows, n, DTYPES[dy_kind], pad, seed=22)
+    gamma, beta = weights(n)
+    y, mean, rstd = ibwd.layer_norm_fwd(x, gamma, beta)
+    check_norm_fwd((y, mean, rstd), x, gamma, beta, 1e-5, dt, f"{rows}x{n}+{pad}")
+    got = ibwd.layer_norm_bwd(dy, x, mean, rstd, gamma)
+    check_norm_bwd(got, dy, x, mean, rstd, gamma, f"{rows}x{n}+{pad}")
+    again = ibwd.layer_norm_bwd(dy, x, mean, rstd, gamma)
+    assert all(same(a, b) for a, b in zip(got, again))
+    # another alignment of dy and dx
+    dy2 = torch.cat([dy[:, :1], dy], 1)[:, 1:]
+    out = torch.empty((rows, n + 3), device="cuda", dtype=dt)[:, :n]
+    check_norm_bwd(ibwd.layer_norm_bwd(dy2, x, mean, rstd, gamma, out=out), dy, x, mean, rstd, gamma, "other alignment")
+
+
 @pytest.mark.parametrize("n", [96, 128, 2047, 4096, 12000, 40000])
 def test_in_place_and_reproducible(n):
     x, dy = matrix(301, n, torch.bfloat16, seed=9), matrix(301, n, torch.bfloat16, seed=10)
