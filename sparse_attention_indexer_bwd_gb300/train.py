@@ -66,6 +66,8 @@ def _rows(t, name):
     if t.is_contiguous():
         return t.numel() // width, width, width
     stride = t.stride()
+    if len(shape) == 2 and stride[1] == 1 and stride[0] >= width:
+        return shape[0], width, stride[0]
     rows, step = 1, width
     for d in range(len(shape) - 2, -1, -1):
         if shape[d] == 1:
@@ -112,8 +114,7 @@ def _matrix_out(out, like, dtype, name):
         if like.is_contiguous():
             out = torch.empty_like(like) if dtype == like.dtype else torch.empty_like(like, dtype=dtype)
         else:
-            rows, width, step = _rows(like, name)
-            out = torch.empty(rows * step, dtype=dtype, device=like.device).as_strided(like.shape, like.stride())
+            out = torch.empty_strided(like.shape, like.stride(), dtype=dtype, device=like.device)
         return out, None
     if isinstance(out, torch.Tensor) and (out.shape != like.shape or out.dtype != dtype or out.device != like.device):
         raise ValueError(f"{name}: expected {dtype} {tuple(like.shape)} on {like.device}, "
