@@ -160,7 +160,7 @@ __device__ __forceinline__ unsigned long long order_key(float x, int v) {
 constexpr int kHot = 1024;  // segments looked at again
 
 struct TopShared {
-  alignas(16) unsigned long long cand[kCand + 2];
+  alignas(16) unsigned long long cand[kCand + 4];
   unsigned long long merge[kMaxTop * kMaxCluster];
   int merge_n[kMaxCluster];
   uint16_t segment[kSegments * kThreads];
@@ -319,21 +319,11 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
   // (a thread without logits above kFloor stops there: no bound then)
   const uint32_t half = sh.bound > order_bits(kFloor) >> 16 ? sh.bound : 0;
   const uint32_t bound = max(half << 16, order_bits(NEG_INF) + 1);
-  if (my_key >= half) {
-    const int mine = p.nvec > t ? (p.nvec - t + kThreads - 1) / kThreads : 0;  // vectors of this thread
-    const int segments = (mine + (kUnroll << shift) - 1) / (kUnroll << shift);
-    for (int s = 0; s < segments; ++s)
-      if (sh.segment[s * kThreads + t] >= half) {
-        const int at = atomicAdd(&sh.nhot, 1);
-        if (at < kHot) sh.hot[at] = s * kThreads + t;
-      }
-  }
-  __syncthreads();
-  const int nhot = sh.nhot;
   const float cut = half ? order_value(bound) : NEG_INF;
   auto wanted = [&](float x) { return half ? x >= cut : x > cut; };
-  // Appends the wanted ones of a lane's E values: one addition a warp.
-  auto append = [&](unsigned mask, auto key_of) {
+  // Places for the set bits of every lane's mask behind `count`: one addition
+  // a warp; put(place, bit) for each.
+  auto append = [&](int& count, unsigned mask, auto put) {
     const int mine = __popc(mask);
     int upto = mine;
 #pragma unroll
@@ -342,11 +332,25 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
       if (lane >= o) upto += v;
     }
     int base = 0;
-    if (lane == 31 && upto) base = atomicAdd(&sh.ncand, upto);
+    if (lane == 31 && upto) base = atomicAdd(&count, upto);
     base = __shfl_sync(0xffffffffu, base, 31) + upto - mine;
-    for (; mask; mask &= mask - 1, ++base)
-      if (base < kCand) sh.cand[base] = key_of(__ffs(mask) - 1);
+    for (; mask; mask &= mask - 1, ++base) put(base, __ffs(mask) - 1);
   };
+  {
+    const int mine = p.nvec > t ? (p.nvec - t + kThreads - 1) / kThreads : 0;  // vectors of this thread
+    const int segments = (mine + (kUnroll << shift) - 1) / (kUnroll << shift);
+    unsigned mask = 0;
+    if (my_key >= half) {
+#pragma unroll
+      for (int s = 0; s < kSegments; ++s)
+        mask |= s < segments && sh.segment[s * kThreads + t] >= half ? 1u << s : 0u;
+    }
+    append(sh.nhot, mask, [&](int at, int s) {
+      if (at < kHot) sh.hot[at] = s * kThreads + t;
+    });
+  }
+  __syncthreads();
+  const int nhot = sh.nhot;
   if (nhot <= kHot) {
     static_assert(kUnroll == 4, "a segment has 4 << shift vectors");
     const int bits = 2 + shift, items = nhot << bits;
@@ -365,51 +369,59 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
         if (at[k] < p.nvec) r[k] = ld_stream(p.vec(at[k]));
       }
       unsigned mask = 0;
-      float v[TAKE][V];
 #pragma unroll
       for (int k = 0; k < TAKE; ++k)
         if (at[k] < p.nvec) {
-          unpack(r[k], v[k], T{});
+          float v[V];
+          unpack(r[k], v, T{});
 #pragma unroll
-          for (int j = 0; j < V; ++j) mask |= wanted(v[k][j]) ? 1u << (k * V + j) : 0u;
+          for (int j = 0; j < V; ++j) mask |= wanted(v[j]) ? 1u << (k * V + j) : 0u;
         }
-      append(mask, [&](int i) {
-        float x = 0.f;
-        int index = 0;
+      append(sh.ncand, mask, [&](int place, int i) {
+        // element i % V of vector i / V
+        uint4 q = r[0];
+        int vec = at[0];
 #pragma unroll
-        for (int k = 0; k < TAKE; ++k)
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (i == k * V + j) {
-              x = v[k][j];
-              index = lo + p.nhead + at[k] * V + j;
-            }
-        return order_key(x, index);
+        for (int k = 1; k < TAKE; ++k)
+          if (i / V == k) {
+            q = r[k];
+            vec = at[k];
+          }
+        const int word = i % V * (int)sizeof(T) / 4;
+        const uint32_t w = word == 0 ? q.x : word == 1 ? q.y : word == 2 ? q.z : q.w;
+        float x;
+        if constexpr (sizeof(T) == 4)
+          x = __uint_as_float(w);
+        else
+          x = i & 1 ? unpack2(w, T{}).y : unpack2(w, T{}).x;
+        if (place < kCand) sh.cand[place] = order_key(x, lo + p.nhead + vec * V + i % V);
       });
     }
     if (warp == 0) {
       const int o = lane < p.singles() ? p.single_at(lane) : 0;
       const float x = lane < p.singles() ? to_f32(p.head[o]) : NEG_INF;
-      append(wanted(x) ? 1u : 0u, [&](int) { return order_key(x, lo + o); });
+      append(sh.ncand, wanted(x) ? 1u : 0u, [&](int place, int) {
+        if (place < kCand) sh.cand[place] = order_key(x, lo + o);
+      });
     }
   }
   __syncthreads();
   if (nhot > kHot || sh.ncand > kCand) top_exact(p, lo, hi, n, bound - 1, sh);  // uniform
   const int count = sh.ncand;
-  if (count & 1) {
-    if (t == 0) sh.cand[count] = 0;
-    __syncthreads();
-  }
-  for (int i = t; i < count; i += kThreads) {
-    const unsigned long long key = sh.cand[i];
+  if (t < 4) sh.cand[count + t] = 0;  // below every key: they are read four at a time, by two lanes
+  __syncthreads();
+  for (int i0 = 0; i0 < count; i0 += kThreads / 2) {
+    const int i = i0 + (t >> 1);
+    if (i0 + (warp << 4) >= count) break;  // uniform in a warp
+    const unsigned long long key = i < count ? sh.cand[i] : ~0ull;
     int r = 0;
-    // (one slot past the end is read; it is below every key)
 #pragma unroll 4
-    for (int k = 0; k < count; k += 2) {
+    for (int k = 2 * (t & 1); k < count; k += 4) {
       const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.cand[k]);
       r += (o.x > key) + (o.y > key);
     }
-    if (r < n) out[r] = key;
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    if (i < count && !(t & 1) && r < n) out[r] = key;
   }
   return min(count, n);
 }
