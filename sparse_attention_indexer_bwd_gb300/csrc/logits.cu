@@ -508,8 +508,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
     my_max = own.m;
   }
   if (kStat) prefetch_part<T>(a, row, lo, hi, kAhead);
-  // The student's logits of the teacher's slots; the first one of a thread is
-  // used after the row's statistic and comes in meanwhile.
+  // The student's logits of the teacher's slots (without the loss, of those
+  // in this part); the first one of a thread is used after the row's statistic
+  // and comes in meanwhile.
   float x_first = 0.f;
   if (kDistill) {
     cp_async_wait_all();
@@ -517,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
     for (int j = t; j < a.K; j += NT) {
       const int id = kept.id[j];
       const bool ok = id >= 0 && id < a.V;
-      const float x = ok ? to_f32(xr[id]) : 0.f;
+      const bool used = OP == RowOp::kDistillBwd ? id >= lo && id < hi : ok;
+      const float x = used ? to_f32(xr[id]) : 0.f;
       if (ok)
         tmax = fmaxf(tmax, kept.p[j]);
       else {
@@ -674,9 +676,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
       kept_gap[warp] = gap;
     }
     if (OP != RowOp::kDistillFwd) {
-      // every block has read its logits of kept tokens before any is
-      // overwritten (with statistics, they have met since)
-      if (!kStat && C > 1) cg::this_cluster().sync();
+      // (every logit of a kept token has been read, by this block or, with
+      // statistics, before the blocks met)
       float g = a.dloss ? a.dloss[row] * a.temperature : a.temperature;
       if (OP == RowOp::kDistillGrad) g *= a.grad_scale;
       const float2 c2 = both(c), nref = both(-ref), off = both(-l2s), g2 = both(g);
@@ -736,7 +737,8 @@ cudaError_t launch_rows_t(RowArgs a, int C, cudaStream_t st) {
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  // (the blocks of a row meet for its statistic; without one they only share it)
+  cfg.numAttrs = C > 1 && OP != RowOp::kLogpBwd && OP != RowOp::kDistillBwd ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP>, a, C);
 }
 
@@ -747,10 +749,16 @@ cudaError_t launch_typed(RowOp op, const RowArgs& a, cudaStream_t st) {
   // share only where SMs would be idle, and parts keep some work: 8 rows of
   // 65536 bf16 with 20 alternatives take 8.5 us in one block each, 8.8 in
   // two, 16.6 in eight; 32 rows of 32768 with their gradient 7.6 and 6.6.
-  // The plain backward has no joins and takes as many as fill the SMs.
+  // A backward pass has no joins: its blocks take 32 KB at least, and so many
+  // that the last ones do not leave the SMs idle for long (4096 rows of 131072
+  // bf16: 339 us in one block a row, 315 in two) -- with a teacher's slots,
+  // which every block of a row goes through, as many as fill the SMs.
+  const bool bwd = op == RowOp::kLogpBwd || op == RowOp::kDistillBwd;
   const bool top = op == RowOp::kLogpFwd && a.top_n;
-  const long long blocks = op == RowOp::kLogpBwd ? (long long)kBlocks * a.num_sms : a.num_sms;
-  const int least = (top ? 8 : 4) * kThreads * kVec<T>;
+  const long long blocks = op == RowOp::kLogpBwd      ? 8LL * kBlocks * a.num_sms
+                           : op == RowOp::kDistillBwd ? (long long)kBlocks * a.num_sms
+                                                      : a.num_sms;
+  const int least = (bwd ? 8 : top ? 8 : 4) * kThreads * kVec<T>;
   int C = 1;
   while (C < kMaxCluster && a.rows * 2 * C <= blocks && a.V >= 2LL * C * least) C *= 2;
   switch (op) {

@@ -350,3 +350,27 @@ def test_loss_and_gradient_over_row_sizes(rows, v, kind):
     z = x.clone()
     l2, d2 = ibwd.distill_grad(z, ids, teacher, w, out=z)
     assert same(l2, loss) and same(z, dx)
+
+
+@pytest.mark.parametrize("tau", [1e-7, 1e-3, 50.0, 1e4, 1e21])
+@pytest.mark.parametrize("kind", ["fp16", "fp32"])
+def test_extreme_temperatures(tau, kind):
+    """From an argmax to a uniform row, with masks of -inf and of the lowest value."""
+    for rows, v in ((3, 40001), (320, 1500)):
+        x = logits(rows, v, kind, seed=14)
+        x[:, ::3] = -INF
+        x[:, 1::7] = torch.finfo(x.dtype).min
+        tok = some_tokens(rows, v, padding=False)
+        got = ibwd.token_logprobs_fwd(x, tok, top_n=9, temperature=tau)
+        assert not any(torch.isnan(t.float()).any() for t in got)
+        check_logp_fwd(got, x, tok, 9, tau, f"temperature {tau}")
+        ids, teacher = kept(x, 12, padding=False)
+        w = torch.ones(rows, device="cuda")
+        loss, lse = ibwd.distill_fwd(x, ids, teacher, temperature=tau)
+        dx = ibwd.distill_bwd(x, ids, teacher, lse, w, temperature=tau)
+        whole = ibwd.distill_grad(x, ids, teacher, temperature=tau)
+        # (a gradient of T (q - p) may pass the type's range, a NaN it never is)
+        assert not torch.isnan(dx).any() and not torch.isnan(whole[1]).any()
+        if tau >= 1e-3:
+            check_distill(loss, lse, dx, w, x, ids, teacher, tau, f"temperature {tau}")
+            check_distill(whole[0], None, whole[1], w, x, ids, teacher, tau, f"temperature {tau}, whole")

@@ -30,6 +30,8 @@ def sum_bound(n):
 
 def within(got, ref, tol, what):
     """Elementwise |got - ref| <= tol, with NaN and infinities where the reference has them."""
+    if got.dtype == torch.float32:
+        ref = ref.float()  # (what fp32 cannot hold is an infinity)
     got, ref = got.double().cpu(), ref.double().cpu()
     tol = torch.as_tensor(tol, dtype=torch.float64).cpu().expand_as(ref)
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
