@@ -105,7 +105,7 @@ def test_workspace_size(lib):
     assert ibwd.layer_norm_bwd_workspace_size(4, 0) == 0
 
 
-def test_host_tensors_and_other_types_are_refused():
+def test_host_tensors_and_other_types_are_refused(lib):
     x = torch.zeros((4, 16))
     with pytest.raises(ValueError):
         ibwd.layer_norm_fwd(x)

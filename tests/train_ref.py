@@ -30,9 +30,9 @@ def sum_bound(n):
 
 def within(got, ref, tol, what):
     """Elementwise |got - ref| <= tol, with NaN and infinities where the reference has them."""
-    if got.dtype == torch.float32:
-        ref = ref.float()  # (what fp32 cannot hold is an infinity)
+    most = torch.finfo(got.dtype).max * (1 + torch.finfo(got.dtype).eps / 4)
     got, ref = got.double().cpu(), ref.double().cpu()
+    ref = torch.where(ref.abs() >= most, ref.sign() * math.inf, ref)  # what the type cannot hold is an infinity
     tol = torch.as_tensor(tol, dtype=torch.float64).cpu().expand_as(ref)
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     fine = torch.isfinite(ref)
