@@ -38,10 +38,11 @@ template <int NT>
 constexpr int kRoom = kGroups * kUnroll * NT;  // vectors of a part that NT threads hold
 constexpr int kMaxWarps = 256 / 32;
 // Blocks of an SM: registers for four of 256 threads, of which three find
-// room for 64 KB, or eight of 128 with parts of at most 32 KB.
+// room for 64 KB, eight of 128 with parts of at most 32 KB, or 16 of 64: what
+// a small part costs is the latency of its steps, and more of them overlap.
 template <int NT>
-constexpr int kBlocks = NT == 256 ? 4 : 8;
-constexpr int kSmallPart = 32 * 1024;
+constexpr int kBlocks = 1024 / NT;
+constexpr int kSmallPart = 32 * 1024, kTinyPart = 8 * 1024;
 
 // What the blocks of a cluster tell each other about a row: the part's
 // maximum and sum, and of the kept tokens in it the sums of w (x - m) / T and
@@ -353,8 +354,10 @@ cudaError_t launch_parts(RowArgs a, int C, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_typed(const RowArgs& a, cudaStream_t st) {
   const int C = blocks_of(a);
-  return part_len(a.V, C) * (int)sizeof(T) <= kSmallPart ? launch_parts<T, 128>(a, C, st)
-                                                         : launch_parts<T, 256>(a, C, st);
+  const int bytes = part_len(a.V, C) * (int)sizeof(T);
+  if (a.rows * C <= 2 * a.num_sms) return launch_parts<T, 256>(a, C, st);
+  if (bytes <= kTinyPart) return launch_parts<T, 64>(a, C, st);
+  return bytes <= kSmallPart ? launch_parts<T, 128>(a, C, st) : launch_parts<T, 256>(a, C, st);
 }
 
 }  // namespace

@@ -29,11 +29,13 @@ namespace cg = cooperative_groups;
 namespace ibwd {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxWarps = kThreads / 32;
+constexpr int kMaxThreads = 256;  // of a block: 256 for long rows, 128 or 64 for short ones
+constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxTop = 128;
-constexpr int kBlocks = 4;     // of an SM
+template <int NT>
+constexpr int kBlocks = 1024 / NT;  // of an SM
 constexpr int kAhead = 64 * 1024;  // bytes of the next row
+constexpr int kSmallPart = 32 * 1024, kTinyPart = 8 * 1024;
 constexpr int kCand = 1024;    // candidates a block ranks for the top alternatives
 constexpr int kSegments = 16;  // maxima a thread keeps of its logits
 
@@ -46,56 +48,76 @@ __device__ __forceinline__ float order_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// Maxima of a thread's vectors in runs of kUnroll << shift of them, at most
-// kSegments, by the upper half of their order.
+// Maxima of a thread's vectors in runs of 1 << bits of them, at most
+// kSegments, by the upper half of their order: single vectors of short rows,
+// else multiples of kUnroll.
+template <int NT>
 struct Segments {
-  uint16_t* at;  // [kSegments][kThreads], or nullptr
-  int shift;
+  uint16_t* at;  // [kSegments][NT], or nullptr
+  int bits;
   float run;
   template <typename T>
-  __device__ Segments(uint16_t* a, const Part<T>& p) : at(a), shift(0), run(NEG_INF) {
-    const int blocks = (p.nvec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
-    while ((blocks - 1) >> shift >= kSegments) ++shift;
+  __device__ Segments(uint16_t* a, const Part<T>& p) : at(a), bits(0), run(NEG_INF) {
+    static_assert(kUnroll == 4, "two bits");
+    const int vectors = (p.nvec + NT - 1) / NT;  // of a thread
+    if (vectors > kSegments) bits = 2;
+    while ((vectors - 1) >> bits >= kSegments) ++bits;
   }
-  __device__ __forceinline__ void put(int block, float most) {
-    run = (block & ((1 << shift) - 1)) ? fmaxf(run, most) : most;
-    at[(block >> shift) * kThreads + threadIdx.x] = (uint16_t)(order_bits(run) >> 16);
+  __device__ __forceinline__ bool single() const { return bits == 0; }
+  // vector number `v` of the thread; a run begins where v is a multiple of its length
+  __device__ __forceinline__ void put(int v, float most) {
+    run = (v & ((1 << bits) - 1)) ? fmaxf(run, most) : most;
+    at[(v >> bits) * NT + threadIdx.x] = (uint16_t)(order_bits(run) >> 16);
   }
 };
 
 // Streamed from global memory, the next vectors' loads ahead of the sums.
-template <typename T, bool U, bool TOP>
-__device__ __forceinline__ Stat part_stat(const Part<T>& p, Segments& seg, float c) {
+template <int NT, typename T, bool U, bool TOP>
+__device__ __forceinline__ Stat part_stat(const Part<T>& p, Segments<NT>& seg, float c) {
   Run t{kFloor, {0.f, 0.f}, {0.f, 0.f}};
-  int i = threadIdx.x, block = 0;
-  constexpr int kStep = kUnroll * kThreads;
-  if (i + (kUnroll - 1) * kThreads < p.nvec) {
+  int i = threadIdx.x, v = 0;  // the thread's next vector, and its number
+  constexpr int kStep = kUnroll * NT;
+  auto four = [&](const uint4(&r)[kUnroll]) {
+    const float most = max_of<T>(r);
+    if (TOP) {
+      if (seg.single()) {
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const uint4 one[1] = {r[k]};
+          seg.put(v + k, max_of<T>(one));
+        }
+      } else {
+        seg.put(v, most);
+      }
+      v += kUnroll;
+    }
+    add_vectors<T, U>(t, r, most, c);
+  };
+  if (i + (kUnroll - 1) * NT < p.nvec) {
     uint4 r[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) r[k] = ld_stream(p.vec(i + k * kThreads));
-    for (i += kStep; i + (kUnroll - 1) * kThreads < p.nvec; i += kStep) {
+    for (int k = 0; k < kUnroll; ++k) r[k] = ld_stream(p.vec(i + k * NT));
+    for (i += kStep; i + (kUnroll - 1) * NT < p.nvec; i += kStep) {
       uint4 n[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) n[k] = ld_stream(p.vec(i + k * kThreads));
-      const float most = max_of<T>(r);
-      if (TOP) seg.put(block++, most);
-      add_vectors<T, U>(t, r, most, c);
+      for (int k = 0; k < kUnroll; ++k) n[k] = ld_stream(p.vec(i + k * NT));
+      four(r);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) r[k] = n[k];
     }
-    const float most = max_of<T>(r);
-    if (TOP) seg.put(block++, most);
-    add_vectors<T, U>(t, r, most, c);
+    four(r);
   }
   if (i < p.nvec) {
     float all = NEG_INF;
-    for (; i < p.nvec; i += kThreads) {
+    int first = v;
+    for (; i < p.nvec; i += NT) {
       const uint4 r[1] = {ld_stream(p.vec(i))};
       const float most = max_of<T>(r);
       all = fmaxf(all, most);
+      if (TOP && seg.single()) seg.put(v++, most);
       add_vectors<T, U>(t, r, most, c);
     }
-    if (TOP) seg.put(block, all);
+    if (TOP && !seg.single()) seg.put(first, all);
   }
   return finish<T, U>(t, p, c);
 }
@@ -157,14 +179,16 @@ __device__ __forceinline__ unsigned long long order_key(float x, int v) {
   return ((unsigned long long)order_bits(x) << 32) | (uint32_t)~v;
 }
 
-constexpr int kHot = 1024;  // segments looked at again
+constexpr int kHot = 1024;       // segments looked at again
+constexpr int kDistances = 256;  // distances of the maxima from the largest that are counted
 
+template <int NT>
 struct TopShared {
   alignas(16) unsigned long long cand[kCand + 4];
   unsigned long long merge[kMaxTop * kMaxCluster];
   int merge_n[kMaxCluster];
-  uint16_t segment[kSegments * kThreads];
-  int count_at[kThreads];  // threads by the distance of their maximum from the largest one
+  uint16_t segment[kSegments * NT];
+  int count_at[kDistances];  // maxima by their distance from the largest one
   int hot[kHot];
   int nhot, ncand;
   uint32_t least, below;
@@ -176,8 +200,8 @@ struct TopShared {
 // logits, or logits whose order follows the threads): the exact order of the
 // n-th largest by bisection, then everything above it and the equal ones of
 // lowest index.
-template <typename T>
-__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, uint32_t bound, TopShared& sh) {
+template <int NT, typename T>
+__device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, uint32_t bound, TopShared<NT>& sh) {
   // masked logits and NaN are no entries
   auto order = [](float x) { return x > NEG_INF ? order_bits(x) : 0u; };
   // entries of the part above `cut`: their number, the least of them, and the
@@ -192,7 +216,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
     __syncthreads();
     int k = 0;
     uint32_t l = ~0u, h = 0;
-    for_each<kThreads>(p, lo, [&](float x, int) {
+    for_each<NT>(p, lo, [&](float x, int) {
       const uint32_t key = order(x);
       if (key > cut) {
         ++k;
@@ -235,7 +259,7 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
   __syncthreads();
   if (threadIdx.x == 0) sh.ncand = 0;
   __syncthreads();
-  for_each<kThreads>(p, lo, [&](float x, int v) {
+  for_each<NT>(p, lo, [&](float x, int v) {
     if (order(x) > a) sh.cand[atomicAdd(&sh.ncand, 1)] = order_key(x, v);
   });
   __syncthreads();
@@ -243,14 +267,14 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
   // the lowest indices among the equal ones, in order
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int have = sh.ncand;
-  for (int v0 = lo; v0 < hi && have < n; v0 += kThreads) {
+  for (int v0 = lo; v0 < hi && have < n; v0 += NT) {
     const int v = v0 + threadIdx.x;
     const bool eq = v < hi && order(to_f32(p.head[v - lo])) == a;
     const unsigned mask = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) sh.warp_n[warp] = __popc(mask);
     __syncthreads();
     int at = have + __popc(mask & ((1u << lane) - 1u)), total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) at += sh.warp_n[w];
       total += sh.warp_n[w];
     }
@@ -271,17 +295,27 @@ __device__ __noinline__ void top_exact(const Part<T>& p, int lo, int hi, int n, 
 // a bf16) by counting the maxima at each distance from the largest, or by
 // bisection where it is further away than that.
 // sh.count_at is zero and sh.nhot, sh.ncand are 0 on entry.
-template <typename T>
-__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, float most, int shift,
-                                        TopShared& sh, unsigned long long* out) {
+template <int NT, typename T>
+__device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n, float my_max, float most, int bits,
+                                        TopShared<NT>& sh, unsigned long long* out) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t my_key = order_bits(my_max) >> 16, top_key = order_bits(most) >> 16;
-  const bool near = top_key - my_key < kThreads;
-  if (near) atomicAdd(&sh.count_at[top_key - my_key], 1);
+  const int mine = p.nvec > t ? (p.nvec - t + NT - 1) / NT : 0;  // vectors of this thread
+  const int segments = (mine + (1 << bits) - 1) >> bits;
+  // Short rows count their vectors' maxima, which are many enough for them;
+  // a thread's single elements are left out of those.
+  if (bits == 0) {
+    for (int s = 0; s < segments; ++s) {
+      const uint32_t d = top_key - sh.segment[s * NT + t];
+      if (d < kDistances) atomicAdd(&sh.count_at[d], 1);
+    }
+  } else if (top_key - my_key < kDistances) {
+    atomicAdd(&sh.count_at[top_key - my_key], 1);
+  }
   __syncthreads();
   if (t < 32) {
     // lane i has distances 8 i .. 8 i + 7
-    constexpr int PER = kThreads / 32;
+    constexpr int PER = kDistances / 32;
     int c[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -311,8 +345,20 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
   __syncthreads();
   if (sh.bound == ~0u) {  // uniform: bisection over all 16 bits
     uint32_t key = 0;
-    for (uint32_t bit = 1u << 15; bit; bit >>= 1)
-      if (__syncthreads_count(my_key >= (key | bit)) >= n) key |= bit;
+    for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
+      unsigned k = my_key >= (key | bit);
+      if (bits == 0) {
+        k = 0;
+        for (int s = 0; s < segments; ++s) k += sh.segment[s * NT + t] >= (key | bit);
+      }
+      if (t == 0) sh.least = 0;
+      __syncthreads();
+      k = __reduce_add_sync(0xffffffffu, k);
+      if (lane == 0 && k) atomicAdd(&sh.least, k);
+      __syncthreads();
+      if (sh.least >= (unsigned)n) key |= bit;
+      __syncthreads();
+    }
     if (t == 0) sh.bound = key;
     __syncthreads();
   }
@@ -337,34 +383,31 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
     for (; mask; mask &= mask - 1, ++base) put(base, __ffs(mask) - 1);
   };
   {
-    const int mine = p.nvec > t ? (p.nvec - t + kThreads - 1) / kThreads : 0;  // vectors of this thread
-    const int segments = (mine + (kUnroll << shift) - 1) / (kUnroll << shift);
     unsigned mask = 0;
     if (my_key >= half) {
 #pragma unroll
       for (int s = 0; s < kSegments; ++s)
-        mask |= s < segments && sh.segment[s * kThreads + t] >= half ? 1u << s : 0u;
+        mask |= s < segments && sh.segment[s * NT + t] >= half ? 1u << s : 0u;
     }
     append(sh.nhot, mask, [&](int at, int s) {
-      if (at < kHot) sh.hot[at] = s * kThreads + t;
+      if (at < kHot) sh.hot[at] = s * NT + t;
     });
   }
   __syncthreads();
   const int nhot = sh.nhot;
   if (nhot <= kHot) {
-    static_assert(kUnroll == 4, "a segment has 4 << shift vectors");
-    const int bits = 2 + shift, items = nhot << bits;
+    const int items = nhot << bits;
     constexpr int V = kVec<T>, TAKE = kUnroll;  // vectors a lane takes together: 32 values at most
-    for (int e0 = warp * 32; e0 < items; e0 += TAKE * kThreads) {
+    for (int e0 = warp * 32; e0 < items; e0 += TAKE * NT) {
       uint4 r[TAKE];
       int at[TAKE];
 #pragma unroll
       for (int k = 0; k < TAKE; ++k) {
-        const int e = e0 + lane + k * kThreads;
+        const int e = e0 + lane + k * NT;
         at[k] = p.nvec;
         if (e < items) {
           const int h = sh.hot[e >> bits];
-          at[k] = h % kThreads + (((h / kThreads) << bits) + (e & ((1 << bits) - 1))) * kThreads;
+          at[k] = h % NT + (((h / NT) << bits) + (e & ((1 << bits) - 1))) * NT;
         }
         if (at[k] < p.nvec) r[k] = ld_stream(p.vec(at[k]));
       }
@@ -406,11 +449,11 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
     }
   }
   __syncthreads();
-  if (nhot > kHot || sh.ncand > kCand) top_exact(p, lo, hi, n, bound - 1, sh);  // uniform
+  if (nhot > kHot || sh.ncand > kCand) top_exact<NT>(p, lo, hi, n, bound - 1, sh);  // uniform
   const int count = sh.ncand;
   if (t < 4) sh.cand[count + t] = 0;  // below every key: they are read four at a time, by two lanes
   __syncthreads();
-  for (int i0 = 0; i0 < count; i0 += kThreads / 2) {
+  for (int i0 = 0; i0 < count; i0 += NT / 2) {
     const int i = i0 + (t >> 1);
     if (i0 + (warp << 4) >= count) break;  // uniform in a warp
     const unsigned long long key = i < count ? sh.cand[i] : ~0ull;
@@ -464,16 +507,16 @@ struct Kept {  // [K] each, in shared memory
   float* x;  // the student's logit of it (read by the thread that wrote it)
 };
 
-template <typename T, RowOp OP, bool TOP>
-__global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int C) {
-  constexpr int NT = kThreads, NW = NT / 32;
+template <typename T, RowOp OP, bool TOP, int NT>
+__global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C) {
+  constexpr int NW = NT / 32;
   constexpr bool kDistill = OP == RowOp::kDistillFwd || OP == RowOp::kDistillBwd || OP == RowOp::kDistillGrad;
   constexpr bool kStat = OP == RowOp::kLogpFwd || OP == RowOp::kDistillFwd || OP == RowOp::kDistillGrad;
   constexpr bool kEntropy = OP == RowOp::kLogpFwd;
   __shared__ Stage stage;
   __shared__ float kept_max[kMaxWarps], kept_z[kMaxWarps], kept_gap[kMaxWarps];
   extern __shared__ __align__(16) unsigned char raw[];  // TopShared, or the kept tokens
-  TopShared& top = *reinterpret_cast<TopShared*>(raw);
+  TopShared<NT>& top = *reinterpret_cast<TopShared<NT>*>(raw);
   Kept kept;
   kept.id = reinterpret_cast<int*>(raw);
   kept.p = reinterpret_cast<float*>(kept.id + a.K);
@@ -501,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
 
   Stat st{0.f, 1.f, 0.f};
   float my_max = NEG_INF, most = NEG_INF;  // of the thread's and of the block's logits
-  Segments segments(TOP ? top.segment : nullptr, part);
+  Segments<NT> segments(TOP ? top.segment : nullptr, part);
   Stat own{NEG_INF, 0.f, 0.f};
   if (kStat) {
-    own = part_stat<T, kEntropy, TOP>(part, segments, c);
+    own = part_stat<NT, T, kEntropy, TOP>(part, segments, c);
     my_max = own.m;
   }
   if (kStat) prefetch_part<T>(a, row, lo, hi, kAhead);
@@ -539,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
   if (OP == RowOp::kLogpFwd && token >= 0 && token < a.V) x_token = to_f32(xr[token]);
   if (kStat) {
     if (TOP) {  // (before the statistic's barriers)
-      top.count_at[t] = 0;
+      for (int i = t; i < kDistances; i += NT) top.count_at[i] = 0;
       if (t == 0) top.nhot = top.ncand = 0;
     }
     st = row_stat<NT, kEntropy>(own, c, stage, C, most);
@@ -580,12 +623,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
       };
       int total = 0;
       if (C == 1) {
-        total = part_top(part, lo, hi, n, my_max, most, segments.shift, top, top.merge);
+        total = part_top<NT>(part, lo, hi, n, my_max, most, segments.bits, top, top.merge);
         __syncthreads();
         for (int i = t; i < total; i += NT) put(i, top.merge[i]);
       } else {
         cg::cluster_group cl = cg::this_cluster();
-        const int count = part_top(part, lo, hi, n, my_max, most, segments.shift, top,
+        const int count = part_top<NT>(part, lo, hi, n, my_max, most, segments.bits, top,
                                    cl.map_shared_rank(top.merge, 0) + rank * kMaxTop);
         if (t == 0) *(cl.map_shared_rank(top.merge_n, 0) + rank) = count;
         cl.sync();
@@ -723,13 +766,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(RowArgs a, int 
   }
 }
 
-template <typename T, RowOp OP, bool TOP>
-cudaError_t launch_rows_t(RowArgs a, int C, cudaStream_t st) {
-  const size_t smem = TOP ? sizeof(TopShared) : (size_t)a.K * 12;
+template <typename T, RowOp OP, bool TOP, int NT>
+cudaError_t launch_threads(RowArgs a, int C, cudaStream_t st) {
+  const size_t smem = TOP ? sizeof(TopShared<NT>) : (size_t)a.K * 12;
   cudaLaunchConfig_t cfg{};
-  a.ahead = std::max(1, kBlocks * a.num_sms / C);
+  a.ahead = std::max(1, kBlocks<NT> * a.num_sms / C);
   cfg.gridDim = dim3((unsigned)(a.rows * C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -739,7 +782,20 @@ cudaError_t launch_rows_t(RowArgs a, int C, cudaStream_t st) {
   cfg.attrs = attr;
   // (the blocks of a row meet for its statistic; without one they only share it)
   cfg.numAttrs = C > 1 && OP != RowOp::kLogpBwd && OP != RowOp::kDistillBwd ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP>, a, C);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<T, OP, TOP, NT>, a, C);
+}
+
+// Threads of a block by the bytes of its part: a short part costs the latency
+// of its steps, and more blocks of fewer threads overlap them (4864 rows of
+// 2048 bf16, 64 alternatives: 56 us by 256 threads, 32 by 64) -- unless the
+// rows are too few to fill the SMs (8 of 65536: 12.6 us by 128, 9.4 by 256).
+template <typename T, RowOp OP, bool TOP>
+cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
+  const int bytes = part_len(a.V, C) * (int)sizeof(T);
+  if (a.rows * C <= 2 * a.num_sms) return launch_threads<T, OP, TOP, 256>(a, C, st);
+  if (bytes <= kTinyPart) return launch_threads<T, OP, TOP, 64>(a, C, st);
+  if (bytes <= kSmallPart) return launch_threads<T, OP, TOP, 128>(a, C, st);
+  return launch_threads<T, OP, TOP, 256>(a, C, st);
 }
 
 template <typename T>
@@ -755,10 +811,10 @@ cudaError_t launch_typed(RowOp op, const RowArgs& a, cudaStream_t st) {
   // which every block of a row goes through, as many as fill the SMs.
   const bool bwd = op == RowOp::kLogpBwd || op == RowOp::kDistillBwd;
   const bool top = op == RowOp::kLogpFwd && a.top_n;
-  const long long blocks = op == RowOp::kLogpBwd      ? 8LL * kBlocks * a.num_sms
-                           : op == RowOp::kDistillBwd ? (long long)kBlocks * a.num_sms
+  const long long blocks = op == RowOp::kLogpBwd      ? 32LL * a.num_sms
+                           : op == RowOp::kDistillBwd ? 4LL * a.num_sms
                                                       : a.num_sms;
-  const int least = (bwd ? 8 : top ? 8 : 4) * kThreads * kVec<T>;
+  const int least = (bwd ? 8 : top ? 8 : 4) * kMaxThreads * kVec<T>;
   int C = 1;
   while (C < kMaxCluster && a.rows * 2 * C <= blocks && a.V >= 2LL * C * least) C *= 2;
   switch (op) {
