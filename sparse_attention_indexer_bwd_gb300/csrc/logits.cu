@@ -531,6 +531,8 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
   const Part<T> part(xr, lo, hi);
   const float inv_t = 1.f / a.temperature, c = kLog2e / a.temperature;
 
+  // (a gradient's logits come to L2 while its first small loads arrive)
+  if (!kStat) prefetch_bytes(xr + lo, xr + hi, kAhead);
   // what the row needs besides its logits is on its way before them
   int token = -1;
   if (OP == RowOp::kLogpFwd && rank == 0 && t == 0 && a.tokens) token = a.tokens[row];
@@ -636,10 +638,10 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
         for (int i = 0; i < C; ++i) total += top.merge_n[i];
         // place of an entry: its own place plus, in every other sorted list,
         // the number of larger keys
-        for (int e = t; e < C * kMaxTop; e += NT) {
-          const int l = e / kMaxTop, i = e % kMaxTop;
+        for (int e = t; e < C * n; e += NT) {
+          const int l = e / n, i = e % n;
           if (i >= top.merge_n[l]) continue;
-          const unsigned long long key = top.merge[e];
+          const unsigned long long key = top.merge[l * kMaxTop + i];
           int r = i;
           for (int k = 0; k < C; ++k) {
             if (k == l) continue;
@@ -801,10 +803,11 @@ cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_typed(RowOp op, const RowArgs& a, cudaStream_t st) {
   // Blocks a row.  Rows that meet in a cluster or select a top pay for each
-  // block (2-3 us of joins; a top's selection and merging more), so they
-  // share only where SMs would be idle, and parts keep some work: 8 rows of
-  // 65536 bf16 with 20 alternatives take 8.5 us in one block each, 8.8 in
-  // two, 16.6 in eight; 32 rows of 32768 with their gradient 7.6 and 6.6.
+  // block, so they share only where SMs would be idle, and parts keep some
+  // work: 16 KB, or 128 KB with a selection and its merge (4 rows of 131072
+  // bf16: 7.4 us in one block each, 4.2 in eight; with 20 alternatives 8 rows
+  // of 65536 take 8.2 us in one, 9.7 in two, and one fp32 row of 131072 12.7
+  // in one, 9.3 in four, 10.1 in eight).
   // A backward pass has no joins: its blocks take 32 KB at least, and so many
   // that the last ones do not leave the SMs idle for long (4096 rows of 131072
   // bf16: 339 us in one block a row, 315 in two) -- with a teacher's slots,
@@ -814,7 +817,7 @@ cudaError_t launch_typed(RowOp op, const RowArgs& a, cudaStream_t st) {
   const long long blocks = op == RowOp::kLogpBwd      ? 32LL * a.num_sms
                            : op == RowOp::kDistillBwd ? 4LL * a.num_sms
                                                       : a.num_sms;
-  const int least = (bwd ? 8 : top ? 8 : 4) * kMaxThreads * kVec<T>;
+  const int least = (bwd ? 8 : top ? 32 : 4) * kMaxThreads * kVec<T>;
   int C = 1;
   while (C < kMaxCluster && a.rows * 2 * C <= blocks && a.V >= 2LL * C * least) C *= 2;
   switch (op) {

@@ -220,20 +220,24 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // so that aligned rows have aligned parts.
 __host__ __device__ __forceinline__ int part_len(int V, int C) { return (((V + C - 1) / C) + 63) & ~63; }
 
-// Starts the next part that a block of this place will take on its way to L2
-// (its first `most` bytes), while this one has no more loads to make: blocks
-// that began together are in their joins and selections together, and HBM
-// would idle meanwhile.
+// Starts [from, to), or its first `most` bytes, on its way to L2 (one thread).
+__device__ __forceinline__ void prefetch_bytes(const void* from, const void* to, int most) {
+  if (threadIdx.x != 0) return;
+  const uintptr_t p = (reinterpret_cast<uintptr_t>(from) + 15) & ~(uintptr_t)15, e = reinterpret_cast<uintptr_t>(to);
+  if (p + 16 > e) return;
+  const uint32_t bytes = (uint32_t)min((unsigned long long)most, (unsigned long long)(e - p)) & ~15u;
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// The same for the next part that a block of this place will take, while this
+// one has no more loads to make: blocks that began together are in their
+// joins and selections together, and HBM would idle meanwhile.
 template <typename T>
 __device__ __forceinline__ void prefetch_part(const RowArgs& a, long long row, int lo, int hi, int most) {
   const long long next = row + a.ahead;
-  if (threadIdx.x != 0 || a.ahead == 0 || next >= a.rows || lo >= hi) return;
-  const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + next * a.x_stride + lo);
-  const uintptr_t to = from + (uintptr_t)(hi - lo) * sizeof(T);
-  const uintptr_t p = (from + 15) & ~(uintptr_t)15;
-  if (p + 16 > to) return;
-  const uint32_t bytes = (uint32_t)min((unsigned long long)most, (unsigned long long)(to - p)) & ~15u;
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+  if (a.ahead == 0 || next >= a.rows || lo >= hi) return;
+  const T* x = static_cast<const T*>(a.x) + next * a.x_stride;
+  prefetch_bytes(x + lo, x + hi, most);
 }
 
 }  // namespace

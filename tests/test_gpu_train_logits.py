@@ -80,7 +80,7 @@ def test_vocabularies(v, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 @pytest.mark.parametrize("rows,v", [(1, 50001), (3, 131072), (17, 65536), (40, 131071), (80, 32768), (160, 50001),
-                                    (400, 32000)])
+                                    (400, 32000), (2, 300001)])
 def test_few_and_many_rows(rows, v, kind):
     """From one row, which a cluster of blocks shares, to one block a row."""
     check_all(logits(rows, v, kind, seed=rows), 0.7, 20, 64, f"{rows}x{v}")
