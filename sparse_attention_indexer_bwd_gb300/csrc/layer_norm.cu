@@ -11,8 +11,8 @@ size_t norm_bwd_workspace(long long rows, int N) {
   if (N <= kMaxLateWidth) {
     // blocks of several teams, or of a team of at least N / 16 threads (with 8
     // elements each a block has more threads by more than an SM has)
-    const int per_sm = N <= 32 * kElems ? bwd_per_sm(kFewElems) / kThreads
-                                        : std::max(1, bwd_per_sm(kElems) * kElems / N);
+    const int per_sm = N <= 32 * kElems ? bwd_per_sm(kFewElems, false) / kThreads
+                                        : std::max(1, bwd_per_sm(kElems, N > kThreads * kElems) * kElems / N);
     groups = std::min<long long>((rows + 3) / 4 + 8, (long long)kMaxSms * per_sm);
     groups = std::max<long long>(groups, std::min<long long>(kMaxWideGroups, (rows + 31) / 32));
   }

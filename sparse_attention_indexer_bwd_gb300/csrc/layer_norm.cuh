@@ -5,15 +5,16 @@
 // About ten operations an element beside four to twelve bytes: bound by HBM,
 // or by the launch where rows are few.
 //
-// A team of threads holds a row in registers (16 elements a thread at most),
-// so every element is read once: 8 to 32 lanes of a warp for short rows, a
-// thread block for longer ones.  Teams stay resident and walk the rows; each
-// thread copies its own elements of the next rows into its own slots of a
+// A team of threads holds a row in registers (16 elements a thread at most)
+// or, where registers would leave an SM too few threads, in shared memory, so
+// every element is read once: 8 to 32 lanes of a warp for short rows, a thread
+// block for longer ones.  Teams stay resident and walk the rows; each thread
+// copies its own elements of the next rows into its own slots of a
 // shared-memory ring (cp.async), so several rows are in flight without
-// registers or barriers.  gamma and beta stay in registers, and so do the
-// backward pass's column sums of the team's rows.  Those meet in a fixed
-// order: a block's teams in shared memory, the blocks in a second small
-// kernel.  Rows too wide for a block take several passes.
+// registers or barriers.  The weights stay in registers or shared memory, the
+// backward pass's column sums of the team's rows in registers.  Those meet in
+// a fixed order: a block's teams in shared memory, the blocks in a second
+// small kernel.  Rows too wide for a block take several passes.
 #pragma once
 #include <algorithm>
 
@@ -28,24 +29,39 @@ namespace {
 constexpr int kThreads = 256;     // block of several teams, and of the kernels for wide rows
 constexpr int kMaxTeam = 512;     // threads of a block that is one team
 constexpr int kElems = 16;        // elements of a row a thread holds at most
-// Threads of an SM by the elements each holds (64 to 128 registers): rows of
-// up to 2048 elements take eight a thread, which leaves more warps.
+// Threads of an SM by the elements each holds (64 to 128 registers).  Shorter
+// rows take eight elements a thread, which leaves more warps: fp32 rows of up
+// to 2048 (14648x2047: 41 us, with sixteen 50), 16-bit ones of under 1024
+// (46152x650: 32 against 35; 14648x2048: 25 against 18).  The backward pass
+// of shifted fp32 rows gains from sixteen at over 1024 already (14648x2047: 75
+// against 67).
 constexpr int kFewElems = 8;
-constexpr int fwd_per_sm(int elems, int team) {
-  return elems <= kFewElems ? 1024 : elems <= kElems && team == 0 ? 768 : 512;
+template <typename T>
+constexpr int kFewWidth = kThreads * kFewElems / (sizeof(T) == 4 ? 1 : 2) - (sizeof(T) == 4 ? 0 : 1);
+constexpr int fwd_per_sm(int elems, int team, bool late) {
+  return elems <= kFewElems || late ? 1024 : team == 0 ? 768 : 512;
 }
-constexpr int bwd_per_sm(int elems) { return elems > kFewElems ? 512 : 768; }
-// Rows of a team in flight or in work: four, or as many as 192 KB of shared
-// memory hold of the widest row of E elements a thread.
-template <typename TX, int E>
-constexpr int kFwdStages = 512 * E * (int)sizeof(TX) * 4 <= 192 * 1024 ? 4 : 3;
-template <typename TX, typename TD, int E>
-constexpr int kBwdStages = 512 * E * (int)(sizeof(TX) + sizeof(TD)) * 4 <= 192 * 1024   ? 4
-                           : 512 * E * (int)(sizeof(TX) + sizeof(TD)) * 3 <= 192 * 1024 ? 3
-                                                                                        : 2;
-constexpr int kManyElems = 32;    // with the weights left in L1
+constexpr int bwd_per_sm(int elems, bool late) { return late ? 1024 : elems > kFewElems ? 512 : 768; }
 constexpr int kMaxTeamWidth = kMaxTeam * kElems;
-constexpr int kMaxLateWidth = kMaxTeam * kManyElems;
+// Wider rows: teams of up to 1024 threads with 64 registers each, two blocks
+// an SM up to 8192 elements.  The weights wait in shared memory beside the
+// ring, in the order of their use, and a row's place in the ring is fetched
+// into as soon as it was read.  From 4097 elements on this beats 512 threads
+// of 128 registers, of which an SM holds but one block, in the forward pass of
+// 16-bit rows (8192x4104: 44 us against 30; x8192: 54 against 52) and shifted
+// fp32 ones (8192x5003: 68 against 59; but 4096x8192, not shifted, 44 against
+// 49), and in the backward pass of fp32 rows (8192x5120: 112 against 90; but
+// 8192x8192 in bf16, where the weights are read twice for every two bytes, 79
+// against 96).  Beyond 8192 it is the only one (weights from L1 instead:
+// 8192x12288 in bf16 100 us against 86, shifted 278 against 112).
+constexpr int kLateTeam = 1024;
+constexpr int kMaxLateWidth = kLateTeam * kElems;
+// Rows of a team in flight or in work: four, or as many of the widest rows as
+// 192 KB of shared memory hold (beside the weights).
+constexpr int ring_stages(int maxt, int row_bytes, int weights) {
+  return maxt > kMaxTeam ? std::min(4, (192 * 1024 - weights * 4 * kMaxLateWidth) / (kLateTeam * row_bytes))
+                         : std::min(4, 192 * 1024 / (kMaxTeam * row_bytes));
+}
 
 // VEC consecutive elements as they lie in memory.
 template <typename T, int VEC>
@@ -123,6 +139,29 @@ struct Ring {
         *reinterpret_cast<uint32_t*>(c.e) = v;
       }
     }
+  }
+};
+
+// A thread's slots for its weights of a row in shared memory, in pieces of 16
+// bytes that lie side by side for neighbouring threads.
+template <int VEC>
+struct WeightSlots {
+  static constexpr int kPieces = VEC / 4;
+  uint32_t base, pitch;
+  __device__ WeightSlots(unsigned char* smem, int t, int threads) : base(smem_u32(smem) + t * 16), pitch(threads * 16) {}
+  __device__ __forceinline__ void put(int k, const float2 (&w)[VEC / 2]) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(base + (k * kPieces + i) * pitch), "f"(w[2 * i].x),
+                   "f"(w[2 * i].y), "f"(w[2 * i + 1].x), "f"(w[2 * i + 1].y)
+                   : "memory");
+  }
+  __device__ __forceinline__ void get(int k, float2 (&w)[VEC / 2]) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(w[2 * i].x), "=f"(w[2 * i].y), "=f"(w[2 * i + 1].x), "=f"(w[2 * i + 1].y)
+                   : "r"(base + (k * kPieces + i) * pitch));
   }
 };
 
@@ -267,9 +306,10 @@ __device__ __forceinline__ float over_n(float s, float n, float inv_n) {
 }
 
 template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT, bool SHIFT>
-__global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_fwd_team(NormFwdArgs a) {
-  constexpr int kStages = kFwdStages<TX, VEC * K>;
-  constexpr bool kLate = VEC * K > kElems;  // weights come from L1 for each row
+__global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM, MAXT > kMaxTeam) / MAXT) norm_fwd_team(NormFwdArgs a) {
+  constexpr bool kLate = MAXT > kMaxTeam;  // weights come from shared memory for each row
+  constexpr int kStages = ring_stages(MAXT, VEC * K * (int)sizeof(TX), 2);
+  constexpr int kAhead = kLate ? kStages : kStages - 1;  // rows fetched before the loop
   extern __shared__ __align__(16) unsigned char smem[];  // the ring
   __shared__ __align__(16) float stage[64];
   constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
@@ -292,9 +332,20 @@ __global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_f
   xr += sp.head + t * VEC;
   yr += sp.head + t * VEC;
   float2 g[kLate ? 1 : P], b[kLate ? 1 : P];
+  const WeightSlots<VEC> gs(smem + kStages * K * VEC * sizeof(TX) * T, t, T);
+  const WeightSlots<VEC> bs(smem + K * VEC * (kStages * sizeof(TX) + sizeof(float)) * T, t, T);
   if constexpr (!kLate) {
     weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec, sp.head);
     weights<TX, VEC, K>(b, a.beta, a.w_type == 0, 0.f, t, T, nvec, sp.head);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+      float2 w[VEC / 2];
+      weights<TX, VEC, 1>(w, a.gamma, a.w_type == 0, 1.f, t + k * T, T, nvec, sp.head);
+      gs.put(k, w);
+      weights<TX, VEC, 1>(w, a.beta, a.w_type == 0, 0.f, t + k * T, T, nvec, sp.head);
+      bs.put(k, w);
+    }
   }
   float g1 = 0.f, b1 = 0.f, next1 = 0.f;  // of the thread's single element
   if (SHIFT && sp.has_single) {
@@ -316,12 +367,12 @@ __global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_f
   int turn = 0, slot = 0;
   if (XRing::kAsync)
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * step < a.rows);
+    for (int i = 0; i < kAhead; ++i) fetch(i, first + i * step < a.rows);
   // (a block's teams leave together: their rows differ by less than a step)
   for (long long r = first; r - team < a.rows; r += step) {
     const bool on = r < a.rows;
     if (XRing::kAsync) {
-      fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
+      if (!kLate) fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
       cp_async_wait<kStages - 1>();
     }
 #pragma unroll
@@ -333,17 +384,19 @@ __global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_f
           cur[k].load(xr + k * T * VEC);
       }
     if (!XRing::kAsync) xr += x_step;
+    if (kLate && XRing::kAsync) fetch(slot, r + kStages * step < a.rows);  // into the place just read
     slot = slot == kStages - 1 ? 0 : slot + 1;
     float v1 = next1;
     if (SHIFT) {
       x1 += x_step;
       if (sp.has_single && r + step < a.rows) next1 = to_f32(*x1);
     }
-    float2 v[P], sum = both(0.f);
+    float2 v[kLate ? 1 : P], sum = both(0.f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      v[i] = pair_of(cur, i);
-      sum = add2(sum, v[i]);
+      const float2 e = pair_of(cur, i);
+      if (!kLate) v[kLate ? 0 : i] = e;
+      sum = add2(sum, e);
     }
     float s[1] = {sum.x + sum.y};
     if (SHIFT && sp.has_single) s[0] += v1;
@@ -353,12 +406,13 @@ __global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_f
     // elements the thread does not have are left out of the squares
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      v[i] = add2(v[i], both(-mean));
+      const float2 e = add2(kLate ? pair_of(cur, i) : v[kLate ? 0 : i], both(-mean));
+      if (!kLate) v[kLate ? 0 : i] = e;
       if constexpr (VEC > 1) {
-        if (t + 2 * i / VEC * T < nvec) sum = fma2(v[i], v[i], sum);
+        if (t + 2 * i / VEC * T < nvec) sum = fma2(e, e, sum);
       } else {
-        if (t + 2 * i * T < nvec) sum.x = fmaf(v[i].x, v[i].x, sum.x);
-        if (t + (2 * i + 1) * T < nvec) sum.y = fmaf(v[i].y, v[i].y, sum.y);
+        if (t + 2 * i * T < nvec) sum.x = fmaf(e.x, e.x, sum.x);
+        if (t + (2 * i + 1) * T < nvec) sum.y = fmaf(e.y, e.y, sum.y);
       }
     }
     float q[1] = {sum.x + sum.y};
@@ -369,24 +423,29 @@ __global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_f
     team_sums<TEAM>(q, stage, turn);
     const float rstd = rsqrtf(fmaf(q[0], inv_n, a.eps));
     if (on) {
-      Chunk<TY, VEC> o[K];
       if constexpr (!kLate) {
+        Chunk<TY, VEC> o[K];
 #pragma unroll
         for (int i = 0; i < P; ++i) set_pair(o, i, fma2(mul2(v[i], both(rstd)), g[i], b[i]));
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (t + k * T < nvec) o[k].store(yr + k * T * VEC);
       } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+          if (t + k * T >= nvec) break;
+          Chunk<TY, VEC> o[1];
           float2 gk[VEC / 2], bk[VEC / 2];
-          weights<TX, VEC, 1>(gk, a.gamma, a.w_type == 0, 1.f, t + k * T, T, nvec, sp.head);
-          weights<TX, VEC, 1>(bk, a.beta, a.w_type == 0, 0.f, t + k * T, T, nvec, sp.head);
+          gs.get(k, gk);
+          bs.get(k, bk);
 #pragma unroll
-          for (int i = 0; i < VEC / 2; ++i)
-            set_pair(o, k * VEC / 2 + i, fma2(mul2(v[k * VEC / 2 + i], both(rstd)), gk[i], bk[i]));
+          for (int i = 0; i < VEC / 2; ++i) {
+            const float2 e = add2(pair_of(cur, k * VEC / 2 + i), both(-mean));
+            set_pair(o, i, fma2(mul2(e, both(rstd)), gk[i], bk[i]));
+          }
+          o[0].store(yr + k * T * VEC);
         }
       }
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (t + k * T < nvec) o[k].store(yr + k * T * VEC);
       if (SHIFT && sp.has_single) *y1 = from_f32<TY>(fmaf(v1 * rstd, g1, b1));
       if (t == 0) {
         if (a.mean) a.mean[r] = mean;
@@ -400,10 +459,11 @@ __global__ void __launch_bounds__(MAXT, fwd_per_sm(VEC * K, TEAM) / MAXT) norm_f
 }
 
 template <typename TX, typename TD, int VEC, int K, int TEAM, int MAXT, bool SHIFT>
-__global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_team(NormBwdArgs a) {
-  constexpr int kStages = kBwdStages<TX, TD, VEC * K>;
-  // weights come from L1, and x and dy twice from the ring, for each row
-  constexpr bool kLate = VEC * K > kElems;
+__global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K, MAXT > kMaxTeam) / MAXT) norm_bwd_team(NormBwdArgs a) {
+  // weights come from shared memory, and x and dy twice from the ring, for each row
+  constexpr bool kLate = MAXT > kMaxTeam;
+  constexpr int kStages = ring_stages(MAXT, VEC * K * (int)(sizeof(TX) + sizeof(TD)), 1);
+  constexpr int kAhead = kLate ? kStages : kStages - 1;  // rows fetched before the loop
   extern __shared__ __align__(16) unsigned char smem[];  // the rings of x and dy; at the end the teams' column sums
   __shared__ __align__(16) float stage[128];
   constexpr int TPB = TEAM ? kThreads / (TEAM ? TEAM : 1) : 1;
@@ -429,7 +489,17 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_tea
   dr += sp.head + t * VEC;
   or_ += sp.head + t * VEC;
   float2 g[kLate ? 1 : P], dg[P], db[P];
-  if constexpr (!kLate) weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec, sp.head);
+  const WeightSlots<VEC> gs(smem + kStages * K * VEC * (sizeof(TX) + sizeof(TD)) * T, t, T);
+  if constexpr (!kLate) {
+    weights<TX, VEC, K>(g, a.gamma, a.w_type == 0, 1.f, t, T, nvec, sp.head);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+      float2 w[VEC / 2];
+      weights<TX, VEC, 1>(w, a.gamma, a.w_type == 0, 1.f, t + k * T, T, nvec, sp.head);
+      gs.put(k, w);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < P; ++i) dg[i] = db[i] = both(0.f);
   // of the thread's single element
@@ -464,7 +534,7 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_tea
   int turn = 0, slot = 0;
   if (kAsync)
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * step < a.rows);
+    for (int i = 0; i < kAhead; ++i) fetch(i, first + i * step < a.rows);
   float nm = 0.f, nr = 0.f;  // the next row's statistics
   if (first < a.rows) {
     nm = a.mean[first];
@@ -478,12 +548,12 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_tea
       nr = a.rstd[r + step];
     }
     if (kAsync) {
-      fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
+      if (!kLate) fetch(slot == 0 ? kStages - 1 : slot - 1, r + (kStages - 1) * step < a.rows);
       cp_async_wait<kStages - 1>();
     }
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (on && t + k * T < nvec) {
+      if (!kLate && on && t + k * T < nvec) {
         if constexpr (kAsync) {
           xring.read(slot, k, cx[k]);
           dring.read(slot, k, cd[k]);
@@ -513,12 +583,21 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_tea
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float2 gk[VEC > 1 ? VEC / 2 : 1];
-        if constexpr (kLate) weights<TX, VEC, 1>(gk, a.gamma, a.w_type == 0, 1.f, t + k * T, T, nvec, sp.head);
+        Chunk<TX, VEC> x[1];
+        Chunk<TD, VEC> y[1];
+        if constexpr (kLate) {
+          if (t + k * T >= nvec) break;
+          xring.read(here, k, x[0]);
+          dring.read(here, k, y[0]);
+          gs.get(k, gk);
+        }
 #pragma unroll
         for (int h = 0; h < VEC / 2 || (VEC == 1 && h < 1); ++h) {
           if (VEC == 1 && (k & 1)) continue;  // single elements pair up
           const int i = VEC == 1 ? k / 2 : k * VEC / 2 + h;
-          const float2 xh = mul2(add2(pair_of(cx, i), both(-cm)), both(cr)), dy = pair_of(cd, i);
+          const float2 xv = kLate ? pair_of(x, kLate ? h : 0) : pair_of(cx, i);
+          const float2 dy = kLate ? pair_of(y, kLate ? h : 0) : pair_of(cd, i);
+          const float2 xh = mul2(add2(xv, both(-cm)), both(cr));
           const float2 d = mul2(dy, kLate ? gk[h] : g[kLate ? 0 : i]);
           dg[i] = fma2(dy, xh, dg[i]);
           db[i] = add2(db[i], dy);
@@ -559,7 +638,7 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_tea
           xring.read(here, k, x[0]);
           dring.read(here, k, d[0]);
           float2 gk[VEC / 2];
-          weights<TX, VEC, 1>(gk, a.gamma, a.w_type == 0, 1.f, t + k * T, T, nvec, sp.head);
+          gs.get(k, gk);
 #pragma unroll
           for (int i = 0; i < VEC / 2; ++i) {
             const float2 xh = mul2(add2(pair_of(x, i), both(-cm)), both(cr));
@@ -573,6 +652,7 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K) / MAXT) norm_bwd_tea
         *o1 = from_f32<TX>(cr * (fmaf(vd, g1, -ma) - xh * mb));
       }
     }
+    if (kLate) fetch(here, r + kStages * step < a.rows);  // into the place just read
     if (SHIFT) o1 += o_step;
     or_ += o_step;
   }
@@ -811,10 +891,11 @@ bool shifts_alike(const void* x, long long x_stride, int x_size, const void* o, 
 template <typename TX, typename TY, int VEC, int E, int TEAM, int MAXT, bool SHIFT>
 cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
   constexpr int K = E / VEC;
-  const TeamShape s = team_shape(a.rows, a.N, E, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, fwd_per_sm(E, TEAM), a.num_sms,
+  const TeamShape s = team_shape(a.rows, a.N, E, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, fwd_per_sm(E, TEAM, MAXT > kMaxTeam), a.num_sms,
                                  false, SHIFT);
   using XRing = Ring<TX, VEC, K>;
-  const size_t smem = XRing::kAsync ? (size_t)kFwdStages<TX, E> * XRing::kRow * s.threads : 0;
+  constexpr int stages = ring_stages(MAXT, XRing::kRow, 2);
+  const size_t smem = ((XRing::kAsync ? (size_t)stages * XRing::kRow : 0) + (MAXT > kMaxTeam ? 8 * E : 0)) * s.threads;
   return launch_team(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT, SHIFT>, s, smem, st, a);
 }
 
@@ -828,10 +909,11 @@ cudaError_t fwd_vectors(const NormFwdArgs& a, cudaStream_t st) {
     if (a.N <= 32 * V) return fwd_team<TX, TY, V, V, 32, kThreads, false>(a, st);
   }
   if (a.N <= 32 * kElems) return fwd_team<TX, TY, V, kElems, 32, kThreads, SHIFT>(a, st);
-  if (a.N <= kThreads * kFewElems) return fwd_team<TX, TY, V, kFewElems, 0, kThreads, SHIFT>(a, st);
+  if (a.N <= kFewWidth<TX>) return fwd_team<TX, TY, V, kFewElems, 0, kThreads, SHIFT>(a, st);
   if (a.N <= kThreads * kElems) return fwd_team<TX, TY, V, kElems, 0, kThreads, SHIFT>(a, st);
-  if (a.N <= kMaxTeamWidth) return fwd_team<TX, TY, V, kElems, 0, kMaxTeam, SHIFT>(a, st);
-  return fwd_team<TX, TY, V, kManyElems, 0, kMaxTeam, SHIFT>(a, st);
+  if constexpr (sizeof(TX) == 4 && !SHIFT)
+    if (a.N <= kMaxTeamWidth) return fwd_team<TX, TY, V, kElems, 0, kMaxTeam, SHIFT>(a, st);
+  return fwd_team<TX, TY, V, kElems, 0, kLateTeam, SHIFT>(a, st);
 }
 
 template <typename TX, typename TY>
@@ -857,11 +939,12 @@ template <typename TX, typename TD, int VEC, int E, int TEAM, int MAXT, bool SHI
 cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
   constexpr int K = E / VEC;
   const bool sums = a.dgamma || a.dbeta;
-  const TeamShape s = team_shape(a.rows, a.N, E, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, bwd_per_sm(E), a.num_sms,
+  const TeamShape s = team_shape(a.rows, a.N, E, TEAM ? kThreads / (TEAM ? TEAM : 1) : 0, bwd_per_sm(E, MAXT > kMaxTeam), a.num_sms,
                                  sums, SHIFT);
   using XRing = Ring<TX, VEC, K>;
   using DRing = Ring<TD, VEC, K>;
-  const size_t rings = (size_t)kBwdStages<TX, TD, E> * (XRing::kRow + DRing::kRow) * s.threads;
+  constexpr int stages = ring_stages(MAXT, XRing::kRow + DRing::kRow, 1);
+  const size_t rings = ((size_t)stages * (XRing::kRow + DRing::kRow) + (MAXT > kMaxTeam ? 4 * E : 0)) * s.threads;
   const size_t teams = TEAM && sums ? kThreads / (TEAM ? TEAM : 1) * 2 * a.N * sizeof(float) : 0;
   const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, teams);
   cudaError_t e = launch_team(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT, SHIFT>, s, smem, st, a);
@@ -878,11 +961,11 @@ cudaError_t bwd_vectors(const NormBwdArgs& a, cudaStream_t st) {
     if (a.N <= 32 * V) return bwd_team<TX, TD, V, V, 32, kThreads, false>(a, st);
   }
   if (a.N <= 32 * kElems) return bwd_team<TX, TD, V, kElems, 32, kThreads, SHIFT>(a, st);
-  if (a.N <= kThreads * kFewElems) return bwd_team<TX, TD, V, kFewElems, 0, kThreads, SHIFT>(a, st);
+  if (a.N <= kFewWidth<TX> / (SHIFT && sizeof(TX) == 4 ? 2 : 1)) return bwd_team<TX, TD, V, kFewElems, 0, kThreads, SHIFT>(a, st);
   if (a.N <= kThreads * kElems) return bwd_team<TX, TD, V, kElems, 0, kThreads, SHIFT>(a, st);
-  if (a.N <= kMaxTeamWidth) return bwd_team<TX, TD, V, kElems, 0, kMaxTeam, SHIFT>(a, st);
-  if constexpr (sizeof(TX) == 2) return bwd_team<TX, TD, V, kManyElems, 0, kMaxTeam, SHIFT>(a, st);
-  return cudaErrorInvalidValue;  // (not reached: fp32 rows of that width are wide ones)
+  if constexpr (sizeof(TX) == 2)
+    if (a.N <= kMaxTeamWidth) return bwd_team<TX, TD, V, kElems, 0, kMaxTeam, SHIFT>(a, st);
+  return bwd_team<TX, TD, V, kElems, 0, kLateTeam, SHIFT>(a, st);
 }
 
 template <typename TX, typename TD>
@@ -894,7 +977,7 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
     if (a.dbeta) cudaMemsetAsync(a.dbeta, 0, a.N * sizeof(float), st);
     return cudaGetLastError();
   }
-  if (a.N <= (sizeof(TX) == 2 ? kMaxLateWidth : kMaxTeamWidth)) {
+  if (a.N <= kMaxLateWidth) {
     constexpr int piece = std::min(16, V * ds);
     if (a.N % V == 0 && aligned(a.x, a.x_stride, xs, 16) && aligned(a.dx, a.dx_stride, xs, 16) &&
         aligned(a.dy, a.dy_stride, ds, piece))

@@ -46,7 +46,8 @@ def test_forward_and_backward_over_widths(n, kind):
         check_norm_bwd(got, dy, x, mean, rstd, gamma, f"{rows}x{n}")
 
 
-@pytest.mark.parametrize("rows,n", [(4099, 128), (3001, 96), (2500, 1024), (20011, 40), (700, 4096), (450, 6000)])
+@pytest.mark.parametrize("rows,n", [(4099, 128), (3001, 96), (2500, 1024), (20011, 40), (700, 4096), (450, 6000),
+                                    (1500, 4104), (1400, 8192), (1300, 12288), (900, 16384)])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_many_rows(rows, n, kind):
     dt = DTYPES[kind]
