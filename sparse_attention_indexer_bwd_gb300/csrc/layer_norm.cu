@@ -13,10 +13,10 @@ size_t norm_bwd_workspace(long long rows, int N) {
     // elements each a block has more threads by more than an SM has)
     const int per_sm = N <= 32 * kElems ? bwd_per_sm(kFewElems, false) / kThreads
                                         : std::max(1, bwd_per_sm(kElems, N > kThreads * kElems) * kElems / N);
-    groups = std::min<long long>((rows + 3) / 4 + 8, (long long)kMaxSms * per_sm);
+    groups = std::min<long long>(rows + 8, (long long)kMaxSms * per_sm);
     groups = std::max<long long>(groups, std::min<long long>(kMaxWideGroups, (rows + 31) / 32));
   }
-  return (size_t)std::max<long long>(1, groups) * 2 * N * sizeof(float);
+  return (size_t)std::max<long long>(1, groups) * 2 * part_pitch(N) * sizeof(float);
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t st) {

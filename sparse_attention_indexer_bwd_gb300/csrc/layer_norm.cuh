@@ -17,6 +17,7 @@
 // small kernel.  Rows too wide for a block take several passes.
 #pragma once
 #include <algorithm>
+#include <cmath>
 
 #include "elem.cuh"
 #include "kcommon.cuh"
@@ -252,6 +253,9 @@ struct Split {
     }
   }
 };
+
+// Columns of a group's sums in the workspace: 16-byte pieces.
+__host__ __device__ constexpr int part_pitch(int N) { return (N + 3) / 4 * 4; }
 
 // Two consecutive column sums at an even column: 8 bytes where the row of
 // sums begins on an even one, too.
@@ -659,10 +663,10 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K, MAXT > kMaxTeam) / M
   cp_async_wait_all();
   if (!a.dgamma && !a.dbeta) return;
   griddep_launch_dependents();  // the join's blocks come as these leave
-  // The block's column sums: a group of part[groups][2][N] -- or, where it is
-  // the only block, dgamma and dbeta.
-  float* const out_g = gridDim.x > 1 ? a.part + (long long)blockIdx.x * 2 * a.N : a.dgamma;
-  float* const out_b = gridDim.x > 1 ? out_g + a.N : a.dbeta;
+  // The block's column sums: a group of part[groups][2][part_pitch] -- or,
+  // where it is the only block, dgamma and dbeta.
+  float* const out_g = gridDim.x > 1 ? a.part + (long long)blockIdx.x * 2 * part_pitch(a.N) : a.dgamma;
+  float* const out_b = gridDim.x > 1 ? out_g + part_pitch(a.N) : a.dbeta;
   if constexpr (TEAM == 0) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -710,31 +714,51 @@ __global__ void __launch_bounds__(MAXT, bwd_per_sm(VEC * K, MAXT > kMaxTeam) / M
   }
 }
 
-// dgamma and dbeta from the groups' column sums [groups][2][N]: 32 columns a
-// block, 32 interleaved sums of groups each, joined in order.
-constexpr int kJoinThreads = 1024;
-__global__ void __launch_bounds__(kJoinThreads) norm_bwd_join(const float* part, int groups, int N, float* dgamma,
+// dgamma and dbeta from the groups' column sums [groups][2][part_pitch]: 32
+// columns a block, eight threads by NT / 8 interleaved sums of groups, joined
+// in order.
+template <int NT>
+__global__ void __launch_bounds__(NT) norm_bwd_join(const float* part, int groups, int N, float* dgamma,
                                                               float* dbeta) {
-  __shared__ float s[32][33];
+  constexpr int kSlices = NT / 8;
+  __shared__ float s[kSlices][33];
+  const int pitch = part_pitch(N);
+  const int q = threadIdx.x & 7, w = threadIdx.x >> 3;
+  const int c = blockIdx.x * 32 + 4 * q;
   griddep_wait();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < 2 * N) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < 2 * pitch) {
     const float* p = part + c;
-#pragma unroll 8
-    for (int i = w; i < groups; i += 32) v += p[(long long)i * 2 * N];
+#pragma unroll 4
+    for (int i = w; i < groups; i += kSlices) {
+      const float4 o = *reinterpret_cast<const float4*>(p + (long long)i * 2 * pitch);
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
   }
-  s[w][lane] = v;
+  s[w][4 * q] = v.x;
+  s[w][4 * q + 1] = v.y;
+  s[w][4 * q + 2] = v.z;
+  s[w][4 * q + 3] = v.w;
   __syncthreads();
-  // warp w adds up column w
-  v = warp_sum(s[lane][w]);
-  const int cw = blockIdx.x * 32 + w;
-  if (lane == 0 && cw < 2 * N) {
-    if (cw < N) {
-      if (dgamma) dgamma[cw] = v;
-    } else if (dbeta)
-      dbeta[cw - N] = v;
+  // a column (or several) a warp
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < 1024 / NT; ++e) {
+    const int col = threadIdx.x / 32 + e * (NT / 32), cw = blockIdx.x * 32 + col;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSlices; i += 32) sum += s[i + lane][col];
+    sum = warp_sum(sum);
+    if (lane == 0) {
+      if (cw < N) {
+        if (dgamma) dgamma[cw] = sum;
+      } else if (cw >= pitch && cw - pitch < N) {
+        if (dbeta) dbeta[cw - pitch] = sum;
+      }
+    }
   }
 }
 
@@ -824,8 +848,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_wide_columns(NormBwdArgs a,
       g += sg[i][c];
       b += sb[i][c];
     }
-    a.part[((long long)blockIdx.y * 2) * a.N + n] = g;
-    a.part[((long long)blockIdx.y * 2 + 1) * a.N + n] = b;
+    a.part[((long long)blockIdx.y * 2) * part_pitch(a.N) + n] = g;
+    a.part[((long long)blockIdx.y * 2 + 1) * part_pitch(a.N) + n] = b;
   }
 }
 
@@ -839,18 +863,23 @@ struct TeamShape {
   int threads, blocks;
 };
 
-// All blocks resident: `per_sm` threads an SM.  With column sums fewer blocks
-// where that leaves a team less than four rows: each block's sums are written
-// and read again (4096x128: 12.3 us by 256 blocks, 6.0 by 64), and few rows go
-// to one.  shift: a team's rows lie a multiple of eight rows apart.
+// All blocks resident: `per_sm` threads an SM.  Column sums: each block writes
+// 8 N bytes that the join reads, so of R rows a block takes sqrt(R / 60) at
+// least, or sqrt(R / 30) where its teams share them (64x16384 in bf16: 26.6 us
+// with four rows a block, 17.5 with one; 8192x1024: 16.7 with seven, 13.7 with
+// eleven).  shift: a team's rows lie a multiple of eight rows apart.
 TeamShape team_shape(long long rows, int N, int elems, int teams_per_block, int per_sm, int num_sms, bool sums,
                      bool shift) {
   TeamShape s;
   s.threads = teams_per_block ? kThreads : std::max(32, ((N + elems - 1) / elems + 31) / 32 * 32);
   const int per_block = std::max(1, teams_per_block);
-  const long long teams = sums ? (rows + 3) / 4 : rows;
-  s.blocks = (int)std::min<long long>((teams + per_block - 1) / per_block,
-                                      (long long)std::min(num_sms, kMaxSms) * std::max(1, per_sm / s.threads));
+  const long long resident = (long long)std::min(num_sms, kMaxSms) * std::max(1, per_sm / s.threads);
+  const long long all = (rows + per_block - 1) / per_block;  // blocks of one row a team
+  s.blocks = (int)std::min(all, resident);
+  if (sums) {
+    const long long each = (long long)std::sqrt((double)all / (teams_per_block ? 30 : 60));
+    if (each > 1) s.blocks = (int)std::min<long long>(s.blocks, (all + each - 1) / each);
+  }
   if (shift) {
     // a multiple of eight, or one row a team
     if (s.blocks >= 8)
@@ -931,8 +960,15 @@ cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t st) {
 }
 
 cudaError_t join_sums(const NormBwdArgs& a, int groups, cudaStream_t st) {
-  return launch_ex(norm_bwd_join, (2 * a.N + 31) / 32, kJoinThreads, 0, st, true, (const float*)a.part, groups, a.N,
-                   a.dgamma, a.dbeta);
+  // two groups a thread or more, and 256 threads or more (64x16384: 17.5 us by
+  // 256 threads, 22 by 1024; 8192x1024, 745 groups: 20 and 14)
+  const auto join = [&](auto* kern, int threads) {
+    return launch_ex(kern, (2 * part_pitch(a.N) + 31) / 32, threads, 0, st, true, (const float*)a.part, groups, a.N,
+                     a.dgamma, a.dbeta);
+  };
+  return groups >= 256   ? join(norm_bwd_join<1024>, 1024)
+         : groups >= 128 ? join(norm_bwd_join<512>, 512)
+                         : join(norm_bwd_join<256>, 256);
 }
 
 template <typename TX, typename TD, int VEC, int E, int TEAM, int MAXT, bool SHIFT>
