@@ -304,9 +304,12 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
   const uint32_t my_key = order_bits(my_max) >> 16, top_key = order_bits(most) >> 16;
   const int mine = p.nvec > t ? (p.nvec - t + NT - 1) / NT : 0;  // vectors of this thread
   const int segments = (mine + (1 << bits) - 1) >> bits;
-  // Short rows count their vectors' maxima, which are many enough for them;
-  // a thread's single elements are left out of those.
-  if (bits == 0) {
+  // Short rows count their vectors' maxima where the threads' own are too few
+  // to bound n entries well; a thread's single elements are left out of those.
+  // (2432 rows of 32768 bf16 in 256 threads, 8 alternatives: 47 us by the
+  // vectors' maxima, 43 by the threads'; 128 alternatives: 57 and 60.)
+  const bool fine = bits == 0 && 2 * n >= NT;
+  if (fine) {
     for (int s = 0; s < segments; ++s) {
       const uint32_t d = top_key - sh.segment[s * NT + t];
       if (d < kDistances) atomicAdd(&sh.count_at[d], 1);
@@ -349,7 +352,7 @@ __device__ __forceinline__ int part_top(const Part<T>& p, int lo, int hi, int n,
     uint32_t key = 0;
     for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
       unsigned k = my_key >= (key | bit);
-      if (bits == 0) {
+      if (fine) {
         k = 0;
         for (int s = 0; s < segments; ++s) k += sh.segment[s * NT + t] >= (key | bit);
       }
@@ -793,12 +796,17 @@ cudaError_t launch_threads(RowArgs a, int C, cudaStream_t st) {
 // of its steps, and more blocks of fewer threads overlap them (4864 rows of
 // 2048 bf16, 64 alternatives: 56 us by 256 threads, 32 by 64) -- unless the
 // rows are too few to fill the SMs (8 of 65536: 12.6 us by 128, 9.4 by 256).
+// Log probabilities take 128 threads for up to 64 KB (2432 rows of 32768 bf16:
+// 28.2 us by 256, 26.8 by 128; 8 alternatives: 43 and 37), but not with many
+// alternatives, which as few maxima bound badly (64: 47 and 55); nor do the
+// gradients (2048 rows of 65536 in parts of 32768: 81.5 and 82.9).
 template <typename T, RowOp OP, bool TOP>
 cudaError_t launch_rows_t(const RowArgs& a, int C, cudaStream_t st) {
   const int bytes = part_len(a.V, C) * (int)sizeof(T);
   if (a.rows * C <= 2 * a.num_sms) return launch_threads<T, OP, TOP, 256>(a, C, st);
   if (bytes <= kTinyPart) return launch_threads<T, OP, TOP, 64>(a, C, st);
-  if (bytes <= kSmallPart) return launch_threads<T, OP, TOP, 128>(a, C, st);
+  const bool more = OP == RowOp::kLogpFwd && (!TOP || a.top_n <= 32);
+  if (bytes <= (more ? 2 : 1) * kSmallPart) return launch_threads<T, OP, TOP, 128>(a, C, st);
   return launch_threads<T, OP, TOP, 256>(a, C, st);
 }
 
