@@ -3,7 +3,9 @@
  * model with sparse attention is trained or converted: the layer norm of the
  * indexer's keys (or of hidden states), the log probabilities of a model's
  * logits, and the distillation of a student from a teacher's top logits.
- * Status codes, streams and device status are those of indexer_bwd.h.
+ * Status codes, streams and device status are those of indexer_bwd.h.  Pointers
+ * are to memory of the current device, or managed memory: another device's is
+ * refused.
  *
  * Conventions of this header (where they differ from indexer_bwd.h)
  *  - A matrix is [rows, width] with unit stride along a row and `stride`

@@ -56,8 +56,8 @@ int device_info(DeviceInfo** out) {
 
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Non-null, 16-byte aligned and addressable by the device.
-bool dev_ptr_ok(const void* p) { return ibwd::device_pointer_ok(p, 16); }
+// Non-null, 16-byte aligned and device memory.
+bool dev_ptr_ok(const void* p) { return ibwd::device_pointer_ok(p, 16, -1); }
 
 bool shape_ok(int B, int S_q, int S_k, int H, int D, int L) {
   if (B < 1 || S_q < 1 || S_k < 1 || L < 1) return false;
@@ -198,21 +198,23 @@ int gemm_common(const uint16_t* q, const uint16_t* k, const float* w, const floa
 
 namespace ibwd {
 
-int current_device(int* num_sms) {
+int current_device(int* device, int* num_sms) {
   DeviceInfo* dv = nullptr;
   const int rc = device_info(&dv);
-  if (!rc) *num_sms = dv->num_sms;
+  if (rc) return rc;
+  *device = (int)(dv - g_dev);
+  *num_sms = dv->num_sms;
   return rc;
 }
 
-bool device_pointer_ok(const void* p, size_t align) {
+bool device_pointer_ok(const void* p, size_t align, int device) {
   if (!p || (reinterpret_cast<uintptr_t>(p) & (align - 1))) return false;
   cudaPointerAttributes at{};
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
+  return memory_fits(at.type, at.device, device);
 }
 
 }  // namespace ibwd

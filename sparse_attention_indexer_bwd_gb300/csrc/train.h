@@ -8,10 +8,15 @@
 
 namespace ibwd {
 
-// The current device: IBWD_OK with its SM count, or the status that refuses it.
-int current_device(int* num_sms);
-// Non-null, aligned to `align` bytes and addressable by the device.
-bool device_pointer_ok(const void* p, size_t align);
+// The current device: IBWD_OK with its number and SM count, or the status that refuses it.
+int current_device(int* device, int* num_sms);
+// Whether memory of `type` that lies on device `of` may be given to a kernel
+// of `device`: its own or managed memory; of any device where that is -1.
+inline bool memory_fits(cudaMemoryType type, int of, int device) {
+  return type == cudaMemoryTypeManaged || (type == cudaMemoryTypeDevice && (device < 0 || of == device));
+}
+// Non-null, aligned to `align` bytes and memory that fits.
+bool device_pointer_ok(const void* p, size_t align, int device);
 
 struct NormFwdArgs {
   const void* x;

@@ -27,8 +27,8 @@ struct Pointer {
   bool optional;  // NULL is allowed
 };
 
-// Null and alignment checks, then (with the device) residency; a matrix
-// without rows may be NULL and is never dereferenced.
+// Null and alignment checks, then (with the device) that the memory is the
+// current device's; a matrix without rows may be NULL and is never dereferenced.
 template <int N>
 int pointers_aligned(const Pointer (&list)[N]) {
   for (const Pointer& q : list)
@@ -36,9 +36,9 @@ int pointers_aligned(const Pointer (&list)[N]) {
   return IBWD_OK;
 }
 template <int N>
-int pointers_resident(const Pointer (&list)[N]) {
+int pointers_resident(const Pointer (&list)[N], int device) {
   for (const Pointer& q : list)
-    if (q.p && !ibwd::device_pointer_ok(q.p, q.size)) return IBWD_ERR_INVALID_ARG;
+    if (q.p && !ibwd::device_pointer_ok(q.p, q.size, device)) return IBWD_ERR_INVALID_ARG;
   return IBWD_OK;
 }
 
@@ -71,8 +71,9 @@ int ibwd_layer_norm_fwd(const void* x, int x_type, int64_t x_stride, const void*
   if ((rc = pointers_aligned(list))) return rc;
   if (!in_place_ok(y, y_stride, y_type, x, x_stride, x_type)) return IBWD_ERR_INVALID_ARG;
   ibwd::NormFwdArgs a{};
-  if ((rc = ibwd::current_device(&a.num_sms))) return rc;
-  if ((rc = pointers_resident(list))) return rc;
+  int device;
+  if ((rc = ibwd::current_device(&device, &a.num_sms))) return rc;
+  if ((rc = pointers_resident(list, device))) return rc;
   a.x = x;
   a.gamma = gamma;
   a.beta = beta;
@@ -117,9 +118,10 @@ int ibwd_layer_norm_bwd(const void* dy, int dy_type, int64_t dy_stride, const vo
   const bool sums = dgamma || dbeta;
   if (sums && !natural(workspace, 16)) return IBWD_ERR_WORKSPACE;
   ibwd::NormBwdArgs a{};
-  if ((rc = ibwd::current_device(&a.num_sms))) return rc;
-  if ((rc = pointers_resident(list))) return rc;
-  if (sums && (workspace_bytes < ibwd::norm_bwd_workspace(rows, width) || !ibwd::device_pointer_ok(workspace, 16)))
+  int device;
+  if ((rc = ibwd::current_device(&device, &a.num_sms))) return rc;
+  if ((rc = pointers_resident(list, device))) return rc;
+  if (sums && (workspace_bytes < ibwd::norm_bwd_workspace(rows, width) || !ibwd::device_pointer_ok(workspace, 16, device)))
     return IBWD_ERR_WORKSPACE;
   a.dy = dy;
   a.x = x;
@@ -156,8 +158,9 @@ int ibwd_token_logprobs_fwd(const void* logits, int type, int64_t stride, const 
                           {lse, 4, true},                 {top_ids, 4, true}, {top_logprobs, 4, true}};
   if ((rc = pointers_aligned(list))) return rc;
   ibwd::RowArgs a{};
-  if ((rc = ibwd::current_device(&a.num_sms))) return rc;
-  if ((rc = pointers_resident(list))) return rc;
+  int device;
+  if ((rc = ibwd::current_device(&device, &a.num_sms))) return rc;
+  if ((rc = pointers_resident(list, device))) return rc;
   a.x = logits;
   a.type = type;
   a.x_stride = stride;
@@ -189,8 +192,9 @@ int ibwd_token_logprobs_bwd(const void* logits, int type, int64_t stride, const 
   if ((rc = pointers_aligned(list))) return rc;
   if (!in_place_ok(dlogits, dlogits_stride, type, logits, stride, type)) return IBWD_ERR_INVALID_ARG;
   ibwd::RowArgs a{};
-  if ((rc = ibwd::current_device(&a.num_sms))) return rc;
-  if ((rc = pointers_resident(list))) return rc;
+  int device;
+  if ((rc = ibwd::current_device(&device, &a.num_sms))) return rc;
+  if ((rc = pointers_resident(list, device))) return rc;
   a.x = logits;
   a.type = type;
   a.x_stride = stride;
@@ -230,8 +234,9 @@ int distill_common(ibwd::RowOp op, const void* logits, int type, int64_t stride,
   if ((rc = pointers_aligned(list))) return rc;
   if (grad && !in_place_ok(dlogits, dlogits_stride, type, logits, stride, type)) return IBWD_ERR_INVALID_ARG;
   ibwd::RowArgs a{};
-  if ((rc = ibwd::current_device(&a.num_sms))) return rc;
-  if ((rc = pointers_resident(list))) return rc;
+  int device;
+  if ((rc = ibwd::current_device(&device, &a.num_sms))) return rc;
+  if ((rc = pointers_resident(list, device))) return rc;
   a.x = logits;
   a.type = type;
   a.x_stride = stride;

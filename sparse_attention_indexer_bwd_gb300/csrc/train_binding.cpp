@@ -8,6 +8,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -60,6 +61,9 @@ Matrix matrix(PyObject* o, const char* name) {
   m.code = code_of(t.scalar_type());
   if (!t.is_cuda() || m.code < 0)
     refuse(PyExc_ValueError, name, "expected a CUDA tensor of float32, bfloat16 or float16");
+  // the library runs on the current device, on the stream that is current there
+  if (t.device().index() != c10::cuda::current_device())
+    refuse(PyExc_ValueError, name, "expected a tensor of the current device");
   const auto size = t.sizes();
   const auto stride = t.strides();
   const int64_t dims = t.dim();

@@ -2,9 +2,9 @@
 and distillation from a teacher's top logits, each with its gradient
 (declared in include/indexer_train.h; the functions drop the C names' ibwd_).
 
-A matrix argument is any [..., width] CUDA tensor whose last dimension has
-unit stride and whose leading dimensions step evenly (a slice of columns of a
-contiguous tensor is taken as it is; nothing is copied).  Per-row arguments
+A matrix argument is any [..., width] tensor of the current CUDA device whose
+last dimension has unit stride and whose leading dimensions step evenly (a
+slice of columns of a contiguous tensor is taken as it is; nothing is copied).  Per-row arguments
 and results have the leading dimensions as their shape.  Every call is
 asynchronous on the current stream or on `stream=`; there the results belong
 to that stream, and the arguments are recorded on it.
