@@ -25,7 +25,7 @@
 
 #include <algorithm>
 
-#include "indexer_bwd.h"
+#include "indexer_train.h"
 #include "logits.cuh"
 
 namespace cg = cooperative_groups;
@@ -332,10 +332,9 @@ cudaError_t launch_parts(RowArgs a, int C, cudaStream_t st) {
   const int room = part_len(a.V, C) / kVec<T>;
   const size_t smem = (size_t)room * 16 + a.K * 12;
   const auto kern = distill_grad_kernel<T, NT>;
-  if (smem > 40 * 1024) {  // beyond 48 KB with the static part
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<size_t> limit[64];
+  const cudaError_t e = raise_smem((const void*)kern, (size_t)kRoom<NT> * 16 + IBWD_MAX_KEPT * 12, limit);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   a.ahead = std::max(1, 2 * a.num_sms / C);  // (two or three blocks an SM: 368 and 370 us)
   cfg.gridDim = dim3((unsigned)(a.rows * C));

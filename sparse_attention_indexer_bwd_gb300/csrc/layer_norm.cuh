@@ -890,12 +890,12 @@ TeamShape team_shape(long long rows, int N, int elems, int teams_per_block, int 
   return s;
 }
 
+// most: the shared memory of the kernel's largest launch; limit: of this kernel alone.
 template <typename Args>
-cudaError_t launch_team(void (*kern)(Args), const TeamShape& s, size_t smem, cudaStream_t st, const Args& a) {
-  if (smem > 40 * 1024) {  // beyond 48 KB with the static part
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+cudaError_t launch_team(void (*kern)(Args), const TeamShape& s, size_t smem, size_t most, std::atomic<size_t>* limit,
+                        cudaStream_t st, const Args& a) {
+  const cudaError_t e = raise_smem((const void*)kern, most, limit);
+  if (e != cudaSuccess) return e;
   kern<<<s.blocks, s.threads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -924,8 +924,9 @@ cudaError_t fwd_team(const NormFwdArgs& a, cudaStream_t st) {
                                  false, SHIFT);
   using XRing = Ring<TX, VEC, K>;
   constexpr int stages = ring_stages(MAXT, XRing::kRow, 2);
-  const size_t smem = ((XRing::kAsync ? (size_t)stages * XRing::kRow : 0) + (MAXT > kMaxTeam ? 8 * E : 0)) * s.threads;
-  return launch_team(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT, SHIFT>, s, smem, st, a);
+  constexpr size_t each = (XRing::kAsync ? (size_t)stages * XRing::kRow : 0) + (MAXT > kMaxTeam ? 8 * E : 0);
+  static std::atomic<size_t> limit[64];
+  return launch_team(norm_fwd_team<TX, TY, VEC, K, TEAM, MAXT, SHIFT>, s, each * s.threads, each * MAXT, limit, st, a);
 }
 
 // Rows by 16-byte vectors of x, all aligned or (SHIFT) all of them shifted.
@@ -980,10 +981,15 @@ cudaError_t bwd_team(const NormBwdArgs& a, cudaStream_t st) {
   using XRing = Ring<TX, VEC, K>;
   using DRing = Ring<TD, VEC, K>;
   constexpr int stages = ring_stages(MAXT, XRing::kRow + DRing::kRow, 1);
-  const size_t rings = ((size_t)stages * (XRing::kRow + DRing::kRow) + (MAXT > kMaxTeam ? 4 * E : 0)) * s.threads;
-  const size_t teams = TEAM && sums ? kThreads / (TEAM ? TEAM : 1) * 2 * a.N * sizeof(float) : 0;
-  const size_t smem = std::max(XRing::kAsync && DRing::kAsync ? rings : 0, teams);
-  cudaError_t e = launch_team(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT, SHIFT>, s, smem, st, a);
+  constexpr size_t each = XRing::kAsync && DRing::kAsync
+                              ? (size_t)stages * (XRing::kRow + DRing::kRow) + (MAXT > kMaxTeam ? 4 * E : 0)
+                              : 0;
+  // the teams' column sums: rows of up to TEAM E elements
+  constexpr size_t team_sums = TEAM ? kThreads / (TEAM ? TEAM : 1) * 2 * sizeof(float) : 0;
+  const size_t smem = std::max(each * s.threads, sums ? team_sums * a.N : 0);
+  constexpr size_t most = std::max(each * MAXT, team_sums * TEAM * E);
+  static std::atomic<size_t> limit[64];
+  cudaError_t e = launch_team(norm_bwd_team<TX, TD, VEC, K, TEAM, MAXT, SHIFT>, s, smem, most, limit, st, a);
   if (e == cudaSuccess && sums && s.blocks > 1) e = join_sums(a, s.blocks, st);
   return e;
 }

@@ -2,6 +2,7 @@
 // distillation), shared by train_api.cu and their kernels' files.  Each
 // returns a cudaError_t from its launches.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -17,6 +18,19 @@ inline bool memory_fits(cudaMemoryType type, int of, int device) {
 }
 // Non-null, aligned to `align` bytes and memory that fits.
 bool device_pointer_ok(const void* p, size_t align, int device);
+
+// Lets launches of a kernel have up to `bytes` of dynamic shared memory, once a
+// device: the most that any of its launches has, since the limit is the
+// process's and a smaller one would refuse another thread's launch.  `done`
+// [64]: what each device's limit was raised to.
+inline cudaError_t raise_smem(const void* kern, size_t bytes, std::atomic<size_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire) >= bytes)) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done[dev].store(bytes, std::memory_order_release);
+  return e;
+}
 
 struct NormFwdArgs {
   const void* x;
