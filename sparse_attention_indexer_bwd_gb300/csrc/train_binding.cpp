@@ -230,6 +230,9 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     count(n, 8);
+    // it is written by its address and size
+    if (a[6] == Py_True && a[7] != Py_None && !tensor(a[7], "workspace").is_contiguous())
+      refuse(PyExc_ValueError, "workspace", "expected a contiguous tensor");
     const Matrix x = matrix(a[1], "x"), dy = matrix(a[0], "dy");
     if (dy.t->sizes() != x.t->sizes() || dy.t->device() != x.t->device())
       refuse(PyExc_ValueError, "dy", "expected the shape and device of x");

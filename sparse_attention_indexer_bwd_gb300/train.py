@@ -108,8 +108,8 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, weight_grads: bool =
     dgamma and dbeta float32 (None without `weight_grads`).
 
     dy has x's type or float32 (any type for a float32 x).  `out` may supply
-    dx: x, or dy where the types agree, among it.  `workspace`: device memory
-    of layer_norm_bwd_workspace_size bytes (allocated when not given)."""
+    dx: x, or dy where the types agree, among it.  `workspace`: a contiguous
+    tensor of layer_norm_bwd_workspace_size bytes (allocated when not given)."""
     if stream is not None:
         return _on(stream, layer_norm_bwd, dy, x, mean, rstd, gamma, out, weight_grads, workspace)
     return (_n or _native()).layer_norm_bwd(dy, x, mean, rstd, gamma, out, bool(weight_grads), workspace)
