@@ -13,6 +13,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <climits>
+
 #include "indexer_train.h"
 
 namespace {
@@ -61,14 +64,15 @@ Matrix matrix(PyObject* o, const char* name) {
   m.code = code_of(t.scalar_type());
   if (!t.is_cuda() || m.code < 0)
     refuse(PyExc_ValueError, name, "expected a CUDA tensor of float32, bfloat16 or float16");
-  // the library runs on the current device, on the stream that is current there
-  if (t.device().index() != c10::cuda::current_device())
-    refuse(PyExc_ValueError, name, "expected a tensor of the current device");
   const auto size = t.sizes();
   const auto stride = t.strides();
   const int64_t dims = t.dim();
   if (dims < 2 || size[dims - 1] < 1) refuse(PyExc_ValueError, name, "expected [..., width >= 1]");
   m.width = size[dims - 1];
+  if (m.width > INT_MAX) refuse(PyExc_ValueError, name, "the rows are too wide");
+  // the library runs on the current device, on the stream that is current there
+  if (t.device().index() != c10::cuda::current_device())
+    refuse(PyExc_ValueError, name, "expected a tensor of the current device");
   m.rows = t.numel() / m.width;
   m.step = m.width;
   if (m.rows == 0 || t.is_contiguous()) return m;
@@ -268,12 +272,12 @@ PyObject* token_logprobs_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     count(n, 4);
     const Matrix x = matrix(a[0], "logits");
     const auto tokens = static_cast<const int32_t*>(like_or_null(a[1], "tokens", x.lead(), -1, at::kInt, *x.t));
-    const long top = integer(a[2]);
+    const int top = (int)std::min<long>(std::max<long>(integer(a[2]), INT_MIN), INT_MAX);
     const float tau = number(a[3]);
     Tensor logprob, entropy = vector_out(x.lead(), at::kFloat, *x.t), lse = vector_out(x.lead(), at::kFloat, *x.t);
     if (tokens || a[1] != Py_None) logprob = vector_out(x.lead(), at::kFloat, *x.t);
     Tensor ids, best;
-    if (top > 0) {
+    if (top > 0 && top <= IBWD_MAX_TOP) {  // (the library refuses more)
       auto shape = x.lead().vec();
       shape.push_back(top);
       ids = vector_out(shape, at::kInt, *x.t);
@@ -281,7 +285,7 @@ PyObject* token_logprobs_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     check(ibwd_token_logprobs_fwd(x.t->const_data_ptr(), x.code, x.step, tokens, tau, data<float>(logprob),
                                   data<float>(entropy), data<float>(lse), data<int32_t>(ids), data<float>(best),
-                                  (int)top, x.rows, (int)x.width, stream_of(*x.t)),
+                                  top, x.rows, (int)x.width, stream_of(*x.t)),
           "ibwd_token_logprobs_fwd");
     return tuple_of(std::move(logprob), std::move(entropy), std::move(lse), std::move(ids), std::move(best));
   });
@@ -320,6 +324,7 @@ Kept kept(const Matrix& x, PyObject* ids, PyObject* teacher) {
   const Tensor& t = tensor(ids, "ids");
   if (t.dim() != x.t->dim()) refuse(PyExc_ValueError, "ids", "expected [..., K] beside the logits");
   const int64_t k = t.size(t.dim() - 1);
+  if (k > INT_MAX) refuse(PyExc_ValueError, "ids", "too many slots");
   return {static_cast<const int32_t*>(like(ids, "ids", x.lead(), k, at::kInt, *x.t)),
           static_cast<const float*>(like(teacher, "teacher", x.lead(), k, at::kFloat, *x.t)), k};
 }

@@ -100,6 +100,8 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, out_dtype=None, 
 
 
 def layer_norm_bwd_workspace_size(rows: int, width: int) -> int:
+    if width >= 1 << 31:  # (beyond the C type, and unsupported)
+        return 0
     return int(load().ibwd_layer_norm_bwd_workspace_size(rows, width))
 
 
