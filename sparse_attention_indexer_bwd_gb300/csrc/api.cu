@@ -9,7 +9,8 @@
 namespace {
 
 struct DeviceInfo {
-  bool ready = false;
+  bool known = false;  // supported and num_sms are read
+  bool ready = false;  // the rest is made
   bool supported = false;
   int num_sms = 0;
   unsigned* status = nullptr;  // one device word, allocated once
@@ -23,13 +24,12 @@ struct DeviceInfo {
 std::mutex g_mu;
 DeviceInfo g_dev[64];
 
-// Current device's info; allocates its status word on first use.
-int device_info(DeviceInfo** out) {
+// Current device's capability and SM count (g_mu is held); allocates nothing.
+int device_known(DeviceInfo** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IBWD_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_mu);
   DeviceInfo& d = g_dev[dev];
-  if (!d.ready) {
+  if (!d.known) {
     int major = 0, minor = 0, sms = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
@@ -37,20 +37,29 @@ int device_info(DeviceInfo** out) {
       return IBWD_ERR_CUDA;
     d.supported = (major == 10 && minor == 3);
     d.num_sms = sms;
-    if (d.supported) {
-      if (cudaMalloc(&d.status, sizeof(unsigned)) != cudaSuccess) return IBWD_ERR_CUDA;
-      if (cudaMemset(d.status, 0, sizeof(unsigned)) != cudaSuccess) return IBWD_ERR_CUDA;
-      int least = 0, greatest = 0;
-      if (cudaDeviceGetStreamPriorityRange(&least, &greatest) != cudaSuccess ||
-          cudaStreamCreateWithPriority(&d.side, cudaStreamNonBlocking, greatest) != cudaSuccess ||
-          cudaEventCreateWithFlags(&d.fork, cudaEventDisableTiming) != cudaSuccess ||
-          cudaEventCreateWithFlags(&d.sel, cudaEventDisableTiming) != cudaSuccess)
-        return IBWD_ERR_CUDA;
-    }
-    d.ready = true;
+    d.known = true;
   }
   if (!d.supported) return IBWD_ERR_UNSUPPORTED;
   *out = &d;
+  return IBWD_OK;
+}
+
+// Current device's info; allocates its status word on first use.
+int device_info(DeviceInfo** out) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (const int rc = device_known(out)) return rc;
+  DeviceInfo& d = **out;
+  if (!d.ready) {
+    if (cudaMalloc(&d.status, sizeof(unsigned)) != cudaSuccess) return IBWD_ERR_CUDA;
+    if (cudaMemset(d.status, 0, sizeof(unsigned)) != cudaSuccess) return IBWD_ERR_CUDA;
+    int least = 0, greatest = 0;
+    if (cudaDeviceGetStreamPriorityRange(&least, &greatest) != cudaSuccess ||
+        cudaStreamCreateWithPriority(&d.side, cudaStreamNonBlocking, greatest) != cudaSuccess ||
+        cudaEventCreateWithFlags(&d.fork, cudaEventDisableTiming) != cudaSuccess ||
+        cudaEventCreateWithFlags(&d.sel, cudaEventDisableTiming) != cudaSuccess)
+      return IBWD_ERR_CUDA;
+    d.ready = true;
+  }
   return IBWD_OK;
 }
 
@@ -200,11 +209,11 @@ namespace ibwd {
 
 int current_device(int* device, int* num_sms) {
   DeviceInfo* dv = nullptr;
-  const int rc = device_info(&dv);
-  if (rc) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (const int rc = device_known(&dv)) return rc;
   *device = (int)(dv - g_dev);
   *num_sms = dv->num_sms;
-  return rc;
+  return IBWD_OK;
 }
 
 bool device_pointer_ok(const void* p, size_t align, int device) {
