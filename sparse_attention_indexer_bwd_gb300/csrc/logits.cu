@@ -606,10 +606,17 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
     ref = finite_max(st.m);
     l2s = log2f(st.s);
   } else {
+    // x / T - lse as (x - lse T) / T, lse T in two parts: the difference is
+    // rounded, not its terms, which for a row of the type's lowest value pass
+    // the range, and at T = 1e-3 are some 1e4
     const float lse = a.lse[row];
     empty = lse == NEG_INF;
-    ref = 0.f;
-    l2s = lse * kLog2e;
+    ref = lse * a.temperature;
+    l2s = c * fmaf(lse, a.temperature, -ref);
+    if (isinf(ref)) {
+      if (!isinf(lse)) ref = copysignf(kLargest, ref);
+      l2s = 0.f;
+    }
   }
 
   if (OP == RowOp::kLogpFwd) {
@@ -685,10 +692,11 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
       map_part<NT>(part, dst, [](float2) { return both(0.f); });
       return;
     }
-    // -p (g + b (log p + h))
-    const float2 c2 = both(c), off = both(-l2s), k0 = both(-fmaf(b, h, g)), k1 = both(-b * kLn2);
+    // -p (g + b (log p + h)), log2 p = d - l2s: the part l2s is in the factors
+    const float f = ex2(-l2s), b2 = -b * kLn2;
+    const float2 c2 = both(c), nref = both(-ref), k0 = both(f * -fmaf(b2, l2s, fmaf(b, h, g))), k1 = both(f * b2);
     auto grad = [&](float2 x) {
-      float2 d = fma2(x, c2, off);
+      float2 d = mul2(add2(x, nref), c2);
       const float2 p = make_float2(ex2(d.x), ex2(d.y));
       d.x = fmaxf(d.x, kLeast);
       d.y = fmaxf(d.y, kLeast);

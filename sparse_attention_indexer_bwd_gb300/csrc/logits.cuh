@@ -15,6 +15,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 // An exponent whose power of two is 0, kept finite so that 0 times it is 0.
 constexpr float kLeast = -1e20f;
+constexpr float kLargest = 3.40282347e38f;
 #define NEG_INF (-INFINITY)
 
 struct Stat {

@@ -1,0 +1,30 @@
+"""Values at the ends of the types' ranges, and NaN, where a result still has one value."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_indexer_bwd_gb300 as ibwd
+
+pytestmark = pytest.mark.gpu
+
+INF = math.inf
+SHAPES = [(3, 40000), (320, 1504)]
+
+
+@pytest.mark.parametrize("tau", [1.0, 4.0])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_gradients_of_a_row_of_the_lowest_value(kind, tau):
+    """log p = x / T - lse is 0 in fp32 for every token of such a row: p = 1, by the lse that the forward pass can give."""
+    for rows, v in SHAPES:
+        x = torch.full((rows, v), torch.finfo(kind).min, device="cuda", dtype=kind)
+        tok = torch.full((rows,), 5, device="cuda", dtype=torch.int32)
+        _, entropy, lse, _, _ = ibwd.token_logprobs_fwd(x, tok, temperature=tau)
+        assert torch.isfinite(lse).all()
+        one = torch.ones(rows, device="cuda")
+        dx = ibwd.token_logprobs_bwd(x, tok, lse, entropy, one, None, temperature=tau).float()
+        assert (dx[:, 5] == 0).all() and (dx[:, 6:] + 1 / tau).abs().max() < 0.01
+        ids, teacher = tok[:, None].contiguous(), one[:, None].contiguous()
+        _, lse = ibwd.distill_fwd(x, ids, teacher, temperature=tau)
+        dx = ibwd.distill_bwd(x, ids, teacher, lse, one, temperature=tau).float()
+        assert (dx[:, 5] == 0).all() and (dx[:, 6:] - tau).abs().max() < 0.02 * tau
