@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
       if (t == 0) top.nhot = top.ncand = 0;
     }
     st = row_stat<NT, kEntropy>(own, c, stage, C, most);
-    if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale) {  // uniform over the cluster
+    if (!(st.m > kFloor) || c < kLeastScale || c > kMostScale || (kEntropy && st.m * c > kMostScaledMax)) {
+      // (uniform over the cluster)
       float ignored;
       st = row_stat<NT, kEntropy>(part_stat_any<NT, T, kEntropy>(part, c), c, stage, C, ignored);
     }

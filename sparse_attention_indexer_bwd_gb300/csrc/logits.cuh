@@ -83,9 +83,10 @@ __device__ __noinline__ Stat part_stat_any(const Part<T>& p, float c) {
 // The fast statistic starts from the maximum kFloor, so that x - m is always
 // finite: a logit far below it (a mask) adds 2^-huge = 0.  It does not hold
 // for rows without a logit above kFloor, nor for scales that make kFloor
-// small or huge; those take the careful one.
+// small or huge, nor its moment for a maximum so far above kFloor that the
+// distance passes the range (0 times it is NaN); those take the careful one.
 constexpr float kFloor = -9.9499216e29f;  // 0xF1490000: also a bf16
-constexpr float kLeastScale = 1e-20f, kMostScale = 1e6f;
+constexpr float kLeastScale = 1e-20f, kMostScale = 1e6f, kMostScaledMax = 1e38f;
 
 struct Run {
   float m;

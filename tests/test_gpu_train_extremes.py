@@ -28,3 +28,22 @@ def test_gradients_of_a_row_of_the_lowest_value(kind, tau):
         _, lse = ibwd.distill_fwd(x, ids, teacher, temperature=tau)
         dx = ibwd.distill_bwd(x, ids, teacher, lse, one, temperature=tau).float()
         assert (dx[:, 5] == 0).all() and (dx[:, 6:] - tau).abs().max() < 0.02 * tau
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_a_logit_near_the_largest_value(kind):
+    """Such a token has all of the probability: entropy 0, and a gradient that is 0 beside it."""
+    for rows, v in SHAPES:
+        x = torch.randn((rows, v), device="cuda").to(kind)
+        x[:, 7] = 3e38
+        tok = torch.full((rows,), 7, device="cuda", dtype=torch.int32)
+        logprob, entropy, lse, ids, _ = ibwd.token_logprobs_fwd(x, tok, top_n=2)
+        assert (logprob == 0).all() and (entropy == 0).all() and (lse == x[:, 7].float()).all() and (ids[:, 0] == 7).all()
+        one = torch.ones(rows, device="cuda")
+        assert (ibwd.token_logprobs_bwd(x, tok, lse, entropy, one, one) == 0).all()
+        kept = tok[:, None].contiguous()
+        loss, dx = ibwd.distill_grad(x, kept, one[:, None].contiguous())
+        assert (loss == 0).all() and (dx == 0).all()
+        loss, lse = ibwd.distill_fwd(x, kept, one[:, None].contiguous())
+        assert (loss == 0).all()
+        assert (ibwd.distill_bwd(x, kept, one[:, None].contiguous(), lse, one) == 0).all()
