@@ -303,10 +303,10 @@ __device__ __forceinline__ void team_sums(float (&v)[K], float* stage, int& turn
 }
 
 // s / n given 1 / n, to the last bit but one (a constant row gets its value):
-// the remainder of the product is added back.
+// the remainder of the product is added back (an infinity has none).
 __device__ __forceinline__ float over_n(float s, float n, float inv_n) {
   const float q = s * inv_n;
-  return fmaf(fmaf(-q, n, s), inv_n, q);
+  return isinf(q) ? q : fmaf(fmaf(-q, n, s), inv_n, q);
 }
 
 template <typename TX, typename TY, int VEC, int K, int TEAM, int MAXT, bool SHIFT>

@@ -47,3 +47,15 @@ def test_a_logit_near_the_largest_value(kind):
         loss, lse = ibwd.distill_fwd(x, kept, one[:, None].contiguous())
         assert (loss == 0).all()
         assert (ibwd.distill_bwd(x, kept, one[:, None].contiguous(), lse, one) == 0).all()
+
+
+def test_mean_of_a_row_with_an_infinity():
+    """Sum / N is that infinity, at every width."""
+    for n in (8, 100, 512, 2047, 4096, 9001, 16384, 20000):
+        for kind in (torch.bfloat16, torch.float32):
+            x = torch.randn((12, n), device="cuda").to(kind)
+            x[3, n // 2] = INF
+            x[4, 0] = -INF
+            x[5, 1], x[5, 3] = INF, -INF
+            mean = ibwd.layer_norm_fwd(x)[1]
+            assert mean[3] == INF and mean[4] == -INF and torch.isnan(mean[5]), n
