@@ -116,7 +116,8 @@ IBWD_API int ibwd_token_logprobs_bwd(const void* logits, int type, int64_t strid
  * token kept in several slots has the sum of their probabilities in the
  * gradient, and a row that keeps nothing, or whose logits are all -inf, has
  * loss 0 and gradient 0.  A kept token of p > 0 whose logit is -inf makes the
- * loss +inf (its gradient stays finite).
+ * loss +inf (its gradient stays finite).  A kept slot's NaN is the row's loss
+ * and the kept tokens' gradient; a padding slot's value is not looked at.
  *   logits   type [rows, vocab], stride `stride`
  *   ids int32, teacher fp32 [rows, K]; 1 <= K <= IBWD_MAX_KEPT
  *   loss, lse  fp32 [rows] (lse of logits / T)

@@ -68,7 +68,7 @@ template <int NW>
 __device__ __forceinline__ float max_of_warps(const float* v) {
   float m = v[0];
 #pragma unroll
-  for (int i = 1; i < NW; ++i) m = fmaxf(m, v[i]);
+  for (int i = 1; i < NW; ++i) m = max_nan(m, v[i]);
   return m;
 }
 
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
   float tmax = NEG_INF;
   for (int j = t; j < a.K; j += NT) {
     if (id[j] >= 0 && id[j] < a.V) {
-      tmax = fmaxf(tmax, w[j]);
+      tmax = max_nan(tmax, w[j]);
     } else {
       id[j] = -1;
       w[j] = NEG_INF;

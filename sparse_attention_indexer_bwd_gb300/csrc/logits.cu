@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
       const bool used = OP == RowOp::kDistillBwd ? id >= lo && id < hi : ok;
       const float x = used ? to_f32(xr[id]) : 0.f;
       if (ok)
-        tmax = fmaxf(tmax, kept.p[j]);
+        tmax = max_nan(tmax, kept.p[j]);
       else {
         kept.id[j] = -1;
         kept.p[j] = NEG_INF;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
     // p_j = w_j / z with w_j = 2^((teacher_j - tmax) c)
     float tmax = kept_max[0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) tmax = fmaxf(tmax, kept_max[w]);
+    for (int w = 1; w < NW; ++w) tmax = max_nan(tmax, kept_max[w]);
     const bool zero = tmax == NEG_INF || empty;
     const float tref = finite_max(tmax);
     float z = 0.f, gap = 0.f;

@@ -103,12 +103,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half) {
   asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// max(a, kFloor) that keeps a NaN.
-__device__ __forceinline__ float floor_nan(float a) {
+// max(a, b) that is NaN where either is, always the same one: a positive NaN,
+// which warp_max_f takes as the largest number.
+__device__ __forceinline__ float max_nan(float a, float b) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(kFloor));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+// max(a, kFloor) that keeps a NaN.
+__device__ __forceinline__ float floor_nan(float a) { return max_nan(a, kFloor); }
 
 template <typename T, int N>
 __device__ __forceinline__ float max_of(const uint4 (&r)[N]) {

@@ -59,3 +59,28 @@ def test_mean_of_a_row_with_an_infinity():
             x[5, 1], x[5, 3] = INF, -INF
             mean = ibwd.layer_norm_fwd(x)[1]
             assert mean[3] == INF and mean[4] == -INF and torch.isnan(mean[5]), n
+
+
+def test_nan_among_the_teacher():
+    """A kept slot's NaN is the loss's, whatever the other slots hold; a padding slot's is not."""
+    for rows, v in SHAPES:
+        x = torch.randn((rows, v), device="cuda")
+        ids = torch.arange(4, device="cuda", dtype=torch.int32).expand(rows, 4).contiguous()
+        teacher = torch.zeros((rows, 4), device="cuda")
+        teacher[0] = torch.tensor([math.nan, -INF, -INF, -INF])
+        teacher[1, 2] = math.nan
+        teacher[2] = -math.nan
+        ids[2, 1:] = -1
+        other = [i for i in range(rows) if i > 2]
+        for k in (1, 2, 4):
+            loss = [ibwd.distill_grad(x, ids[:, :k].contiguous(), teacher[:, :k].contiguous())[0],
+                    ibwd.distill_fwd(x, ids[:, :k].contiguous(), teacher[:, :k].contiguous())[0]]
+            for got in loss:
+                assert torch.isnan(got[0]) and torch.isnan(got[1]) == (k > 2) and torch.isnan(got[2])
+                assert torch.isfinite(got[other]).all()
+        teacher[:3] = math.nan
+        ids[:3] = -1
+        ids[:3, 3] = 9
+        teacher[:3, 3] = 0
+        for got in (ibwd.distill_grad(x, ids, teacher)[0], ibwd.distill_fwd(x, ids, teacher)[0]):
+            assert torch.isfinite(got).all()
