@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
         z += w;
         // in natural units: a lowest-value mask stays finite there
         const float x = j == t ? x_first : kept.x[j];
-        if (w > 0.f) gap += w * (d * inv_t - (x - ref) * inv_t);
+        if (w > 0.f) gap += w * kShare * (d * inv_t - (x - ref) * inv_t);
         kept.p[j] = w;
       }
       z = warp_sum(z);
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
         z += kept_z[w];
         gap += kept_gap[w];
       }
-      if (a.loss) a.loss[row] = zero ? 0.f : a.temperature * a.temperature * (gap / z + kLn2 * (l2s - log2f(z)));
+      if (a.loss) a.loss[row] = zero ? 0.f : a.temperature * a.temperature * (gap / (z * kShare) + kLn2 * (l2s - log2f(z)));
       if (OP == RowOp::kDistillFwd) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
     }
   }
