@@ -79,7 +79,8 @@ IBWD_API int ibwd_layer_norm_bwd(const void* dy, int dy_type, int64_t dy_stride,
  * A logit of -inf is a masked token: probability 0, log probability -inf,
  * never among the top (free places at the end hold id -1 and -inf).  A row
  * with every token masked has lse = logprob = -inf and entropy 0.  A NaN or
- * +inf makes the row's lse, logprob, entropy and top log probabilities NaN.
+ * +inf makes the row's lse, logprob, entropy and top log probabilities NaN; the
+ * top ids are those of the largest numbers, never of a NaN.
  *   logits   type [rows, vocab], stride `stride`
  *   tokens   int32 [rows] or NULL; an id outside [0, vocab) is padding: logprob 0
  *   logprob  fp32 [rows], NULL exactly when tokens is

@@ -66,9 +66,11 @@ struct Segments {
     while ((vectors - 1) >> bits >= kSegments) ++bits;
   }
   __device__ __forceinline__ bool single() const { return bits == 0; }
-  // vector number `v` of the thread; a run begins where v is a multiple of its length
+  // vector number `v` of the thread; a run begins where v is a multiple of its
+  // length, from kFloor (the bits of a NaN, where a run holds nothing else, are
+  // no maximum)
   __device__ __forceinline__ void put(int v, float most) {
-    run = (v & ((1 << bits) - 1)) ? fmaxf(run, most) : most;
+    run = fmaxf((v & ((1 << bits) - 1)) ? run : kFloor, most);
     at[(v >> bits) * NT + threadIdx.x] = (uint16_t)(order_bits(run) >> 16);
   }
 };

@@ -99,3 +99,20 @@ def test_several_kept_tokens_that_the_student_masks_by_the_lowest_value(kind):
         want = -low * 63 / 64
         for got in (ibwd.distill_grad(x, ids, teacher)[0], ibwd.distill_fwd(x, ids, teacher)[0]):
             assert ((got.double() - want).abs() <= 1e-5 * want).all()
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+def test_top_of_a_row_with_vectors_of_nan(kind):
+    """NaN is no alternative: the ids are those of the largest other logits."""
+    for rows, v in ((2, 2048), (400, 2048), (2, 20000)):
+        x = torch.full((rows, v), -1000.0, device="cuda")
+        x[:, 11] = 5  # far above all others: the bound is searched for
+        x += torch.arange(v, device="cuda") % 97
+        for y in (x, x - 16, -(torch.arange(v, device="cuda") % 97).expand(rows, v) - 1e-3):  # (the last: all but 0)
+            y = y.to(kind)
+            y[:, v // 4:3 * v // 4] = math.nan
+            for n in (1, 64, 128):
+                got = ibwd.token_logprobs_fwd(y, None, top_n=n)[3]
+                key = torch.where(torch.isnan(y), -INF, y.double())
+                want = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :n]
+                assert torch.equal(got.long(), want), (rows, v, n)
