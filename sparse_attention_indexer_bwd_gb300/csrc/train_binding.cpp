@@ -156,6 +156,16 @@ void check(int status, const char* where) {
   throw Refused{};
 }
 
+// Calls the library without the interpreter lock, since a launch waits while
+// the launch queue is full; a status other than OK becomes an IndexerBwdError.
+template <typename... P, typename... A>
+void call(const char* where, int (*f)(P...), A... a) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int status = f(static_cast<P>(a)...);
+  PyEval_RestoreThread(state);
+  check(status, where);
+}
+
 PyObject* wrap(Tensor t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(t));
@@ -238,9 +248,9 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       mean = vector_out(x.lead(), at::kFloat, *x.t);
       rstd = vector_out(x.lead(), at::kFloat, *x.t);
     }
-    check(ibwd_layer_norm_fwd(x.t->const_data_ptr(), x.code, x.step, pg, pb, wt, y.t.data_ptr(), code, y.step,
-                              data<float>(mean), data<float>(rstd), x.rows, (int)x.width, eps, stream_of(*x.t)),
-          "ibwd_layer_norm_fwd");
+    call("ibwd_layer_norm_fwd", ibwd_layer_norm_fwd, x.t->const_data_ptr(), x.code, x.step, pg, pb, wt,
+         y.t.data_ptr(), code, y.step, data<float>(mean), data<float>(rstd), x.rows, (int)x.width, eps,
+         stream_of(*x.t));
     return tuple_of(std::move(y.t), std::move(mean), std::move(rstd));
   });
 }
@@ -273,10 +283,9 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = work.data_ptr();
       bytes = work.nbytes();
     }
-    check(ibwd_layer_norm_bwd(dy.t->const_data_ptr(), dy.code, dy.step, x.t->const_data_ptr(), x.code, x.step, pg, wt,
-                              mean, rstd, dx.t.data_ptr(), dx.step, data<float>(dgamma), data<float>(dbeta), x.rows,
-                              (int)x.width, ws, bytes, stream_of(*x.t)),
-          "ibwd_layer_norm_bwd");
+    call("ibwd_layer_norm_bwd", ibwd_layer_norm_bwd, dy.t->const_data_ptr(), dy.code, dy.step, x.t->const_data_ptr(),
+         x.code, x.step, pg, wt, mean, rstd, dx.t.data_ptr(), dx.step, data<float>(dgamma), data<float>(dbeta),
+         x.rows, (int)x.width, ws, bytes, stream_of(*x.t));
     return tuple_of(std::move(dx.t), std::move(dgamma), std::move(dbeta));
   });
 }
@@ -298,10 +307,9 @@ PyObject* token_logprobs_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ids = vector_out(shape, at::kInt, *x.t);
       best = vector_out(shape, at::kFloat, *x.t);
     }
-    check(ibwd_token_logprobs_fwd(x.t->const_data_ptr(), x.code, x.step, tokens, tau, data<float>(logprob),
-                                  data<float>(entropy), data<float>(lse), data<int32_t>(ids), data<float>(best),
-                                  top, x.rows, (int)x.width, stream_of(*x.t)),
-          "ibwd_token_logprobs_fwd");
+    call("ibwd_token_logprobs_fwd", ibwd_token_logprobs_fwd, x.t->const_data_ptr(), x.code, x.step, tokens, tau,
+         data<float>(logprob), data<float>(entropy), data<float>(lse), data<int32_t>(ids), data<float>(best), top,
+         x.rows, (int)x.width, stream_of(*x.t));
     return tuple_of(std::move(logprob), std::move(entropy), std::move(lse), std::move(ids), std::move(best));
   });
 }
@@ -323,9 +331,8 @@ PyObject* token_logprobs_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 *dh = rows(5, "dentropy");
     const float tau = number(a[6]);
     Output dx = matrix_out(a[7], x, x.code);
-    check(ibwd_token_logprobs_bwd(x.t->const_data_ptr(), x.code, x.step, tokens, tau, lse, entropy, da, dh,
-                                  dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t)),
-          "ibwd_token_logprobs_bwd");
+    call("ibwd_token_logprobs_bwd", ibwd_token_logprobs_bwd, x.t->const_data_ptr(), x.code, x.step, tokens, tau, lse,
+         entropy, da, dh, dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t));
     return wrap(std::move(dx.t));
   });
 }
@@ -352,9 +359,8 @@ PyObject* distill_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Kept k = kept(x, a[1], a[2]);
     const float tau = number(a[3]);
     Tensor loss = vector_out(x.lead(), at::kFloat, *x.t), lse = vector_out(x.lead(), at::kFloat, *x.t);
-    check(ibwd_distill_fwd(x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k, tau, data<float>(loss),
-                           data<float>(lse), x.rows, (int)x.width, stream_of(*x.t)),
-          "ibwd_distill_fwd");
+    call("ibwd_distill_fwd", ibwd_distill_fwd, x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k, tau,
+         data<float>(loss), data<float>(lse), x.rows, (int)x.width, stream_of(*x.t));
     return tuple_of(std::move(loss), std::move(lse));
   });
 }
@@ -369,9 +375,8 @@ PyObject* distill_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto dloss = static_cast<const float*>(like(a[4], "dloss", x.lead(), -1, at::kFloat, *x.t));
     const float tau = number(a[5]);
     Output dx = matrix_out(a[6], x, x.code);
-    check(ibwd_distill_bwd(x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k, tau, lse, dloss,
-                           dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t)),
-          "ibwd_distill_bwd");
+    call("ibwd_distill_bwd", ibwd_distill_bwd, x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k, tau,
+         lse, dloss, dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t));
     return wrap(std::move(dx.t));
   });
 }
@@ -387,9 +392,8 @@ PyObject* distill_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = number(a[4]), tau = number(a[5]);
     Tensor loss = vector_out(x.lead(), at::kFloat, *x.t);
     Output dx = matrix_out(a[6], x, x.code);
-    check(ibwd_distill_grad(x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k, tau, weight, scale,
-                            data<float>(loss), dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t)),
-          "ibwd_distill_grad");
+    call("ibwd_distill_grad", ibwd_distill_grad, x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k,
+         tau, weight, scale, data<float>(loss), dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t));
     return tuple_of(std::move(loss), std::move(dx.t));
   });
 }

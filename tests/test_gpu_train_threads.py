@@ -1,6 +1,7 @@
 """The training operators called from several host threads."""
 import ctypes
 import threading
+import time
 
 import torch
 import pytest
@@ -69,3 +70,43 @@ def test_sizes_of_one_kernel_in_two_threads():
     for pair in ((norm(5000), norm(8000)), (norm(9000), norm(16000)), (norm_bwd(5000), norm_bwd(16000)),
                  (distill(21000, 8), distill(31000, 900)), (norm(9000), norm(16000), distill(21000, 8), distill(31000, 900))):
         assert run(pair, 3000) == []
+
+
+def test_other_threads_run_while_the_launch_queue_is_full():
+    """A call that waits for room in the launch queue does not hold the interpreter."""
+    x = torch.randn((4, 128), device="cuda")
+    ids = torch.zeros((4, 2), device="cuda", dtype=torch.int32)
+    teacher = torch.zeros((4, 2), device="cuda")
+    y, mean, rstd = ibwd.layer_norm_fwd(x)
+    _, entropy, lse, _, _ = ibwd.token_logprobs_fwd(x, ids[:, 0].contiguous())
+    calls = [lambda: ibwd.layer_norm_fwd(x, out=y), lambda: ibwd.layer_norm_bwd(x, x, mean, rstd, out=y, weight_grads=False),
+             lambda: ibwd.token_logprobs_fwd(x, None), lambda: ibwd.token_logprobs_bwd(x, None, lse, entropy, None, lse, out=y),
+             lambda: ibwd.distill_fwd(x, ids, teacher), lambda: ibwd.distill_bwd(x, ids, teacher, lse, lse, out=y),
+             lambda: ibwd.distill_grad(x, ids, teacher, out=y)]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        stop, gaps = threading.Event(), []
+
+        def tick():
+            last = time.perf_counter()
+            while not stop.is_set():
+                time.sleep(0.001)
+                now = time.perf_counter()
+                gaps.append(now - last)
+                last = now
+
+        t = threading.Thread(target=tick)
+        t.start()
+        begin = time.perf_counter()
+        torch.cuda._sleep(int(0.4 * 1.9e9))  # 0.4 s of GPU time, while more calls come than the queue holds
+        longest = 0.0
+        while time.perf_counter() - begin < 3.0 and longest < 0.1:
+            at = time.perf_counter()
+            call()
+            longest = max(longest, time.perf_counter() - at)
+        stop.set()
+        t.join()
+        torch.cuda.synchronize()
+        assert longest >= 0.1, "the queue was never full"
+        assert max(gaps) < 0.5 * longest
