@@ -122,6 +122,11 @@ int64_t result_step(const Matrix& of) {
 struct Output {
   Tensor t;
   int64_t step;
+  bool given = false;
+  // After it was written: autograd finds an overwritten tensor by its version.
+  void written() const {
+    if (given && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
 };
 Output matrix_out(PyObject* o, const Matrix& of, int code) {
   const auto type = type_of(code);
@@ -136,7 +141,7 @@ Output matrix_out(PyObject* o, const Matrix& of, int code) {
   const Matrix m = matrix(o, "out");
   if (m.t->sizes() != of.t->sizes() || m.code != code || m.t->device() != of.t->device())
     refuse(PyExc_ValueError, "out", "expected the shape and device of the input and the result's type");
-  return {*m.t, m.step};
+  return {*m.t, m.step, true};
 }
 
 Tensor vector_out(at::IntArrayRef shape, at::ScalarType type, const Tensor& of) {
@@ -251,6 +256,7 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call("ibwd_layer_norm_fwd", ibwd_layer_norm_fwd, x.t->const_data_ptr(), x.code, x.step, pg, pb, wt,
          y.t.data_ptr(), code, y.step, data<float>(mean), data<float>(rstd), x.rows, (int)x.width, eps,
          stream_of(*x.t));
+    y.written();
     return tuple_of(std::move(y.t), std::move(mean), std::move(rstd));
   });
 }
@@ -286,6 +292,7 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call("ibwd_layer_norm_bwd", ibwd_layer_norm_bwd, dy.t->const_data_ptr(), dy.code, dy.step, x.t->const_data_ptr(),
          x.code, x.step, pg, wt, mean, rstd, dx.t.data_ptr(), dx.step, data<float>(dgamma), data<float>(dbeta),
          x.rows, (int)x.width, ws, bytes, stream_of(*x.t));
+    dx.written();
     return tuple_of(std::move(dx.t), std::move(dgamma), std::move(dbeta));
   });
 }
@@ -333,6 +340,7 @@ PyObject* token_logprobs_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Output dx = matrix_out(a[7], x, x.code);
     call("ibwd_token_logprobs_bwd", ibwd_token_logprobs_bwd, x.t->const_data_ptr(), x.code, x.step, tokens, tau, lse,
          entropy, da, dh, dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t));
+    dx.written();
     return wrap(std::move(dx.t));
   });
 }
@@ -377,6 +385,7 @@ PyObject* distill_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Output dx = matrix_out(a[6], x, x.code);
     call("ibwd_distill_bwd", ibwd_distill_bwd, x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k, tau,
          lse, dloss, dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t));
+    dx.written();
     return wrap(std::move(dx.t));
   });
 }
@@ -394,6 +403,7 @@ PyObject* distill_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Output dx = matrix_out(a[6], x, x.code);
     call("ibwd_distill_grad", ibwd_distill_grad, x.t->const_data_ptr(), x.code, x.step, k.ids, k.teacher, (int)k.k,
          tau, weight, scale, data<float>(loss), dx.t.data_ptr(), dx.step, x.rows, (int)x.width, stream_of(*x.t));
+    dx.written();
     return tuple_of(std::move(loss), std::move(dx.t));
   });
 }

@@ -4,13 +4,16 @@ and distillation from a teacher's top logits, each with its gradient
 
 A matrix argument is any [..., width] tensor of the current CUDA device whose
 last dimension has unit stride and whose leading dimensions step evenly (a
-slice of columns of a contiguous tensor is taken as it is; nothing is copied).  Per-row arguments
-and results have the leading dimensions as their shape.  Results of a matrix's
-shape are contiguous, but for rows that are no whole 16-byte blocks or do not
-all begin on one: those keep the input's pitch, less whole lines of 128 bytes,
-so that both are read and written by vectors.  Every call is
-asynchronous on the current stream or on `stream=`; there the results belong
-to that stream, and the arguments are recorded on it.
+slice of columns of a contiguous tensor is taken as it is; nothing is copied).
+Per-row arguments and results have the leading dimensions as their shape.
+Results of a matrix's shape are contiguous, but for rows that are no whole
+16-byte blocks or do not all begin on one: those keep the input's pitch, less
+whole lines of 128 bytes, so that both are read and written by vectors.
+
+Every call is asynchronous on the current stream or on `stream=`; there the
+results belong to that stream, and the arguments are recorded on it.  Autograd
+does not track the calls: their gradients are the functions named after them,
+and a tensor written as `out` gets a new version.
 
 The arguments are checked and passed on by _train.so (csrc/train_binding.cpp),
 a native module, because a small call takes less time on the GPU than its

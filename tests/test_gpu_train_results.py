@@ -1,4 +1,4 @@
-"""The tensors that the training operators give back: their layout."""
+"""The tensors that the training operators give back: their layout, and their versions."""
 import pytest
 import torch
 
@@ -60,3 +60,31 @@ def test_keys_of_a_fused_projection():
     _, _, dk = ibwd.indexer_backward(q, k, w, scores, target, idx)
     draw, _, _ = ibwd.layer_norm_bwd(dk, raw, mean, rstd)
     assert draw.is_contiguous() and torch.isfinite(draw).all()
+
+
+def test_a_tensor_written_as_out_has_a_new_version():
+    """What autograd saved before it was overwritten is found out by its version."""
+    x = torch.randn((4, 64), device="cuda")
+    ids = torch.zeros((4, 2), device="cuda", dtype=torch.int32)
+    teacher = torch.zeros((4, 2), device="cuda")
+    _, mean, rstd = ibwd.layer_norm_fwd(x)
+    _, entropy, lse, _, _ = ibwd.token_logprobs_fwd(x)
+    out = torch.empty_like(x)
+    before = x._version
+    for call in (lambda: ibwd.layer_norm_fwd(x, out=out), lambda: ibwd.layer_norm_bwd(x, x, mean, rstd, out=out),
+                 lambda: ibwd.token_logprobs_bwd(x, None, lse, entropy, None, lse, out=out),
+                 lambda: ibwd.distill_bwd(x, ids, teacher, lse, lse, out=out),
+                 lambda: ibwd.distill_grad(x, ids, teacher, out=out)):
+        at = out._version
+        call()
+        assert out._version > at
+    assert x._version == before
+    with torch.inference_mode():
+        y = torch.empty_like(x)
+    ibwd.layer_norm_fwd(x, out=y)
+    a = torch.randn((4, 64), device="cuda", requires_grad=True)
+    b = a * 2
+    loss = (b * b).sum()  # saves b
+    ibwd.layer_norm_fwd(b.detach(), out=b.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
