@@ -61,7 +61,8 @@ IBWD_API size_t ibwd_layer_norm_bwd_workspace_size(int64_t rows, int width);
  *   dy      dy_type [rows, width]: x_type or fp32, or any type for an fp32 x
  *   x, gamma, mean, rstd  as the forward pass took and gave them
  *   dx      x_type [rows, width]; may be x, or dy where that has x_type, itself (same stride)
- *   dgamma, dbeta  fp32 [width], each NULL when not wanted, written (not accumulated)
+ *   dgamma, dbeta  fp32 [width], each NULL when not wanted, written (not accumulated);
+ *           widths of up to 2^30 - 64 with either
  *   workspace  at least ibwd_layer_norm_bwd_workspace_size bytes, 16-byte
  *              aligned (may be NULL when dgamma and dbeta are)
  */

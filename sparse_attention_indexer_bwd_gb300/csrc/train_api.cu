@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMaxWidth = 1 << 30;
 constexpr int64_t kMaxRows = 1LL << 27;
+constexpr int kMaxSumWidth = kMaxWidth - 64;  // with column sums: twice a padded width is an int
 
 size_t size_of(int type) { return type == IBWD_F32 ? 4 : 2; }
 bool type_ok(int type) { return type == IBWD_F32 || type == IBWD_BF16 || type == IBWD_F16; }
@@ -92,7 +93,7 @@ int ibwd_layer_norm_fwd(const void* x, int x_type, int64_t x_stride, const void*
 }
 
 size_t ibwd_layer_norm_bwd_workspace_size(int64_t rows, int width) {
-  if (matrix_status(rows, width, width)) return 0;
+  if (matrix_status(rows, width, width) || width > kMaxSumWidth) return 0;
   return ibwd::norm_bwd_workspace(rows, width);
 }
 
@@ -105,6 +106,8 @@ int ibwd_layer_norm_bwd(const void* dy, int dy_type, int64_t dy_stride, const vo
   if (!rc) rc = matrix_status(rows, width, dy_stride);
   if (!rc) rc = matrix_status(rows, width, dx_stride);
   if (rc) return rc;
+  const bool sums = dgamma || dbeta;
+  if (sums && width > kMaxSumWidth) return IBWD_ERR_UNSUPPORTED;
   if (x_type != IBWD_F32 && dy_type != x_type && dy_type != IBWD_F32) return IBWD_ERR_UNSUPPORTED;
   if (w_type != IBWD_F32 && w_type != x_type) return IBWD_ERR_UNSUPPORTED;
   const bool none = rows == 0;  // only the column sums are written then
@@ -115,7 +118,6 @@ int ibwd_layer_norm_bwd(const void* dy, int dy_type, int64_t dy_stride, const vo
   if (!none && (!in_place_ok(dx, dx_stride, x_type, x, x_stride, x_type) ||
                 !in_place_ok(dx, dx_stride, x_type, dy, dy_stride, dy_type)))
     return IBWD_ERR_INVALID_ARG;
-  const bool sums = dgamma || dbeta;
   if (sums && !natural(workspace, 16)) return IBWD_ERR_WORKSPACE;
   ibwd::NormBwdArgs a{};
   int device;

@@ -1,4 +1,6 @@
 """Sizes beyond the C types are refused before they are cut to them."""
+import ctypes
+
 import pytest
 import torch
 
@@ -19,6 +21,20 @@ def test_wide_rows():
         with pytest.raises(ValueError, match="too wide"):
             call()
     assert ibwd.layer_norm_bwd_workspace_size(4, WIDE) == 0
+
+
+@pytest.mark.parametrize("n,fits", [(1 << 30, False), ((1 << 30) - 20, False), ((1 << 30) - 64, True), (1 << 20, True)])
+def test_widths_whose_column_sums_pass_an_int(n, fits):
+    """Refused before the first kernel, which would write what the second one cannot be launched for."""
+    lib = ibwd.load()
+    p, out = ctypes.c_void_p(4096), ctypes.c_void_p(8192)  # never dereferenced
+
+    def call(sums):
+        return lib.ibwd_layer_norm_bwd(p, 0, n, p, 0, n, None, 0, p, p, out, n, sums, sums, 1, n, p, 0, None)
+
+    assert (call(p) != ibwd.IBWD_ERR_UNSUPPORTED) == fits
+    assert (ibwd.layer_norm_bwd_workspace_size(1, n) > 0) == fits
+    assert call(None) != ibwd.IBWD_ERR_UNSUPPORTED  # without sums any width
 
 
 @pytest.mark.gpu
