@@ -724,9 +724,9 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
         const float d = kept.p[j] - tref;
         const float w = ex2(d * c);
         z += w;
-        // in natural units: a lowest-value mask stays finite there
+        // in the logits' units: a lowest-value mask stays finite there
         const float x = j == t ? x_first : kept.x[j];
-        if (w > 0.f) gap += w * kShare * (d * inv_t - (x - ref) * inv_t);
+        if (w > 0.f) gap += w * kShare * (d - (x - ref));
         kept.p[j] = w;
       }
       z = warp_sum(z);
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
         z += kept_z[w];
         gap += kept_gap[w];
       }
-      if (a.loss) a.loss[row] = zero ? 0.f : a.temperature * a.temperature * (gap / (z * kShare) + kLn2 * (l2s - log2f(z)));
+      if (a.loss) a.loss[row] = zero ? 0.f : loss_of(gap / (z * kShare), l2s - log2f(z), a.temperature);
       if (OP == RowOp::kDistillFwd) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
     }
   }

@@ -206,6 +206,13 @@ __device__ __forceinline__ void rescale(Stat& t, float m, float c) {
   t.m = m;
 }
 
+// T^2 sum p (log p - log q), given gap = sum p (teacher - x) relative to their
+// maxima and l2 = log2 sum 2^.. of the logits less that of the teacher: each
+// part is multiplied by T as often as it has to be and never divided by it.
+__device__ __forceinline__ float loss_of(float gap, float l2, float temperature) {
+  return temperature * (gap + temperature * (kLn2 * l2));
+}
+
 // f of each pair of a vector of logits, rounded to their type.
 template <typename T, typename F>
 __device__ __forceinline__ uint4 map_vector(uint4 r, F f) {

@@ -86,9 +86,10 @@ def test_nan_among_the_teacher():
             assert torch.isfinite(got).all()
 
 
+@pytest.mark.parametrize("tau", [1.0, 0.7, 0.01])
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
-def test_several_kept_tokens_that_the_student_masks_by_the_lowest_value(kind):
-    """The loss is the mean of what they cost, about the largest value itself and no infinity."""
+def test_several_kept_tokens_that_the_student_masks_by_the_lowest_value(kind, tau):
+    """The loss is T times the mean of what they cost, about the largest value itself and no infinity."""
     low = torch.finfo(kind).min
     for rows, v in SHAPES:
         x = torch.randn((rows, v), device="cuda").to(kind)
@@ -96,8 +97,9 @@ def test_several_kept_tokens_that_the_student_masks_by_the_lowest_value(kind):
         x[:, 40:104] = low
         x[:, 48] = 1
         teacher = torch.zeros((rows, 64), device="cuda")
-        want = -low * 63 / 64
-        for got in (ibwd.distill_grad(x, ids, teacher)[0], ibwd.distill_fwd(x, ids, teacher)[0]):
+        want = -low * 63 / 64 * tau
+        for call in (ibwd.distill_grad, ibwd.distill_fwd):
+            got = call(x, ids, teacher, temperature=tau)[0]
             assert ((got.double() - want).abs() <= 1e-5 * want).all()
 
 
