@@ -177,10 +177,10 @@ __device__ __forceinline__ void dk_chunk_u16(char* u, const int* ids, uint32_t t
 // may start before the previous one on the stream completes and must call
 // griddep_wait() before reading what that one writes.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_ex(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t st,
                       bool pdl, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

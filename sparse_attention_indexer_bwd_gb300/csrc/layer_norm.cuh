@@ -896,8 +896,7 @@ cudaError_t launch_team(void (*kern)(Args), const TeamShape& s, size_t smem, siz
                         cudaStream_t st, const Args& a) {
   const cudaError_t e = raise_smem((const void*)kern, most, limit);
   if (e != cudaSuccess) return e;
-  kern<<<s.blocks, s.threads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(kern, s.blocks, s.threads, smem, st, false, a);
 }
 
 bool aligned(const void* p, long long stride, int size, int bytes) {
@@ -956,8 +955,7 @@ cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t st) {
   }
   if (a.N <= 32 * kElems) return fwd_team<TX, TY, 1, kElems, 32, kThreads, false>(a, st);
   if (a.N <= kMaxTeamWidth) return fwd_team<TX, TY, 1, kElems, 0, kMaxTeam, false>(a, st);
-  norm_fwd_wide<TX, TY><<<(int)std::min<long long>(a.rows, 8LL * a.num_sms), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(norm_fwd_wide<TX, TY>, (int)std::min<long long>(a.rows, 8LL * a.num_sms), kThreads, 0, st, false, a);
 }
 
 cudaError_t join_sums(const NormBwdArgs& a, int groups, cudaStream_t st) {
@@ -1015,9 +1013,10 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
   constexpr int V = kVec<TX>, xs = (int)sizeof(TX), ds = (int)sizeof(TD);
   const bool sums = a.dgamma || a.dbeta;
   if (!a.rows) {
-    if (a.dgamma) cudaMemsetAsync(a.dgamma, 0, a.N * sizeof(float), st);
-    if (a.dbeta) cudaMemsetAsync(a.dbeta, 0, a.N * sizeof(float), st);
-    return cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (a.dgamma) e = cudaMemsetAsync(a.dgamma, 0, a.N * sizeof(float), st);
+    if (a.dbeta && e == cudaSuccess) e = cudaMemsetAsync(a.dbeta, 0, a.N * sizeof(float), st);
+    return e;
   }
   if (a.N <= kMaxLateWidth) {
     constexpr int piece = std::min(16, V * ds);
@@ -1033,13 +1032,12 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
   if (sums) {  // before the rows: dx may be x or dy
     const int groups = (int)std::min<long long>(kMaxWideGroups, (a.rows + 31) / 32);
     const int group_rows = (int)((a.rows + groups - 1) / groups);
-    norm_bwd_wide_columns<TX, TD><<<dim3((a.N + 31) / 32, groups), kThreads, 0, st>>>(a, group_rows);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_ex(norm_bwd_wide_columns<TX, TD>, dim3((a.N + 31) / 32, groups), kThreads, 0, st, false, a,
+                              group_rows);
     if (e == cudaSuccess) e = join_sums(a, groups, st);
     if (e != cudaSuccess) return e;
   }
-  norm_bwd_wide<TX, TD><<<(int)std::min<long long>(a.rows, 8LL * a.num_sms), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(norm_bwd_wide<TX, TD>, (int)std::min<long long>(a.rows, 8LL * a.num_sms), kThreads, 0, st, false, a);
 }
 
 }  // namespace

@@ -43,7 +43,13 @@ int pointers_resident(const Pointer (&list)[N], int device) {
   return IBWD_OK;
 }
 
-int done(cudaError_t e) { return e == cudaSuccess ? IBWD_OK : IBWD_ERR_CUDA; }
+// A launch's error is this call's alone: the runtime keeps it for whoever asks
+// for the last one next.
+int done(cudaError_t e) {
+  if (e == cudaSuccess) return IBWD_OK;
+  cudaGetLastError();
+  return IBWD_ERR_CUDA;
+}
 
 bool temperature_ok(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(1.f / t); }
 
