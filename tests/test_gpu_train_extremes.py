@@ -118,3 +118,27 @@ def test_top_of_a_row_with_vectors_of_nan(kind):
                 key = torch.where(torch.isnan(y), -INF, y.double())
                 want = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :n]
                 assert torch.equal(got.long(), want), (rows, v, n)
+
+
+def test_nan_stays_in_its_row():
+    """Every operator over logits, forward and backward: NaN in one row's logits or statistics and in no other's."""
+    for rows, v in SHAPES:
+        x = torch.randn((rows, v), device="cuda")
+        tok = torch.full((rows,), 3, device="cuda", dtype=torch.int32)
+        ids = torch.arange(4, device="cuda", dtype=torch.int32).expand(rows, 4).contiguous()
+        teacher, one = torch.zeros((rows, 4), device="cuda"), torch.ones(rows, device="cuda")
+
+        def all_of(x):
+            logprob, entropy, lse, _, best = ibwd.token_logprobs_fwd(x, tok, top_n=3)
+            loss, lse2 = ibwd.distill_fwd(x, ids, teacher)
+            whole, dw = ibwd.distill_grad(x, ids, teacher)
+            return (logprob, entropy, lse, best, ibwd.token_logprobs_bwd(x, tok, lse, entropy, one, one), loss, lse2,
+                    ibwd.distill_bwd(x, ids, teacher, lse2, one), whole, dw)
+
+        clean = all_of(x)
+        y = x.clone()
+        y[1, v // 3] = math.nan
+        y[1, 5] = -INF
+        for a, b in zip(all_of(y), clean):
+            assert torch.isnan(a[1]).all()
+            assert torch.equal(a[0], b[0]) and torch.equal(a[2:], b[2:])
