@@ -46,7 +46,7 @@ constexpr int kSmallPart = 32 * 1024, kTinyPart = 8 * 1024;
 
 // What the blocks of a cluster tell each other about a row: the part's
 // maximum and sum, and of the kept tokens in it the sums of
-// kShare w (x - m) and of w, with w_j = 2^((teacher_j - max) c).
+// w (x - m) and of w, with w_j = kShare 2^((teacher_j - max) c).
 struct Share {
   float m, s, gap, w;
 };
@@ -75,7 +75,7 @@ __device__ __forceinline__ float max_of_warps(const float* v) {
 // A row as the gradient needs it.
 struct Joined {
   float ref, l2s;  // log2 q_v = (x_v - ref) c - l2s
-  float gap;       // sum kShare w (x - ref) over the kept tokens
+  float gap;       // sum w (x - ref) over the kept tokens
   bool empty;      // every logit is masked
   bool fast;       // the fast statistic holds
 };
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
   const T* part = reinterpret_cast<const T*>(raw);  // from p.vec(0) on
   const uint32_t mine = smem_u32(raw) + t * 16;     // this thread's first vector
   int* id = reinterpret_cast<int*>(raw + (size_t)room * 16);  // kept token, or -1
-  float* w = reinterpret_cast<float*>(id + a.K);              // teacher's value, then 2^((value - max) c)
+  float* w = reinterpret_cast<float*>(id + a.K);              // teacher's value, then kShare 2^((value - max) c)
   float* x = w + a.K;                                         // the student's logit, by the thread that has the slot
 
   // everything the row needs is on its way at once
@@ -172,16 +172,16 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
   tmax = max_of_warps<NW>(sh.tmax);
   const float tref = finite_max(tmax);
   rescale(own, m, c);
-  // of the teacher's slots: z = sum w, sum kShare w (teacher - max); of those
-  // in this part sum kShare w (x - m) and sum w
+  // of the teacher's slots: z = sum w, sum w (teacher - max); of those in this
+  // part sum w (x - m) and sum w
   float z = 0.f, w_log_w = 0.f, gap = 0.f, here = 0.f;
   if (warp * 32 < a.K) {
     for (int j = t; j < a.K; j += NT) {
-      const float d = w[j] - tref, wj = ex2(d * c);
+      const float d = w[j] - tref, wj = ex2(d * c) * kShare;
       w[j] = wj;
       z += wj;
       // in the logits' units: a lowest-value mask stays finite there
-      if (wj > 0.f) w_log_w += wj * kShare * d;
+      if (wj > 0.f) w_log_w += wj * d;
       if (id[j] >= lo && id[j] < hi) {
         const int e = id[j] - lo - p.nhead;
         float xj;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
         else
           xj = to_f32(part[e]);
         x[j] = xj;
-        if (wj > 0.f) gap += wj * kShare * (xj - m);
+        if (wj > 0.f) gap += wj * (xj - m);
         here += wj;
       }
     }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
       Stat o{of[i].m, of[i].s, 0.f};
       rescale(o, top, c);
       s += o.s;
-      if (of[i].w > 0.f) r.gap += of[i].gap + of[i].w * kShare * (of[i].m - r.ref);
+      if (of[i].w > 0.f) r.gap += of[i].gap + of[i].w * (of[i].m - r.ref);
     }
     r.empty = top == NEG_INF && s == 0.f;  // (s is NaN where the row holds a NaN)
     r.l2s = log2f(s);
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
     r = join(sh.careful);
     gap = 0.f;
     for (int j = t; j < a.K; j += NT)
-      if (w[j] > 0.f) gap += w[j] * kShare * (to_f32(xr[id[j]]) - r.ref);
+      if (w[j] > 0.f) gap += w[j] * (to_f32(xr[id[j]]) - r.ref);
     gap = warp_sum(gap);
     if (lane == 0) sh.gap[warp] = gap;
     __syncthreads();
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) distill_grad_kernel(RowArgs a
   const bool zero = tmax == NEG_INF || r.empty;
   if (rank == 0 && t == 0 && a.loss)
     a.loss[row] =
-        zero ? 0.f : loss_of((sum_of<NW>(sh.own) - r.gap) / (z * kShare), r.l2s - log2f(z), a.temperature);
+        zero ? 0.f : loss_of((sum_of<NW>(sh.own) - r.gap) / z, r.l2s - log2f(z / kShare), a.temperature);
   T* dst = static_cast<T*>(a.dx) + row * a.dx_stride + lo;
   if (zero) {
     for (int i = t; i < hi - lo; i += NT) dst[i] = from_f32<T>(0.f);

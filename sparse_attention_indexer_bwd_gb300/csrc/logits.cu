@@ -510,7 +510,7 @@ __device__ __forceinline__ void map_part(const Part<T>& p, T* dst, F f) {
 
 struct Kept {  // [K] each, in shared memory
   int* id;   // kept token, or -1
-  float* p;  // the teacher's value, then 2^((value - max) c)
+  float* p;  // the teacher's value, then kShare 2^((value - max) c)
   float* x;  // the student's logit of it (read by the thread that wrote it)
 };
 
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
   }
 
   if (kDistill) {
-    // p_j = w_j / z with w_j = 2^((teacher_j - tmax) c)
+    // p_j = w_j / z with w_j = kShare 2^((teacher_j - tmax) c)
     float tmax = kept_max[0];
 #pragma unroll
     for (int w = 1; w < NW; ++w) tmax = max_nan(tmax, kept_max[w]);
@@ -722,11 +722,11 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
     if (warp * 32 < a.K) {
       for (int j = t; j < a.K; j += NT) {
         const float d = kept.p[j] - tref;
-        const float w = ex2(d * c);
+        const float w = ex2(d * c) * kShare;
         z += w;
         // in the logits' units: a lowest-value mask stays finite there
         const float x = j == t ? x_first : kept.x[j];
-        if (w > 0.f) gap += w * kShare * (d - (x - ref));
+        if (w > 0.f) gap += w * (d - (x - ref));
         kept.p[j] = w;
       }
       z = warp_sum(z);
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(NT, kBlocks<NT>) rows_kernel(RowArgs a, int C)
         z += kept_z[w];
         gap += kept_gap[w];
       }
-      if (a.loss) a.loss[row] = zero ? 0.f : loss_of(gap / (z * kShare), l2s - log2f(z), a.temperature);
+      if (a.loss) a.loss[row] = zero ? 0.f : loss_of(gap / z, l2s - log2f(z / kShare), a.temperature);
       if (OP == RowOp::kDistillFwd) a.lse[row] = empty ? NEG_INF : ref * inv_t + kLn2 * l2s;
     }
   }

@@ -15,8 +15,8 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 // An exponent whose power of two is 0, kept finite so that 0 times it is 0.
 constexpr float kLeast = -1e20f;
-// What the teacher's weights (1 at most, of 1024 slots) are taken by in the
-// loss's sums, so that several tokens at the type's lowest value stay in range.
+// The largest of a teacher's weights, of which there are 1024 at most, so that
+// the loss's sums over tokens at the type's lowest value stay in range.
 constexpr float kShare = 1.f / 2048.f;
 constexpr float kLargest = 3.40282347e38f;
 #define NEG_INF (-INFINITY)
