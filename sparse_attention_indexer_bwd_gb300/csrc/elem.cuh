@@ -1,5 +1,5 @@
-// Element types of the training operators: loads and stores of 16 bytes (or
-// single elements) with conversion to and from fp32, and block reductions.
+// Element types of the training operators: conversion to and from fp32, single
+// or by pairs, streamed loads and stores of 16 bytes, a warp's sum.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,28 +62,6 @@ __device__ __forceinline__ void unpack(uint4 r, float (&v)[8], __half) {
     v[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[4], float) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-__device__ __forceinline__ uint4 pack(const float (&v)[8], __nv_bfloat16) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 pack(const float (&v)[8], __half) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Streamed 16-byte accesses: no allocation in L1.
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 r;

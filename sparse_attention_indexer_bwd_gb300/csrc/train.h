@@ -55,7 +55,7 @@ struct NormBwdArgs {
   void* dx;
   float* dgamma;  // [N] or nullptr
   float* dbeta;
-  float* part;  // workspace: [groups][2][N] column sums
+  float* part;  // workspace: [groups][2][N rounded up to 4] column sums
   long long rows, dy_stride, x_stride, dx_stride;
   int N, x_type, dy_type, w_type;
   int num_sms;
