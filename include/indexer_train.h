@@ -18,7 +18,8 @@
  *    once, to nearest even, from the fp32 result.
  *  - Outputs must not overlap inputs except where a function says so.
  *  - All results are bitwise reproducible from run to run.
- *  - Nothing is allocated; only ibwd_layer_norm_bwd takes a workspace.
+ *  - Nothing is allocated; only ibwd_layer_norm_bwd and ibwd_qk_norm_rope_bwd
+ *    take a workspace.
  */
 #ifndef INDEXER_TRAIN_H
 #define INDEXER_TRAIN_H
@@ -144,6 +145,75 @@ IBWD_API int ibwd_distill_grad(const void* logits, int type, int64_t stride, con
                                const float* teacher, int K, float temperature, const float* row_weight,
                                float grad_scale, float* loss, void* dlogits, int64_t dlogits_stride, int64_t rows,
                                int vocab, void* stream);
+
+/*
+ * Norm of each head of queries and keys, and their position rotation, in one
+ * pass over both. With x one head of one token (dim elements),
+ *   IBWD_NORM_NONE   z = x
+ *   IBWD_NORM_RMS    z = x * rstd * gamma,  rstd = 1 / sqrt(sum x^2 / dim + eps)
+ *   IBWD_NORM_LAYER  z = (x - mean) * rstd * gamma + beta, as ibwd_layer_norm_fwd
+ * and of the 2 * pairs dimensions from `start` on, pair i with the angle
+ * t = position * freq[i] becomes
+ *   y_a = z_a cos t - z_b sin t,   y_b = z_b cos t + z_a sin t;
+ * the other dimensions are y = z. The angle is taken modulo a turn without
+ * rounding (2^-53 of the frequency and 2^-32 turns), so that far positions
+ * keep their accuracy. All results are of the heads' type.
+ */
+typedef enum { IBWD_NORM_NONE = 0, IBWD_NORM_RMS = 1, IBWD_NORM_LAYER = 2 } ibwd_norm;
+
+#define IBWD_MAX_HEAD_DIM 512
+
+/* The heads of the queries, or of the keys: [tokens, heads, dim] with unit
+ * stride along a head, and `token` and `head` elements from a token and a head
+ * to the next. */
+typedef struct ibwd_heads {
+  const void* x;
+  int64_t x_token, x_head;
+  int heads;          /* 0: absent, nothing else is read */
+  int norm;           /* ibwd_norm */
+  const void* gamma;  /* w_type [dim], NULL for 1; NULL without a norm */
+  const void* beta;   /* w_type [dim], NULL for 0; a layer norm's only, forward */
+  void* y;            /* the result: y, or dx of a backward pass; may be x itself (same strides), or dy of its type */
+  int64_t y_token, y_head;
+  const void* dy;     /* backward: the gradient of y, dy_type */
+  int dy_type;        /* the heads' type or IBWD_F32 */
+  int64_t dy_token, dy_head;
+  float* dgamma;      /* backward: fp32 [dim], written; NULL when not wanted; NULL without a norm */
+  float* dbeta;
+} ibwd_heads;
+
+/* Which dimensions turn by which angles. */
+typedef struct ibwd_rotation {
+  const void* positions;  /* int32 [tokens], or [axes][tokens] with axis_stride elements between axes; NULL: no rotation */
+  int positions_int64;    /* they are int64 */
+  int64_t axis_stride;
+  int axes;               /* 1 for one position a token; up to 8 */
+  const int32_t* axis_of; /* [pairs] the axis of each pair's position; NULL for 0. Of one outside [0, axes) the angle is 0 */
+  const void* freq;       /* [pairs] radians a position, finite; fp32, or fp64 */
+  int freq_f64;
+  int pairs;              /* 2 * pairs <= dim - start */
+  int start;
+  int interleaved;        /* pairs (start + 2i, start + 2i + 1); otherwise (start + i, start + i + pairs) */
+} ibwd_rotation;
+
+/* k or rotation may be NULL. dim <= IBWD_MAX_HEAD_DIM; eps finite, >= 0. */
+IBWD_API int ibwd_qk_norm_rope_fwd(const ibwd_heads* q, const ibwd_heads* k, const ibwd_rotation* rotation, int type,
+                                   int w_type, int64_t tokens, int dim, float eps, void* stream);
+
+/* Bytes of device workspace of the backward pass's dgamma and dbeta; 0 for unsupported arguments. */
+IBWD_API size_t ibwd_qk_norm_rope_bwd_workspace_size(int dim);
+
+/*
+ * Backward pass: with dz = dy turned by -t, xh the normed x without gamma and
+ * beta, and d = dz * gamma,
+ *   dx = rstd * (d - [layer: sum(d) / dim] - xh * sum(d xh) / dim)   (dz without a norm)
+ *   dgamma = sum over tokens and heads of dz * xh,   dbeta = sum of dz
+ * x is the forward pass's input, not read without a norm. workspace: 16-byte
+ * aligned, NULL when no dgamma or dbeta is wanted.
+ */
+IBWD_API int ibwd_qk_norm_rope_bwd(const ibwd_heads* q, const ibwd_heads* k, const ibwd_rotation* rotation, int type,
+                                   int w_type, int64_t tokens, int dim, float eps, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

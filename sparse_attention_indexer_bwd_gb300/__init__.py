@@ -109,6 +109,7 @@ def load() -> ctypes.CDLL:
     lib.indexer_bwd_status_string.argtypes = [i]
     lib.indexer_bwd_status_string.restype = ctypes.c_char_p
     train.declare(lib)
+    cache.declare(lib)
     _lib = lib
     return lib
 
@@ -406,6 +407,12 @@ def indexer_backward(q, k, w, index_score, attn_score, topk_idx=None, grad_scale
 
 from . import train  # noqa: E402  (it uses the helpers above)
 from .train import (distill_bwd, distill_fwd, distill_grad, layer_norm_bwd,  # noqa: E402,F401
-                    layer_norm_bwd_workspace_size, layer_norm_fwd, token_logprobs_bwd, token_logprobs_fwd)
+                    layer_norm_bwd_workspace_size, layer_norm_fwd, qk_norm_rope_bwd, qk_norm_rope_bwd_workspace_size,
+                    qk_norm_rope_fwd, token_logprobs_bwd, token_logprobs_fwd)
 
-EXPORTS += train.EXPORTS
+# ------------------------------------------------------- the 8-bit cache ---
+
+from . import cache  # noqa: E402
+from .cache import (cache_attention, cache_attention_workspace_size, cache_read, cache_write)  # noqa: E402,F401
+
+EXPORTS += train.EXPORTS + cache.EXPORTS

@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libindexer_bwd.so")
 TRAIN = os.path.join(PKG, "_train.so")
-TRAIN_SOURCE = os.path.join(CSRC, "train_binding.cpp")
+TRAIN_SOURCES = [os.path.join(CSRC, name) for name in ("train_binding.cpp", "heads_binding.cpp")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
@@ -30,7 +30,7 @@ def _sources():
 
 
 def _inputs():
-    return _sources() + [TRAIN_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return _sources() + TRAIN_SOURCES + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
@@ -81,9 +81,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
             objs.append(obj)
         compile_, link = _train_flags()
-        train_obj = os.path.join(tmp, "train_binding.o")
-        procs.append((TRAIN_SOURCE, subprocess.Popen(["g++", *compile_, "-c", TRAIN_SOURCE, "-o", train_obj],
-                                                     stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        train_objs = []
+        for src in TRAIN_SOURCES:
+            train_objs.append(os.path.join(tmp, os.path.basename(src) + ".o"))
+            procs.append((src, subprocess.Popen(["g++", *compile_, "-c", src, "-o", train_objs[-1]],
+                                                stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         errs = []
         for src, pr in procs:
             out, _ = pr.communicate()
@@ -98,7 +100,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         shutil.copyfile(tmp_lib, LIB + f".tmp{os.getpid()}")
         os.replace(LIB + f".tmp{os.getpid()}", LIB)
         tmp_train = TRAIN + f".tmp{os.getpid()}"
-        subprocess.check_call(["g++", train_obj, "-o", tmp_train, f"-L{PKG}", "-l:libindexer_bwd.so", *link])
+        subprocess.check_call(["g++", *train_objs, "-o", tmp_train, f"-L{PKG}", "-l:libindexer_bwd.so", *link])
         os.replace(tmp_train, TRAIN)
     return LIB
 

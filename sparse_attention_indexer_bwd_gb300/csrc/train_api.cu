@@ -2,54 +2,14 @@
 // declarations, with their contracts, are in indexer_train.h.
 #include <cmath>
 
-#include "indexer_train.h"
-#include "train.h"
+#include "checks.h"
+#include "head_norm.h"
 
 namespace {
 
-constexpr int kMaxWidth = 1 << 30;
-constexpr int64_t kMaxRows = 1LL << 27;
+using namespace ibwd;
+
 constexpr int kMaxSumWidth = kMaxWidth - 64;  // with column sums: twice a padded width is an int
-
-size_t size_of(int type) { return type == IBWD_F32 ? 4 : 2; }
-bool type_ok(int type) { return type == IBWD_F32 || type == IBWD_BF16 || type == IBWD_F16; }
-bool natural(const void* p, size_t size) { return p && (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
-
-// Shape and stride of a [rows, width] matrix.
-int matrix_status(int64_t rows, int width, int64_t stride) {
-  if (rows < 0 || width < 1 || stride < width) return IBWD_ERR_INVALID_ARG;
-  if (rows > kMaxRows || width > kMaxWidth || (rows > 0 && stride > (1LL << 60) / rows)) return IBWD_ERR_UNSUPPORTED;
-  return IBWD_OK;
-}
-
-struct Pointer {
-  const void* p;
-  size_t size;    // of an element
-  bool optional;  // NULL is allowed
-};
-
-// Null and alignment checks, then (with the device) that the memory is the
-// current device's; a matrix without rows may be NULL and is never dereferenced.
-template <int N>
-int pointers_aligned(const Pointer (&list)[N]) {
-  for (const Pointer& q : list)
-    if (q.p ? !natural(q.p, q.size) : !q.optional) return IBWD_ERR_INVALID_ARG;
-  return IBWD_OK;
-}
-template <int N>
-int pointers_resident(const Pointer (&list)[N], int device) {
-  for (const Pointer& q : list)
-    if (q.p && !ibwd::device_pointer_ok(q.p, q.size, device)) return IBWD_ERR_INVALID_ARG;
-  return IBWD_OK;
-}
-
-// A launch's error is this call's alone: the runtime keeps it for whoever asks
-// for the last one next.
-int done(cudaError_t e) {
-  if (e == cudaSuccess) return IBWD_OK;
-  cudaGetLastError();
-  return IBWD_ERR_CUDA;
-}
 
 bool temperature_ok(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(1.f / t); }
 
@@ -285,6 +245,144 @@ int ibwd_distill_grad(const void* logits, int type, int64_t stride, const int32_
                       int64_t dlogits_stride, int64_t rows, int vocab, void* stream) {
   return distill_common(ibwd::RowOp::kDistillGrad, logits, type, stride, ids, teacher, K, temperature, row_weight,
                         grad_scale, loss, nullptr, dlogits, dlogits_stride, rows, vocab, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool any_sum(const ibwd_heads* q) { return q && q->heads > 0 && (q->dgamma || q->dbeta); }
+
+// Steps between a result's tokens and heads: any that do not overlap, whatever their order.
+bool steps_ok(int64_t token, int64_t head, int64_t tokens, int heads, int dim) {
+  if (token < 0 || head < 0) return false;
+  if (heads > 1 && head < dim) return false;
+  if (tokens > 1 && token < dim) return false;
+  if (tokens <= 1 || heads <= 1) return true;
+  return token >= (heads - 1) * head + dim || head >= (tokens - 1) * token + dim;
+}
+bool steps_far(int64_t token, int64_t head, int64_t tokens, int heads) {
+  constexpr int64_t far = 1LL << 58;
+  return (tokens > 1 && token > far / tokens) || (heads > 1 && head > far / heads);
+}
+
+// Checks one operand; fills `o` and appends its pointers to `list`.
+int head_op(const ibwd_heads& h, bool backward, int type, int w_type, int64_t tokens, int dim, bool none, HeadOp* o,
+            Pointer* list, int* n) {
+  if (h.heads < 0) return IBWD_ERR_INVALID_ARG;
+  if (!h.heads) return IBWD_OK;
+  if (h.heads > 1 << 16) return IBWD_ERR_UNSUPPORTED;
+  if (h.norm != IBWD_NORM_NONE && h.norm != IBWD_NORM_RMS && h.norm != IBWD_NORM_LAYER) return IBWD_ERR_INVALID_ARG;
+  if ((h.gamma && h.norm == IBWD_NORM_NONE) || (h.beta && h.norm != IBWD_NORM_LAYER)) return IBWD_ERR_INVALID_ARG;
+  if (steps_far(h.x_token, h.x_head, tokens, h.heads) || steps_far(h.y_token, h.y_head, tokens, h.heads) ||
+      (backward && steps_far(h.dy_token, h.dy_head, tokens, h.heads)))
+    return IBWD_ERR_UNSUPPORTED;
+  if (h.x_token < 0 || h.x_head < 0 || !steps_ok(h.y_token, h.y_head, tokens, h.heads, dim)) return IBWD_ERR_INVALID_ARG;
+  const size_t size = size_of(type);
+  list[(*n)++] = {h.x, size, none || (backward && h.norm == IBWD_NORM_NONE)};
+  list[(*n)++] = {h.y, size, none};
+  list[(*n)++] = {h.gamma, size_of(w_type), true};
+  if (!backward) list[(*n)++] = {h.beta, size_of(w_type), true};
+  if (h.y == h.x && h.y && (h.y_token != h.x_token || h.y_head != h.x_head)) return IBWD_ERR_INVALID_ARG;
+  if (backward) {
+    if (h.dy_type != type && h.dy_type != IBWD_F32) return type_ok(h.dy_type) ? IBWD_ERR_UNSUPPORTED : IBWD_ERR_INVALID_ARG;
+    // (a gradient that several heads or tokens share may have steps of 0)
+    if (h.dy_token < 0 || h.dy_head < 0) return IBWD_ERR_INVALID_ARG;
+    if ((h.dgamma || h.dbeta) && h.norm == IBWD_NORM_NONE) return IBWD_ERR_INVALID_ARG;
+    list[(*n)++] = {h.dy, size_of(h.dy_type), none};
+    list[(*n)++] = {h.dgamma, 4, true};
+    list[(*n)++] = {h.dbeta, 4, true};
+    if (h.y == h.dy && h.y && (h.y_token != h.dy_token || h.y_head != h.dy_head || h.dy_type != type))
+      return IBWD_ERR_INVALID_ARG;
+    o->dy = h.dy;
+    o->dy_token = h.dy_token;
+    o->dy_head = h.dy_head;
+    o->dy_f32 = h.dy_type == IBWD_F32;
+    o->dgamma = h.dgamma;
+    o->dbeta = h.dbeta;
+  } else {
+    o->beta = h.beta;
+  }
+  o->x = h.x;
+  o->y = h.y;
+  o->gamma = h.gamma;
+  o->x_token = h.x_token;
+  o->x_head = h.x_head;
+  o->y_token = h.y_token;
+  o->y_head = h.y_head;
+  o->heads = h.heads;
+  o->norm = h.norm;
+  return IBWD_OK;
+}
+
+int heads_common(bool backward, const ibwd_heads* q, const ibwd_heads* k, const ibwd_rotation* r, int type, int w_type,
+                 int64_t tokens, int dim, float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !type_ok(type) || !type_ok(w_type) || tokens < 0 || dim < 1) return IBWD_ERR_INVALID_ARG;
+  if (tokens > kMaxRows || dim > IBWD_MAX_HEAD_DIM || (w_type != IBWD_F32 && w_type != type)) return IBWD_ERR_UNSUPPORTED;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return IBWD_ERR_INVALID_ARG;
+  const bool none = tokens == 0;  // only the weights' sums are written then
+  HeadArgs a{};
+  Pointer list[17];
+  int n = 0, rc = head_op(*q, backward, type, w_type, tokens, dim, none, &a.op[0], list, &n);
+  if (!rc && k) rc = head_op(*k, backward, type, w_type, tokens, dim, none, &a.op[1], list, &n);
+  if (rc) return rc;
+  if (r && r->positions) {
+    if (r->pairs < 0 || r->start < 0 || r->axes < 1 || r->pairs > dim / 2 || r->start > dim - 2 * r->pairs)
+      return IBWD_ERR_INVALID_ARG;
+    if (r->axes > 8) return IBWD_ERR_UNSUPPORTED;
+    if (r->axes > 1 && (r->axis_stride < tokens || r->axis_stride > (1LL << 40))) return IBWD_ERR_INVALID_ARG;
+    if (r->pairs) {
+      list[n++] = {r->positions, r->positions_int64 ? 8u : 4u, none};
+      list[n++] = {r->freq, r->freq_f64 ? 8u : 4u, none};
+      list[n++] = {r->axis_of, 4, true};
+    }
+    a.positions = r->positions;
+    a.positions64 = r->positions_int64;
+    a.axis_stride = r->axis_stride;
+    a.axes = r->axes;
+    a.axis_of = r->axis_of;
+    a.freq = r->freq;
+    a.freq64 = r->freq_f64;
+    a.pairs = r->pairs;
+    a.start = r->start;
+    a.interleaved = r->interleaved != 0;
+  }
+  const bool sums = backward && (any_sum(q) || any_sum(k));
+  if (none && !sums) return IBWD_OK;
+  for (int i = 0; i < n; ++i)
+    if (list[i].p ? !natural(list[i].p, list[i].size) : !list[i].optional) return IBWD_ERR_INVALID_ARG;
+  if (sums && !natural(workspace, 16)) return IBWD_ERR_WORKSPACE;
+  int device;
+  if ((rc = current_device(&device, &a.num_sms))) return rc;
+  for (int i = 0; i < n; ++i)
+    if (list[i].p && !device_pointer_ok(list[i].p, list[i].size, device)) return IBWD_ERR_INVALID_ARG;
+  if (sums && (workspace_bytes < ibwd_qk_norm_rope_bwd_workspace_size(dim) || !device_pointer_ok(workspace, 16, device)))
+    return IBWD_ERR_WORKSPACE;
+  a.tokens = tokens;
+  a.D = dim;
+  a.type = type;
+  a.w_type = w_type;
+  a.eps = eps;
+  a.part = static_cast<float*>(workspace);
+  return done(launch_heads(a, backward, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ibwd_qk_norm_rope_fwd(const ibwd_heads* q, const ibwd_heads* k, const ibwd_rotation* rotation, int type, int w_type,
+                          int64_t tokens, int dim, float eps, void* stream) {
+  return heads_common(false, q, k, rotation, type, w_type, tokens, dim, eps, nullptr, 0, stream);
+}
+
+size_t ibwd_qk_norm_rope_bwd_workspace_size(int dim) {
+  return dim < 1 || dim > IBWD_MAX_HEAD_DIM ? 0 : (size_t)kHeadBlocks * 2 * dim * 4;
+}
+
+int ibwd_qk_norm_rope_bwd(const ibwd_heads* q, const ibwd_heads* k, const ibwd_rotation* rotation, int type, int w_type,
+                          int64_t tokens, int dim, float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  return heads_common(true, q, k, rotation, type, w_type, tokens, dim, eps, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

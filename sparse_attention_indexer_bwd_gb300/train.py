@@ -1,6 +1,6 @@
-"""Training operators around the indexer: layer norm, token log probabilities
-and distillation from a teacher's top logits, each with its gradient
-(declared in include/indexer_train.h; the functions drop the C names' ibwd_).
+"""Training operators around the indexer: layer norm, the norm and rotation of
+queries and keys, token log probabilities and distillation from a teacher's
+top logits, each with its gradient (declared in include/indexer_train.h; the functions drop the C names' ibwd_).
 
 A matrix argument is any [..., width] tensor of the current CUDA device whose
 last dimension has unit stride and whose leading dimensions step evenly (a
@@ -42,6 +42,9 @@ EXPORTS = (
     "ibwd_distill_fwd",
     "ibwd_distill_bwd",
     "ibwd_distill_grad",
+    "ibwd_qk_norm_rope_fwd",
+    "ibwd_qk_norm_rope_bwd_workspace_size",
+    "ibwd_qk_norm_rope_bwd",
 )
 
 
@@ -56,9 +59,11 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.ibwd_distill_fwd.argtypes = [p, i, n, p, p, i, f, p, p, n, i, p]
     lib.ibwd_distill_bwd.argtypes = [p, i, n, p, p, i, f, p, p, p, n, n, i, p]
     lib.ibwd_distill_grad.argtypes = [p, i, n, p, p, i, f, p, f, p, p, n, n, i, p]
+    lib.ibwd_qk_norm_rope_fwd.argtypes = [p, p, p, i, i, n, i, f, p]
+    lib.ibwd_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.ibwd_qk_norm_rope_bwd.argtypes = [p, p, p, i, i, n, i, f, p, sz, p]
     for name in EXPORTS:
-        getattr(lib, name).restype = i
-    lib.ibwd_layer_norm_bwd_workspace_size.restype = sz
+        getattr(lib, name).restype = sz if name.endswith("workspace_size") else i
 
 
 _n = None  # the native module
@@ -121,6 +126,61 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, out=None, weight_grads: bool =
     if stream is not None:
         return _on(stream, layer_norm_bwd, dy, x, mean, rstd, gamma, out, weight_grads, workspace)
     return (_n or _native()).layer_norm_bwd(dy, x, mean, rstd, gamma, out, bool(weight_grads), workspace)
+
+
+# -------------------------------------------- norm and rotation of heads ---
+
+_NORM = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _norm(kind):
+    return _NORM.get(kind, -1)
+
+
+def qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, q_norm: str = "rms", k_norm: str = "rms", q_gamma=None, q_beta=None,
+                     k_gamma=None, k_beta=None, eps: float = 1e-6, axes=None, start: int = 0, interleaved: bool = False,
+                     q_out=None, k_out=None, stream=None):
+    """Norm of each head of q [..., heads, dim] and k [..., kv_heads, dim] (or
+    None) and their position rotation, in one pass: (yq, yk), of their type.
+
+    q_norm, k_norm: "rms", "layer" or "none"; the weights are float32 or of the
+    heads' type, all alike, betas a layer norm's only. Heads may lie anywhere in a wider
+    buffer (columns of a fused projection); results are contiguous, or go to q_out
+    and k_out, q and k themselves among them.
+
+    Pair i of the 2 len(inv_freq) dimensions from `start` on turns by position *
+    inv_freq[i] (float32 or float64): dimensions start + i and start + i +
+    len(inv_freq), or with `interleaved` start + 2i and start + 2i + 1.
+    positions: int32 or int64, one a token; with `axes` (int32, the axis of
+    each pair: time, height, width) [axes, ...]. Without positions nothing turns."""
+    if stream is not None:
+        return _on(stream, qk_norm_rope_fwd, q, k, positions, inv_freq, q_norm, k_norm, q_gamma, q_beta, k_gamma, k_beta, eps,
+                   axes, start, interleaved, q_out, k_out)
+    return (_n or _native()).qk_norm_rope_fwd(q, k, positions, inv_freq, axes, start, bool(interleaved), _norm(q_norm),
+                                              _norm(k_norm), q_gamma, q_beta, k_gamma, k_beta, eps, q_out, k_out)
+
+
+def qk_norm_rope_bwd_workspace_size(dim: int) -> int:
+    return int(load().ibwd_qk_norm_rope_bwd_workspace_size(dim)) if 0 < dim < 1 << 31 else 0
+
+
+def qk_norm_rope_bwd(dyq, dyk, q, k, positions=None, inv_freq=None, q_norm: str = "rms", k_norm: str = "rms", q_gamma=None,
+                     k_gamma=None, eps: float = 1e-6, axes=None, start: int = 0, interleaved: bool = False, q_out=None,
+                     k_out=None, weight_grads: bool = True, workspace=None, stream=None):
+    """Backward pass of qk_norm_rope_fwd: (dq, dk, dq_gamma, dq_beta, dk_gamma,
+    dk_beta), dq and dk of the heads' type, the weights' float32, each None where
+    there is none (betas of a layer norm only; none without `weight_grads`).
+
+    q and k are the forward pass's inputs; dyq and dyk have their type or
+    float32 (as indexer_backward gives dq and dk). q_out and k_out may supply dq
+    and dk: q and k, or dyq and dyk where the types agree, among them. `workspace`:
+    a contiguous tensor of qk_norm_rope_bwd_workspace_size bytes (allocated when not given)."""
+    if stream is not None:
+        return _on(stream, qk_norm_rope_bwd, dyq, dyk, q, k, positions, inv_freq, q_norm, k_norm, q_gamma, k_gamma, eps, axes,
+                   start, interleaved, q_out, k_out, weight_grads, workspace)
+    return (_n or _native()).qk_norm_rope_bwd(dyq, dyk, q, k, positions, inv_freq, axes, start, bool(interleaved),
+                                              _norm(q_norm), _norm(k_norm), q_gamma, k_gamma, eps, q_out, k_out,
+                                              bool(weight_grads), workspace)
 
 
 # ------------------------------------------------- token log probabilities ---
