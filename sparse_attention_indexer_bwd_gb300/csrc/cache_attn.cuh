@@ -6,21 +6,22 @@
 // queries are few: each code is read once for all rows (query tokens x heads of
 // the group) of a KV head, 16 or 32 rows a tile.
 //
-// The work is a list of tiles of 64 positions (sequences, KV heads, row tiles,
+// The work is a list of tiles of 128 positions (64 for heads of 256; sequences, KV heads, row tiles,
 // positions, in that order), cut into equal runs, one a block, wherever that
-// falls: lengths are read on the device, so ragged batches and single long
-// sequences fill the SMs alike. A block joins its four warps at the end of an
+// falls, an item of any length counted as one tile more: lengths are read on the
+// device, so ragged batches and single long sequences fill the SMs alike. A block joins its four warps at the end of an
 // item (a row tile of a KV head of a sequence); an item that lies in several
 // blocks is joined by a second kernel, launched programmatically behind the
 // first, in the order of the blocks.
 //
-// A warp works alone on 16 positions of a tile: cp.async brings their codes to
-// its own ring of stages, mma.sync takes them as fp16 (each code, e4m3 or
-// int8, is exact there). The contraction over D runs in an order that gives a
-// lane 16 contiguous codes of a key, the same for the query; values are
-// transposed by ldmatrix in pairs of bytes. tcgen05 would want 128 rows of
-// queries and the codes written to shared memory once more in fp16: with 4 to
-// 32 rows its tiles would be mostly padding.
+// A warp works alone on 32 positions of a tile (16 where heads are 256 wide):
+// cp.async brings their codes to its own ring of stages, mma.sync takes them as
+// fp16 (each code, e4m3 or int8, is exact there). The contraction over D runs in
+// an order that gives a lane 16 contiguous codes of a key, the same for the
+// query; ldmatrix transposes values by bytes. e4m3 keys straight into mma.sync,
+// against a query taken apart into e4m3 terms, took longer (157 us for 356 MB).
+// tcgen05 would want 128 rows of queries and the codes written to shared memory
+// once more in fp16: with 4 to 32 rows its tiles would be mostly padding.
 //
 // Two running maxima a row: m of the logits (base 2) for the sum l, and M of
 // logit + log2(scale of the value's block), which is what the outputs' unit
@@ -40,10 +41,10 @@
 
 namespace ibwd {
 
-constexpr int kTile = 64;          // positions of a block's step
-constexpr int kAttnThreads = 128;  // four warps, 16 positions each
+constexpr int kAttnThreads = 128;  // four warps
 constexpr int kAttnGrid = 456;     // blocks at most, which is what the workspace holds
 constexpr float kUnit = 15.f;      // log2 of the largest weight in fp16
+constexpr int kItemCost = 1;       // what beginning and ending an item costs, in tiles
 
 // What a block leaves for the join: the item that it ends without having begun it.
 struct JoinRecord {
@@ -83,19 +84,6 @@ __device__ __forceinline__ void adjacent(uint32_t w, uint32_t& a, uint32_t& b) {
     b = e4m3_pair(w >> 16);
   }
 }
-// The same: (0, 2) and (1, 3).
-template <bool INT8>
-__device__ __forceinline__ void alternate(uint32_t w, uint32_t& a, uint32_t& b) {
-  if (INT8) {
-    w ^= 0x80808080u;
-    a = int8_pair<0x4240>(w);
-    b = int8_pair<0x4341>(w);
-  } else {
-    w = __byte_perm(w, 0, 0x3120);
-    a = e4m3_pair(w & 0xFFFFu);
-    b = e4m3_pair(w >> 16);
-  }
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -112,6 +100,7 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 // What a maximum is subtracted as: -inf (nothing yet) as 0.
 __device__ __forceinline__ float basis(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float capped(float e) { return e > 126.f ? 126.f : e; }  // (NaN stays)
 
 // Where 16 bytes of a stage's row lie: ldmatrix takes eight rows at once, and a
 // lane's quarter of a key two, without a bank conflict.
@@ -122,14 +111,14 @@ __device__ __forceinline__ int stage_at(int row, int chunk) {
 }
 
 // The items in their order, and the tiles of the current one.
-template <int ROWS, bool SEL>
+template <int ROWS, int TILE, bool SEL>
 struct Cursor {
-  int b;        // sequence; with SEL the query token
+  int b;        // sequence; SEL: the query token
   int head, rt;
   int tile, tiles;
   int row_tiles, rows;  // row tiles and rows of a KV head
   int token;            // first query token
-  int len;              // positions held; with SEL places of the list
+  int len;              // positions held; SEL: places of the list
   int seen;             // positions that the first query token sees
   int seq;
 
@@ -161,7 +150,7 @@ struct Cursor {
       rows = (int)min((long long)n * a.group, 1ll << 30);
     }
     row_tiles = (rows + ROWS - 1) / ROWS;
-    tiles = max(1, (len + kTile - 1) / kTile);
+    tiles = max(1, (len + TILE - 1) / TILE);
   }
   // Moves on by one tile; whether that ends the item.
   __device__ bool step(const CacheAttnArgs& a) {
@@ -180,19 +169,25 @@ struct Cursor {
   }
 };
 
-// Tiles of sequence b.
-template <int ROWS>
+// What sequence b costs, in tiles.
+template <int ROWS, int TILE>
 __device__ __forceinline__ long long tiles_of(const CacheAttnArgs& a, int b) {
   const CacheSeqs& s = a.seqs;
   const long long n = s.begin(b + 1) - s.begin(b);
   if (n <= 0) return 0;
-  return (n * a.group + ROWS - 1) / ROWS * a.heads * max(1, (s.length(b) + kTile - 1) / kTile);
+  return (n * a.group + ROWS - 1) / ROWS * a.heads * (kItemCost + max(1, (s.length(b) + TILE - 1) / TILE));
 }
+
+// Groups of 16 positions in a warp's step.
+constexpr int attn_subs(int D) { return D == 256 ? 1 : 2; }
+// Bytes of a stage: keys, values, a mask, and the scales of each group (SEL: each position).
+constexpr int attn_stage(int D, bool sel) { return attn_subs(D) * (32 * D + (sel ? 128 : 0)) + 32; }
 
 template <int D, int MT, bool INT8, bool SEL, int STAGES, int BLOCKS>
 __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid_constant__ CacheAttnArgs a, bool vec) {
-  constexpr int ROWS = 16 * MT, kRowChunks = D / 16, kBytes = 16 * D;
-  constexpr int kStage = 2 * kBytes + 160;  // keys, values, 16 scales of each, a mask
+  constexpr int ROWS = 16 * MT, kRowChunks = D / 16;
+  constexpr int SUBS = attn_subs(D), STEP = 16 * SUBS, kTile = 4 * STEP;  // positions of a warp's step, of a block's
+  constexpr int kBytes = STEP * D, kStage = attn_stage(D, SEL);
   constexpr int kLane = D / 64;             // 16-byte chunks of a key that a lane takes
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scan[5];
@@ -202,14 +197,14 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   const CacheSeqs& s = a.seqs;
 
   // ------------------------------------------------- this block's run of tiles
-  using Place = Cursor<ROWS, SEL>;
+  using Place = Cursor<ROWS, kTile, SEL>;
   Place c;
   long long total, t0, t1;
   long long blocks;  // that have tiles: at least one each, since the join takes a part of each
   c.head = c.rt = c.tile = 0;
   if (SEL) {
     const int tokens = s.cu ? s.begin(s.batch) : (int)s.tokens;
-    const long long each = (long long)((a.group + ROWS - 1) / ROWS) * a.heads * ((a.kept + kTile - 1) / kTile);
+    const long long each = (long long)((a.group + ROWS - 1) / ROWS) * a.heads * (kItemCost + (a.kept + kTile - 1) / kTile);
     total = each * tokens;
     blocks = min((long long)gridDim.x, total);
     t0 = blockIdx.x < blocks ? total * blockIdx.x / blocks : 0;
@@ -220,7 +215,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     const int per = (s.batch + kAttnThreads - 1) / kAttnThreads;
     const int b0 = min((int)threadIdx.x * per, s.batch), b1 = min(b0 + per, s.batch);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles_of<ROWS>(a, b);
+    for (int b = b0; b < b1; ++b) sum += tiles_of<ROWS, kTile>(a, b);
     long long upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -242,7 +237,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       long long rest = t0 - (upto - sum);
       int b = b0;
       for (; b < b1; ++b) {
-        const long long n = tiles_of<ROWS>(a, b);
+        const long long n = tiles_of<ROWS, kTile>(a, b);
         if (rest < n) break;
         rest -= n;
       }
@@ -262,15 +257,19 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   if (SEL) __syncthreads();
   long long rest = found_rest;
   c.enter(a);
+  const int units = (int)min(t1 - t0, (long long)INT_MAX);
+  int skipped;  // of the first item's own cost
   {
-    const long long per_head = (long long)c.row_tiles * c.tiles;
+    const long long per_tile = c.tiles + kItemCost, per_head = c.row_tiles * per_tile;
     c.head = (int)(rest / per_head);
     rest -= c.head * per_head;
-    c.rt = (int)(rest / c.tiles);
-    c.tile = (int)(rest - (long long)c.rt * c.tiles);
+    c.rt = (int)(rest / per_tile);
+    rest -= c.rt * per_tile;
+    c.tile = (int)max(0ll, rest - kItemCost);
+    skipped = (int)max(0ll, kItemCost - rest);
   }
   if (threadIdx.x == 0) {
-    const long long begin = t0 - c.tile;
+    const long long begin = t0 - rest + kItemCost;  // of the item's first tile
     JoinRecord r{};
     if (c.tile > 0 && begin + c.tiles <= t1) {
       r.valid = 1;
@@ -282,29 +281,49 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     }
     *record = r;
   }
+  if (units <= skipped) {
+    griddep_launch_dependents();
+    return;
+  }
 
   // ------------------------------------------------------------------- loads
   unsigned char* ring = smem + warp * (STAGES * kStage);
-  float* stats = reinterpret_cast<float*>(smem + 4 * STAGES * kStage);  // [4][ROWS][3]
-  float* join = stats + 4 * ROWS * 3 + 16;                              // [2][16][D + 4]
+  uint4* queries = reinterpret_cast<uint4*>(smem + 4 * STAGES * kStage);  // [MT][D / 16][32] fragments
+  float* stats = reinterpret_cast<float*>(queries + MT * D * 2);          // [4][ROWS][3]
   const int P = 1 << s.page_log;
   Place l = c;
-  int left = (int)min(t1 - t0, (long long)INT_MAX);  // tiles to be loaded
-  // what the next load takes: this lane's position (dense: the first one) and its page
-  int at = 0, page = -1, listed = -1;
+  int left = units - skipped;  // of the run, to be loaded
+  // What the next load takes. Dense: its first position, and of each 16 positions their page and its scales; SEL: this
+  // lane's position and its page.
+  int at = 0, page[SUBS], listed = -1;
+  float next_k[SUBS], next_v[SUBS];
+#pragma unroll
+  for (int i = 0; i < SUBS; ++i) {
+    page[i] = -1;
+    next_k[i] = next_v[i] = 0.f;
+  }
   auto look_up = [&]() {
-    at = l.tile * kTile + warp * 16;
+    at = l.tile * kTile + warp * STEP;
     if (SEL) {
-      const int place = at + (lane & 15);
-      listed = left > 0 && place < a.kept ? a.select[(long long)l.token * a.kept + place] : -1;
+      const int place = at + lane;
+      listed = left > 0 && lane < STEP && place < a.kept ? a.select[(long long)l.token * a.kept + place] : -1;
     } else {
-      page = left > 0 && at < l.len ? s.page_at(l.seq, at) : -1;
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i) page[i] = left > 0 && at + 16 * i < l.len ? s.page_at(l.seq, at + 16 * i) : -1;
     }
   };
   auto look_up_page = [&]() {
     if (SEL) {
       at = listed;
-      page = listed >= 0 && listed < l.seen ? s.page_at(l.seq, listed) : -1;
+      page[0] = listed >= 0 && listed < l.seen ? s.page_at(l.seq, listed) : -1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+        if (page[i] >= 0) {
+          const long long block = (long long)page[i] * a.heads + l.head;
+          next_k[i] = a.k_scale[block];
+          next_v[i] = a.v_scale[block];
+        }
     }
   };
   auto load = [&](int stage) {
@@ -312,33 +331,64 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       unsigned char* to = ring + stage * kStage;
       const uint32_t to32 = smem_u32(to);
       unsigned mask;
-      long long row = 0;
-      const long long block = (long long)page * a.heads + l.head;
       if (SEL) {
-        mask = __ballot_sync(0xffffffffu, page >= 0) & 0xFFFFu;
-        if (page >= 0) row = (block << s.page_log) + (at & (P - 1));
-      } else {
-        mask = page < 0 ? 0u : l.len - at >= 16 ? 0xFFFFu : (1u << (l.len - at)) - 1u;
-        if (page >= 0) row = (block << s.page_log) + (at & (P - 1));
-      }
-      if (mask) {
+        mask = __ballot_sync(0xffffffffu, page[0] >= 0);
+        const long long block = (long long)page[0] * a.heads + l.head;
+        const long long row = page[0] >= 0 ? (block << s.page_log) + (at & (P - 1)) : 0;
+        if (mask) {
 #pragma unroll
-        for (int i = 0; i < kRowChunks / 2; ++i) {
-          const int idx = i * 32 + lane, r = idx / kRowChunks, ch = idx % kRowChunks;
-          const long long src = ((SEL ? __shfl_sync(0xffffffffu, row, r) : row + r) * D) + ch * 16;
-          const uint32_t bytes = mask >> r & 1 ? 16u : 0u;
-          const uint32_t dst = to32 + stage_at<D>(r, ch);
-          cp_async16(dst, static_cast<const uint8_t*>(a.k) + (bytes ? src : 0), bytes);
-          cp_async16(dst + kBytes, static_cast<const uint8_t*>(a.v) + (bytes ? src : 0), bytes);
+          for (int i = 0; i < SUBS * kRowChunks / 2; ++i) {
+            const int idx = i * 32 + lane, r = idx / kRowChunks, ch = idx % kRowChunks;
+            const long long src = __shfl_sync(0xffffffffu, row, r) * D + ch * 16;
+            const uint32_t bytes = mask >> r & 1 ? 16u : 0u;
+            const uint32_t dst = to32 + stage_at<D>(r, ch);
+            cp_async16(dst, static_cast<const uint8_t*>(a.k) + src, bytes);
+            cp_async16(dst + kBytes, static_cast<const uint8_t*>(a.v) + src, bytes);
+          }
+          if (lane < STEP) {
+            const bool on = page[0] >= 0;
+            cp_async4(to32 + 2 * kBytes + 32 + 4 * lane, a.k_scale + (on ? block : 0), on ? 4u : 0u);
+            cp_async4(to32 + 2 * kBytes + 32 + 4 * (STEP + lane), a.v_scale + (on ? block : 0), on ? 4u : 0u);
+          }
         }
-        if (lane < 16) {
-          const bool on = mask >> lane & 1;
-          cp_async4(to32 + 2 * kBytes + 4 * lane, a.k_scale + (on ? block : 0), on ? 4u : 0u);
-          cp_async4(to32 + 2 * kBytes + 64 + 4 * lane, a.v_scale + (on ? block : 0), on ? 4u : 0u);
+      } else {
+        const int count = l.len - at;
+        mask = count >= 32 ? 0xFFFFFFFFu : count <= 0 ? 0u : (1u << count) - 1u;
+        if (SUBS == 1) mask &= 0xFFFFu;
+#pragma unroll
+        for (int i = 0; i < SUBS; ++i) {
+          if (page[i] < 0) mask &= ~(0xFFFFu << (16 * i));
+          const unsigned part = mask >> (16 * i) & 0xFFFFu;
+          if (!part) continue;
+          // sixteen rows side by side in the cache
+          const long long row = (((long long)page[i] * a.heads + l.head) << s.page_log) + ((at + 16 * i) & (P - 1));
+          const uint8_t *k = static_cast<const uint8_t*>(a.k) + row * D + lane * 16, *v = static_cast<const uint8_t*>(a.v) + row * D + lane * 16;
+          const bool all = part == 0xFFFFu;
+#pragma unroll
+          for (int n = 0; n < kRowChunks / 2; ++n) {
+            const int r = (n * 32 + lane) / kRowChunks;
+            const uint32_t dst = to32 + stage_at<D>(16 * i + r, (n * 32 + lane) % kRowChunks);
+            const uint32_t bytes = all || (part >> r & 1) ? 16u : 0u;
+            cp_async16(dst, k + n * 512, bytes);
+            cp_async16(dst + kBytes, v + n * 512, bytes);
+          }
         }
       }
-      if (lane == 0) *reinterpret_cast<unsigned*>(to + 2 * kBytes + 128) = mask;
-      if (--left > 0) l.step(a);
+      if (lane == 0) {
+        *reinterpret_cast<unsigned*>(to + 2 * kBytes) = mask;
+        if (!SEL) *reinterpret_cast<float4*>(to + 2 * kBytes + 16) = make_float4(next_k[0], next_v[0], next_k[SUBS - 1], next_v[SUBS - 1]);
+      }
+      if (--left > 0 && l.tile + 1 == l.tiles) left -= kItemCost;
+      if (left > 0 && l.step(a) && warp == 0) {
+        // the next item's queries on their way to L2
+        const int r = l.rt * ROWS + lane, i = r / a.group;
+        if (lane < ROWS && r < l.rows) {
+          const uint16_t* q = static_cast<const uint16_t*>(a.q) + (long long)(l.token + i) * a.q_token +
+                              (long long)(l.head * a.group + r - i * a.group) * a.q_head;
+#pragma unroll
+          for (int n = 0; n < D; n += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + n));
+        }
+      }
     }
     cp_async_commit();
   };
@@ -352,68 +402,82 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   }
 
   // ------------------------------------------------------------------- items
-  uint32_t q[MT][D / 16][4];
   float qs[MT][2], m[MT][2], big[MT][2], sum[MT][2];
   int lim[MT][2], lim_min = 0;
   float o[MT][D / 8][4];
   bool begun = c.tile == 0;  // the segment at hand holds its item's first tile
 
+  // The item's queries as fragments in shared memory, the same for all warps: each writes a quarter.
   auto enter_item = [&]() {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      uint4 raw[2][kLane][2];
+      float down[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int r = c.rt * ROWS + mt * 16 + hf * 8 + (lane >> 2);
         const bool on = r < c.rows;
         const int i = r / a.group;
         lim[mt][hf] = SEL ? 0 : on ? c.seen + i : -1;
-        const long long from = on ? (long long)(c.token + i) * a.q_token + (long long)(c.head * a.group + r - i * a.group) * a.q_head : 0;
-        const uint16_t* p = static_cast<const uint16_t*>(a.q) + from;
-        float amax = 0.f;
-        uint4 raw[kLane][2];
+        const uint16_t* p = static_cast<const uint16_t*>(a.q) +
+                            (on ? (long long)(c.token + i) * a.q_token + (long long)(c.head * a.group + r - i * a.group) * a.q_head : 0);
 #pragma unroll
         for (int k = 0; k < kLane; ++k) {
           const int ch = D == 64 ? j : (k >> 1) * 8 + 2 * j + (k & 1);
-          raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
+          raw[hf][k][0] = raw[hf][k][1] = make_uint4(0, 0, 0, 0);
           if (on) {
             if (vec) {
-              raw[k][0] = *reinterpret_cast<const uint4*>(p + ch * 16);
-              raw[k][1] = *reinterpret_cast<const uint4*>(p + ch * 16 + 8);
+              raw[hf][k][0] = *reinterpret_cast<const uint4*>(p + ch * 16);
+              raw[hf][k][1] = *reinterpret_cast<const uint4*>(p + ch * 16 + 8);
             } else {
               uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[e] = (uint32_t)p[ch * 16 + 2 * e] | (uint32_t)p[ch * 16 + 2 * e + 1] << 16;
-              raw[k][0] = make_uint4(w[0], w[1], w[2], w[3]);
-              raw[k][1] = make_uint4(w[4], w[5], w[6], w[7]);
+              raw[hf][k][0] = make_uint4(w[0], w[1], w[2], w[3]);
+              raw[hf][k][1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
-          const uint32_t w[8] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w,
-                                 raw[k][1].x, raw[k][1].y, raw[k][1].z, raw[k][1].w};
+        }
+      }
+      auto two = [&](uint32_t w) { return a.type == IBWD_BF16 ? unpack2(w, __nv_bfloat16{}) : unpack2(w, __half{}); };
+      auto word = [&](int hf, int k, int e) {
+        const uint4 x = raw[hf][k][e >> 2];
+        return (e & 3) == 0 ? x.x : (e & 3) == 1 ? x.y : (e & 3) == 2 ? x.z : x.w;
+      };
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < kLane; ++k)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 f = a.type == IBWD_BF16 ? unpack2(w[e], __nv_bfloat16{}) : unpack2(w[e], __half{});
+            const float2 f = two(word(hf, k, e));
             amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-        }
         amax = quad_max(amax);
-        // the row in units of 2^e with its largest entry in [1, 2), and 2^-e; an infinity leaves its finite neighbours finite
-        const int e = amax == INFINITY ? 113 : min((int)(__float_as_uint(amax) >> 23) - 127, 126);
-        const float down = amax == 0.f || e < -126 ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
-        qs[mt][hf] = (amax == 0.f || e < -126 ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23)) * a.scale_log2;
-#pragma unroll
-        for (int k = 0; k < kLane; ++k) {
-          const uint32_t w[8] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w,
-                                 raw[k][1].x, raw[k][1].y, raw[k][1].z, raw[k][1].w};
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float2 f = a.type == IBWD_BF16 ? unpack2(w[g], __nv_bfloat16{}) : unpack2(w[g], __half{});
-            // word g / 2 of the chunk is a step of 16 dimensions: its first pair, then its second
-            q[mt][k * 4 + g / 2][(g & 1) * 2 + hf] = half_pair(f.x * down, f.y * down);
-          }
-        }
+        // The row in units of 2^e with its largest entry in [1, 2). An infinite query gives NaN.
+        const int e = min((int)(__float_as_uint(amax) >> 23) - 127, 126);
+        const bool none = amax == 0.f || e < -126;
+        down[hf] = none ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
+        qs[mt][hf] = (none ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23)) * a.scale_log2;
+        if (amax == INFINITY) qs[mt][hf] = __uint_as_float(0x7FC00000u);
         m[mt][hf] = big[mt][hf] = -INFINITY;
         sum[mt][hf] = 0.f;
       }
+#pragma unroll
+      for (int k = 0; k < kLane; ++k)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (warp == g) {  // words 2 g, 2 g + 1 of a chunk are a step of 16 dimensions
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = two(word(e & 1, k, 2 * g + (e >> 1)));
+              w[e] = half_pair(f.x * down[e & 1], f.y * down[e & 1]);
+            }
+            queries[(mt * (D / 16) + k * 4 + g) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+    }
     lim_min = c.seen + c.rt * ROWS / a.group;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -421,10 +485,13 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+    __syncthreads();
   };
 
-  // Joins the warps' results of the segment: to `out` where it is the whole item, else to the block's parts.
-  auto leave_item = [&](bool whole) {
+  // Joins the warps' results of the segment: to `out` where it is the whole item, else to the block's parts. They meet in
+  // the stages that were just used, which nothing is loaded into before the last barrier.
+  auto leave_item = [&](bool whole, int stage) {
+    constexpr int DC = D > 128 ? 128 : D;  // dimensions at a time: 16 rows of them in fp32 fill a stage
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -437,166 +504,188 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           p[2] = big[mt][hf];
         }
       }
-    __syncthreads();
-    float tm[MT][2], tl[MT][2], tb[MT][2];
+    // 8-byte units of a row, turned by the row so that eight rows lie in different banks
+    auto at = [&](int w, int row, int unit) {
+      return reinterpret_cast<float*>(smem + (w * STAGES + stage) * kStage + row * DC * 4 + ((unit ^ (4 * (row & 7))) << 3));
+    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float* p = stats + (mt * 16 + hf * 8 + (lane >> 2)) * 3;
-        float mm = -INFINITY, bb = -INFINITY, ll = 0.f;
+      for (int d0 = 0; d0 < D; d0 += DC) {
+        if (mt || d0) __syncthreads();
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          mm = fmaxf(mm, p[w * ROWS * 3]);
-          bb = fmaxf(bb, p[w * ROWS * 3 + 2]);
-        }
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) ll += p[w * ROWS * 3 + 1] * ex2(p[w * ROWS * 3] - basis(mm));
-        tm[mt][hf] = mm;
-        tl[mt][hf] = ll;
-        tb[mt][hf] = bb;
-        const float f = ex2(big[mt][hf] - basis(bb));
+          for (int i = 0; i < DC / 8; ++i)
+            *reinterpret_cast<float2*>(at(warp, hf * 8 + (lane >> 2), i * 4 + j)) =
+                make_float2(o[mt][d0 / 8 + i][2 * hf], o[mt][d0 / 8 + i][2 * hf + 1]);
+        __syncthreads();
+        // a warp a row
+#pragma unroll 1
+        for (int row = warp; row < 16; row += 4) {
+          const int r = mt * 16 + row, R = c.rt * ROWS + r;
+          if (R >= c.rows) break;
+          const float* p = stats + r * 3;
+          float mm = -INFINITY, bb = -INFINITY, ll = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[mt][i][2 * hf] *= f;
-          o[mt][i][2 * hf + 1] *= f;
-        }
-      }
-    // (of each pair of n-tiles a lane has four dimensions side by side)
-    auto put = [&](float* to, int mt) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float4*>(to + (hf * 8 + (lane >> 2)) * (D + 4) + i * 16 + 4 * j) =
-              make_float4(o[mt][2 * i][2 * hf], o[mt][2 * i + 1][2 * hf], o[mt][2 * i][2 * hf + 1], o[mt][2 * i + 1][2 * hf + 1]);
-    };
-    auto add = [&](const float* from, int mt) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(from + (hf * 8 + (lane >> 2)) * (D + 4) + i * 16 + 4 * j);
-          o[mt][2 * i][2 * hf] += v.x;
-          o[mt][2 * i + 1][2 * hf] += v.y;
-          o[mt][2 * i][2 * hf + 1] += v.z;
-          o[mt][2 * i + 1][2 * hf + 1] += v.w;
-        }
-    };
-    constexpr int kHalf = 16 * (D + 4);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt) __syncthreads();
-      if (warp >= 2) put(join + (warp - 2) * kHalf, mt);
-      __syncthreads();
-      if (warp < 2) add(join + warp * kHalf, mt);
-      __syncthreads();
-      if (warp == 1) put(join, mt);
-      __syncthreads();
-      if (warp == 0) add(join, mt);
-    }
-    if (warp) return;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = mt * 16 + hf * 8 + (lane >> 2), R = c.rt * ROWS + r;
-        if (R >= c.rows) continue;
-        if (whole) {
-          const int i = R / a.group;
-          const long long row = (long long)(c.token + i) * a.heads * a.group + c.head * a.group + R - i * a.group;
-          const float l2 = tl[mt][hf];
-          const float f = l2 == 0.f ? 0.f : ex2(tb[mt][hf] - kUnit - basis(tm[mt][hf])) / l2;
-          uint16_t* to = static_cast<uint16_t*>(a.out) + row * D + 4 * j;
-#pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            const float2 x = make_float2(o[mt][2 * n][2 * hf] * f, o[mt][2 * n + 1][2 * hf] * f);
-            const float2 y = make_float2(o[mt][2 * n][2 * hf + 1] * f, o[mt][2 * n + 1][2 * hf + 1] * f);
-            *reinterpret_cast<uint2*>(to + n * 16) = a.type == IBWD_BF16
-                ? make_uint2(pack2_of(x, __nv_bfloat16{}), pack2_of(y, __nv_bfloat16{}))
-                : make_uint2(pack2_of(x, __half{}), pack2_of(y, __half{}));
+          for (int w = 0; w < 4; ++w) {
+            mm = fmaxf(mm, p[w * ROWS * 3]);
+            bb = fmaxf(bb, p[w * ROWS * 3 + 2]);
           }
-          if (a.lse && j == 0) a.lse[row] = l2 == 0.f ? -INFINITY : (tm[mt][hf] + log2f(l2)) * 0.69314718055994531f;
-        } else {
-          float* to = parts + ((long long)(blockIdx.x * 2 + (begun ? 1 : 0)) * ROWS + r) * part_row(D);
+          constexpr int V = DC / 32;
+          float x[V];
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n)
-            *reinterpret_cast<float4*>(to + n * 16 + 4 * j) = make_float4(
-                o[mt][2 * n][2 * hf], o[mt][2 * n + 1][2 * hf], o[mt][2 * n][2 * hf + 1], o[mt][2 * n + 1][2 * hf + 1]);
-          if (j == 0) *reinterpret_cast<float4*>(to + D) = make_float4(tm[mt][hf], tl[mt][hf], tb[mt][hf], 0.f);
+          for (int e = 0; e < V; ++e) x[e] = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            ll = fmaf(p[w * ROWS * 3 + 1], ex2(p[w * ROWS * 3] - basis(mm)), ll);
+            const float f = ex2(p[w * ROWS * 3 + 2] - basis(bb));
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(at(w, row, (lane * V + e) / 2));
+              x[e] = fmaf(v.x, f, x[e]);
+              x[e + 1] = fmaf(v.y, f, x[e + 1]);
+            }
+          }
+          if (whole) {
+            const int i = R / a.group;
+            const long long out_row = (long long)(c.token + i) * a.heads * a.group + c.head * a.group + R - i * a.group;
+            const float f = ll == 0.f ? 0.f : ex2(bb - kUnit - basis(mm)) / ll;
+            uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out_row * D + d0 + lane * V);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const float2 v = make_float2(x[e] * f, x[e + 1] * f);
+              to[e / 2] = a.type == IBWD_BF16 ? pack2_of(v, __nv_bfloat16{}) : pack2_of(v, __half{});
+            }
+            if (a.lse && lane == 0 && d0 == 0) a.lse[out_row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+          } else {
+            float* to = parts + ((long long)(blockIdx.x * 2 + (begun ? 1 : 0)) * ROWS + r) * part_row(D);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) *reinterpret_cast<float2*>(to + d0 + lane * V + e) = make_float2(x[e], x[e + 1]);
+            if (lane == 0 && d0 == 0) *reinterpret_cast<float4*>(to + D) = make_float4(mm, ll, bb, 0.f);
+          }
         }
       }
+    __syncthreads();
   };
 
   // ------------------------------------------------------- one step of a warp
-  auto compute = [&](const unsigned char* st, unsigned mask) {
-    const int first = c.tile * kTile + warp * 16;
-    const float* ksc = reinterpret_cast<const float*>(st + 2 * kBytes);
-    const float* vsc = ksc + 16;
-    float sc[MT][2][4];
+  auto compute = [&](const unsigned char* st) {
+    const int first = c.tile * kTile + warp * STEP;
+    const unsigned mask = *reinterpret_cast<const unsigned*>(st + 2 * kBytes);
+    if (!mask) return;
+    // Scores of 16 x STEP: column n of n-tile t is position 16 (t / 2) + 4 (n / 2) + (n & 1) + 2 (t & 1), so that a lane has
+    // four positions side by side of each 16, as the values' fragments want them.
+    constexpr int NT = 2 * SUBS;
+    float sc[MT][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-      const int r = nt * 8 + (lane >> 2);
+    const int g8 = lane >> 2, key = 4 * (g8 >> 1) + (g8 & 1);
 #pragma unroll
-      for (int k = 0; k < kLane; ++k) {
-        const int ch = D == 64 ? j : (k >> 1) * 8 + 2 * j + (k & 1);
-        const uint4 w4 = *reinterpret_cast<const uint4*>(st + stage_at<D>(r, ch));
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+    for (int k = 0; k < kLane; ++k) {
+      const int ch = D == 64 ? j : (k >> 1) * 8 + 2 * j + (k & 1);
+      uint4 w[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        w[nt] = *reinterpret_cast<const uint4*>(st + stage_at<D>(16 * (nt >> 1) + 2 * (nt & 1) + key, ch));
+      uint32_t b[4][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        adjacent<INT8>(w[nt].x, b[0][nt][0], b[0][nt][1]);
+        adjacent<INT8>(w[nt].y, b[1][nt][0], b[1][nt][1]);
+        adjacent<INT8>(w[nt].z, b[2][nt][0], b[2][nt][1]);
+        adjacent<INT8>(w[nt].w, b[3][nt][0], b[3][nt][1]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          uint32_t b0, b1;
-          adjacent<INT8>(w[g], b0, b1);
+          const uint4 f = queries[(mt * (D / 16) + k * 4 + g) * 32 + lane];
+          const uint32_t q[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][nt], q[mt][k * 4 + g], b0, b1);
+          for (int nt = 0; nt < NT; ++nt) mma_f16(sc[mt][nt], q, b[g][nt][0], b[g][nt][1]);
         }
       }
     }
-    // this lane's positions of the 16: 2j, 2j + 1, 8 + 2j, 9 + 2j
-    float ks[2][2], lv[2][2];
+    // this lane's positions: 16 u + 4 j + e. The scales of each 16 of them, or (SEL) their own.
+    float ks[SUBS][SEL ? 4 : 1], vs[SUBS][SEL ? 4 : 1], lv[SUBS][SEL ? 4 : 1];
+    if (SEL) {
+      const float* own = reinterpret_cast<const float*>(st + 2 * kBytes + 32) + 4 * j;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const float2 x = *reinterpret_cast<const float2*>(ksc + nt * 8 + 2 * j), y = *reinterpret_cast<const float2*>(vsc + nt * 8 + 2 * j);
-      ks[nt][0] = x.x;
-      ks[nt][1] = x.y;
-      lv[nt][0] = __log2f(y.x);
-      lv[nt][1] = __log2f(y.y);
+      for (int u = 0; u < SUBS; ++u) {
+        const float4 x = *reinterpret_cast<const float4*>(own + 16 * u), y = *reinterpret_cast<const float4*>(own + STEP + 16 * u);
+        const float xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < (SEL ? 4 : 1); ++e) {
+          ks[u][e] = xx[e];
+          vs[u][e] = yy[e];
+          lv[u][e] = __log2f(yy[e]);
+        }
+      }
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(st + 2 * kBytes + 16);
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        ks[u][0] = u ? x.z : x.x;
+        vs[u][0] = u ? x.w : x.y;
+        lv[u][0] = __log2f(vs[u][0]);
+      }
     }
-    const bool full = mask == 0xFFFFu && (SEL || first + 16 <= lim_min);
-    uint32_t p[MT][4];
+    constexpr unsigned kAll = SUBS == 2 ? 0xFFFFFFFFu : 0xFFFFu;
+    const bool full = mask == kAll && (SEL || first + STEP <= lim_min);
+    uint32_t p[MT][SUBS][4];
     bool moved = false;
     float shift[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float y[4], z[4];
+        float y[SUBS][4], top = -INFINITY, over = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int nt = i >> 1, e = i & 1, t = nt * 8 + 2 * j + e;
-          y[i] = sc[mt][nt][hf * 2 + e] * (qs[mt][hf] * ks[nt][e]);
-          z[i] = y[i] + lv[nt][e];
-          if (!full && !((mask >> t & 1) && (SEL || first + t < lim[mt][hf]))) y[i] = z[i] = -INFINITY;
+        for (int u = 0; u < SUBS; ++u) {
+          float t4 = -INFINITY;
+          const float unit = qs[mt][hf] * ks[u][0];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[u][e] = sc[mt][2 * u + (e >> 1)][2 * hf + (e & 1)] * (SEL ? qs[mt][hf] * ks[u][SEL ? e : 0] : unit);
+            const int t = 16 * u + 4 * j + e;
+            if (!full && !((mask >> t & 1) && (SEL || first + t < lim[mt][hf]))) y[u][e] = -INFINITY;
+            t4 = fmaxf(t4, y[u][e]);
+            if (SEL) over = fmaxf(over, y[u][e] + lv[u][SEL ? e : 0]);
+          }
+          top = fmaxf(top, t4);
+          if (!SEL) over = fmaxf(over, t4 + lv[u][0]);
         }
-        const float mn = fmaxf(m[mt][hf], quad_max(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]))));
-        const float bn = fmaxf(big[mt][hf], quad_max(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]))));
-        const float mb = basis(mn), bb = basis(bn) - kUnit;
-        float add = 0.f, w[4];
+        const float mn = fmaxf(m[mt][hf], quad_max(top)), bn = fmaxf(big[mt][hf], quad_max(over));
+        const float mb = basis(mn), bb = basis(bn);
+        // A weight is its probability 2^(y - mb) times 2^(mb + log2(scale) - bb), in units of 2^-15. A probability below 2^-126
+        // is 0, whatever its value's scale.
+        float add = 0.f;
+        const float unit = ex2(capped(mb - bb + kUnit));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          add += ex2(y[i] - mb);
-          w[i] = ex2(z[i] - bb);
+        for (int u = 0; u < SUBS; ++u) {
+          const float f = SEL ? 0.f : ex2(capped(mb + lv[u][0] - bb + kUnit));
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = ex2(y[u][e] - mb);
+            add += w[e];
+            const float of = SEL ? unit * vs[u][SEL ? e : 0] : f;
+            // (an invisible position's scale may be NaN, or its block's factor infinite)
+            w[e] = !full && y[u][e] == -INFINITY ? 0.f : w[e] * of;
+          }
+          p[mt][u][hf] = half_pair(w[0], w[1]);
+          p[mt][u][2 + hf] = half_pair(w[2], w[3]);
         }
         sum[mt][hf] = fmaf(sum[mt][hf], ex2(m[mt][hf] - mb), add);
-        shift[mt][hf] = ex2(big[mt][hf] - basis(bn));
+        shift[mt][hf] = ex2(big[mt][hf] - bb);
         moved = moved || bn != big[mt][hf];
         m[mt][hf] = mn;
         big[mt][hf] = bn;
-        p[mt][hf] = half_pair(w[0], w[1]);
-        p[mt][2 + hf] = half_pair(w[2], w[3]);
       }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -606,49 +695,51 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[mt][i][e] *= shift[mt][e >> 1];
     }
-    // values: 16 dimensions a pair of n-tiles, the even ones and the odd ones
+    // Values: of 32 dimensions four n-tiles, a lane's four positions side by side.
     const unsigned char* sv = st + kBytes;
-    const int vr = (lane & 7) + (lane >> 3 & 1) * 8, vc = lane >> 4;
-    auto values = [&](int i, uint32_t (&b)[4][2]) {  // dimensions 32 i on
+    auto values = [&](int u, int i, uint32_t (&b)[4][2]) {
       uint32_t w[4];
-      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+      asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(smem_u32(sv + stage_at<D>(vr, 2 * i + vc)))
+                   : "r"(smem_u32(sv + stage_at<D>(16 * u + (lane & 15), 2 * i + (lane >> 4))))
                    : "memory");
-      alternate<INT8>(w[0], b[0][0], b[1][0]);
-      alternate<INT8>(w[1], b[0][1], b[1][1]);
-      alternate<INT8>(w[2], b[2][0], b[3][0]);
-      alternate<INT8>(w[3], b[2][1], b[3][1]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) adjacent<INT8>(w[n], b[n][0], b[n][1]);
     };
     if (!INT8 && !SEL && !full) {
       // A NaN that some rows see and others do not: its 0 weight would not keep it out of the others. One position at a time then.
       bool nan = false;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < STEP * D / 512; ++i) {
         const uint4 w = *reinterpret_cast<const uint4*>(sv + (i * 32 + lane) * 16);
+        const int r = (i * 32 + lane) / kRowChunks;
         const uint32_t x = ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
                            ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
-        nan = nan || (x & 0x80808080u);
+        nan = nan || ((x & 0x80808080u) && (mask >> r & 1));
       }
       if (__any_sync(0xffffffffu, nan)) {
 #pragma unroll 1
-        for (int t = 0; t < 16; ++t) {
-          const uint32_t keep = (t >> 1 & 3) != j ? 0u : t & 1 ? 0xFFFF0000u : 0xFFFFu;
-          const uint32_t lo = t < 8 ? keep : 0u, hi = t < 8 ? 0u : keep;
+        for (int t = 0; t < STEP; ++t) {
+          if (!(mask >> t & 1)) continue;
+          const int u = t >> 4;
+          const uint32_t keep = (t >> 2 & 3) != j ? 0u : t & 1 ? 0xFFFF0000u : 0xFFFFu;
+          const uint32_t lo = t & 2 ? 0u : keep, hi = t & 2 ? keep : 0u;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t b[4][2];
-            values(i, b);
+            values(u, i, b);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                const uint32_t one[4] = {p[mt][0] & lo, p[mt][1] & lo, p[mt][2] & hi, p[mt][3] & hi};
+                uint32_t one[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) one[e] = (u && SUBS == 2 ? p[mt][SUBS - 1][e] : p[mt][0][e]) & (e < 2 ? lo : hi);
                 float x[4] = {0.f, 0.f, 0.f, 0.f};
                 mma_f16(x, one, b[n][0] & lo, b[n][1] & hi);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if ((mask >> t & 1) && first + t < lim[mt][e >> 1]) o[mt][4 * i + n][e] += x[e];
+                  if (first + t < lim[mt][e >> 1]) o[mt][4 * i + n][e] += x[e];
               }
           }
         }
@@ -656,110 +747,160 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       }
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t b[4][2];
-      values(i, b);
+    for (int u = 0; u < SUBS; ++u) {
+      // (16 positions that nothing was loaded for: what lies there may be any bits)
+      if (!(mask >> (16 * u) & 0xFFFFu)) continue;
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t b[4][2];
+        values(u, i, b);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][4 * i + n], p[mt], b[n][0], b[n][1]);
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][4 * i + n], p[mt][u], b[n][0], b[n][1]);
+      }
     }
   };
 
   // -------------------------------------------------------------------- loop
   enter_item();
-  int stage = 0;
-  for (long long t = t0; t < t1; ++t) {
+  int stage = 0, run = units - skipped;
+  while (true) {
     cp_async_wait<STAGES - 2>();
     __syncwarp();
     load(stage == 0 ? STAGES - 1 : stage - 1);
     look_up();
-    const unsigned char* st = ring + stage * kStage;
-    const unsigned mask = *reinterpret_cast<const unsigned*>(st + 2 * kBytes + 128);
-    if (mask) compute(st, mask);
+    compute(ring + stage * kStage);
     look_up_page();
-    if (++stage == STAGES) stage = 0;
     const bool ends = c.tile + 1 == c.tiles;
-    if (ends || t + 1 == t1) leave_item(ends && begun);
-    if (t + 1 < t1) {
-      if (c.step(a)) {
-        begun = true;
-        enter_item();
-      }
+    --run;
+    if (ends) run -= kItemCost;
+    if (ends || run <= 0) leave_item(ends && begun, stage);
+    if (run <= 0) break;
+    if (++stage == STAGES) stage = 0;
+    if (c.step(a)) {
+      begun = true;
+      enter_item();
     }
   }
   griddep_launch_dependents();
 }
 
 // Joins the parts of items that lie in several blocks: x the block that ends
-// one, y four of its rows, four warps a row. 456 parts of one item, the most there
-// are, cost their bytes over 4 to 8 SMs.
+// one, y two of its rows. A thread takes the statistics of a part or two, then
+// the eight warps share out the parts' outputs, eight in flight each, and meet in
+// shared memory in their order: of a single item in all blocks (one sequence of
+// 131072 tokens, one KV head) the parts are 600 KB.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
-  constexpr int V = D / 32;
-  __shared__ float acc[4][4][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & 3;
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
+  constexpr int V = D / 32, U = D == 256 ? 4 : 8;
+  __shared__ float factor[2][kAttnGrid];
+  __shared__ float red[2][3][8];
+  __shared__ float acc[8][2][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   const JoinRecord rec = static_cast<const JoinRecord*>(a.work)[blockIdx.x];
-  const int r = blockIdx.y * 4 + (warp >> 2), R = rec.row + r;
-  if (!rec.valid || rec.row + (int)blockIdx.y * 4 >= rec.rows) return;
+  const int r0 = blockIdx.y * 2;
+  if (!rec.valid || rec.row + r0 >= rec.rows) return;
   const float* parts = reinterpret_cast<const float*>(static_cast<const JoinRecord*>(a.work) + kAttnGrid);
-  const int n = (int)blockIdx.x - rec.first + 1;
-  auto part = [&](int i) { return parts + ((long long)((rec.first + i) * 2 + (i == 0)) * ROWS + r) * part_row(D); };
-  float m = -INFINITY, big = -INFINITY, l = 0.f, o[V];
+  const int n = (int)blockIdx.x - rec.first + 1, rows = min(2, rec.rows - rec.row - r0);
+  auto part = [&](int i, int r) { return parts + ((long long)((rec.first + i) * 2 + (i == 0)) * ROWS + r0 + r) * part_row(D); };
+  constexpr int S = (kAttnGrid + 255) / 256;
+  float4 st[2][S];
+  float m[2], big[2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.f;
-  const bool on = R < rec.rows;
-  if (on) {
-    for (int i = lane; i < n; i += 32) {
-      const float4 st = *reinterpret_cast<const float4*>(part(i) + D);
-      m = fmaxf(m, st.x);
-      big = fmaxf(big, st.z);
+  for (int r = 0; r < 2; ++r) {
+    m[r] = big[r] = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int i = threadIdx.x + 256 * k;
+      st[r][k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      if (i < n && r < rows) st[r][k] = *reinterpret_cast<const float4*>(part(i, r) + D);
+      m[r] = fmaxf(m[r], st[r][k].x);
+      big[r] = fmaxf(big[r], st[r][k].z);
     }
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, w));
+      m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], w));
+      big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], w));
     }
-    for (int i = lane; i < n; i += 32) {
-      const float4 st = *reinterpret_cast<const float4*>(part(i) + D);
-      l += st.y * ex2(st.x - basis(m));
+    if (lane == 0) {
+      red[r][0][warp] = m[r];
+      red[r][1][warp] = big[r];
     }
-    l = warp_sum(l);
-#pragma unroll 8
-    for (int i = sub; i < n; i += 4) {
-      const float* p = part(i);
-      const float f = ex2(p[D + 2] - basis(big));
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = fmaf(p[e * 32 + lane], f, o[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[warp >> 2][sub][e * 32 + lane] = o[e];
   }
   __syncthreads();
-  if (!on || sub) return;
-  const float f = l == 0.f ? 0.f : ex2(big - kUnit - basis(m)) / l;
-  const int i = R / a.group;
-  const long long row = (long long)(rec.token + i) * a.heads * a.group + rec.head * a.group + R - i * a.group;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int d = e * 32 + lane;
-    float v = 0.f;
+  for (int r = 0; r < 2; ++r) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) v += acc[warp >> 2][w][d];
-    v *= f;
+    for (int w = 0; w < 8; ++w) {
+      m[r] = fmaxf(m[r], red[r][0][w]);
+      big[r] = fmaxf(big[r], red[r][1][w]);
+    }
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int i = threadIdx.x + 256 * k;
+      l = fmaf(st[r][k].y, ex2(st[r][k].x - basis(m[r])), l);
+      if (i < n) factor[r][i] = ex2(st[r][k].z - basis(big[r]));
+    }
+    l = warp_sum(l);
+    if (lane == 0) red[r][2][warp] = l;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+    if (r < rows) {
+      int i = warp;
+      for (; i + 8 * (U - 1) < n; i += 8 * U) {
+        float x[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float* p = part(i + 8 * u, r) + lane;
+#pragma unroll
+          for (int e = 0; e < V; ++e) asm volatile("ld.global.f32 %0, [%1];" : "=f"(x[u][e]) : "l"(p + e * 32));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = fmaf(x[u][e], factor[r][i + 8 * u], o[e]);
+      }
+      for (; i < n; i += 8) {
+        const float* p = part(i, r) + lane;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(p[e * 32], factor[r][i], o[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[warp][r][e * 32 + lane] = o[e];
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < rows * D; idx += 256) {
+    const int r = idx / D, d = idx - r * D, R = rec.row + r0 + r, i = R / a.group;
+    const long long row = (long long)(rec.token + i) * a.heads * a.group + rec.head * a.group + R - i * a.group;
+    const float mr = r ? m[1] : m[0], br = r ? big[1] : big[0];
+    float v = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      v += acc[w][r][d];
+      l += red[r][2][w];
+    }
+    v *= l == 0.f ? 0.f : ex2(br - kUnit - basis(mr)) / l;
     if (a.type == IBWD_BF16)
       static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(v);
     else
       static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(v);
+    if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.69314718055994531f;
   }
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, int MT, bool INT8, bool SEL>
 cudaError_t attn_launch(const CacheAttnArgs& a, cudaStream_t st) {
-  constexpr int STAGES = D == 256 ? 2 : D == 128 ? 4 : 6, BLOCKS = 2;
-  constexpr size_t bytes = 4 * STAGES * (2 * 16 * D + 160) + (4 * 16 * MT * 3 + 16) * 4 + 2 * 16 * (D + 4) * 4;
+  constexpr int BLOCKS = D * MT <= 128 && (D == 128 || MT == 1) ? 3 : 2, STAGES = D == 64 ? 4 : BLOCKS == 3 ? 2 : 3;
+  constexpr size_t bytes = 4 * STAGES * attn_stage(D, SEL) + MT * D * 32 + 4 * 16 * MT * 3 * 4;
   static std::atomic<size_t> done[64];
   const auto kern = attn_kernel<D, MT, INT8, SEL, STAGES, BLOCKS>;
   cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), bytes, done);
@@ -768,7 +909,9 @@ cudaError_t attn_launch(const CacheAttnArgs& a, cudaStream_t st) {
   const bool vec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token % 8 == 0 && a.q_head % 8 == 0;
   e = launch_ex(kern, grid, kAttnThreads, bytes, st, false, a, vec);
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_join_kernel<D, 16 * MT>, dim3(grid, 4 * MT), 512, 0, st, true, a);
+  // rows that an item can have
+  const int rows = (a.select || !a.seqs.cu) && a.group < 16 * MT ? a.group : 16 * MT;
+  return launch_ex(attn_join_kernel<D, 16 * MT>, dim3(grid, (rows + 1) / 2), 256, 0, st, true, a);
 }
 
 template <int D>

@@ -19,6 +19,7 @@
 #include "head_norm.h"
 #include "indexer_train.h"
 #include "kcommon.cuh"
+#include "packed.cuh"
 
 namespace ibwd {
 
@@ -30,29 +31,64 @@ __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
   return to_f32(static_cast<const __half*>(w)[i]);
 }
 
-// Eight elements of a row, 16-byte aligned.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) { unpack(ld_stream(p), v, __nv_bfloat16{}); }
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) { unpack(ld_stream(p), v, __half{}); }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  float a[4], b[4];
-  unpack(ld_stream(p), a, 0.f);
-  unpack(ld_stream(p + 4), b, 0.f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
+// Four elements side by side, as they lie in memory.
+template <typename T>
+struct Quad {
+  uint2 w;
+  __device__ void load(const T* p) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+  }
+  __device__ void zero() { w = make_uint2(0, 0); }
+  __device__ void get(float (&v)[4]) const {
+    const float2 a = unpack2(w.x, T{}), b = unpack2(w.y, T{});
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+  }
+  __device__ static void store(T* p, const float (&v)[4]) {
+    const uint32_t a = pack2_of(make_float2(v[0], v[1]), T{}), b = pack2_of(make_float2(v[2], v[3]), T{});
+    asm volatile("st.global.L1::no_allocate.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(a), "r"(b) : "memory");
+  }
+};
+template <>
+struct Quad<float> {
+  uint4 w;
+  __device__ void load(const float* p) { w = ld_stream(p); }
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void get(float (&v)[4]) const { unpack(w, v, 0.f); }
+  __device__ static void store(float* p, const float (&v)[4]) {
+    st_stream(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+  }
+};
+
+// A lane's eight elements of a row: partners a_i and b_i of four pairs, packed by twos.
+struct Eight {
+  float2 a[2], b[2];
+};
+// INTER: quads (a0 b0 a1 b1) and (a2 b2 a3 b3); otherwise (a0 .. a3) and (b0 .. b3).
+template <bool INTER>
+__device__ __forceinline__ Eight paired(const float (&x)[4], const float (&y)[4]) {
+  Eight e;
+  if (INTER) {
+    e.a[0] = make_float2(x[0], x[2]), e.b[0] = make_float2(x[1], x[3]);
+    e.a[1] = make_float2(y[0], y[2]), e.b[1] = make_float2(y[1], y[3]);
+  } else {
+    e.a[0] = make_float2(x[0], x[1]), e.a[1] = make_float2(x[2], x[3]);
+    e.b[0] = make_float2(y[0], y[1]), e.b[1] = make_float2(y[2], y[3]);
+  }
+  return e;
+}
+template <bool INTER>
+__device__ __forceinline__ void apart(const Eight& e, float (&x)[4], float (&y)[4]) {
+  if (INTER) {
+    x[0] = e.a[0].x, x[1] = e.b[0].x, x[2] = e.a[0].y, x[3] = e.b[0].y;
+    y[0] = e.a[1].x, y[1] = e.b[1].x, y[2] = e.a[1].y, y[3] = e.b[1].y;
+  } else {
+    x[0] = e.a[0].x, x[1] = e.a[0].y, x[2] = e.a[1].x, x[3] = e.a[1].y;
+    y[0] = e.b[0].x, y[1] = e.b[0].y, y[2] = e.b[1].x, y[3] = e.b[1].y;
   }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack2_of(make_float2(v[2 * i], v[2 * i + 1]), T{});
-  st_stream(p, make_uint4(w[0], w[1], w[2], w[3]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  st_stream(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-  st_stream(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+__device__ __forceinline__ float sum_of(float2 v, float2 w) {
+  const float2 t = add2(v, w);
+  return t.x + t.y;
 }
 
 // Sum over a group of L lanes, in every one of them.
@@ -66,38 +102,38 @@ __device__ __forceinline__ float group_sum(float v) {
 // The rotation of a tile's tokens in shared memory: [tokens][pairs] cosines,
 // then sines, filled by the whole block; every head of a token takes them from
 // there, so that their 40 instructions a pair are spent once a token and
-// operand (per head they would be three times the norm's).
+// operand (per head they would be three times the norm's). A thread has one
+// pair, whose frequency stays in registers.
 struct Turns {
-  unsigned long long* freq;  // [pairs] fraction of a turn
-  int* axis;
   float* cs;
   float* sn;
+  unsigned long long freq = 0;  // fraction of a turn
+  int pair = 0, token = 0, step = 1, axis = -1;
 
   __device__ Turns(unsigned char* smem, const HeadArgs& a, int tokens) {
-    freq = reinterpret_cast<unsigned long long*>(smem);
-    cs = reinterpret_cast<float*>(freq + a.pairs);
+    cs = reinterpret_cast<float*>(smem);
     sn = cs + tokens * a.pairs;
-    axis = reinterpret_cast<int*>(sn + tokens * a.pairs);
-  }
-  __device__ void init(const HeadArgs& a) const {
-    for (int i = threadIdx.x; i < a.pairs; i += kHeadThreads) {
-      const double f = a.freq64 ? static_cast<const double*>(a.freq)[i] : (double)static_cast<const float*>(a.freq)[i];
-      const double turns = f * 0.15915494309189533577;  // 1 / 2 pi
-      freq[i] = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
-      axis[i] = a.axis_of ? a.axis_of[i] : 0;
-    }
+    if (!a.pairs) return;
+    step = kHeadThreads / a.pairs;
+    token = threadIdx.x / a.pairs;
+    pair = threadIdx.x - token * a.pairs;
+    if (token >= step) return;
+    const double f = a.freq64 ? static_cast<const double*>(a.freq)[pair] : (double)static_cast<const float*>(a.freq)[pair];
+    const double turns = f * 0.15915494309189533577;  // 1 / 2 pi
+    freq = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
+    axis = a.axis_of ? a.axis_of[pair] : 0;
   }
   __device__ void fill(const HeadArgs& a, long long first, int tokens) const {
-    const long long left = a.tokens - first;
-    for (int idx = threadIdx.x; idx < tokens * a.pairs; idx += kHeadThreads) {
-      const int t = idx / a.pairs, i = idx - t * a.pairs;
+    if (!a.pairs || token >= step) return;
+    const int end = (int)min((long long)tokens, a.tokens - first);
+    for (int t = token; t < end; t += step) {
       float s = 0.f, c = 1.f;
       // an axis that does not exist turns nothing
-      if (t < left && (unsigned)axis[i] < (unsigned)a.axes) {
-        const long long at = axis[i] * a.axis_stride + first + t;
+      if ((unsigned)axis < (unsigned)a.axes) {
+        const long long at = axis * a.axis_stride + first + t;
         const long long pos = a.positions64 ? static_cast<const long long*>(a.positions)[at]
                                             : (long long)static_cast<const int*>(a.positions)[at];
-        const int turn = (int)((freq[i] * (unsigned long long)pos) >> 32);  // 2^-32 turns
+        const int turn = (int)((freq * (unsigned long long)pos) >> 32);  // 2^-32 turns
         const int quarter = (int)(((unsigned)turn + 0x20000000u) >> 30);
         const float r = (float)(int)((unsigned)turn - ((unsigned)quarter << 30)) * 0x1p-31f;  // half turns
         float sr, cr;
@@ -107,19 +143,24 @@ struct Turns {
         if (quarter & 2) s = -s;
         if ((quarter + 1) & 2) c = -c;
       }
-      cs[idx] = c;
-      sn[idx] = s;
+      cs[t * a.pairs + pair] = c;
+      sn[t * a.pairs + pair] = s;
     }
   }
-  static size_t bytes(int pairs, int tokens) { return (size_t)pairs * 12 + (size_t)pairs * tokens * 8; }
+  static size_t bytes(int pairs, int tokens) { return (size_t)pairs * tokens * 8; }
 };
 
-// Heads whose rows are 16-byte blocks: L lanes a row, eight elements a lane,
-// 256 / L rows at once. A group walks the heads of its tokens with U rows in
-// flight; the rotation's factors and the weights stay in registers. A lane's
-// partners in the other half of the rotated dimensions come by shuffles.
-template <typename T, int L, bool BWD>
-__global__ void __launch_bounds__(kHeadThreads) head_rows(const __grid_constant__ HeadArgs a) {
+// Heads whose rows are whole quads: L lanes a row, eight elements a lane, 256 /
+// L rows at once. A lane holds both elements of its pairs, so that a rotation is
+// within the lane: with pairs half the rotated dimensions apart it has one quad
+// of each half (two 8-byte loads of a 16-bit type), otherwise two quads side by
+// side. A group walks the heads of its tokens with U rows in flight, kept as
+// they lie in memory; the rotation's factors and the weights stay in registers.
+// Arithmetic is packed, two fp32 an instruction: with single instructions, and
+// partners fetched by shuffles, 16381x32x128 took 146 us, bound by issue at
+// 16 warps an SM.
+template <typename T, int L, bool BWD, bool INTER>
+__global__ void __launch_bounds__(kHeadThreads, BWD || sizeof(T) == 4 ? 2 : 3) head_rows(const __grid_constant__ HeadArgs a) {
   constexpr int U = BWD ? 2 : 4;
   constexpr int kGroups = kHeadThreads / L;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -127,156 +168,205 @@ __global__ void __launch_bounds__(kHeadThreads) head_rows(const __grid_constant_
   const HeadOp& o = a.op[which];
   const int block = blockIdx.x - (which ? a.op[0].blocks : 0);
   const Turns turns(smem, a, o.tokens);
-  turns.init(a);
 
   const int li = threadIdx.x % L, group = threadIdx.x / L;
   const int side = 1 << o.shift;  // groups side by side on a token's heads
   const int hh = group & (side - 1), tt = group >> o.shift, step = kGroups >> o.shift;
-  const int dim = li * 8;
-  const bool on = dim < a.D;
-  const int turned = 2 * a.pairs, rel = dim - a.start;
-  const bool mine = on && rel >= 0 && rel < turned;
-  // lane of the other half's eight dimensions
-  const int partner = mine && !a.interleaved ? (threadIdx.x & 31) + (rel < a.pairs ? a.pairs / 8 : -(a.pairs / 8))
-                                             : (threadIdx.x & 31);
-  float g[8], b[8], ag[8], ab[8];
+  const bool on = li * 8 < a.D;
+  // the lane's quads, its first pair, and which of its four pairs turn
+  int d0 = li * 8, d1 = li * 8 + 4, pair = 0;
+  unsigned turned = 0;
+  if (INTER) {
+    const int rel = d0 - a.start;
+    pair = rel / 2;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    g[i] = on && o.gamma ? weight_at(o.gamma, a.w_type, dim + i) : 1.f;
-    b[i] = !BWD && on && o.beta ? weight_at(o.beta, a.w_type, dim + i) : 0.f;
-    ag[i] = ab[i] = 0.f;
+    for (int i = 0; i < 4; ++i)
+      if (on && rel + 2 * i >= 0 && rel + 2 * i < 2 * a.pairs) turned |= 1u << i;
+  } else if (li < a.pairs / 4) {
+    d0 = a.start + 4 * li;
+    d1 = d0 + a.pairs;
+    pair = 4 * li;
+    turned = 15u;
+  } else {  // quads that do not turn, by twos
+    auto place = [&](int k) { return 4 * (k < a.start / 4 ? k : k + a.pairs / 2); };
+    d0 = place(2 * (li - a.pairs / 4));
+    d1 = place(2 * (li - a.pairs / 4) + 1);
   }
+  auto weights = [&](const void* w, float none) {
+    float x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = on && w ? weight_at(w, a.w_type, d0 + i) : none;
+      y[i] = on && w ? weight_at(w, a.w_type, d1 + i) : none;
+    }
+    return paired<INTER>(x, y);
+  };
+  const Eight g = weights(o.gamma, 1.f), bt = weights(BWD ? nullptr : o.beta, 0.f);
+  Eight ag{}, ab{};
   const float inv_d = 1.f / (float)a.D;
+  const long long x_step = side * o.x_head, y_step = side * o.y_head, dy_step = side * o.dy_head;
 
   for (long long tile = block; tile < o.tiles; tile += o.blocks) {
     const long long first = tile * o.tokens;
-    __syncthreads();  // freq, or the tile before
+    __syncthreads();  // the tile before
     turns.fill(a, first, o.tokens);
     __syncthreads();
     for (int t0 = 0; t0 < o.tokens; t0 += step) {
       const int t = t0 + tt;
-      const bool there = first + t < a.tokens && t < o.tokens;
-      // y_e = z_e c_e + z_partner(e) s_e
-      float c[8], s[8];
+      const bool there = on && t < o.tokens && first + t < a.tokens;
+      float2 c[2], s[2];
+      {
+        float cc[4], ss[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-      }
-      if (mine && there) {
-        const float *pc = turns.cs + t * a.pairs, *ps = turns.sn + t * a.pairs;
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (rel + 2 * i < turned) {
-              const int p = rel / 2 + i;
-              c[2 * i] = c[2 * i + 1] = pc[p];
-              s[2 * i] = BWD ? ps[p] : -ps[p];
-              s[2 * i + 1] = -s[2 * i];
-            }
-        } else {
-          const bool low = rel < a.pairs;
-          const int p = low ? rel : rel - a.pairs;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            c[i] = pc[p + i];
-            s[i] = low != BWD ? -ps[p + i] : ps[p + i];
-          }
+        for (int i = 0; i < 4; ++i) {
+          const bool use = there && (turned >> i & 1);
+          cc[i] = use ? turns.cs[t * a.pairs + pair + i] : 1.f;
+          ss[i] = use ? turns.sn[t * a.pairs + pair + i] : 0.f;
+          if (BWD) ss[i] = -ss[i];
         }
+        c[0] = make_float2(cc[0], cc[1]), c[1] = make_float2(cc[2], cc[3]);
+        s[0] = make_float2(ss[0], ss[1]), s[1] = make_float2(ss[2], ss[3]);
       }
-      auto rotate = [&](float (&z)[8]) {
-        if (a.interleaved) {
+      // y_a = z_a c - z_b s, y_b = z_b c + z_a s
+      auto rotate = [&](Eight& z) {
+        if (turned == 15u) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = z[2 * i], v = z[2 * i + 1];
-            if (mine && rel + 2 * i < turned) {
-              z[2 * i] = fmaf(u, c[2 * i], v * s[2 * i]);
-              z[2 * i + 1] = fmaf(v, c[2 * i], u * s[2 * i + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const float2 u = z.a[i], v = z.b[i], n = make_float2(-s[i].x, -s[i].y);
+            z.a[i] = fma2(v, n, mul2(u, c[i]));
+            z.b[i] = fma2(u, s[i], mul2(v, c[i]));
+          }
+        } else if (turned) {  // (a rotation that begins or ends within the lane)
+          auto one = [&](unsigned bit, float& u, float& v, float cs, float sn) {
+            if (turned & bit) {
+              const float w = u;
+              u = fmaf(v, -sn, u * cs);
+              v = fmaf(w, sn, v * cs);
             }
-          }
-        } else if (a.pairs) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float v = __shfl_sync(0xffffffffu, z[i], partner);
-            z[i] = mine ? fmaf(z[i], c[i], v * s[i]) : z[i];
-          }
+          };
+          one(1u, z.a[0].x, z.b[0].x, c[0].x, s[0].x);
+          one(2u, z.a[0].y, z.b[0].y, c[0].y, s[0].y);
+          one(4u, z.a[1].x, z.b[1].x, c[1].x, s[1].x);
+          one(8u, z.a[1].y, z.b[1].y, c[1].y, s[1].y);
         }
       };
       const long long token = first + t;
+      const T* px = static_cast<const T*>(o.x) + token * o.x_token + hh * o.x_head;
+      T* py = static_cast<T*>(o.y) + token * o.y_token + hh * o.y_head;
+      long long pd = token * o.dy_token + hh * o.dy_head;
+      const bool read_x = !BWD || o.norm != IBWD_NORM_NONE;
       for (int h0 = 0; h0 < o.heads; h0 += U * side) {
-        float x[U][8], dy[BWD ? U : 1][8];
+        Quad<T> x[U][2], dy[BWD ? U : 1][2];
+        Quad<float> dyf[BWD ? U : 1][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * side + hh;
-          const bool live = there && on && h < o.heads;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[u][i] = 0.f;
-            if (BWD) dy[BWD ? u : 0][i] = 0.f;
+          const bool live = there && h0 + u * side + hh < o.heads;
+          x[u][0].zero();
+          x[u][1].zero();
+          if (live && read_x) {
+            x[u][0].load(px + d0);
+            x[u][1].load(px + d1);
           }
-          if (live) {
-            if (!BWD || o.norm != IBWD_NORM_NONE) load8(static_cast<const T*>(o.x) + token * o.x_token + h * o.x_head + dim, x[u]);
-            if (BWD) {
-              const long long at = token * o.dy_token + h * o.dy_head + dim;
-              if (o.dy_f32)
-                load8(static_cast<const float*>(o.dy) + at, dy[BWD ? u : 0]);
-              else
-                load8(static_cast<const T*>(o.dy) + at, dy[BWD ? u : 0]);
+          px += x_step;
+          if constexpr (BWD) {
+            if (o.dy_f32) {
+              dyf[u][0].zero();
+              dyf[u][1].zero();
+              if (live) {
+                dyf[u][0].load(static_cast<const float*>(o.dy) + pd + d0);
+                dyf[u][1].load(static_cast<const float*>(o.dy) + pd + d1);
+              }
+            } else {
+              dy[u][0].zero();
+              dy[u][1].zero();
+              if (live) {
+                dy[u][0].load(static_cast<const T*>(o.dy) + pd + d0);
+                dy[u][1].load(static_cast<const T*>(o.dy) + pd + d1);
+              }
             }
+            pd += dy_step;
           }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * side + hh;
           if (h0 + u * side >= o.heads) break;  // (alike in all groups)
-          float(&v)[8] = x[u];
+          const bool live = there && h0 + u * side + hh < o.heads;
+          float p[4], r[4];
+          x[u][0].get(p);
+          x[u][1].get(r);
+          Eight v = paired<INTER>(p, r);
           float rstd = 1.f;
           if (o.norm != IBWD_NORM_NONE) {
             if (o.norm == IBWD_NORM_LAYER) {
-              float m = 0.f;
+              const float m = group_sum<L>(sum_of(add2(v.a[0], v.a[1]), add2(v.b[0], v.b[1]))) * -inv_d;
+              const float2 mm = both(on ? m : 0.f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) m += v[i];
-              m = group_sum<L>(m) * inv_d;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = on ? v[i] - m : 0.f;
+              for (int i = 0; i < 2; ++i) {
+                v.a[i] = add2(v.a[i], mm);
+                v.b[i] = add2(v.b[i], mm);
+              }
             }
-            float q = 0.f;
+            const float2 q = fma2(v.b[1], v.b[1], fma2(v.b[0], v.b[0], fma2(v.a[1], v.a[1], mul2(v.a[0], v.a[0]))));
+            rstd = rsqrtf(fmaf(group_sum<L>(q.x + q.y), inv_d, a.eps));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q = fmaf(v[i], v[i], q);
-            rstd = 1.f / sqrtf(group_sum<L>(q) * inv_d + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= rstd;
+            for (int i = 0; i < 2; ++i) {
+              v.a[i] = mul2(v.a[i], both(rstd));
+              v.b[i] = mul2(v.b[i], both(rstd));
+            }
           }
-          if (!BWD) {
+          if constexpr (!BWD) {
+            if (o.gamma || o.beta)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], g[i], b[i]);
+              for (int i = 0; i < 2; ++i) {
+                v.a[i] = fma2(v.a[i], g.a[i], bt.a[i]);
+                v.b[i] = fma2(v.b[i], g.b[i], bt.b[i]);
+              }
             rotate(v);
           } else {
-            float(&d)[8] = dy[BWD ? u : 0];
+            if (o.dy_f32) {
+              dyf[u][0].get(p);
+              dyf[u][1].get(r);
+            } else {
+              dy[u][0].get(p);
+              dy[u][1].get(r);
+            }
+            Eight d = paired<INTER>(p, r);
             rotate(d);
             if (o.norm == IBWD_NORM_NONE) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = d[i];
+              v = d;
             } else {
-              float s1 = 0.f, s2 = 0.f;
-              const bool live = there && h < o.heads;
+              if (live) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (live) {
-                  ag[i] = fmaf(d[i], v[i], ag[i]);
-                  ab[i] += d[i];
+                for (int i = 0; i < 2; ++i) {
+                  ag.a[i] = fma2(d.a[i], v.a[i], ag.a[i]);
+                  ag.b[i] = fma2(d.b[i], v.b[i], ag.b[i]);
+                  ab.a[i] = add2(ab.a[i], d.a[i]);
+                  ab.b[i] = add2(ab.b[i], d.b[i]);
                 }
-                d[i] *= g[i];
-                s1 += d[i];
-                s2 = fmaf(d[i], v[i], s2);
               }
-              s1 = o.norm == IBWD_NORM_LAYER ? group_sum<L>(on ? s1 : 0.f) * inv_d : 0.f;
-              s2 = group_sum<L>(on ? s2 : 0.f) * inv_d;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = rstd * (d[i] - s1 - v[i] * s2);
+              for (int i = 0; i < 2; ++i) {
+                d.a[i] = mul2(d.a[i], g.a[i]);
+                d.b[i] = mul2(d.b[i], g.b[i]);
+              }
+              const float2 q = fma2(d.b[1], v.b[1], fma2(d.b[0], v.b[0], fma2(d.a[1], v.a[1], mul2(d.a[0], v.a[0]))));
+              const float2 s2 = both(group_sum<L>(on ? q.x + q.y : 0.f) * -inv_d);
+              float s1 = 0.f;
+              if (o.norm == IBWD_NORM_LAYER)
+                s1 = group_sum<L>(on ? sum_of(add2(d.a[0], d.a[1]), add2(d.b[0], d.b[1])) : 0.f) * -inv_d;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                v.a[i] = mul2(fma2(v.a[i], s2, add2(d.a[i], both(s1))), both(rstd));
+                v.b[i] = mul2(fma2(v.b[i], s2, add2(d.b[i], both(s1))), both(rstd));
+              }
             }
           }
-          if (there && on && h < o.heads) store8(static_cast<T*>(o.y) + token * o.y_token + h * o.y_head + dim, v);
+          if (live) {
+            apart<INTER>(v, p, r);
+            Quad<T>::store(py + d0, p);
+            Quad<T>::store(py + d1, r);
+          }
+          py += y_step;
         }
       }
     }
@@ -287,19 +377,25 @@ __global__ void __launch_bounds__(kHeadThreads) head_rows(const __grid_constant_
     // the block's column sums: groups of a warp, then the warps, in a fixed order
     __syncthreads();
     float* red = reinterpret_cast<float*>(smem);  // [warps][2][D]
+    float x[2][8];
+    {
+      float p[4], r[4];
+      apart<INTER>(ag, p, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) x[0][i] = p[i], x[0][4 + i] = r[i];
+      apart<INTER>(ab, p, r);
 #pragma unroll
-      for (int w = L; w < 32; w <<= 1) {
-        ag[i] += __shfl_xor_sync(0xffffffffu, ag[i], w);
-        ab[i] += __shfl_xor_sync(0xffffffffu, ab[i], w);
-      }
-      if (on && (threadIdx.x & 31) < L) {
-        float* r = red + (threadIdx.x >> 5) * 2 * a.D + dim + i;
-        r[0] = ag[i];
-        r[a.D] = ab[i];
-      }
+      for (int i = 0; i < 4; ++i) x[1][i] = p[i], x[1][4 + i] = r[i];
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int w = L; w < 32; w <<= 1) x[k][i] += __shfl_xor_sync(0xffffffffu, x[k][i], w);
+        if (on && (threadIdx.x & 31) < L)
+          red[((threadIdx.x >> 5) * 2 + k) * a.D + (i < 4 ? d0 + i : d1 + i - 4)] = x[k][i];
+      }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.D; i += kHeadThreads) {
       float v = 0.f;
@@ -322,7 +418,6 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = reinterpret_cast<float*>(smem) + warp * a.D;
   const Turns turns(smem + (size_t)kWarps * a.D * 4, a, o.tokens);
-  turns.init(a);
   const int side = 1 << o.shift;
   const int hh = warp & (side - 1), tt = warp >> o.shift, step = kWarps >> o.shift;
   const float inv_d = 1.f / (float)a.D;
@@ -384,7 +479,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
           float q = 0.f;
 #pragma unroll
           for (int i = 0; i < NE; ++i) q = fmaf(v[i], v[i], q);
-          rstd = 1.f / sqrtf(warp_sum(q) * inv_d + a.eps);
+          rstd = rsqrtf(fmaf(warp_sum(q), inv_d, a.eps));
 #pragma unroll
           for (int i = 0; i < NE; ++i) v[i] *= rstd;
         }
@@ -459,7 +554,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
 // them where that would leave SMs without a tile.  Blocks of a backward pass
 // are as many as the workspace holds sums of, shared out by heads.
 inline void plan_heads(HeadArgs* a, int groups, bool backward) {
-  const int budget = backward ? kHeadBlocks : 1 << 30;
+  const int budget = !backward ? 1 << 30 : 2 * a->num_sms < kHeadBlocks ? 2 * a->num_sms : kHeadBlocks;
   const int all = a->op[0].heads + a->op[1].heads;
   for (int w = 0; w < 2; ++w) {
     HeadOp& o = a->op[w];
@@ -478,17 +573,17 @@ inline void plan_heads(HeadArgs* a, int groups, bool backward) {
     o.tiles = tiles(o.tokens);
     int share = budget;
     if (backward && a->op[0].heads && a->op[1].heads) {
-      share = (int)((long long)kHeadBlocks * a->op[0].heads / all);
-      share = share < 1 ? 1 : share > kHeadBlocks - 1 ? kHeadBlocks - 1 : share;
-      if (w) share = kHeadBlocks - share;
+      share = (int)((long long)budget * a->op[0].heads / all);
+      share = share < 1 ? 1 : share > budget - 1 ? budget - 1 : share;
+      if (w) share = budget - share;
     }
     o.blocks = (int)(o.tiles < share ? o.tiles : share);
   }
 }
 
-// Whether every row of an operand is whole 16-byte blocks.
+// Whether every row of an operand is whole quads.
 inline bool heads_aligned(const void* p, long long token, long long head, int size) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && token * size % 16 == 0 && head * size % 16 == 0);
+  return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && token % 4 == 0 && head % 4 == 0);
 }
 
 // [blocks][2][D] column sums of the kernels above to dgamma and dbeta; `behind`: launched right behind them.
@@ -496,12 +591,12 @@ cudaError_t join_heads(const HeadArgs& a, bool behind, cudaStream_t st);
 
 template <typename T, bool BWD>
 cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
-  bool rows = a.D % 8 == 0 && a.D <= 256 && a.start % 8 == 0 && (a.interleaved || a.pairs % 8 == 0);
+  bool rows = a.D % 8 == 0 && a.D <= 256 && (a.interleaved ? a.start % 2 == 0 : a.start % 4 == 0 && a.pairs % 4 == 0);
   for (const HeadOp& o : a.op)
     if (o.heads)
       rows = rows && heads_aligned(o.x, o.x_token, o.x_head, sizeof(T)) && heads_aligned(o.y, o.y_token, o.y_head, sizeof(T)) &&
              (!BWD || heads_aligned(o.dy, o.dy_token, o.dy_head, o.dy_f32 ? 4 : (int)sizeof(T)));
-  int lanes = 4;
+  int lanes = 8;
   while (lanes * 8 < a.D) lanes *= 2;
   if (!rows) lanes = 32;
   plan_heads(&a, kHeadThreads / lanes, BWD);
@@ -516,14 +611,12 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
     auto go = [&](auto kern) { return launch_ex(kern, grid, kHeadThreads, bytes, st, false, a); };
     if (!rows)
       e = a.D <= 128 ? go(head_any<T, 4, BWD>) : go(head_any<T, 16, BWD>);
-    else if (lanes == 4)
-      e = go(head_rows<T, 4, BWD>);
     else if (lanes == 8)
-      e = go(head_rows<T, 8, BWD>);
+      e = a.interleaved ? go(head_rows<T, 8, BWD, true>) : go(head_rows<T, 8, BWD, false>);
     else if (lanes == 16)
-      e = go(head_rows<T, 16, BWD>);
+      e = a.interleaved ? go(head_rows<T, 16, BWD, true>) : go(head_rows<T, 16, BWD, false>);
     else
-      e = go(head_rows<T, 32, BWD>);
+      e = a.interleaved ? go(head_rows<T, 32, BWD, true>) : go(head_rows<T, 32, BWD, false>);
     if (e != cudaSuccess) return e;
   }
   if (!BWD) return cudaSuccess;
