@@ -291,49 +291,71 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   uint4* queries = reinterpret_cast<uint4*>(smem + 4 * STAGES * kStage);  // [MT][D / 16][32] fragments
   float* stats = reinterpret_cast<float*>(queries + MT * D * 2);          // [4][ROWS][3]
   const int P = 1 << s.page_log;
-  Place l = c;
-  int left = units - skipped;  // of the run, to be loaded
-  // What the next load takes. Dense: its first position, and of each 16 positions their page and its scales; SEL: this
-  // lane's position and its page.
-  int at = 0, page[SUBS], listed = -1;
+  // Two steps are on their way before a load: its pages (SEL: its places of the list) are looked up, then their scales (the
+  // pages) are; each answer has a step's time to arrive.
+  Place n = c;                  // the step that is looked up
+  int ahead = units - skipped;  // of the run, from there on
+  int found[SUBS];              // dense: the pages of its positions; SEL: this lane's position
+  // what the next load takes. Dense: its first position, and of each 16 positions their page and its scales; SEL: this
+  // lane's position and its page
+  bool more = false;
+  int at = 0, head = 0, len = 0, page[SUBS];
   float next_k[SUBS], next_v[SUBS];
 #pragma unroll
   for (int i = 0; i < SUBS; ++i) {
-    page[i] = -1;
+    page[i] = found[i] = -1;
     next_k[i] = next_v[i] = 0.f;
   }
   auto look_up = [&]() {
-    at = l.tile * kTile + warp * STEP;
+    if (ahead <= 0) return;
+    const int first = n.tile * kTile + warp * STEP;
     if (SEL) {
-      const int place = at + lane;
-      listed = left > 0 && lane < STEP && place < a.kept ? a.select[(long long)l.token * a.kept + place] : -1;
+      found[0] = lane < STEP && first + lane < a.kept ? a.select[(long long)n.token * a.kept + first + lane] : -1;
     } else {
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i) page[i] = left > 0 && at + 16 * i < l.len ? s.page_at(l.seq, at + 16 * i) : -1;
+      for (int i = 0; i < SUBS; ++i) found[i] = first + 16 * i < n.len ? s.page_at(n.seq, first + 16 * i) : -1;
     }
   };
-  auto look_up_page = [&]() {
+  auto settle = [&]() {
+    more = ahead > 0;
+    if (!more) return;
+    head = n.head;
+    len = n.len;
     if (SEL) {
-      at = listed;
-      page[0] = listed >= 0 && listed < l.seen ? s.page_at(l.seq, listed) : -1;
+      at = found[0];
+      page[0] = at >= 0 && at < n.seen ? s.page_at(n.seq, at) : -1;
     } else {
+      at = n.tile * kTile + warp * STEP;
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i)
+      for (int i = 0; i < SUBS; ++i) {
+        page[i] = found[i];
         if (page[i] >= 0) {
-          const long long block = (long long)page[i] * a.heads + l.head;
+          const long long block = (long long)page[i] * a.heads + head;
           next_k[i] = a.k_scale[block];
           next_v[i] = a.v_scale[block];
         }
+      }
+    }
+    if (--ahead > 0 && n.tile + 1 == n.tiles) ahead -= kItemCost;
+    if (ahead > 0 && n.step(a) && warp == 0) {
+      // the next item's queries on their way to L2
+      const int r = n.rt * ROWS + lane, i = r / a.group;
+      if (lane < ROWS && r < n.rows) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (long long)(n.token + i) * a.q_token +
+                            (long long)(n.head * a.group + r - i * a.group) * a.q_head;
+#pragma unroll
+        for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
+      }
     }
   };
   auto load = [&](int stage) {
-    if (left > 0) {
+    if (more) {
       unsigned char* to = ring + stage * kStage;
       const uint32_t to32 = smem_u32(to);
       unsigned mask;
       if (SEL) {
         mask = __ballot_sync(0xffffffffu, page[0] >= 0);
-        const long long block = (long long)page[0] * a.heads + l.head;
+        const long long block = (long long)page[0] * a.heads + head;
         const long long row = page[0] >= 0 ? (block << s.page_log) + (at & (P - 1)) : 0;
         if (mask) {
 #pragma unroll
@@ -352,7 +374,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           }
         }
       } else {
-        const int count = l.len - at;
+        const int count = len - at;
         mask = count >= 32 ? 0xFFFFFFFFu : count <= 0 ? 0u : (1u << count) - 1u;
         if (SUBS == 1) mask &= 0xFFFFu;
 #pragma unroll
@@ -361,16 +383,24 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           const unsigned part = mask >> (16 * i) & 0xFFFFu;
           if (!part) continue;
           // sixteen rows side by side in the cache
-          const long long row = (((long long)page[i] * a.heads + l.head) << s.page_log) + ((at + 16 * i) & (P - 1));
+          const long long row = (((long long)page[i] * a.heads + head) << s.page_log) + ((at + 16 * i) & (P - 1));
           const uint8_t *k = static_cast<const uint8_t*>(a.k) + row * D + lane * 16, *v = static_cast<const uint8_t*>(a.v) + row * D + lane * 16;
-          const bool all = part == 0xFFFFu;
+          if (part == 0xFFFFu) {
 #pragma unroll
-          for (int n = 0; n < kRowChunks / 2; ++n) {
-            const int r = (n * 32 + lane) / kRowChunks;
-            const uint32_t dst = to32 + stage_at<D>(16 * i + r, (n * 32 + lane) % kRowChunks);
-            const uint32_t bytes = all || (part >> r & 1) ? 16u : 0u;
-            cp_async16(dst, k + n * 512, bytes);
-            cp_async16(dst + kBytes, v + n * 512, bytes);
+            for (int n = 0; n < kRowChunks / 2; ++n) {
+              const uint32_t dst = to32 + stage_at<D>(16 * i + (n * 32 + lane) / kRowChunks, (n * 32 + lane) % kRowChunks);
+              cp_async16(dst, k + n * 512, 16u);
+              cp_async16(dst + kBytes, v + n * 512, 16u);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kRowChunks / 2; ++n) {
+              const int r = (n * 32 + lane) / kRowChunks;
+              const uint32_t dst = to32 + stage_at<D>(16 * i + r, (n * 32 + lane) % kRowChunks);
+              const uint32_t bytes = part >> r & 1 ? 16u : 0u;
+              cp_async16(dst, k + n * 512, bytes);
+              cp_async16(dst + kBytes, v + n * 512, bytes);
+            }
           }
         }
       }
@@ -378,27 +408,17 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         *reinterpret_cast<unsigned*>(to + 2 * kBytes) = mask;
         if (!SEL) *reinterpret_cast<float4*>(to + 2 * kBytes + 16) = make_float4(next_k[0], next_v[0], next_k[SUBS - 1], next_v[SUBS - 1]);
       }
-      if (--left > 0 && l.tile + 1 == l.tiles) left -= kItemCost;
-      if (left > 0 && l.step(a) && warp == 0) {
-        // the next item's queries on their way to L2
-        const int r = l.rt * ROWS + lane, i = r / a.group;
-        if (lane < ROWS && r < l.rows) {
-          const uint16_t* q = static_cast<const uint16_t*>(a.q) + (long long)(l.token + i) * a.q_token +
-                              (long long)(l.head * a.group + r - i * a.group) * a.q_head;
-#pragma unroll
-          for (int n = 0; n < D; n += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + n));
-        }
-      }
     }
     cp_async_commit();
   };
   look_up();
-  look_up_page();
+  settle();
+  look_up();
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
     load(i);
+    settle();
     look_up();
-    look_up_page();
   }
 
   // ------------------------------------------------------------------- items
@@ -647,18 +667,29 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         float y[SUBS][4], top = -INFINITY, over = -INFINITY;
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
-          float t4 = -INFINITY;
           const float unit = qs[mt][hf] * ks[u][0];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; ++e)
             y[u][e] = sc[mt][2 * u + (e >> 1)][2 * hf + (e & 1)] * (SEL ? qs[mt][hf] * ks[u][SEL ? e : 0] : unit);
-            const int t = 16 * u + 4 * j + e;
-            if (!full && !((mask >> t & 1) && (SEL || first + t < lim[mt][hf]))) y[u][e] = -INFINITY;
-            t4 = fmaxf(t4, y[u][e]);
-            if (SEL) over = fmaxf(over, y[u][e] + lv[u][SEL ? e : 0]);
-          }
+        }
+        if (!full) {
+#pragma unroll
+          for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = 16 * u + 4 * j + e;
+              if (!((mask >> t & 1) && (SEL || first + t < lim[mt][hf]))) y[u][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u) {
+          const float t4 = fmaxf(fmaxf(y[u][0], y[u][1]), fmaxf(y[u][2], y[u][3]));
           top = fmaxf(top, t4);
-          if (!SEL) over = fmaxf(over, t4 + lv[u][0]);
+          if (SEL)
+            over = fmaxf(over, fmaxf(fmaxf(y[u][0] + lv[u][0], y[u][1] + lv[u][SEL ? 1 : 0]),
+                                     fmaxf(y[u][2] + lv[u][SEL ? 2 : 0], y[u][3] + lv[u][SEL ? 3 : 0])));
+          else
+            over = fmaxf(over, t4 + lv[u][0]);
         }
         const float mn = fmaxf(m[mt][hf], quad_max(top)), bn = fmaxf(big[mt][hf], quad_max(over));
         const float mb = basis(mn), bb = basis(bn);
@@ -672,11 +703,14 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            w[e] = ex2(y[u][e] - mb);
-            add += w[e];
-            const float of = SEL ? unit * vs[u][SEL ? e : 0] : f;
-            // (an invisible position's scale may be NaN, or its block's factor infinite)
-            w[e] = !full && y[u][e] == -INFINITY ? 0.f : w[e] * of;
+            const float pr = ex2(y[u][e] - mb);
+            add += pr;
+            w[e] = pr * (SEL ? unit * vs[u][SEL ? e : 0] : f);
+          }
+          if (!full) {  // (an invisible position's scale may be NaN, or its block's factor infinite)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (y[u][e] == -INFINITY) w[e] = 0.f;
           }
           p[mt][u][hf] = half_pair(w[0], w[1]);
           p[mt][u][2 + hf] = half_pair(w[2], w[3]);
@@ -769,9 +803,9 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     cp_async_wait<STAGES - 2>();
     __syncwarp();
     load(stage == 0 ? STAGES - 1 : stage - 1);
+    settle();
     look_up();
     compute(ring + stage * kStage);
-    look_up_page();
     const bool ends = c.tile + 1 == c.tiles;
     --run;
     if (ends) run -= kItemCost;
