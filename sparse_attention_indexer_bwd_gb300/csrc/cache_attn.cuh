@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   __shared__ long long found_rest;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 3;
   const CacheSeqs& s = a.seqs;
+  griddep_launch_dependents();  // the join's blocks come in as these leave
 
   // ------------------------------------------------- this block's run of tiles
   using Place = Cursor<ROWS, kTile, SEL>;
@@ -251,7 +252,6 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   float* parts = reinterpret_cast<float*>(static_cast<JoinRecord*>(a.work) + kAttnGrid);
   if (t0 >= t1) {
     if (threadIdx.x == 0) record->valid = 0;
-    griddep_launch_dependents();
     return;
   }
   if (SEL) __syncthreads();
@@ -281,10 +281,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     }
     *record = r;
   }
-  if (units <= skipped) {
-    griddep_launch_dependents();
-    return;
-  }
+  if (units <= skipped) return;
 
   // ------------------------------------------------------------------- loads
   unsigned char* ring = smem + warp * (STAGES * kStage);
@@ -817,7 +814,6 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       enter_item();
     }
   }
-  griddep_launch_dependents();
 }
 
 // Joins the parts of items that lie in several blocks: x the block that ends
