@@ -33,7 +33,7 @@
 #include "elem.cuh"
 #include "indexer_cache.h"
 #include "kcommon.cuh"
-#include "ptx.cuh"
+#include "packed.cuh"
 #include "train.h"
 
 #include <climits>
@@ -89,6 +89,11 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
+}
 __device__ __forceinline__ uint32_t half_pair(float a, float b) { return pack2_of(make_float2(a, b), __half{}); }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -103,11 +108,12 @@ __device__ __forceinline__ float basis(float m) { return m == -INFINITY ? 0.f : 
 __device__ __forceinline__ float capped(float e) { return e > 126.f ? 126.f : e; }  // (NaN stays)
 
 // Where 16 bytes of a stage's row lie: ldmatrix takes eight rows at once, and a
-// lane's quarter of a key two, without a bank conflict.
+// lane's quarter of a key two, without a bank conflict. Stages begin on 256
+// bytes, so that another chunk of the row is an exclusive or away, and 16 rows
+// further 16 D bytes: a step's addresses are few.
 template <int D>
-__device__ __forceinline__ int stage_at(int row, int chunk) {
-  if (D == 64) return row * 64 + ((chunk ^ (row >> 1 & 3)) << 4);
-  return row * D + ((chunk ^ (row & 7)) << 4);
+__device__ __forceinline__ uint32_t stage_at(int row, int chunk) {
+  return row * D + ((chunk ^ (D == 64 ? row >> 1 & 3 : row & 7)) << 4);
 }
 
 // The items in their order, and the tiles of the current one.
@@ -181,7 +187,7 @@ __device__ __forceinline__ long long tiles_of(const CacheAttnArgs& a, int b) {
 // Groups of 16 positions in a warp's step.
 constexpr int attn_subs(int D) { return D == 256 ? 1 : 2; }
 // Bytes of a stage: keys, values, a mask, and the scales of each group (SEL: each position).
-constexpr int attn_stage(int D, bool sel) { return attn_subs(D) * (32 * D + (sel ? 128 : 0)) + 32; }
+constexpr int attn_stage(int D, bool sel) { return (attn_subs(D) * (32 * D + (sel ? 128 : 0)) + 32 + 255) / 256 * 256; }
 
 template <int D, int MT, bool INT8, bool SEL, int STAGES, int BLOCKS>
 __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid_constant__ CacheAttnArgs a, bool vec) {
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   constexpr int SUBS = attn_subs(D), STEP = 16 * SUBS, kTile = 4 * STEP;  // positions of a warp's step, of a block's
   constexpr int kBytes = STEP * D, kStage = attn_stage(D, SEL);
   constexpr int kLane = D / 64;             // 16-byte chunks of a key that a lane takes
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(256) unsigned char smem[];
   __shared__ long long scan[5];
   __shared__ int found_b;
   __shared__ long long found_rest;
@@ -345,10 +351,16 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       }
     }
   };
+  const uint32_t put = stage_at<D>(lane / kRowChunks, lane % kRowChunks);
   auto load = [&](int stage) {
     if (more) {
       unsigned char* to = ring + stage * kStage;
       const uint32_t to32 = smem_u32(to);
+      // this lane's chunk of the 512 bytes after n times 512
+      auto place = [&](int n) {
+        const int turn = D == 64 ? 0 : D == 128 ? (n & 1) * 64 : (2 * n & 7) << 4;
+        return ((to32 + put) ^ turn) + n * 512;
+      };
       unsigned mask;
       if (SEL) {
         mask = __ballot_sync(0xffffffffu, page[0] >= 0);
@@ -357,10 +369,10 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         if (mask) {
 #pragma unroll
           for (int i = 0; i < SUBS * kRowChunks / 2; ++i) {
-            const int idx = i * 32 + lane, r = idx / kRowChunks, ch = idx % kRowChunks;
-            const long long src = __shfl_sync(0xffffffffu, row, r) * D + ch * 16;
+            const int r = (i * 32 + lane) / kRowChunks;
+            const long long src = __shfl_sync(0xffffffffu, row, r) * D + (lane % kRowChunks) * 16;
             const uint32_t bytes = mask >> r & 1 ? 16u : 0u;
-            const uint32_t dst = to32 + stage_at<D>(r, ch);
+            const uint32_t dst = place(i);
             cp_async16(dst, static_cast<const uint8_t*>(a.k) + src, bytes);
             cp_async16(dst + kBytes, static_cast<const uint8_t*>(a.v) + src, bytes);
           }
@@ -385,7 +397,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           if (part == 0xFFFFu) {
 #pragma unroll
             for (int n = 0; n < kRowChunks / 2; ++n) {
-              const uint32_t dst = to32 + stage_at<D>(16 * i + (n * 32 + lane) / kRowChunks, (n * 32 + lane) % kRowChunks);
+              const uint32_t dst = place(i * kRowChunks / 2 + n);
               cp_async16(dst, k + n * 512, 16u);
               cp_async16(dst + kBytes, v + n * 512, 16u);
             }
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
 #pragma unroll
             for (int n = 0; n < kRowChunks / 2; ++n) {
               const int r = (n * 32 + lane) / kRowChunks;
-              const uint32_t dst = to32 + stage_at<D>(16 * i + r, (n * 32 + lane) % kRowChunks);
+              const uint32_t dst = place(i * kRowChunks / 2 + n);
               const uint32_t bytes = part >> r & 1 ? 16u : 0u;
               cp_async16(dst, k + n * 512, bytes);
               cp_async16(dst + kBytes, v + n * 512, bytes);
@@ -587,6 +599,8 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   };
 
   // ------------------------------------------------------- one step of a warp
+  const uint32_t key_at = stage_at<D>(4 * (lane >> 3) + (lane >> 2 & 1), D == 64 ? j : 2 * j);
+  const uint32_t value_at = stage_at<D>(lane & 15, lane >> 4);
   auto compute = [&](const unsigned char* st) {
     const int first = c.tile * kTile + warp * STEP;
     const unsigned mask = *reinterpret_cast<const unsigned*>(st + 2 * kBytes);
@@ -601,14 +615,15 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-    const int g8 = lane >> 2, key = 4 * (g8 >> 1) + (g8 & 1);
+    const uint32_t keys = smem_u32(st) + key_at;
 #pragma unroll
     for (int k = 0; k < kLane; ++k) {
-      const int ch = D == 64 ? j : (k >> 1) * 8 + 2 * j + (k & 1);
       uint4 w[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        w[nt] = *reinterpret_cast<const uint4*>(st + stage_at<D>(16 * (nt >> 1) + 2 * (nt & 1) + key, ch));
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t turn = (((k >> 1) * 8 + (k & 1)) << 4) ^ (nt & 1 ? (D == 64 ? 16 : 32) : 0);
+        w[nt] = ld_shared16((keys ^ turn) + (16 * (nt >> 1) + 2 * (nt & 1)) * D);
+      }
       uint32_t b[4][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -692,17 +707,20 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         const float mb = basis(mn), bb = basis(bn);
         // A weight is its probability 2^(y - mb) times 2^(mb + log2(scale) - bb), in units of 2^-15. A probability below 2^-126
         // is 0, whatever its value's scale.
-        float add = 0.f;
+        float2 add = make_float2(0.f, 0.f);
         const float unit = ex2(capped(mb - bb + kUnit));
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
           const float f = SEL ? 0.f : ex2(capped(mb + lv[u][0] - bb + kUnit));
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float pr = ex2(y[u][e] - mb);
-            add += pr;
-            w[e] = pr * (SEL ? unit * vs[u][SEL ? e : 0] : f);
+          for (int e = 0; e < 4; e += 2) {
+            const float2 d = add2(make_float2(y[u][e], y[u][e + 1]), both(-mb));
+            const float2 pr = make_float2(ex2(d.x), ex2(d.y));
+            add = add2(add, pr);
+            const float2 x = mul2(pr, SEL ? mul2(both(unit), make_float2(vs[u][SEL ? e : 0], vs[u][SEL ? e + 1 : 0])) : both(f));
+            w[e] = x.x;
+            w[e + 1] = x.y;
           }
           if (!full) {  // (an invisible position's scale may be NaN, or its block's factor infinite)
 #pragma unroll
@@ -712,7 +730,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           p[mt][u][hf] = half_pair(w[0], w[1]);
           p[mt][u][2 + hf] = half_pair(w[2], w[3]);
         }
-        sum[mt][hf] = fmaf(sum[mt][hf], ex2(m[mt][hf] - mb), add);
+        sum[mt][hf] = fmaf(sum[mt][hf], ex2(m[mt][hf] - mb), add.x + add.y);
         shift[mt][hf] = ex2(big[mt][hf] - bb);
         moved = moved || bn != big[mt][hf];
         m[mt][hf] = mn;
@@ -728,11 +746,12 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     }
     // Values: of 32 dimensions four n-tiles, a lane's four positions side by side.
     const unsigned char* sv = st + kBytes;
+    const uint32_t rows = smem_u32(sv) + value_at;
     auto values = [&](int u, int i, uint32_t (&b)[4][2]) {
       uint32_t w[4];
       asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(smem_u32(sv + stage_at<D>(16 * u + (lane & 15), 2 * i + (lane >> 4))))
+                   : "r"((rows ^ (32 * i)) + 16 * u * D)
                    : "memory");
 #pragma unroll
       for (int n = 0; n < 4; ++n) adjacent<INT8>(w[n], b[n][0], b[n][1]);
