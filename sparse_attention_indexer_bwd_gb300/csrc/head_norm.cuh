@@ -35,8 +35,11 @@ __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
 template <typename T>
 struct Quad {
   uint2 w;
-  __device__ void load(const T* p) {
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+  // Where `live`, into the registers that the quad has: a load that is selected afterwards would be waited for at once.
+  __device__ void load(const T* p, bool live) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
+                 : "+r"(w.x), "+r"(w.y)
+                 : "l"(p), "r"((int)live));
   }
   __device__ void zero() { w = make_uint2(0, 0); }
   __device__ void get(float (&v)[4]) const {
@@ -51,7 +54,11 @@ struct Quad {
 template <>
 struct Quad<float> {
   uint4 w;
-  __device__ void load(const float* p) { w = ld_stream(p); }
+  __device__ void load(const float* p, bool live) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+                 : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+                 : "l"(p), "r"((int)live));
+  }
   __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
   __device__ void get(float (&v)[4]) const { unpack(w, v, 0.f); }
   __device__ static void store(float* p, const float (&v)[4]) {
@@ -154,13 +161,13 @@ struct Turns {
 // L rows at once. A lane holds both elements of its pairs, so that a rotation is
 // within the lane: with pairs half the rotated dimensions apart it has one quad
 // of each half (two 8-byte loads of a 16-bit type), otherwise two quads side by
-// side. A group walks the heads of its tokens with U rows in flight, kept as
-// they lie in memory; the rotation's factors and the weights stay in registers.
+// side. A group walks the heads of its tokens, U rows at once while the next U
+// are on their way, kept as they lie in memory; the weights stay in registers.
 // Arithmetic is packed, two fp32 an instruction: with single instructions, and
 // partners fetched by shuffles, 16381x32x128 took 146 us, bound by issue at
 // 16 warps an SM.
-template <typename T, int L, bool BWD, bool INTER>
-__global__ void __launch_bounds__(kHeadThreads, BWD || sizeof(T) == 4 ? 2 : 3) head_rows(const __grid_constant__ HeadArgs a) {
+template <typename T, typename DT, int L, bool BWD, bool INTER>
+__global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_constant__ HeadArgs a) {
   constexpr int U = BWD ? 2 : 4;
   constexpr int kGroups = kHeadThreads / L;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -206,170 +213,218 @@ __global__ void __launch_bounds__(kHeadThreads, BWD || sizeof(T) == 4 ? 2 : 3) h
   const float inv_d = 1.f / (float)a.D;
   const long long x_step = side * o.x_head, y_step = side * o.y_head, dy_step = side * o.dy_head;
 
-  for (long long tile = block; tile < o.tiles; tile += o.blocks) {
-    const long long first = tile * o.tokens;
-    __syncthreads();  // the tile before
-    turns.fill(a, first, o.tokens);
-    __syncthreads();
-    for (int t0 = 0; t0 < o.tokens; t0 += step) {
-      const int t = t0 + tt;
-      const bool there = on && t < o.tokens && first + t < a.tokens;
-      float2 c[2], s[2];
-      {
-        float cc[4], ss[4];
+  // U rows of a lane. A lane without elements holds zeros; groups without a row what they had, which goes nowhere.
+  struct Rows {
+    Quad<T> x[U][2];
+    Quad<DT> dy[BWD ? U : 1][2];
+  };
+  Rows rows[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool use = there && (turned >> i & 1);
-          cc[i] = use ? turns.cs[t * a.pairs + pair + i] : 1.f;
-          ss[i] = use ? turns.sn[t * a.pairs + pair + i] : 0.f;
-          if (BWD) ss[i] = -ss[i];
-        }
-        c[0] = make_float2(cc[0], cc[1]), c[1] = make_float2(cc[2], cc[3]);
-        s[0] = make_float2(ss[0], ss[1]), s[1] = make_float2(ss[2], ss[3]);
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        rows[i].x[u][k].zero();
+        if (BWD) rows[i].dy[BWD ? u : 0][k].zero();
       }
-      // y_a = z_a c - z_b s, y_b = z_b c + z_a s
-      auto rotate = [&](Eight& z) {
-        if (turned == 15u) {
+  const bool read_x = !BWD || o.norm != IBWD_NORM_NONE;
+
+  // The next rows to load: heads from h0 on of the tokens t0 + tt of a tile.
+  struct {
+    long long tile;
+    int t0, h0;
+    bool there;
+    const T* x;
+    const DT* dy;
+  } in{block, 0, 0, false, nullptr, nullptr};
+  auto seek_in = [&]() {
+    const long long token = in.tile * o.tokens + in.t0 + tt;
+    in.there = on && in.tile < o.tiles && in.t0 + tt < o.tokens && token < a.tokens;
+    in.x = static_cast<const T*>(o.x) + token * o.x_token + hh * o.x_head;
+    if (BWD) in.dy = static_cast<const DT*>(o.dy) + token * o.dy_token + hh * o.dy_head;
+  };
+  auto load = [&](Rows& r) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 u = z.a[i], v = z.b[i], n = make_float2(-s[i].x, -s[i].y);
-            z.a[i] = fma2(v, n, mul2(u, c[i]));
-            z.b[i] = fma2(u, s[i], mul2(v, c[i]));
-          }
-        } else if (turned) {  // (a rotation that begins or ends within the lane)
-          auto one = [&](unsigned bit, float& u, float& v, float cs, float sn) {
-            if (turned & bit) {
-              const float w = u;
-              u = fmaf(v, -sn, u * cs);
-              v = fmaf(w, sn, v * cs);
-            }
-          };
-          one(1u, z.a[0].x, z.b[0].x, c[0].x, s[0].x);
-          one(2u, z.a[0].y, z.b[0].y, c[0].y, s[0].y);
-          one(4u, z.a[1].x, z.b[1].x, c[1].x, s[1].x);
-          one(8u, z.a[1].y, z.b[1].y, c[1].y, s[1].y);
+    for (int u = 0; u < U; ++u) {
+      const bool live = in.there && in.h0 + u * side + hh < o.heads;
+      r.x[u][0].load(in.x + d0, live && read_x);
+      r.x[u][1].load(in.x + d1, live && read_x);
+      if constexpr (BWD) {
+        r.dy[u][0].load(in.dy + d0, live);
+        r.dy[u][1].load(in.dy + d1, live);
+      }
+      in.x += x_step;
+      if (BWD) in.dy += dy_step;
+    }
+    in.h0 += U * side;
+    if (in.h0 >= o.heads) {
+      in.h0 = 0;
+      in.t0 += step;
+      if (in.t0 >= o.tokens) {
+        in.t0 = 0;
+        in.tile += o.blocks;
+      }
+      seek_in();
+    }
+  };
+
+  // The rows that are computed, with their token's factors.
+  struct {
+    long long tile;
+    int t0, h0;
+    bool there;
+    T* y;
+  } out{block, 0, 0, false, nullptr};
+  float2 c[2], s[2];
+  auto seek_out = [&]() {
+    const int t = out.t0 + tt;
+    const long long token = out.tile * o.tokens + t;
+    out.there = on && t < o.tokens && token < a.tokens;
+    out.y = static_cast<T*>(o.y) + token * o.y_token + hh * o.y_head;
+    float cc[4], ss[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool use = out.there && (turned >> i & 1);
+      cc[i] = use ? turns.cs[t * a.pairs + pair + i] : 1.f;
+      ss[i] = use ? turns.sn[t * a.pairs + pair + i] : 0.f;
+      if (BWD) ss[i] = -ss[i];
+    }
+    c[0] = make_float2(cc[0], cc[1]), c[1] = make_float2(cc[2], cc[3]);
+    s[0] = make_float2(ss[0], ss[1]), s[1] = make_float2(ss[2], ss[3]);
+  };
+  // y_a = z_a c - z_b s, y_b = z_b c + z_a s
+  auto rotate = [&](Eight& z) {
+    if (turned == 15u) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 u = z.a[i], v = z.b[i], n = make_float2(-s[i].x, -s[i].y);
+        z.a[i] = fma2(v, n, mul2(u, c[i]));
+        z.b[i] = fma2(u, s[i], mul2(v, c[i]));
+      }
+    } else if (turned) {  // (a rotation that begins or ends within the lane)
+      auto one = [&](unsigned bit, float& u, float& v, float cs, float sn) {
+        if (turned & bit) {
+          const float w = u;
+          u = fmaf(v, -sn, u * cs);
+          v = fmaf(w, sn, v * cs);
         }
       };
-      const long long token = first + t;
-      const T* px = static_cast<const T*>(o.x) + token * o.x_token + hh * o.x_head;
-      T* py = static_cast<T*>(o.y) + token * o.y_token + hh * o.y_head;
-      long long pd = token * o.dy_token + hh * o.dy_head;
-      const bool read_x = !BWD || o.norm != IBWD_NORM_NONE;
-      for (int h0 = 0; h0 < o.heads; h0 += U * side) {
-        Quad<T> x[U][2], dy[BWD ? U : 1][2];
-        Quad<float> dyf[BWD ? U : 1][2];
+      one(1u, z.a[0].x, z.b[0].x, c[0].x, s[0].x);
+      one(2u, z.a[0].y, z.b[0].y, c[0].y, s[0].y);
+      one(4u, z.a[1].x, z.b[1].x, c[1].x, s[1].x);
+      one(8u, z.a[1].y, z.b[1].y, c[1].y, s[1].y);
+    }
+  };
+  // Whether there are more.
+  auto compute = [&](const Rows& r) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool live = there && h0 + u * side + hh < o.heads;
-          x[u][0].zero();
-          x[u][1].zero();
-          if (live && read_x) {
-            x[u][0].load(px + d0);
-            x[u][1].load(px + d1);
-          }
-          px += x_step;
-          if constexpr (BWD) {
-            if (o.dy_f32) {
-              dyf[u][0].zero();
-              dyf[u][1].zero();
-              if (live) {
-                dyf[u][0].load(static_cast<const float*>(o.dy) + pd + d0);
-                dyf[u][1].load(static_cast<const float*>(o.dy) + pd + d1);
-              }
-            } else {
-              dy[u][0].zero();
-              dy[u][1].zero();
-              if (live) {
-                dy[u][0].load(static_cast<const T*>(o.dy) + pd + d0);
-                dy[u][1].load(static_cast<const T*>(o.dy) + pd + d1);
-              }
-            }
-            pd += dy_step;
+    for (int u = 0; u < U; ++u) {
+      if (out.h0 + u * side >= o.heads) break;  // (alike in all groups)
+      const bool live = out.there && out.h0 + u * side + hh < o.heads;
+      float e0[4], e1[4];
+      r.x[u][0].get(e0);
+      r.x[u][1].get(e1);
+      Eight v = paired<INTER>(e0, e1);
+      float rstd = 1.f;
+      if (o.norm != IBWD_NORM_NONE) {
+        if (o.norm == IBWD_NORM_LAYER) {
+          const float m = group_sum<L>(sum_of(add2(v.a[0], v.a[1]), add2(v.b[0], v.b[1]))) * -inv_d;
+          const float2 mm = both(on ? m : 0.f);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            v.a[i] = add2(v.a[i], mm);
+            v.b[i] = add2(v.b[i], mm);
           }
         }
+        const float2 q = fma2(v.b[1], v.b[1], fma2(v.b[0], v.b[0], fma2(v.a[1], v.a[1], mul2(v.a[0], v.a[0]))));
+        rstd = rsqrtf(fmaf(group_sum<L>(q.x + q.y), inv_d, a.eps));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (h0 + u * side >= o.heads) break;  // (alike in all groups)
-          const bool live = there && h0 + u * side + hh < o.heads;
-          float p[4], r[4];
-          x[u][0].get(p);
-          x[u][1].get(r);
-          Eight v = paired<INTER>(p, r);
-          float rstd = 1.f;
-          if (o.norm != IBWD_NORM_NONE) {
-            if (o.norm == IBWD_NORM_LAYER) {
-              const float m = group_sum<L>(sum_of(add2(v.a[0], v.a[1]), add2(v.b[0], v.b[1]))) * -inv_d;
-              const float2 mm = both(on ? m : 0.f);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                v.a[i] = add2(v.a[i], mm);
-                v.b[i] = add2(v.b[i], mm);
-              }
-            }
-            const float2 q = fma2(v.b[1], v.b[1], fma2(v.b[0], v.b[0], fma2(v.a[1], v.a[1], mul2(v.a[0], v.a[0]))));
-            rstd = rsqrtf(fmaf(group_sum<L>(q.x + q.y), inv_d, a.eps));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              v.a[i] = mul2(v.a[i], both(rstd));
-              v.b[i] = mul2(v.b[i], both(rstd));
-            }
-          }
-          if constexpr (!BWD) {
-            if (o.gamma || o.beta)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                v.a[i] = fma2(v.a[i], g.a[i], bt.a[i]);
-                v.b[i] = fma2(v.b[i], g.b[i], bt.b[i]);
-              }
-            rotate(v);
-          } else {
-            if (o.dy_f32) {
-              dyf[u][0].get(p);
-              dyf[u][1].get(r);
-            } else {
-              dy[u][0].get(p);
-              dy[u][1].get(r);
-            }
-            Eight d = paired<INTER>(p, r);
-            rotate(d);
-            if (o.norm == IBWD_NORM_NONE) {
-              v = d;
-            } else {
-              if (live) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  ag.a[i] = fma2(d.a[i], v.a[i], ag.a[i]);
-                  ag.b[i] = fma2(d.b[i], v.b[i], ag.b[i]);
-                  ab.a[i] = add2(ab.a[i], d.a[i]);
-                  ab.b[i] = add2(ab.b[i], d.b[i]);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                d.a[i] = mul2(d.a[i], g.a[i]);
-                d.b[i] = mul2(d.b[i], g.b[i]);
-              }
-              const float2 q = fma2(d.b[1], v.b[1], fma2(d.b[0], v.b[0], fma2(d.a[1], v.a[1], mul2(d.a[0], v.a[0]))));
-              const float2 s2 = both(group_sum<L>(on ? q.x + q.y : 0.f) * -inv_d);
-              float s1 = 0.f;
-              if (o.norm == IBWD_NORM_LAYER)
-                s1 = group_sum<L>(on ? sum_of(add2(d.a[0], d.a[1]), add2(d.b[0], d.b[1])) : 0.f) * -inv_d;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                v.a[i] = mul2(fma2(v.a[i], s2, add2(d.a[i], both(s1))), both(rstd));
-                v.b[i] = mul2(fma2(v.b[i], s2, add2(d.b[i], both(s1))), both(rstd));
-              }
-            }
-          }
-          if (live) {
-            apart<INTER>(v, p, r);
-            Quad<T>::store(py + d0, p);
-            Quad<T>::store(py + d1, r);
-          }
-          py += y_step;
+        for (int i = 0; i < 2; ++i) {
+          v.a[i] = mul2(v.a[i], both(rstd));
+          v.b[i] = mul2(v.b[i], both(rstd));
         }
       }
+      if constexpr (!BWD) {
+        if (o.gamma || o.beta)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            v.a[i] = fma2(v.a[i], g.a[i], bt.a[i]);
+            v.b[i] = fma2(v.b[i], g.b[i], bt.b[i]);
+          }
+        rotate(v);
+      } else {
+        r.dy[u][0].get(e0);
+        r.dy[u][1].get(e1);
+        Eight d = paired<INTER>(e0, e1);
+        rotate(d);
+        if (o.norm == IBWD_NORM_NONE) {
+          v = d;
+        } else {
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              ag.a[i] = fma2(d.a[i], v.a[i], ag.a[i]);
+              ag.b[i] = fma2(d.b[i], v.b[i], ag.b[i]);
+              ab.a[i] = add2(ab.a[i], d.a[i]);
+              ab.b[i] = add2(ab.b[i], d.b[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            d.a[i] = mul2(d.a[i], g.a[i]);
+            d.b[i] = mul2(d.b[i], g.b[i]);
+          }
+          const float2 q = fma2(d.b[1], v.b[1], fma2(d.b[0], v.b[0], fma2(d.a[1], v.a[1], mul2(d.a[0], v.a[0]))));
+          const float2 s2 = both(group_sum<L>(on ? q.x + q.y : 0.f) * -inv_d);
+          if (o.norm == IBWD_NORM_LAYER) {
+            const float2 s1 = both(group_sum<L>(on ? sum_of(add2(d.a[0], d.a[1]), add2(d.b[0], d.b[1])) : 0.f) * -inv_d);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              d.a[i] = add2(d.a[i], s1);
+              d.b[i] = add2(d.b[i], s1);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            v.a[i] = mul2(fma2(v.a[i], s2, d.a[i]), both(rstd));
+            v.b[i] = mul2(fma2(v.b[i], s2, d.b[i]), both(rstd));
+          }
+        }
+      }
+      if (live) {
+        apart<INTER>(v, e0, e1);
+        Quad<T>::store(out.y + d0, e0);
+        Quad<T>::store(out.y + d1, e1);
+      }
+      out.y += y_step;
     }
+    out.h0 += U * side;
+    if (out.h0 < o.heads) return true;
+    out.h0 = 0;
+    out.t0 += step;
+    if (out.t0 >= o.tokens) {
+      out.t0 = 0;
+      out.tile += o.blocks;
+      if (out.tile >= o.tiles) return false;
+      __syncthreads();
+      turns.fill(a, out.tile * o.tokens, o.tokens);
+      __syncthreads();
+    }
+    seek_out();
+    return true;
+  };
+
+  seek_in();
+  load(rows[0]);  // (they come while the angles are computed)
+  turns.fill(a, out.tile * o.tokens, o.tokens);
+  __syncthreads();
+  seek_out();
+  while (true) {
+    load(rows[1]);
+    if (!compute(rows[0])) break;
+    load(rows[0]);
+    if (!compute(rows[1])) break;
   }
 
   if (BWD) griddep_launch_dependents();
@@ -551,11 +606,12 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
 // How a launch splits its tokens: tiles of tokens, whose heads go to the
 // block's `groups` rows at once.  Few groups side by side on a token's heads
 // give a group several heads for one set of the rotation's factors; more of
-// them where that would leave SMs without a tile.  Blocks of a backward pass
-// are as many as the workspace holds sums of, shared out by heads.
+// them where that would leave SMs without a tile. All blocks are resident and
+// walk their tiles, shared out between the operands by cost.
 inline void plan_heads(HeadArgs* a, int groups, bool backward) {
-  const int budget = !backward ? 1 << 30 : 2 * a->num_sms < kHeadBlocks ? 2 * a->num_sms : kHeadBlocks;
-  const int all = a->op[0].heads + a->op[1].heads;
+  const int resident = 2 * a->num_sms, budget = backward && resident > kHeadBlocks ? kHeadBlocks : resident;
+  // what a token costs an operand: its heads, and its angles, as much as about eight heads
+  const int angles = a->pairs ? 8 : 1, first = a->op[0].heads + angles, both = first + a->op[1].heads + angles;
   for (int w = 0; w < 2; ++w) {
     HeadOp& o = a->op[w];
     o.shift = 0;
@@ -563,7 +619,7 @@ inline void plan_heads(HeadArgs* a, int groups, bool backward) {
     o.blocks = 0;
     o.tiles = 0;
     if (!o.heads || !a->tokens) continue;
-    while ((1 << (o.shift + 1)) <= groups && (4 << (o.shift + 1)) <= o.heads) ++o.shift;
+    while ((1 << (o.shift + 1)) <= groups && (16 << (o.shift + 1)) <= o.heads) ++o.shift;
     auto tiles = [&](int tokens) { return (a->tokens + tokens - 1) / tokens; };
     while ((1 << o.shift) < groups && (1 << o.shift) < o.heads && tiles(groups >> o.shift) < a->num_sms) ++o.shift;
     o.tokens = groups >> o.shift;
@@ -572,8 +628,8 @@ inline void plan_heads(HeadArgs* a, int groups, bool backward) {
     for (int m = rows; m < 8 && tiles(2 * o.tokens) >= 4 * a->num_sms && 2 * o.tokens * a->pairs <= 2048; m *= 2) o.tokens *= 2;
     o.tiles = tiles(o.tokens);
     int share = budget;
-    if (backward && a->op[0].heads && a->op[1].heads) {
-      share = (int)((long long)budget * a->op[0].heads / all);
+    if (a->op[0].heads && a->op[1].heads) {
+      share = (int)((long long)budget * first / both);
       share = share < 1 ? 1 : share > budget - 1 ? budget - 1 : share;
       if (w) share = budget - share;
     }
@@ -607,16 +663,30 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
     // at most 36 KB, which a launch has without asking: 512 wide rows, and 2048 pairs' factors
     const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * a.D * 4;
     const size_t bytes = BWD && sums > used ? sums : used;
+    auto launch = [&](const HeadArgs& b, unsigned blocks, bool f32) {
+      auto go = [&](auto kern) { return launch_ex(kern, blocks, kHeadThreads, bytes, st, false, b); };
+      auto by_lanes = [&](auto dt) {
+        using DT = decltype(dt);
+        if (lanes == 8) return a.interleaved ? go(head_rows<T, DT, 8, BWD, true>) : go(head_rows<T, DT, 8, BWD, false>);
+        if (lanes == 16) return a.interleaved ? go(head_rows<T, DT, 16, BWD, true>) : go(head_rows<T, DT, 16, BWD, false>);
+        return a.interleaved ? go(head_rows<T, DT, 32, BWD, true>) : go(head_rows<T, DT, 32, BWD, false>);
+      };
+      if (!rows) return a.D <= 128 ? go(head_any<T, 4, BWD>) : go(head_any<T, 16, BWD>);
+      if constexpr (BWD)
+        if (f32) return by_lanes(float{});
+      return by_lanes(T{});
+    };
     cudaError_t e;
-    auto go = [&](auto kern) { return launch_ex(kern, grid, kHeadThreads, bytes, st, false, a); };
-    if (!rows)
-      e = a.D <= 128 ? go(head_any<T, 4, BWD>) : go(head_any<T, 16, BWD>);
-    else if (lanes == 8)
-      e = a.interleaved ? go(head_rows<T, 8, BWD, true>) : go(head_rows<T, 8, BWD, false>);
-    else if (lanes == 16)
-      e = a.interleaved ? go(head_rows<T, 16, BWD, true>) : go(head_rows<T, 16, BWD, false>);
-    else
-      e = a.interleaved ? go(head_rows<T, 32, BWD, true>) : go(head_rows<T, 32, BWD, false>);
+    if (rows && BWD && a.op[0].heads && a.op[1].heads && a.op[0].dy_f32 != a.op[1].dy_f32) {
+      // gradients of two types: a launch each, its sums where one launch would have them
+      HeadArgs q = a, k = a;
+      q.op[1].blocks = k.op[0].blocks = 0;
+      k.part = a.part ? a.part + (long long)a.op[0].blocks * 2 * a.D : nullptr;
+      e = launch(q, a.op[0].blocks, a.op[0].dy_f32);
+      if (e == cudaSuccess) e = launch(k, a.op[1].blocks, a.op[1].dy_f32);
+    } else {
+      e = launch(a, grid, a.op[a.op[0].heads ? 0 : 1].dy_f32);
+    }
     if (e != cudaSuccess) return e;
   }
   if (!BWD) return cudaSuccess;
