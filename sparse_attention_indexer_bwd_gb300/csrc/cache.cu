@@ -20,7 +20,8 @@ namespace ibwd {
 namespace {
 
 constexpr int kWriteThreads = 128;
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 128;
+constexpr int kReadAhead = 4;  // 16-byte loads in flight a thread
 
 template <typename T>
 __device__ __forceinline__ void load_some(const T* p, float (&v)[8], bool vec) {
@@ -186,33 +187,42 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   const float scale = page >= 0 ? a.scale[block] : 0.f;
   const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.codes) + block * P * a.dim);
   const int chunks = a.dim >> 4;
-  for (int i = threadIdx.x; i < rows * chunks; i += kReadThreads) {
-    const int slot = i / chunks, c = i - slot * chunks;
-    T* out = static_cast<T*>(a.out) + (((long long)b * a.length + base + slot) * a.heads + head) * a.dim + 16 * c;
-    float4 v[4] = {};
-    if (page >= 0 && base + slot < len) {
-      const uint4 r = ld_stream(codes + i);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  const int total = rows * chunks, held = page < 0 ? 0 : min(rows, len - base) * chunks;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kReadAhead * kReadThreads) {
+    uint4 r[kReadAhead];
+#pragma unroll
+    for (int k = 0; k < kReadAhead; ++k) {
+      const int i = i0 + k * kReadThreads;
+      r[k] = i < held ? ld_stream(codes + i) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kReadAhead; ++k) {
+      const int i = i0 + k * kReadThreads, slot = i / chunks, c = i - slot * chunks;
+      if (i >= total) break;
+      T* out = static_cast<T*>(a.out) + (((long long)b * a.length + base + slot) * a.heads + head) * a.dim + 16 * c;
+      const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+      const float by = i < held ? scale : 0.f;  // (behind the end even where the scale is no number)
+      float4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = value4(w[j], INT8);
-        v[j].x *= scale, v[j].y *= scale, v[j].z *= scale, v[j].w *= scale;
+        v[j].x *= by, v[j].y *= by, v[j].z *= by, v[j].w *= by;
       }
-    }
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[8];
+      if constexpr (sizeof(T) == 2) {
+        uint32_t h[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[2 * j] = pack2_of(make_float2(v[j].x, v[j].y), T{});
-        w[2 * j + 1] = pack2_of(make_float2(v[j].z, v[j].w), T{});
+        for (int j = 0; j < 4; ++j) {
+          h[2 * j] = pack2_of(make_float2(v[j].x, v[j].y), T{});
+          h[2 * j + 1] = pack2_of(make_float2(v[j].z, v[j].w), T{});
+        }
+        st_stream(out, make_uint4(h[0], h[1], h[2], h[3]));
+        st_stream(out + 8, make_uint4(h[4], h[5], h[6], h[7]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_stream(out + 4 * j, make_uint4(__float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j].z),
+                                            __float_as_uint(v[j].w)));
       }
-      st_stream(out, make_uint4(w[0], w[1], w[2], w[3]));
-      st_stream(out + 8, make_uint4(w[4], w[5], w[6], w[7]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        st_stream(out + 4 * j, make_uint4(__float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j].z),
-                                          __float_as_uint(v[j].w)));
     }
   }
 }

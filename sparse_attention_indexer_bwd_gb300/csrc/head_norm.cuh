@@ -35,11 +35,12 @@ __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
 template <typename T>
 struct Quad {
   uint2 w;
-  // Where `live`, into the registers that the quad has: a load that is selected afterwards would be waited for at once.
-  __device__ void load(const T* p, bool live) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
-                 : "+r"(w.x), "+r"(w.y)
-                 : "l"(p), "r"((int)live));
+  // Two quads where `live`, into the registers that they have: loads that are selected afterwards would be waited for at once.
+  __device__ static void load(Quad (&q)[2], const T* p0, const T* p1, bool live) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t@p ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%4];\n\t"
+                 "@p ld.global.L1::no_allocate.v2.u32 {%2,%3}, [%5];\n\t}"
+                 : "+r"(q[0].w.x), "+r"(q[0].w.y), "+r"(q[1].w.x), "+r"(q[1].w.y)
+                 : "l"(p0), "l"(p1), "r"((int)live));
   }
   __device__ void zero() { w = make_uint2(0, 0); }
   __device__ void get(float (&v)[4]) const {
@@ -54,10 +55,12 @@ struct Quad {
 template <>
 struct Quad<float> {
   uint4 w;
-  __device__ void load(const float* p, bool live) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-                 : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
-                 : "l"(p), "r"((int)live));
+  __device__ static void load(Quad (&q)[2], const float* p0, const float* p1, bool live) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %10, 0;\n\t@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%8];\n\t"
+                 "@p ld.global.L1::no_allocate.v4.u32 {%4,%5,%6,%7}, [%9];\n\t}"
+                 : "+r"(q[0].w.x), "+r"(q[0].w.y), "+r"(q[0].w.z), "+r"(q[0].w.w), "+r"(q[1].w.x), "+r"(q[1].w.y),
+                   "+r"(q[1].w.z), "+r"(q[1].w.w)
+                 : "l"(p0), "l"(p1), "r"((int)live));
   }
   __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
   __device__ void get(float (&v)[4]) const { unpack(w, v, 0.f); }
@@ -66,7 +69,8 @@ struct Quad<float> {
   }
 };
 
-// A lane's eight elements of a row: partners a_i and b_i of four pairs, packed by twos.
+// A lane's eight elements of a row: partners a_i and b_i of four pairs, packed
+// by twos (two fp32 an instruction).
 struct Eight {
   float2 a[2], b[2];
 };
@@ -93,17 +97,29 @@ __device__ __forceinline__ void apart(const Eight& e, float (&x)[4], float (&y)[
     y[0] = e.b[0].x, y[1] = e.b[0].y, y[2] = e.b[1].x, y[3] = e.b[1].y;
   }
 }
-__device__ __forceinline__ float sum_of(float2 v, float2 w) {
-  const float2 t = add2(v, w);
+__device__ __forceinline__ float total(const Eight& v) {
+  const float2 t = add2(add2(v.a[0], v.a[1]), add2(v.b[0], v.b[1]));
   return t.x + t.y;
 }
-
-// Sum over a group of L lanes, in every one of them.
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float product(const Eight& v, const Eight& w) {
+  const float2 t = fma2(v.b[1], w.b[1], fma2(v.b[0], w.b[0], fma2(v.a[1], w.a[1], mul2(v.a[0], w.a[0]))));
+  return t.x + t.y;
+}
+__device__ __forceinline__ void shift(Eight& v, float by) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int i = 0; i < 2; ++i) {
+    v.a[i] = add2(v.a[i], both(by));
+    v.b[i] = add2(v.b[i], both(by));
+  }
+}
+
+// Sums over a group of L lanes, in every one of them.
+template <int L, int U>
+__device__ __forceinline__ void group_sums(float (&v)[U]) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
 }
 
 // The rotation of a tile's tokens in shared memory: [tokens][pairs] cosines,
@@ -168,7 +184,7 @@ struct Turns {
 // 16 warps an SM.
 template <typename T, typename DT, int L, bool BWD, bool INTER>
 __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_constant__ HeadArgs a) {
-  constexpr int U = BWD ? 2 : 4;
+  constexpr int U = !BWD ? 4 : sizeof(T) == 4 ? 1 : 2;
   constexpr int kGroups = kHeadThreads / L;
   extern __shared__ __align__(16) unsigned char smem[];
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
@@ -199,6 +215,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     d0 = place(2 * (li - a.pairs / 4));
     d1 = place(2 * (li - a.pairs / 4) + 1);
   }
+  const long long apart_by = d1 - d0;
   auto weights = [&](const void* w, float none) {
     float x[4], y[4];
 #pragma unroll
@@ -241,19 +258,15 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
   auto seek_in = [&]() {
     const long long token = in.tile * o.tokens + in.t0 + tt;
     in.there = on && in.tile < o.tiles && in.t0 + tt < o.tokens && token < a.tokens;
-    in.x = static_cast<const T*>(o.x) + token * o.x_token + hh * o.x_head;
-    if (BWD) in.dy = static_cast<const DT*>(o.dy) + token * o.dy_token + hh * o.dy_head;
+    in.x = static_cast<const T*>(o.x) + token * o.x_token + hh * o.x_head + d0;
+    if (BWD) in.dy = static_cast<const DT*>(o.dy) + token * o.dy_token + hh * o.dy_head + d0;
   };
   auto load = [&](Rows& r) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool live = in.there && in.h0 + u * side + hh < o.heads;
-      r.x[u][0].load(in.x + d0, live && read_x);
-      r.x[u][1].load(in.x + d1, live && read_x);
-      if constexpr (BWD) {
-        r.dy[u][0].load(in.dy + d0, live);
-        r.dy[u][1].load(in.dy + d1, live);
-      }
+      if (read_x) Quad<T>::load(r.x[u], in.x, in.x + apart_by, live);
+      if constexpr (BWD) Quad<DT>::load(r.dy[u], in.dy, in.dy + apart_by, live);
       in.x += x_step;
       if (BWD) in.dy += dy_step;
     }
@@ -276,12 +289,12 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     bool there;
     T* y;
   } out{block, 0, 0, false, nullptr};
-  float2 c[2], s[2];
+  float2 c[2], s[2], minus_s[2];
   auto seek_out = [&]() {
     const int t = out.t0 + tt;
     const long long token = out.tile * o.tokens + t;
     out.there = on && t < o.tokens && token < a.tokens;
-    out.y = static_cast<T*>(o.y) + token * o.y_token + hh * o.y_head;
+    out.y = static_cast<T*>(o.y) + token * o.y_token + hh * o.y_head + d0;
     float cc[4], ss[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -290,19 +303,29 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
       ss[i] = use ? turns.sn[t * a.pairs + pair + i] : 0.f;
       if (BWD) ss[i] = -ss[i];
     }
-    c[0] = make_float2(cc[0], cc[1]), c[1] = make_float2(cc[2], cc[3]);
-    s[0] = make_float2(ss[0], ss[1]), s[1] = make_float2(ss[2], ss[3]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = make_float2(cc[2 * i], cc[2 * i + 1]);
+      s[i] = make_float2(ss[2 * i], ss[2 * i + 1]);
+      minus_s[i] = make_float2(-ss[2 * i], -ss[2 * i + 1]);
+    }
   };
-  // y_a = z_a c - z_b s, y_b = z_b c + z_a s
+  auto store = [&](const Eight& v, T* y) {
+    float e0[4], e1[4];
+    apart<INTER>(v, e0, e1);
+    Quad<T>::store(y, e0);
+    Quad<T>::store(y + apart_by, e1);
+  };
+  // y_a = z_a c - z_b s, y_b = z_b c + z_a s, where the pair turns: a rotation may begin or end within the lane
   auto rotate = [&](Eight& z) {
     if (turned == 15u) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 u = z.a[i], v = z.b[i], n = make_float2(-s[i].x, -s[i].y);
-        z.a[i] = fma2(v, n, mul2(u, c[i]));
+        const float2 u = z.a[i], v = z.b[i];
+        z.a[i] = fma2(v, minus_s[i], mul2(u, c[i]));
         z.b[i] = fma2(u, s[i], mul2(v, c[i]));
       }
-    } else if (turned) {  // (a rotation that begins or ends within the lane)
+    } else if (turned) {
       auto one = [&](unsigned bit, float& u, float& v, float cs, float sn) {
         if (turned & bit) {
           const float w = u;
@@ -316,89 +339,119 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
       one(8u, z.a[1].y, z.b[1].y, c[1].y, s[1].y);
     }
   };
-  // Whether there are more.
-  auto compute = [&](const Rows& r) {
+  auto elements = [&](const Quad<T> (&x)[2]) {
+    float e0[4], e1[4];
+    x[0].get(e0);
+    x[1].get(e1);
+    return paired<INTER>(e0, e1);
+  };
+  const bool layer = o.norm == IBWD_NORM_LAYER, normed = o.norm != IBWD_NORM_NONE;
+  // Rows beyond the heads are computed with what the registers hold, and go nowhere. Forward, the sums of all U rows go
+  // through the shuffles together, and the elements are taken apart once more behind them (row after row: 42 us for 40).
+  auto forward = [&](const Rows& r) {
+    float rstd[U], minus[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (out.h0 + u * side >= o.heads) break;  // (alike in all groups)
-      const bool live = out.there && out.h0 + u * side + hh < o.heads;
-      float e0[4], e1[4];
-      r.x[u][0].get(e0);
-      r.x[u][1].get(e1);
-      Eight v = paired<INTER>(e0, e1);
-      float rstd = 1.f;
-      if (o.norm != IBWD_NORM_NONE) {
-        if (o.norm == IBWD_NORM_LAYER) {
-          const float m = group_sum<L>(sum_of(add2(v.a[0], v.a[1]), add2(v.b[0], v.b[1]))) * -inv_d;
-          const float2 mm = both(on ? m : 0.f);
+      rstd[u] = 1.f;
+      minus[u] = 0.f;
+    }
+    if (normed) {
+      if (layer) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            v.a[i] = add2(v.a[i], mm);
-            v.b[i] = add2(v.b[i], mm);
-          }
-        }
-        const float2 q = fma2(v.b[1], v.b[1], fma2(v.b[0], v.b[0], fma2(v.a[1], v.a[1], mul2(v.a[0], v.a[0]))));
-        rstd = rsqrtf(fmaf(group_sum<L>(q.x + q.y), inv_d, a.eps));
+        for (int u = 0; u < U; ++u) minus[u] = total(elements(r.x[u]));
+        group_sums<L>(minus);
+#pragma unroll
+        for (int u = 0; u < U; ++u) minus[u] = on ? minus[u] * -inv_d : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Eight v = elements(r.x[u]);
+        if (layer) shift(v, minus[u]);
+        rstd[u] = product(v, v);
+      }
+      group_sums<L>(rstd);
+#pragma unroll
+      for (int u = 0; u < U; ++u) rstd[u] = rsqrtf(fmaf(rstd[u], inv_d, a.eps));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Eight v = elements(r.x[u]);
+      if (layer) shift(v, minus[u]);
+      if (normed) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          v.a[i] = mul2(v.a[i], both(rstd));
-          v.b[i] = mul2(v.b[i], both(rstd));
+          v.a[i] = fma2(mul2(v.a[i], both(rstd[u])), g.a[i], bt.a[i]);
+          v.b[i] = fma2(mul2(v.b[i], both(rstd[u])), g.b[i], bt.b[i]);
         }
       }
-      if constexpr (!BWD) {
-        if (o.gamma || o.beta)
+      rotate(v);
+      if (out.there && out.h0 + u * side + hh < o.heads) store(v, out.y);
+      out.y += y_step;
+    }
+  };
+  // Backward, row after row (two at once spill: 82 us for 66 at 8192x40x128 bf16), its sums together: with v = x (layer: x - mean),
+  // dx = rstd (d - sum(d)/D) - xh (rstd^2 sum(d v)/D).
+  auto backward = [&](const Rows& r) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            v.a[i] = fma2(v.a[i], g.a[i], bt.a[i]);
-            v.b[i] = fma2(v.b[i], g.b[i], bt.b[i]);
-          }
-        rotate(v);
-      } else {
-        r.dy[u][0].get(e0);
-        r.dy[u][1].get(e1);
-        Eight d = paired<INTER>(e0, e1);
-        rotate(d);
-        if (o.norm == IBWD_NORM_NONE) {
-          v = d;
+    for (int u = 0; u < U; ++u) {
+      const bool live = out.there && out.h0 + u * side + hh < o.heads;
+      float e0[4], e1[4];
+      r.dy[u][0].get(e0);
+      r.dy[u][1].get(e1);
+      Eight d = paired<INTER>(e0, e1);
+      rotate(d);
+      if (normed) {
+        Eight v = elements(r.x[u]);
+        if (layer) {
+          float m[1] = {total(v)};
+          group_sums<L>(m);
+          shift(v, on ? m[0] * -inv_d : 0.f);
+        }
+        Eight e;  // d gamma
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          e.a[i] = mul2(d.a[i], g.a[i]);
+          e.b[i] = mul2(d.b[i], g.b[i]);
+        }
+        float sums[3] = {product(v, v), on ? product(e, v) : 0.f, layer && on ? total(e) : 0.f};
+        if (layer) {
+          group_sums<L>(sums);
         } else {
-          if (live) {
+          float two[2] = {sums[0], sums[1]};
+          group_sums<L>(two);
+          sums[0] = two[0];
+          sums[1] = two[1];
+        }
+        const float rstd = rsqrtf(fmaf(sums[0], inv_d, a.eps)), k = rstd * (rstd * sums[1] * -inv_d), less = sums[2] * -inv_d;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              ag.a[i] = fma2(d.a[i], v.a[i], ag.a[i]);
-              ag.b[i] = fma2(d.b[i], v.b[i], ag.b[i]);
+        for (int i = 0; i < 2; ++i) {
+          const float2 xa = mul2(v.a[i], both(rstd)), xb = mul2(v.b[i], both(rstd));
+          if (live) {
+            ag.a[i] = fma2(d.a[i], xa, ag.a[i]);
+            ag.b[i] = fma2(d.b[i], xb, ag.b[i]);
+            if (layer) {
               ab.a[i] = add2(ab.a[i], d.a[i]);
               ab.b[i] = add2(ab.b[i], d.b[i]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            d.a[i] = mul2(d.a[i], g.a[i]);
-            d.b[i] = mul2(d.b[i], g.b[i]);
+          if (layer) {
+            e.a[i] = add2(e.a[i], both(less));
+            e.b[i] = add2(e.b[i], both(less));
           }
-          const float2 q = fma2(d.b[1], v.b[1], fma2(d.b[0], v.b[0], fma2(d.a[1], v.a[1], mul2(d.a[0], v.a[0]))));
-          const float2 s2 = both(group_sum<L>(on ? q.x + q.y : 0.f) * -inv_d);
-          if (o.norm == IBWD_NORM_LAYER) {
-            const float2 s1 = both(group_sum<L>(on ? sum_of(add2(d.a[0], d.a[1]), add2(d.b[0], d.b[1])) : 0.f) * -inv_d);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              d.a[i] = add2(d.a[i], s1);
-              d.b[i] = add2(d.b[i], s1);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            v.a[i] = mul2(fma2(v.a[i], s2, d.a[i]), both(rstd));
-            v.b[i] = mul2(fma2(v.b[i], s2, d.b[i]), both(rstd));
-          }
+          d.a[i] = fma2(xa, both(k), mul2(e.a[i], both(rstd)));
+          d.b[i] = fma2(xb, both(k), mul2(e.b[i], both(rstd)));
         }
       }
-      if (live) {
-        apart<INTER>(v, e0, e1);
-        Quad<T>::store(out.y + d0, e0);
-        Quad<T>::store(out.y + d1, e1);
-      }
+      if (live) store(d, out.y);
       out.y += y_step;
     }
+  };
+  // Whether there are more.
+  auto compute = [&](const Rows& r) {
+    if constexpr (BWD)
+      backward(r);
+    else
+      forward(r);
     out.h0 += U * side;
     if (out.h0 < o.heads) return true;
     out.h0 = 0;
