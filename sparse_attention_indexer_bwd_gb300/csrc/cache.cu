@@ -10,6 +10,9 @@
 // twice, and again at every token that raises them.
 #include <cuda_fp8.h>
 
+#include <cstring>
+#include <type_traits>
+
 #include "cache.h"
 #include "elem.cuh"
 #include "indexer_cache.h"
@@ -21,23 +24,35 @@ namespace {
 
 constexpr int kWriteThreads = 128;
 constexpr int kReadThreads = 128;
-constexpr int kReadAhead = 4;  // 16-byte loads in flight a thread
+constexpr int kReadAhead = 8;  // loads in flight a thread
 
+// Eight elements as they lie in memory; `vec`: on 16 bytes.
 template <typename T>
-__device__ __forceinline__ void load_some(const T* p, float (&v)[8], bool vec) {
-  if (vec) {
-    if constexpr (sizeof(T) == 2) {
-      unpack(*reinterpret_cast<const uint4*>(p), v, T{});
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-  } else {
+struct Chunk {
+  uint4 w[sizeof(T) / 2];
+  __device__ void load(const T* p, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = *(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+      T v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[i];
+      memcpy(w, v, sizeof(w));
+    }
   }
-}
+  __device__ void get(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      unpack(w[0], v, T{});
+    } else {
+      float a[4], b[4];
+      unpack(w[0], a, 0.f);
+      unpack(w[1], b, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    }
+  }
+};
 
 // The least power of two 2^e, e in [-126, 120], with amax <= M 2^e; amax finite.
 template <bool INT8>
@@ -50,16 +65,22 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float((uint32_t)(s + 127) << 23);
 }
 
-__device__ __forceinline__ uint32_t code4(float4 v, bool int8) {
-  if (int8) {
-    // (NaN becomes 0)
-    auto one = [](float f) { return (uint32_t)(__float2int_rn(fminf(fmaxf(f, -127.f), 127.f)) & 0xFF); };
-    auto num = [&](float f) { return f == f ? one(f) : 0u; };
-    return num(v.x) | num(v.y) << 8 | num(v.z) << 16 | num(v.w) << 24;
+// Four values in units of the scale to codes. int8: `tame` where all are numbers of at most 127, which the sum with
+// 1.5 2^23 rounds into its lowest byte; else they are limited, and NaN becomes 0.
+template <bool INT8>
+__device__ __forceinline__ uint32_t code4(float4 v, bool tame) {
+  if constexpr (INT8) {
+    if (!tame) {
+      auto limited = [](float f) { return f == f ? fminf(fmaxf(f, -127.f), 127.f) : 0.f; };
+      v = make_float4(limited(v.x), limited(v.y), limited(v.z), limited(v.w));
+    }
+    auto byte = [](float f) { return __float_as_uint(f + 12582912.f); };
+    return __byte_perm(__byte_perm(byte(v.x), byte(v.y), 0x0040), __byte_perm(byte(v.z), byte(v.w), 0x0040), 0x5410);
+  } else {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
   }
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
 }
 
 __device__ __forceinline__ float4 value4(uint32_t c, bool int8) {
@@ -90,9 +111,14 @@ __device__ __forceinline__ int last_at_most(int n, long long x, F first) {
 // One block of the cache a block of threads: blockIdx.x is the x-th of at most
 // tokens / page + 2 batch pieces (a sequence's n new tokens touch at most
 // n / page + 2 pages), y the head, z keys or values.
-template <typename T, bool INT8>
+// HOLD of a thread's chunks stay in registers between the block's largest value
+// and its codes: eight (four in fp32) are all of a page of 64 tokens of 128
+// 16-bit elements, one is all of a few tokens a sequence, whose blocks are
+// many and short (128 sequences, 8 heads: 6.8 us with eight, 4.7 with one).
+// Others are read twice.
+template <typename T, bool INT8, int HOLD>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ CacheWriteArgs a, bool vec) {
-  __shared__ uint32_t warp_max[kWriteThreads / 32];
+  __shared__ uint32_t warp_max[kWriteThreads / 32], warp_flags[kWriteThreads / 32];
   const CacheSeqs& s = a.seqs;
   const int head = blockIdx.y, kv = blockIdx.z, P = 1 << s.page_log;
   int b = blockIdx.x, piece = 0;
@@ -118,32 +144,63 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   float* scale = a.scale[kv] + block;
   const float old = s0 ? *scale : 0.f;
 
-  auto row = [&](int slot) { return x + (from + (base + slot - start)) * a.token[kv]; };
-  uint32_t most = 0;  // bits of the largest finite |x|; the highest bit: there is a NaN
-  for (int i = threadIdx.x; i < (s1 - s0) * chunks; i += kWriteThreads) {
-    const int slot = s0 + i / chunks, c = i % chunks;
+  const T* x0 = x + (from + (base + s0 - start)) * a.token[kv];  // the first slot's
+  const int count = (s1 - s0) * chunks;
+  // This thread's chunks: slot and place in it, without a division each.
+  const int slots = kWriteThreads / chunks, places = kWriteThreads % chunks;
+  const int slot0 = threadIdx.x / chunks, c0 = threadIdx.x - slot0 * chunks;
+  auto onward = [&](int& slot, int& c) {
+    slot += slots;
+    c += places;
+    if (c >= chunks) {
+      c -= chunks;
+      ++slot;
+    }
+  };
+  Chunk<T> held[HOLD];
+  uint32_t most = 0;  // bits of the largest finite |x|
+  bool nan = false, odd = false;
+  auto look = [&](const Chunk<T>& w) {
     float v[8];
-    load_some(row(slot) + 8 * c, v, vec);
+    w.get(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t m = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-      if (m < 0x7F800000u)
-        most = max(most, m);
-      else if (INT8 && m > 0x7F800000u)
-        most |= 0x80000000u;
+      most = max(most, m < 0x7F800000u ? m : 0u);
+      odd = odd || m >= 0x7F800000u;
+      if (INT8) nan = nan || m > 0x7F800000u;
     }
+  };
+  int slot = slot0, c = c0;
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    if (threadIdx.x + k * kWriteThreads < count) held[k].load(x0 + slot * a.token[kv] + 8 * c, vec);
+    onward(slot, c);
+  }
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (threadIdx.x + k * kWriteThreads < count) look(held[k]);
+  const int slot_on = slot, c_on = c;
+  for (int i = threadIdx.x + HOLD * kWriteThreads; i < count; i += kWriteThreads) {
+    Chunk<T> w;
+    w.load(x0 + slot * a.token[kv] + 8 * c, vec);
+    look(w);
+    onward(slot, c);
   }
   {
-    const bool nan = __any_sync(0xffffffffu, most >> 31);
-    uint32_t m = __reduce_max_sync(0xffffffffu, most & 0x7FFFFFFFu);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m | (nan ? 0x80000000u : 0u);
+    const unsigned flags = (__any_sync(0xffffffffu, nan) ? 2u : 0u) | (__any_sync(0xffffffffu, odd) ? 1u : 0u);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0) {
+      warp_max[threadIdx.x >> 5] = m;
+      warp_flags[threadIdx.x >> 5] = flags;
+    }
   }
   __syncthreads();
-  uint32_t m = 0, nan = 0;
+  uint32_t m = 0, flags = 0;
 #pragma unroll
   for (int w = 0; w < kWriteThreads / 32; ++w) {
-    m = max(m, warp_max[w] & 0x7FFFFFFFu);
-    nan |= warp_max[w] >> 31;
+    m = max(m, warp_max[w]);
+    flags |= warp_flags[w];
   }
   const float need = scale_for<INT8>(__uint_as_float(m));
   const float kept = s0 ? fmaxf(old, need) : need;
@@ -151,77 +208,90 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   if (s0 && old != kept) {
     const float f = old / kept;
     for (int i = threadIdx.x; i < s0 * chunks; i += kWriteThreads) {
-      uint2 c = codes[i];
-      float4 u = value4(c.x, INT8), w = value4(c.y, INT8);
+      const uint2 w = codes[i];
+      float4 u = value4(w.x, INT8), v = value4(w.y, INT8);
       u.x *= f, u.y *= f, u.z *= f, u.w *= f;
-      w.x *= f, w.y *= f, w.z *= f, w.w *= f;
-      codes[i] = make_uint2(code4(u, INT8), code4(w, INT8));
+      v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+      codes[i] = make_uint2(code4<INT8>(u, false), code4<INT8>(v, false));
     }
   }
   // a power of two has an exact inverse; a scale that someone else made is divided by
   const bool exact = (__float_as_uint(kept) & 0x7FFFFFu) == 0;
   const float inv = 1.f / kept;
-  for (int i = threadIdx.x; i < (s1 - s0) * chunks; i += kWriteThreads) {
-    const int slot = s0 + i / chunks, c = i % chunks;
+  const bool tame = !flags && __uint_as_float(m) <= 127.f * kept;
+  auto put = [&](const Chunk<T>& w, int i) {
     float v[8];
-    load_some(row(slot) + 8 * c, v, vec);
+    w.get(v);
+    if (exact) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = exact ? v[j] * inv : v[j] / kept;
-    codes[slot * chunks + c] = make_uint2(code4(make_float4(v[0], v[1], v[2], v[3]), INT8),
-                                          code4(make_float4(v[4], v[5], v[6], v[7]), INT8));
+      for (int j = 0; j < 8; ++j) v[j] *= inv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] /= kept;
+    }
+    codes[s0 * chunks + i] = make_uint2(code4<INT8>(make_float4(v[0], v[1], v[2], v[3]), tame),
+                                        code4<INT8>(make_float4(v[4], v[5], v[6], v[7]), tame));
+  };
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (threadIdx.x + k * kWriteThreads < count) put(held[k], threadIdx.x + k * kWriteThreads);
+  slot = slot_on;
+  c = c_on;
+  for (int i = threadIdx.x + HOLD * kWriteThreads; i < count; i += kWriteThreads) {
+    Chunk<T> w;
+    w.load(x0 + slot * a.token[kv] + 8 * c, vec);
+    put(w, i);
+    onward(slot, c);
   }
   // whole numbers have no NaN: the block's scale is one instead, and stays it
-  if (threadIdx.x == 0) *scale = INT8 && (nan || old != old) ? __uint_as_float(0x7FC00000u) : kept;
+  if (threadIdx.x == 0) *scale = INT8 && (flags & 2u || old != old) ? __uint_as_float(0x7FC00000u) : kept;
 }
 
-// Sixteen codes a thread, in the cache's order: a warp's reads are one run of
-// 512 bytes. x: a sequence's page, y: a head.
-template <typename T, bool INT8>
+// As many codes a lane as make 16 bytes of the result, in the cache's order: a
+// warp's reads and writes are runs of whole sectors. x: a sequence's page, y: a head.
+// LANES: the threads that share a page, a warp where it has up to 4096 codes
+// (8x8192x8 tokens of 64 in pages of 16: 20 us, a block a page 36).
+template <typename T, bool INT8, int LANES>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ CacheReadArgs a, int pages) {
   const CacheSeqs& s = a.seqs;
-  const int b = blockIdx.x / pages, index = blockIdx.x - b * pages, head = blockIdx.y, P = 1 << s.page_log;
+  const long long at = (long long)blockIdx.x * (kReadThreads / LANES) + threadIdx.x / LANES;
+  const int b = (int)(at / pages), index = (int)(at - (long long)b * pages), head = blockIdx.y, P = 1 << s.page_log;
+  if (b >= s.batch) return;
   const int base = index << s.page_log, rows = min(P, a.length - base);
   const int len = s.length(b);
   const int page = base < len ? s.page_at(b, base) : -1;
   const long long block = (long long)page * a.heads + head;
   const float scale = page >= 0 ? a.scale[block] : 0.f;
-  const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.codes) + block * P * a.dim);
-  const int chunks = a.dim >> 4;
+  constexpr int V = 16 / sizeof(T);  // codes
+  using Codes = typename std::conditional<V == 8, uint2, uint32_t>::type;
+  const Codes* codes = reinterpret_cast<const Codes*>(static_cast<const uint8_t*>(a.codes) + block * P * a.dim);
+  const int chunks = a.dim / V;
   const int total = rows * chunks, held = page < 0 ? 0 : min(rows, len - base) * chunks;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kReadAhead * kReadThreads) {
-    uint4 r[kReadAhead];
+  for (int i0 = threadIdx.x % LANES; i0 < total; i0 += kReadAhead * LANES) {
+    Codes r[kReadAhead];
 #pragma unroll
     for (int k = 0; k < kReadAhead; ++k) {
-      const int i = i0 + k * kReadThreads;
-      r[k] = i < held ? ld_stream(codes + i) : make_uint4(0, 0, 0, 0);
+      const int i = i0 + k * LANES;
+      r[k] = Codes{};
+      if (i < held) r[k] = __ldcs(codes + i);
     }
 #pragma unroll
     for (int k = 0; k < kReadAhead; ++k) {
-      const int i = i0 + k * kReadThreads, slot = i / chunks, c = i - slot * chunks;
+      const int i = i0 + k * LANES, slot = i / chunks, c = i - slot * chunks;
       if (i >= total) break;
-      T* out = static_cast<T*>(a.out) + (((long long)b * a.length + base + slot) * a.heads + head) * a.dim + 16 * c;
-      const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+      T* out = static_cast<T*>(a.out) + (((long long)b * a.length + base + slot) * a.heads + head) * a.dim + V * c;
       const float by = i < held ? scale : 0.f;  // (behind the end even where the scale is no number)
-      float4 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = value4(w[j], INT8);
-        v[j].x *= by, v[j].y *= by, v[j].z *= by, v[j].w *= by;
-      }
-      if constexpr (sizeof(T) == 2) {
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[2 * j] = pack2_of(make_float2(v[j].x, v[j].y), T{});
-          h[2 * j + 1] = pack2_of(make_float2(v[j].z, v[j].w), T{});
-        }
-        st_stream(out, make_uint4(h[0], h[1], h[2], h[3]));
-        st_stream(out + 8, make_uint4(h[4], h[5], h[6], h[7]));
+      auto scaled = [&](uint32_t w) {
+        const float4 v = value4(w, INT8);
+        return make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+      };
+      if constexpr (V == 8) {
+        const float4 v = scaled(r[k].x), w = scaled(r[k].y);
+        st_stream(out, make_uint4(pack2_of(make_float2(v.x, v.y), T{}), pack2_of(make_float2(v.z, v.w), T{}),
+                                  pack2_of(make_float2(w.x, w.y), T{}), pack2_of(make_float2(w.z, w.w), T{})));
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          st_stream(out + 4 * j, make_uint4(__float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j].z),
-                                            __float_as_uint(v[j].w)));
+        const float4 v = scaled(r[k]);
+        st_stream(out, make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)));
       }
     }
   }
@@ -247,18 +317,25 @@ cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)pieces, a.heads, kinds);
   return by_type(a.type, [&](auto t) {
     using T = decltype(t);
-    return launch_ex(a.code == IBWD_INT8 ? write_kernel<T, true> : write_kernel<T, false>, grid, kWriteThreads, 0, st, false, a,
-                     vec);
+    constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
+    auto go = [&](auto kern) { return launch_ex(kern, grid, kWriteThreads, 0, st, false, a, vec); };
+    const bool few = s.tokens * (a.dim / 8) <= (long long)kWriteThreads * s.batch;
+    if (a.code == IBWD_INT8) return few ? go(write_kernel<T, true, 1>) : go(write_kernel<T, true, kMost>);
+    return few ? go(write_kernel<T, false, 1>) : go(write_kernel<T, false, kMost>);
   });
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st) {
   const int P = 1 << a.seqs.page_log, pages = (a.length + P - 1) / P;
-  const dim3 grid((unsigned)((long long)pages * a.seqs.batch), a.heads);
+  const bool small = P * a.dim <= 4096;
+  const long long blocks = small ? ((long long)pages * a.seqs.batch + kReadThreads / 32 - 1) / (kReadThreads / 32)
+                                 : (long long)pages * a.seqs.batch;
+  const dim3 grid((unsigned)blocks, a.heads);
   return by_type(a.type, [&](auto t) {
     using T = decltype(t);
-    return launch_ex(a.code == IBWD_INT8 ? read_kernel<T, true> : read_kernel<T, false>, grid, kReadThreads, 0, st, false, a,
-                     pages);
+    auto go = [&](auto kern) { return launch_ex(kern, grid, kReadThreads, 0, st, false, a, pages); };
+    if (a.code == IBWD_INT8) return small ? go(read_kernel<T, true, 32>) : go(read_kernel<T, true, kReadThreads>);
+    return small ? go(read_kernel<T, false, 32>) : go(read_kernel<T, false, kReadThreads>);
   });
 }
 

@@ -515,10 +515,10 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
 }
 
 // Any other heads, up to 32 NE wide: a warp a row, lane l has the elements
-// l + 32 i, and a row's rotated pairs meet in shared memory.
+// l + 32 i, and a row's rotated pairs meet in shared memory. UH rows are loaded at once.
 template <typename T, int NE, bool BWD>
 __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__ HeadArgs a) {
-  constexpr int kWarps = kHeadThreads / 32;
+  constexpr int kWarps = kHeadThreads / 32, UH = NE > 4 ? 1 : BWD ? 2 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
   const HeadOp& o = a.op[which];
@@ -529,9 +529,26 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
   const int side = 1 << o.shift;
   const int hh = warp & (side - 1), tt = warp >> o.shift, step = kWarps >> o.shift;
   const float inv_d = 1.f / (float)a.D;
-  float ag[BWD ? NE : 1], ab[BWD ? NE : 1];
+  const bool normed = o.norm != IBWD_NORM_NONE, layer = o.norm == IBWD_NORM_LAYER;
+  float ag[BWD ? NE : 1], ab[BWD ? NE : 1], g[NE], bt[BWD ? 1 : NE];
+  // of each element: its pair (-1: it does not turn), its partner, and whether it is the first of the two
+  int pair[NE], other[NE];
+  unsigned first_of = 0;
 #pragma unroll
-  for (int i = 0; i < (BWD ? NE : 1); ++i) ag[i] = ab[i] = 0.f;
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 32 * i, rel = e - a.start;
+    g[i] = e < a.D && o.gamma ? weight_at(o.gamma, a.w_type, e) : 1.f;
+    if (!BWD) bt[BWD ? 0 : i] = e < a.D && o.beta ? weight_at(o.beta, a.w_type, e) : 0.f;
+    if (BWD) ag[BWD ? i : 0] = ab[BWD ? i : 0] = 0.f;
+    pair[i] = -1;
+    other[i] = 0;
+    if (e < a.D && rel >= 0 && rel < 2 * a.pairs) {
+      const bool low = a.interleaved ? !(rel & 1) : rel < a.pairs;
+      pair[i] = a.interleaved ? rel >> 1 : low ? rel : rel - a.pairs;
+      other[i] = a.start + (a.interleaved ? rel ^ 1 : low ? rel + a.pairs : rel - a.pairs);
+      if (low) first_of |= 1u << i;
+    }
+  }
 
   for (long long tile = block; tile < o.tiles; tile += o.blocks) {
     const long long first = tile * o.tokens;
@@ -540,7 +557,13 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
     __syncthreads();
     for (int t = tt; t < o.tokens && first + t < a.tokens; t += step) {
       const long long token = first + t;
-      // z turned by the token's angles, backward by minus them
+      float c[NE], s[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        c[i] = pair[i] >= 0 ? turns.cs[t * a.pairs + pair[i]] : 1.f;
+        s[i] = pair[i] >= 0 ? turns.sn[t * a.pairs + pair[i]] : 0.f;
+        if ((first_of >> i & 1) != (unsigned)BWD) s[i] = -s[i];
+      }
       auto rotate = [&](float (&z)[NE]) {
         __syncwarp();
 #pragma unroll
@@ -548,86 +571,83 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
           if (lane + 32 * i < a.D) row[lane + 32 * i] = z[i];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const int rel = lane + 32 * i - a.start;
-          if (lane + 32 * i < a.D && rel >= 0 && rel < 2 * a.pairs) {
-            const bool low = a.interleaved ? !(rel & 1) : rel < a.pairs;
-            const int p = a.interleaved ? rel >> 1 : low ? rel : rel - a.pairs;
-            const float other = row[a.start + (a.interleaved ? rel ^ 1 : low ? rel + a.pairs : p)];
-            const float c = turns.cs[t * a.pairs + p], s = turns.sn[t * a.pairs + p];
-            z[i] = fmaf(z[i], c, other * (low != BWD ? -s : s));
-          }
-        }
+        for (int i = 0; i < NE; ++i)
+          if (pair[i] >= 0) z[i] = fmaf(z[i], c[i], row[other[i]] * s[i]);
       };
-      for (int h = hh; h < o.heads; h += side) {
-        float v[NE], d[BWD ? NE : 1];
+      for (int h0 = hh; h0 < o.heads; h0 += side * UH) {
+        float x[UH][NE], dy[BWD ? UH : 1][NE];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const int e = lane + 32 * i;
-          v[i] = 0.f;
-          if (e < a.D && (!BWD || o.norm != IBWD_NORM_NONE))
-            v[i] = to_f32(static_cast<const T*>(o.x)[token * o.x_token + h * o.x_head + e]);
-          if (BWD) {
-            const long long at = token * o.dy_token + h * o.dy_head + e;
-            d[BWD ? i : 0] = e >= a.D ? 0.f
-                             : o.dy_f32 ? static_cast<const float*>(o.dy)[at]
-                                        : to_f32(static_cast<const T*>(o.dy)[at]);
-          }
-        }
-        float rstd = 1.f;
-        if (o.norm != IBWD_NORM_NONE) {
-          if (o.norm == IBWD_NORM_LAYER) {
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) m += v[i];
-            m = warp_sum(m) * inv_d;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) v[i] = lane + 32 * i < a.D ? v[i] - m : 0.f;
-          }
-          float q = 0.f;
-#pragma unroll
-          for (int i = 0; i < NE; ++i) q = fmaf(v[i], v[i], q);
-          rstd = rsqrtf(fmaf(warp_sum(q), inv_d, a.eps));
-#pragma unroll
-          for (int i = 0; i < NE; ++i) v[i] *= rstd;
-        }
-        if constexpr (!BWD) {
+        for (int u = 0; u < UH; ++u) {
+          const int h = h0 + u * side;
+          const T* px = static_cast<const T*>(o.x) + token * o.x_token + h * o.x_head + lane;
+          const long long pd = token * o.dy_token + h * o.dy_head + lane;
 #pragma unroll
           for (int i = 0; i < NE; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.D && o.norm != IBWD_NORM_NONE)
-              v[i] = fmaf(v[i], o.gamma ? weight_at(o.gamma, a.w_type, e) : 1.f,
-                          o.beta ? weight_at(o.beta, a.w_type, e) : 0.f);
-          }
-          if (a.pairs) rotate(v);
-        } else {
-          if (a.pairs) rotate(d);
-          if (o.norm == IBWD_NORM_NONE) {
-#pragma unroll
-            for (int i = 0; i < NE; ++i) v[i] = d[i];
-          } else {
-            float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-              const int e = lane + 32 * i;
-              if (e < a.D) {
-                ag[i] = fmaf(d[i], v[i], ag[i]);
-                ab[i] += d[i];
-                if (o.gamma) d[i] *= weight_at(o.gamma, a.w_type, e);
-              }
-              s1 += d[i];
-              s2 = fmaf(d[i], v[i], s2);
+            const bool on = h < o.heads && lane + 32 * i < a.D;
+            x[u][i] = 0.f;
+            if (on && (!BWD || normed)) x[u][i] = to_f32(px[32 * i]);
+            if (BWD) {
+              dy[BWD ? u : 0][i] = 0.f;
+              if (on)
+                dy[BWD ? u : 0][i] = o.dy_f32 ? static_cast<const float*>(o.dy)[pd + 32 * i] : to_f32(static_cast<const T*>(o.dy)[pd + 32 * i]);
             }
-            s1 = o.norm == IBWD_NORM_LAYER ? warp_sum(s1) * inv_d : 0.f;
-            s2 = warp_sum(s2) * inv_d;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) v[i] = rstd * (d[i] - s1 - v[i] * s2);
           }
         }
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const int e = lane + 32 * i;
-          if (e < a.D) static_cast<T*>(o.y)[token * o.y_token + h * o.y_head + e] = from_f32<T>(v[i]);
+        for (int u = 0; u < UH; ++u) {
+          const int h = h0 + u * side;
+          if (h >= o.heads) break;  // (alike in the warp)
+          float(&v)[NE] = x[u];
+          float rstd = 1.f;
+          if (normed) {
+            if (layer) {
+              float m = 0.f;
+#pragma unroll
+              for (int i = 0; i < NE; ++i) m += v[i];
+              m = warp_sum(m) * inv_d;
+#pragma unroll
+              for (int i = 0; i < NE; ++i) v[i] = lane + 32 * i < a.D ? v[i] - m : 0.f;
+            }
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) q = fmaf(v[i], v[i], q);
+            rstd = rsqrtf(fmaf(warp_sum(q), inv_d, a.eps));
+#pragma unroll
+            for (int i = 0; i < NE; ++i) v[i] *= rstd;
+          }
+          if constexpr (!BWD) {
+            if (normed)
+#pragma unroll
+              for (int i = 0; i < NE; ++i) v[i] = fmaf(v[i], g[i], bt[i]);
+            if (a.pairs) rotate(v);
+          } else {
+            float(&d)[NE] = dy[u];
+            if (a.pairs) rotate(d);
+            if (!normed) {
+#pragma unroll
+              for (int i = 0; i < NE; ++i) v[i] = d[i];
+            } else {
+              float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+              for (int i = 0; i < NE; ++i) {
+                if (lane + 32 * i < a.D) {
+                  ag[i] = fmaf(d[i], v[i], ag[i]);
+                  ab[i] += d[i];
+                  d[i] *= g[i];
+                  s1 += d[i];
+                  s2 = fmaf(d[i], v[i], s2);
+                }
+              }
+              s1 = layer ? warp_sum(s1) * inv_d : 0.f;
+              s2 = warp_sum(s2) * inv_d;
+#pragma unroll
+              for (int i = 0; i < NE; ++i) v[i] = rstd * (d[i] - s1 - v[i] * s2);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NE; ++i)
+            if (lane + 32 * i < a.D)
+              static_cast<T*>(o.y)[token * o.y_token + h * o.y_head + lane + 32 * i] = from_f32<T>(v[i]);
         }
       }
     }
