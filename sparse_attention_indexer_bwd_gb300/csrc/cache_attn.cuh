@@ -8,7 +8,7 @@
 //
 // The work is a list of tiles of 128 positions (64 for heads of 256; sequences, KV heads, row tiles,
 // positions, in that order), cut into equal runs, one a block, wherever that
-// falls, an item of any length counted as one tile more: lengths are read on the
+// falls, an item of any length counted as two tiles more: lengths are read on the
 // device, so ragged batches and single long sequences fill the SMs alike. A block joins its four warps at the end of an
 // item (a row tile of a KV head of a sequence); an item that lies in several
 // blocks is joined by a second kernel, launched programmatically behind the
@@ -44,7 +44,7 @@ namespace ibwd {
 constexpr int kAttnThreads = 128;  // four warps
 constexpr int kAttnGrid = 456;     // blocks at most, which is what the workspace holds
 constexpr float kUnit = 15.f;      // log2 of the largest weight in fp16
-constexpr int kItemCost = 1;       // what beginning and ending an item costs, in tiles
+constexpr int kItemCost = 2;       // what beginning and ending an item costs, in tiles
 
 // What a block leaves for the join: the item that it ends without having begun it.
 struct JoinRecord {
@@ -294,6 +294,16 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   uint4* queries = reinterpret_cast<uint4*>(smem + 4 * STAGES * kStage);  // [MT][D / 16][32] fragments
   float* stats = reinterpret_cast<float*>(queries + MT * D * 2);          // [4][ROWS][3]
   const int P = 1 << s.page_log;
+  // An item's queries on their way to L2, before they are asked for.
+  auto fetch_queries = [&](const Place& p) {
+    const int r = p.rt * ROWS + lane, i = r / a.group;
+    if (warp || lane >= ROWS || r >= p.rows) return;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (long long)(p.token + i) * a.q_token +
+                        (long long)(p.head * a.group + r - i * a.group) * a.q_head;
+#pragma unroll
+    for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
+  };
+  fetch_queries(c);
   // Two steps are on their way before a load: its pages (SEL: its places of the list) are looked up, then their scales (the
   // pages) are; each answer has a step's time to arrive.
   Place n = c;                  // the step that is looked up
@@ -340,16 +350,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       }
     }
     if (--ahead > 0 && n.tile + 1 == n.tiles) ahead -= kItemCost;
-    if (ahead > 0 && n.step(a) && warp == 0) {
-      // the next item's queries on their way to L2
-      const int r = n.rt * ROWS + lane, i = r / a.group;
-      if (lane < ROWS && r < n.rows) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (long long)(n.token + i) * a.q_token +
-                            (long long)(n.head * a.group + r - i * a.group) * a.q_head;
-#pragma unroll
-        for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
-      }
-    }
+    if (ahead > 0 && n.step(a)) fetch_queries(n);
   };
   const uint32_t put = stage_at<D>(lane / kRowChunks, lane % kRowChunks);
   auto load = [&](int stage) {

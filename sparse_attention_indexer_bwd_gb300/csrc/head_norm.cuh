@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
 // Any other heads, up to 32 NE wide: a warp a row, lane l has the elements
 // l + 32 i, and a row's rotated pairs meet in shared memory. UH rows are loaded at once.
 template <typename T, int NE, bool BWD>
-__global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__ HeadArgs a) {
+__global__ void __launch_bounds__(kHeadThreads, NE == 4 ? 3 : 1) head_any(const __grid_constant__ HeadArgs a) {
   constexpr int kWarps = kHeadThreads / 32, UH = NE > 4 ? 1 : BWD ? 2 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
@@ -681,8 +681,8 @@ __global__ void __launch_bounds__(kHeadThreads) head_any(const __grid_constant__
 // give a group several heads for one set of the rotation's factors; more of
 // them where that would leave SMs without a tile. All blocks are resident and
 // walk their tiles, shared out between the operands by cost.
-inline void plan_heads(HeadArgs* a, int groups, bool backward) {
-  const int resident = 2 * a->num_sms, budget = backward && resident > kHeadBlocks ? kHeadBlocks : resident;
+inline void plan_heads(HeadArgs* a, int groups, int per_sm, bool backward) {
+  const int resident = per_sm * a->num_sms, budget = backward && resident > kHeadBlocks ? kHeadBlocks : resident;
   // what a token costs an operand: its heads, and its angles, as much as about eight heads
   const int angles = a->pairs ? 8 : 1, first = a->op[0].heads + angles, both = first + a->op[1].heads + angles;
   for (int w = 0; w < 2; ++w) {
@@ -728,7 +728,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
   int lanes = 8;
   while (lanes * 8 < a.D) lanes *= 2;
   if (!rows) lanes = 32;
-  plan_heads(&a, kHeadThreads / lanes, BWD);
+  plan_heads(&a, kHeadThreads / lanes, rows ? 2 : a.D <= 128 ? 3 : 1, BWD);
   const unsigned grid = a.op[0].blocks + a.op[1].blocks;
   if (grid) {
     const int tokens = a.op[0].tokens > a.op[1].tokens ? a.op[0].tokens : a.op[1].tokens;

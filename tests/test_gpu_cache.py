@@ -291,9 +291,10 @@ def test_peaked_and_flat_logits():
         attend([700, 65], None, 2, 4, 128, 64, E4M3, scale=scale)
 
 
-def test_invisible_nan():
+@pytest.mark.parametrize("dim,heads,group", [(64, 2, 4), (64, 1, 8), (128, 2, 3), (128, 1, 8), (256, 1, 4), (256, 2, 8)])
+def test_invisible_nan(dim, heads, group):
     """NaN keys and values that some tokens see and others do not, and behind a sequence's end."""
-    page, dim, heads, group = 16, 64, 2, 4
+    page = 16
     lens, counts = [30, 40], [4, 1]
     table, pages = pages_for([48, 48], page, 1, 1)
     kc, ks = filled(pages, heads, page, dim, E4M3, 1)
@@ -340,6 +341,27 @@ def test_invisible_nan():
     keep = torch.ones((5, heads * group), dtype=torch.bool, device="cuda")
     keep[1, 2] = False
     assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1][keep], clean[1][keep])
+
+
+def test_nan_scales_of_whole_numbers():
+    """A block of int8 values whose scale is NaN is NaN for those that see it, and for nobody else."""
+    page, dim = 16, 64
+    table, pages = pages_for([48, 48], page, 0, 1)
+    kc, ks = filled(pages, 1, page, dim, INT8, 1)
+    vc, vs = filled(pages, 1, page, dim, INT8, 2)
+    q = torch.randn((4, 4, dim), device="cuda", generator=generator(3)).bfloat16()
+    dl, cu = torch.tensor([34, 40], device="cuda", dtype=torch.int32), offsets([3, 1])
+    clean = ibwd.cache_attention(q, kc, vc, ks, vs, table, dl, cu=cu)
+    for which in range(2):
+        scales = [ks.clone(), vs.clone()]
+        scales[which][table[0, 2].long()] = math.nan  # positions 32 on: tokens 1 and 2 of the first sequence see them
+        got = ibwd.cache_attention(q, kc, vc, *scales, table, dl, cu=cu)
+        for t in (0, 3):
+            assert (got[0][t].float() - clean[0][t].float()).abs().max() <= 2.0 ** -7 * clean[0][t].float().abs().max()
+            assert (got[1][t] - clean[1][t]).abs().max() <= 1e-5
+        for t in (1, 2):
+            assert torch.isnan(got[0][t]).all()
+            assert torch.isnan(got[1][t]).all() if which == 0 else torch.equal(got[1][t], clean[1][t])
 
 
 def test_rows_behind_the_last_sequence():

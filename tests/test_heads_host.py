@@ -153,6 +153,8 @@ def test_cache(lib):
     assert read(lib, length=0) == ibwd.IBWD_OK
     assert attend(lib, type_=0) == UNSUPPORTED and attend(lib, s=seqs(dim=80)) == UNSUPPORTED
     assert attend(lib, group=0) == INVALID and attend(lib, group=65536) == UNSUPPORTED
+    assert attend(lib, s=seqs(tokens=1 << 20, batch=1 << 20), group=1 << 11) == UNSUPPORTED     # more rows than are counted
+    assert attend(lib, s=seqs(cu=P, tokens=1 << 24, heads=1 << 12, table_width=1 << 26, table_stride=1 << 26)) == UNSUPPORTED
     for scale in (math.nan, math.inf, 3e38):
         assert attend(lib, scale=scale) == INVALID
     assert attend(lib, select=P, kept=0) == INVALID and attend(lib, select=P + 1, kept=4) == INVALID
