@@ -29,6 +29,13 @@ constexpr int kReadAhead = 8;  // loads in flight a thread
 // Eight elements as they lie in memory; `vec`: on 16 bytes.
 template <typename T>
 struct Chunk {
+  static constexpr uint32_t kInfinity = std::is_same<T, float>::value ? 0x7F800000u : std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+  // A magnitude's bits as fp32's.
+  __device__ static uint32_t bits_of(uint32_t m) {
+    if constexpr (std::is_same<T, float>::value) return m;
+    if constexpr (std::is_same<T, __half>::value) return __float_as_uint(unpack2(m, __half{}).x);
+    return m << 16;
+  }
   uint4 w[sizeof(T) / 2];
   __device__ void load(const T* p, bool vec) {
     if (vec) {
@@ -40,6 +47,17 @@ struct Chunk {
       for (int i = 0; i < 8; ++i) v[i] = p[i];
       memcpy(w, v, sizeof(w));
     }
+  }
+  // The largest magnitude, as its type's bits (which are in their values' order; infinities and NaN above all): of 16-bit
+  // elements in each half.
+  __device__ uint32_t most(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = sizeof(T) == 2 ? __vmaxu2(m, x[j] & 0x7FFF7FFFu) : max(m, x[j] & 0x7FFFFFFFu);
+    }
+    return m;
   }
   __device__ void get(float (&v)[8]) const {
     if constexpr (sizeof(T) == 2) {
@@ -118,7 +136,7 @@ __device__ __forceinline__ int last_at_most(int n, long long x, F first) {
 // Others are read twice.
 template <typename T, bool INT8, int HOLD>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ CacheWriteArgs a, bool vec) {
-  __shared__ uint32_t warp_max[kWriteThreads / 32], warp_flags[kWriteThreads / 32];
+  __shared__ uint32_t warp_max[kWriteThreads / 32];
   const CacheSeqs& s = a.seqs;
   const int head = blockIdx.y, kv = blockIdx.z, P = 1 << s.page_log;
   int b = blockIdx.x, piece = 0;
@@ -158,49 +176,58 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
     }
   };
   Chunk<T> held[HOLD];
-  uint32_t most = 0;  // bits of the largest finite |x|
-  bool nan = false, odd = false;
-  auto look = [&](const Chunk<T>& w) {
-    float v[8];
-    w.get(v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t m = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-      most = max(most, m < 0x7F800000u ? m : 0u);
-      odd = odd || m >= 0x7F800000u;
-      if (INT8) nan = nan || m > 0x7F800000u;
-    }
-  };
   int slot = slot0, c = c0;
 #pragma unroll
   for (int k = 0; k < HOLD; ++k) {
     if (threadIdx.x + k * kWriteThreads < count) held[k].load(x0 + slot * a.token[kv] + 8 * c, vec);
     onward(slot, c);
   }
-#pragma unroll
-  for (int k = 0; k < HOLD; ++k)
-    if (threadIdx.x + k * kWriteThreads < count) look(held[k]);
   const int slot_on = slot, c_on = c;
-  for (int i = threadIdx.x + HOLD * kWriteThreads; i < count; i += kWriteThreads) {
-    Chunk<T> w;
-    w.load(x0 + slot * a.token[kv] + 8 * c, vec);
-    look(w);
-    onward(slot, c);
-  }
-  {
-    const unsigned flags = (__any_sync(0xffffffffu, nan) ? 2u : 0u) | (__any_sync(0xffffffffu, odd) ? 1u : 0u);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, most);
-    if ((threadIdx.x & 31) == 0) {
-      warp_max[threadIdx.x >> 5] = m;
-      warp_flags[threadIdx.x >> 5] = flags;
-    }
-  }
-  __syncthreads();
-  uint32_t m = 0, flags = 0;
+  // f of every chunk of this thread
+  auto every = [&](auto f) {
 #pragma unroll
-  for (int w = 0; w < kWriteThreads / 32; ++w) {
-    m = max(m, warp_max[w]);
-    flags |= warp_flags[w];
+    for (int k = 0; k < HOLD; ++k)
+      if (threadIdx.x + k * kWriteThreads < count) f(held[k], threadIdx.x + k * kWriteThreads);
+    slot = slot_on;
+    c = c_on;
+    for (int i = threadIdx.x + HOLD * kWriteThreads; i < count; i += kWriteThreads) {
+      Chunk<T> w;
+      w.load(x0 + slot * a.token[kv] + 8 * c, vec);
+      f(w, i);
+      onward(slot, c);
+    }
+  };
+  auto block_max = [&](uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWriteThreads / 32; ++w) v = max(v, warp_max[w]);
+    return v;
+  };
+  uint32_t m = 0;
+  every([&](const Chunk<T>& w, int) { m = w.most(m); });
+  if (sizeof(T) == 2) m = max(m & 0xFFFFu, m >> 16);
+  m = block_max(m);
+  unsigned flags = 0;  // 1: there are infinities or NaN, 2: NaN in whole numbers
+  if (m < Chunk<T>::kInfinity) {
+    m = Chunk<T>::bits_of(m);
+  } else {  // the largest of the finite ones then
+    flags = 1u;
+    uint32_t finite = 0, nan = 0;
+    every([&](const Chunk<T>& w, int) {
+      float v[8];
+      w.get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        finite = max(finite, x < 0x7F800000u ? x : 0u);
+        nan |= x > 0x7F800000u;
+      }
+    });
+    m = block_max(finite);
+    if (INT8 && block_max(nan)) flags |= 2u;
   }
   const float need = scale_for<INT8>(__uint_as_float(m));
   const float kept = s0 ? fmaxf(old, need) : need;
@@ -232,17 +259,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
     codes[s0 * chunks + i] = make_uint2(code4<INT8>(make_float4(v[0], v[1], v[2], v[3]), tame),
                                         code4<INT8>(make_float4(v[4], v[5], v[6], v[7]), tame));
   };
-#pragma unroll
-  for (int k = 0; k < HOLD; ++k)
-    if (threadIdx.x + k * kWriteThreads < count) put(held[k], threadIdx.x + k * kWriteThreads);
-  slot = slot_on;
-  c = c_on;
-  for (int i = threadIdx.x + HOLD * kWriteThreads; i < count; i += kWriteThreads) {
-    Chunk<T> w;
-    w.load(x0 + slot * a.token[kv] + 8 * c, vec);
-    put(w, i);
-    onward(slot, c);
-  }
+  every(put);
   // whole numbers have no NaN: the block's scale is one instead, and stays it
   if (threadIdx.x == 0) *scale = INT8 && (flags & 2u || old != old) ? __uint_as_float(0x7FC00000u) : kept;
 }
