@@ -137,6 +137,7 @@ __device__ __forceinline__ int last_at_most(int n, long long x, F first) {
 template <typename T, bool INT8, int HOLD>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ CacheWriteArgs a, bool vec) {
   __shared__ uint32_t warp_max[kWriteThreads / 32];
+  chained();
   const CacheSeqs& s = a.seqs;
   const int head = blockIdx.y, kv = blockIdx.z, P = 1 << s.page_log;
   int b = blockIdx.x, piece = 0;
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
 // (8x8192x8 tokens of 64 in pages of 16: 20 us, a block a page 36).
 template <typename T, bool INT8, int LANES>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ CacheReadArgs a, int pages) {
+  chained();
   const CacheSeqs& s = a.seqs;
   const long long at = (long long)blockIdx.x * (kReadThreads / LANES) + threadIdx.x / LANES;
   const int b = (int)(at / pages), index = (int)(at - (long long)b * pages), head = blockIdx.y, P = 1 << s.page_log;
@@ -335,7 +337,7 @@ cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t st) {
   return by_type(a.type, [&](auto t) {
     using T = decltype(t);
     constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
-    auto go = [&](auto kern) { return launch_ex(kern, grid, kWriteThreads, 0, st, false, a, vec); };
+    auto go = [&](auto kern) { return launch_ex(kern, grid, kWriteThreads, 0, st, true, a, vec); };
     const bool few = s.tokens * (a.dim / 8) <= (long long)kWriteThreads * s.batch;
     if (a.code == IBWD_INT8) return few ? go(write_kernel<T, true, 1>) : go(write_kernel<T, true, kMost>);
     return few ? go(write_kernel<T, false, 1>) : go(write_kernel<T, false, kMost>);
@@ -350,7 +352,7 @@ cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)blocks, a.heads);
   return by_type(a.type, [&](auto t) {
     using T = decltype(t);
-    auto go = [&](auto kern) { return launch_ex(kern, grid, kReadThreads, 0, st, false, a, pages); };
+    auto go = [&](auto kern) { return launch_ex(kern, grid, kReadThreads, 0, st, true, a, pages); };
     if (a.code == IBWD_INT8) return small ? go(read_kernel<T, true, 32>) : go(read_kernel<T, true, kReadThreads>);
     return small ? go(read_kernel<T, false, 32>) : go(read_kernel<T, false, kReadThreads>);
   });

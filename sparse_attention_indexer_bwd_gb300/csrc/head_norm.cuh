@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
   constexpr int U = !BWD ? 4 : sizeof(T) == 4 ? 1 : 2;
   constexpr int kGroups = kHeadThreads / L;
   extern __shared__ __align__(16) unsigned char smem[];
+  chained();
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
   const HeadOp& o = a.op[which];
   const int block = blockIdx.x - (which ? a.op[0].blocks : 0);
@@ -480,7 +481,6 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     if (!compute(rows[1])) break;
   }
 
-  if (BWD) griddep_launch_dependents();
   if (BWD && o.norm != IBWD_NORM_NONE && (o.dgamma || o.dbeta)) {
     // the block's column sums: groups of a warp, then the warps, in a fixed order
     __syncthreads();
@@ -520,6 +520,7 @@ template <typename T, int NE, bool BWD>
 __global__ void __launch_bounds__(kHeadThreads, NE == 4 ? 3 : 1) head_any(const __grid_constant__ HeadArgs a) {
   constexpr int kWarps = kHeadThreads / 32, UH = NE > 4 ? 1 : BWD ? 2 : 4;
   extern __shared__ __align__(16) unsigned char smem[];
+  chained();
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
   const HeadOp& o = a.op[which];
   const int block = blockIdx.x - (which ? a.op[0].blocks : 0);
@@ -653,7 +654,6 @@ __global__ void __launch_bounds__(kHeadThreads, NE == 4 ? 3 : 1) head_any(const 
     }
   }
   if constexpr (BWD) {
-    griddep_launch_dependents();
     if (o.norm != IBWD_NORM_NONE && (o.dgamma || o.dbeta)) {
       __syncthreads();
       float* red = reinterpret_cast<float*>(smem);  // [warps][2][D], over the rows and the table
@@ -715,8 +715,8 @@ inline bool heads_aligned(const void* p, long long token, long long head, int si
   return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && token % 4 == 0 && head % 4 == 0);
 }
 
-// [blocks][2][D] column sums of the kernels above to dgamma and dbeta; `behind`: launched right behind them.
-cudaError_t join_heads(const HeadArgs& a, bool behind, cudaStream_t st);
+// [blocks][2][D] column sums of the kernels above to dgamma and dbeta.
+cudaError_t join_heads(const HeadArgs& a, cudaStream_t st);
 
 template <typename T, bool BWD>
 cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
@@ -737,7 +737,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
     const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * a.D * 4;
     const size_t bytes = BWD && sums > used ? sums : used;
     auto launch = [&](const HeadArgs& b, unsigned blocks, bool f32) {
-      auto go = [&](auto kern) { return launch_ex(kern, blocks, kHeadThreads, bytes, st, false, b); };
+      auto go = [&](auto kern) { return launch_ex(kern, blocks, kHeadThreads, bytes, st, true, b); };
       auto by_lanes = [&](auto dt) {
         using DT = decltype(dt);
         if (lanes == 8) return a.interleaved ? go(head_rows<T, DT, 8, BWD, true>) : go(head_rows<T, DT, 8, BWD, false>);
@@ -763,7 +763,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (!BWD) return cudaSuccess;
-  return join_heads(a, grid != 0, st);
+  return join_heads(a, st);
 }
 
 }  // namespace ibwd

@@ -173,6 +173,16 @@ __device__ __forceinline__ void dk_chunk_u16(char* u, const int* ids, uint32_t t
   }
 }
 
+// The first step of a kernel that is always launched with programmatic stream
+// serialization: whatever comes behind it may be launched now (and waits in the
+// same way, or for this kernel's end), and nothing of memory is touched before
+// what came in front of it has ended. A launch's latency is hidden behind the kernel
+// before it.
+__device__ __forceinline__ void chained() {
+  griddep_launch_dependents();
+  griddep_wait();
+}
+
 // Launch with programmatic stream serialization when pdl is set: the kernel
 // may start before the previous one on the stream completes and must call
 // griddep_wait() before reading what that one writes.

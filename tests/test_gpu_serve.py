@@ -315,3 +315,78 @@ def test_a_refused_launch_is_not_the_next_calls_error():
         for good in calls:
             good()
         torch.cuda.synchronize()
+
+
+def test_captures_with_other_work_between():
+    """Copies, another library's kernels and a second stream between the calls of a captured step."""
+    q, pos, f, w = heads_args(2, 4, 64)
+    c, s, table, _ = cache_args()
+    lens = torch.ones(2, device="cuda", dtype=torch.int32)
+    src, dst = torch.randn_like(q), torch.empty_like(q)
+    state = c.view(torch.uint8).clone(), s.clone()
+
+    def step(stream):
+        dst.copy_(src)
+        y, k = ibwd.qk_norm_rope_fwd(dst, dst[:, :2], pos, f, q_gamma=w)
+        y = y * 2
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            ibwd.cache_write(k, None, c, None, s, None, table, lens)
+        z = torch.zeros_like(y)
+        z.add_(y)
+        torch.cuda.current_stream().wait_stream(side)
+        out, lse = ibwd.cache_attention(z, c, c, s, s, table, lens)
+        back = ibwd.cache_read(c, s, table, lens, 3)
+        g = ibwd.qk_norm_rope_bwd(out, k, dst, dst[:, :2], pos, f, q_gamma=w)
+        back = back + 1
+        return y, out, lse, back, g[0], g[2], g[4]
+
+    want = [t.clone() for t in step(None)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(None)
+    for _ in range(3):
+        c.view(torch.uint8).copy_(state[0])
+        s.copy_(state[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_a_chain_that_reads_what_it_just_wrote():
+    """Each call takes the one before's result, many times without a wait: nothing may begin before it is there."""
+    q, pos, f, _ = heads_args(300, 32, 128)
+    want = q
+    for _ in range(30):
+        want, _ = ibwd.qk_norm_rope_fwd(want, None, pos, f, q_norm="none")
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = q
+        for _ in range(30):
+            got, _ = ibwd.qk_norm_rope_fwd(got, None, pos, f, q_norm="none")
+        assert torch.equal(got, want)
+    c, s, table, _ = cache_args(128)
+    lens = torch.zeros(2, device="cuda", dtype=torch.int32)
+    k = torch.randn((2, 2, 128), device="cuda").bfloat16()
+
+    def loop(wait):
+        c.view(torch.uint8).zero_()
+        s.zero_()
+        lens.zero_()
+        x, outs = k, []
+        for i in range(25):
+            lens.add_(1)
+            ibwd.cache_write(x, None, c, None, s, None, table, lens)
+            x, _ = ibwd.cache_attention(x, c, c, s, s, table, lens, scale=3.0)
+            x = ibwd.cache_read(c, s, table, lens, 32)[:, i] + x
+            outs.append(x)
+            if wait:
+                torch.cuda.synchronize()
+        return torch.stack(outs)
+
+    want = loop(True)
+    for _ in range(5):
+        assert torch.equal(loop(False), want)
