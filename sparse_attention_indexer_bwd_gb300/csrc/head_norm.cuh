@@ -20,6 +20,11 @@
 #include "indexer_train.h"
 #include "kcommon.cuh"
 #include "packed.cuh"
+#include "train.h"
+
+#include <atomic>
+#include <climits>
+#include <type_traits>
 
 namespace ibwd {
 
@@ -31,83 +36,123 @@ __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
   return to_f32(static_cast<const __half*>(w)[i]);
 }
 
-// Four elements side by side, as they lie in memory.
-template <typename T>
-struct Quad {
-  uint2 w;
-  // Two quads where `live`, into the registers that they have: loads that are selected afterwards would be waited for at once.
-  __device__ static void load(Quad (&q)[2], const T* p0, const T* p1, bool live) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t@p ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%4];\n\t"
-                 "@p ld.global.L1::no_allocate.v2.u32 {%2,%3}, [%5];\n\t}"
-                 : "+r"(q[0].w.x), "+r"(q[0].w.y), "+r"(q[1].w.x), "+r"(q[1].w.y)
-                 : "l"(p0), "l"(p1), "r"((int)live));
+// N elements side by side, as they lie in memory: 8, 16 or 32 bytes.
+template <typename T, int N>
+struct Part {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  // A thread's slot in shared memory lies in words of kChunk bytes, the threads' side by side.
+  static constexpr int kChunk = kWords == 2 ? 8 : 16, kChunks = kWords * 4 / kChunk, kStride = kChunk * kHeadThreads;
+  __device__ static void copy(uint32_t slot, const T* p) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const T* from = p + i * kChunk / (int)sizeof(T);
+      if constexpr (kChunk == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + i * kStride), "l"(from) : "memory");
+      else
+        cp_async16(slot + i * kStride, from, 16);
+    }
   }
-  __device__ void zero() { w = make_uint2(0, 0); }
-  __device__ void get(float (&v)[4]) const {
-    const float2 a = unpack2(w.x, T{}), b = unpack2(w.y, T{});
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+  __device__ void take(uint32_t slot) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if constexpr (kChunk == 8)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(slot) : "memory");
+      else
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "r"(slot + i * kStride)
+                     : "memory");
+    }
   }
-  __device__ static void store(T* p, const float (&v)[4]) {
-    const uint32_t a = pack2_of(make_float2(v[0], v[1]), T{}), b = pack2_of(make_float2(v[2], v[3]), T{});
-    asm volatile("st.global.L1::no_allocate.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(a), "r"(b) : "memory");
+  __device__ static void clear(uint32_t slot) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int k = 0; k < kChunk; k += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + i * kStride + k), "r"(0) : "memory");
   }
-};
-template <>
-struct Quad<float> {
-  uint4 w;
-  __device__ static void load(Quad (&q)[2], const float* p0, const float* p1, bool live) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %10, 0;\n\t@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%8];\n\t"
-                 "@p ld.global.L1::no_allocate.v4.u32 {%4,%5,%6,%7}, [%9];\n\t}"
-                 : "+r"(q[0].w.x), "+r"(q[0].w.y), "+r"(q[0].w.z), "+r"(q[0].w.w), "+r"(q[1].w.x), "+r"(q[1].w.y),
-                   "+r"(q[1].w.z), "+r"(q[1].w.w)
-                 : "l"(p0), "l"(p1), "r"((int)live));
+  __device__ void get(float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 a = unpack2(w[i], T{});
+        v[2 * i] = a.x, v[2 * i + 1] = a.y;
+      }
+    }
   }
-  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
-  __device__ void get(float (&v)[4]) const { unpack(w, v, 0.f); }
-  __device__ static void store(float* p, const float (&v)[4]) {
-    st_stream(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+  __device__ static void store(T* p, const float (&v)[N]) {
+    uint32_t x[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4)
+        x[i] = __float_as_uint(v[i]);
+      else
+        x[i] = pack2_of(make_float2(v[2 * i], v[2 * i + 1]), T{});
+    }
+    if constexpr (kWords == 2) {
+      asm volatile("st.global.L1::no_allocate.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(x[0]), "r"(x[1]) : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) st_stream(p + i * 4 / (int)sizeof(T), make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+    }
   }
 };
 
-// A lane's eight elements of a row: partners a_i and b_i of four pairs, packed
+// A lane's 2 N elements of a row: partners a_i and b_i of N pairs, packed
 // by twos (two fp32 an instruction).
-struct Eight {
-  float2 a[2], b[2];
+template <int N>
+struct Pairs {
+  float2 a[N / 2], b[N / 2];
 };
-// INTER: quads (a0 b0 a1 b1) and (a2 b2 a3 b3); otherwise (a0 .. a3) and (b0 .. b3).
-template <bool INTER>
-__device__ __forceinline__ Eight paired(const float (&x)[4], const float (&y)[4]) {
-  Eight e;
-  if (INTER) {
-    e.a[0] = make_float2(x[0], x[2]), e.b[0] = make_float2(x[1], x[3]);
-    e.a[1] = make_float2(y[0], y[2]), e.b[1] = make_float2(y[1], y[3]);
-  } else {
-    e.a[0] = make_float2(x[0], x[1]), e.a[1] = make_float2(x[2], x[3]);
-    e.b[0] = make_float2(y[0], y[1]), e.b[1] = make_float2(y[2], y[3]);
+// INTER: parts (a0 b0 a1 b1 ..) of the row's first half and of its second; otherwise (a0 a1 ..) and (b0 b1 ..).
+template <bool INTER, int N>
+__device__ __forceinline__ Pairs<N> paired(const float (&x)[N], const float (&y)[N]) {
+  Pairs<N> e;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if (INTER) {
+      const float* v = i < N / 4 ? x + 4 * i : y + 4 * (i - N / 4);
+      e.a[i] = make_float2(v[0], v[2]), e.b[i] = make_float2(v[1], v[3]);
+    } else {
+      e.a[i] = make_float2(x[2 * i], x[2 * i + 1]), e.b[i] = make_float2(y[2 * i], y[2 * i + 1]);
+    }
   }
   return e;
 }
-template <bool INTER>
-__device__ __forceinline__ void apart(const Eight& e, float (&x)[4], float (&y)[4]) {
-  if (INTER) {
-    x[0] = e.a[0].x, x[1] = e.b[0].x, x[2] = e.a[0].y, x[3] = e.b[0].y;
-    y[0] = e.a[1].x, y[1] = e.b[1].x, y[2] = e.a[1].y, y[3] = e.b[1].y;
-  } else {
-    x[0] = e.a[0].x, x[1] = e.a[0].y, x[2] = e.a[1].x, x[3] = e.a[1].y;
-    y[0] = e.b[0].x, y[1] = e.b[0].y, y[2] = e.b[1].x, y[3] = e.b[1].y;
+template <bool INTER, int N>
+__device__ __forceinline__ void apart(const Pairs<N>& e, float (&x)[N], float (&y)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if (INTER) {
+      float* v = i < N / 4 ? x + 4 * i : y + 4 * (i - N / 4);
+      v[0] = e.a[i].x, v[1] = e.b[i].x, v[2] = e.a[i].y, v[3] = e.b[i].y;
+    } else {
+      x[2 * i] = e.a[i].x, x[2 * i + 1] = e.a[i].y, y[2 * i] = e.b[i].x, y[2 * i + 1] = e.b[i].y;
+    }
   }
 }
-__device__ __forceinline__ float total(const Eight& v) {
-  const float2 t = add2(add2(v.a[0], v.a[1]), add2(v.b[0], v.b[1]));
-  return t.x + t.y;
-}
-__device__ __forceinline__ float product(const Eight& v, const Eight& w) {
-  const float2 t = fma2(v.b[1], w.b[1], fma2(v.b[0], w.b[0], fma2(v.a[1], w.a[1], mul2(v.a[0], w.a[0]))));
-  return t.x + t.y;
-}
-__device__ __forceinline__ void shift(Eight& v, float by) {
+template <int N>
+__device__ __forceinline__ float total(const Pairs<N>& v) {
+  float2 t = add2(v.a[0], v.b[0]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 1; i < N / 2; ++i) t = add2(t, add2(v.a[i], v.b[i]));
+  return t.x + t.y;
+}
+template <int N>
+__device__ __forceinline__ float product(const Pairs<N>& v, const Pairs<N>& w) {
+  float2 t = mul2(v.a[0], w.a[0]);
+#pragma unroll
+  for (int i = 1; i < N / 2; ++i) t = fma2(v.a[i], w.a[i], t);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) t = fma2(v.b[i], w.b[i], t);
+  return t.x + t.y;
+}
+template <int N>
+__device__ __forceinline__ void shift(Pairs<N>& v, float by) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
     v.a[i] = add2(v.a[i], both(by));
     v.b[i] = add2(v.b[i], both(by));
   }
@@ -143,7 +188,12 @@ struct Turns {
     if (token >= step) return;
     const double f = a.freq64 ? static_cast<const double*>(a.freq)[pair] : (double)static_cast<const float*>(a.freq)[pair];
     const double turns = f * 0.15915494309189533577;  // 1 / 2 pi
-    freq = (unsigned long long)((turns - floor(turns)) * 18446744073709551616.0);
+    // modulo a turn by its bits: fp64's operations are slow here
+    const long long bits = __double_as_longlong(turns);
+    const unsigned long long m = (bits & 0xFFFFFFFFFFFFFll) | 0x10000000000000ll;
+    const int by = (int)(bits >> 52 & 2047) - 1011;  // m 2^by in 2^-64 turns
+    freq = by >= 64 || by <= -64 ? 0 : by >= 0 ? m << by : m >> -by;
+    if (bits < 0) freq = 0 - freq;
     axis = a.axis_of ? a.axis_of[pair] : 0;
   }
   __device__ void fill(const HeadArgs& a, long long first, int tokens) const {
@@ -173,19 +223,37 @@ struct Turns {
   static size_t bytes(int pairs, int tokens) { return (size_t)pairs * tokens * 8; }
 };
 
-// Heads whose rows are whole quads: L lanes a row, eight elements a lane, 256 /
+// Heads whose rows are whole parts: L lanes a row, 2 N elements a lane, 256 /
 // L rows at once. A lane holds both elements of its pairs, so that a rotation is
-// within the lane: with pairs half the rotated dimensions apart it has one quad
-// of each half (two 8-byte loads of a 16-bit type), otherwise two quads side by
-// side. A group walks the heads of its tokens, U rows at once while the next U
-// are on their way, kept as they lie in memory; the weights stay in registers.
-// Arithmetic is packed, two fp32 an instruction: with single instructions, and
-// partners fetched by shuffles, 16381x32x128 took 146 us, bound by issue at
-// 16 warps an SM.
-template <typename T, typename DT, int L, bool BWD, bool INTER>
+// within the lane: with pairs half the rotated dimensions apart it has one part
+// of each half, otherwise a part of each half of the row. A group walks the heads
+// of its tokens, a few rows at once, while the next come by cp.async into a ring in
+// shared memory, each lane's own, so that nobody waits for another; the weights
+// stay in registers. Arithmetic is packed, two fp32 an instruction.
+//
+// What bounds it is instruction issue and latency at 16 warps an SM (58 to 60 %
+// of the issue slots, 19 and 34 million instructions), then HBM. 8192x40x128 in
+// bf16 takes 32 us (78 % of the copy rate) and 54 backward (69 %). One step ahead
+// in registers instead of the ring: 39 and 66. Parts of four elements instead of eight:
+// 36 forward; backward eight spill (62 us). Backward in three blocks an SM: 65; two
+// rows' sums through the shuffles together: 56. Parts side by side in a lane: 53
+// instead of 32 for adjacent pairs (half of each sector an instruction). Single
+// instructions, partners by shuffles: 146 us for 16381x32x128, now 51.
+//
+// Rows that a lane computes at once; kStages times as many are on their way or computed, 48 KB a block (72 KB for 16-bit
+// rows with fp32 gradients, where two stages are 36 us for 34). A fourth stage changes nothing.
+template <typename T, typename DT, int N, bool BWD>
+struct Ring {
+  static constexpr int kRows = !BWD ? 32 / (N * (int)sizeof(T)) : sizeof(T) == 4 ? 1 : 2;
+  static constexpr int kX = Part<T, N>::kStride * Part<T, N>::kChunks, kDy = BWD ? Part<DT, N>::kStride * Part<DT, N>::kChunks : 0;
+  static constexpr int kStage = 2 * kRows * (kX + kDy), kStages = 3;  // bytes
+};
+
+template <typename T, typename DT, int L, int N, bool BWD, bool INTER>
 __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_constant__ HeadArgs a) {
-  constexpr int U = !BWD ? 4 : sizeof(T) == 4 ? 1 : 2;
-  constexpr int kGroups = kHeadThreads / L;
+  using R = Ring<T, DT, N, BWD>;
+  constexpr int U = R::kRows;
+  constexpr int kGroups = kHeadThreads / L, kStages = R::kStages;
   extern __shared__ __align__(16) unsigned char smem[];
   chained();
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
@@ -196,55 +264,71 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
   const int li = threadIdx.x % L, group = threadIdx.x / L;
   const int side = 1 << o.shift;  // groups side by side on a token's heads
   const int hh = group & (side - 1), tt = group >> o.shift, step = kGroups >> o.shift;
-  const bool on = li * 8 < a.D;
-  // the lane's quads, its first pair, and which of its four pairs turn
-  int d0 = li * 8, d1 = li * 8 + 4, pair = 0;
+  const bool on = li * 2 * N < a.D;
+  // the lane's quads, its first pair, and which of its pairs turn
+  constexpr unsigned kAll = (1u << N) - 1;
+  // first and second parts of neighbouring lanes lie side by side: whole sectors
+  int d0, d1, pair, pair1;
   unsigned turned = 0;
   if (INTER) {
-    const int rel = d0 - a.start;
-    pair = rel / 2;
+    d0 = li * N;
+    d1 = a.D / 2 + d0;
+    pair = (d0 - a.start) / 2;
+    pair1 = (d1 - a.start) / 2 - N / 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (on && rel + 2 * i >= 0 && rel + 2 * i < 2 * a.pairs) turned |= 1u << i;
-  } else if (li < a.pairs / 4) {
-    d0 = a.start + 4 * li;
+    for (int i = 0; i < N; ++i) {
+      const int at = (i < N / 2 ? pair : pair1) + i;
+      if (on && at >= 0 && at < a.pairs) turned |= 1u << i;
+    }
+  } else if (li < a.pairs / N) {
+    d0 = a.start + N * li;
     d1 = d0 + a.pairs;
-    pair = 4 * li;
-    turned = 15u;
-  } else {  // quads that do not turn, by twos
-    auto place = [&](int k) { return 4 * (k < a.start / 4 ? k : k + a.pairs / 2); };
-    d0 = place(2 * (li - a.pairs / 4));
-    d1 = place(2 * (li - a.pairs / 4) + 1);
+    pair = pair1 = N * li;
+    turned = kAll;
+  } else {  // parts that do not turn
+    auto place = [&](int k) { return N * (k < a.start / N ? k : k + 2 * a.pairs / N); };
+    d0 = place(li - a.pairs / N);
+    d1 = place(li - a.pairs / N + (a.D - 2 * a.pairs) / (2 * N));
+    pair = pair1 = 0;
   }
   const long long apart_by = d1 - d0;
   auto weights = [&](const void* w, float none) {
-    float x[4], y[4];
+    float x[N], y[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       x[i] = on && w ? weight_at(w, a.w_type, d0 + i) : none;
       y[i] = on && w ? weight_at(w, a.w_type, d1 + i) : none;
     }
-    return paired<INTER>(x, y);
+    return paired<INTER, N>(x, y);
   };
-  const Eight g = weights(o.gamma, 1.f), bt = weights(BWD ? nullptr : o.beta, 0.f);
-  Eight ag{}, ab{};
+  const Pairs<N> g = weights(o.gamma, 1.f), bt = weights(BWD || N == 8 ? nullptr : o.beta, 0.f);
+  // wide lanes have no registers for beta: it lies behind the table, a lane's elements together
+  float* const beta = reinterpret_cast<float*>(smem) + 2 * o.tokens * a.pairs + li * 2 * N;
+  if (!BWD && N == 8 && o.beta && group == 0) {
+    const Pairs<N> e = weights(o.beta, 0.f);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      reinterpret_cast<float2*>(beta)[i] = e.a[i];
+      reinterpret_cast<float2*>(beta)[N / 2 + i] = e.b[i];
+    }
+  }
+  Pairs<N> ag{}, ab{};
   const float inv_d = 1.f / (float)a.D;
   const long long x_step = side * o.x_head, y_step = side * o.y_head, dy_step = side * o.dy_head;
 
-  // U rows of a lane. A lane without elements holds zeros; groups without a row what they had, which goes nowhere.
-  struct Rows {
-    Quad<T> x[U][2];
-    Quad<DT> dy[BWD ? U : 1][2];
-  };
-  Rows rows[2];
+  // A lane's rows on their way: kStages times U rows, each lane copies what it takes itself, so that nobody waits for
+  // another. A lane without elements holds zeros; groups without a row what was there, which goes nowhere.
+  using X = Part<T, N>;
+  using DY = Part<DT, N>;
+  constexpr int kX = R::kX, kDy = R::kDy, kStage = R::kStage;
+  const uint32_t ring = smem_u32(smem + a.ring), x_slot = ring + threadIdx.x * X::kChunk,
+                 dy_slot = ring + 2 * U * kX + threadIdx.x * DY::kChunk;
+  if (!on)
+    for (int i = 0; i < kStages; ++i)
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        rows[i].x[u][k].zero();
-        if (BWD) rows[i].dy[BWD ? u : 0][k].zero();
+      for (int k = 0; k < 2 * U; ++k) {
+        X::clear(x_slot + i * kStage + k * kX);
+        if (BWD) DY::clear(dy_slot + i * kStage + k * kDy);
       }
   const bool read_x = !BWD || o.norm != IBWD_NORM_NONE;
 
@@ -262,15 +346,23 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     in.x = static_cast<const T*>(o.x) + token * o.x_token + hh * o.x_head + d0;
     if (BWD) in.dy = static_cast<const DT*>(o.dy) + token * o.dy_token + hh * o.dy_head + d0;
   };
-  auto load = [&](Rows& r) {
+  auto load = [&](uint32_t stage) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool live = in.there && in.h0 + u * side + hh < o.heads;
-      if (read_x) Quad<T>::load(r.x[u], in.x, in.x + apart_by, live);
-      if constexpr (BWD) Quad<DT>::load(r.dy[u], in.dy, in.dy + apart_by, live);
+      if (in.there && in.h0 + u * side + hh < o.heads) {
+        if (read_x) {
+          X::copy(x_slot + stage + 2 * u * kX, in.x);
+          X::copy(x_slot + stage + (2 * u + 1) * kX, in.x + apart_by);
+        }
+        if constexpr (BWD) {
+          DY::copy(dy_slot + stage + 2 * u * kDy, in.dy);
+          DY::copy(dy_slot + stage + (2 * u + 1) * kDy, in.dy + apart_by);
+        }
+      }
       in.x += x_step;
       if (BWD) in.dy += dy_step;
     }
+    cp_async_commit();
     in.h0 += U * side;
     if (in.h0 >= o.heads) {
       in.h0 = 0;
@@ -290,38 +382,39 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     bool there;
     T* y;
   } out{block, 0, 0, false, nullptr};
-  float2 c[2], s[2], minus_s[2];
+  float2 c[N / 2], s[N / 2], minus_s[N / 2];
   auto seek_out = [&]() {
     const int t = out.t0 + tt;
     const long long token = out.tile * o.tokens + t;
     out.there = on && t < o.tokens && token < a.tokens;
     out.y = static_cast<T*>(o.y) + token * o.y_token + hh * o.y_head + d0;
-    float cc[4], ss[4];
+    float cc[N], ss[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const bool use = out.there && (turned >> i & 1);
-      cc[i] = use ? turns.cs[t * a.pairs + pair + i] : 1.f;
-      ss[i] = use ? turns.sn[t * a.pairs + pair + i] : 0.f;
+      const int at = t * a.pairs + (i < N / 2 ? pair : pair1) + i;
+      cc[i] = use ? turns.cs[at] : 1.f;
+      ss[i] = use ? turns.sn[at] : 0.f;
       if (BWD) ss[i] = -ss[i];
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N / 2; ++i) {
       c[i] = make_float2(cc[2 * i], cc[2 * i + 1]);
       s[i] = make_float2(ss[2 * i], ss[2 * i + 1]);
       minus_s[i] = make_float2(-ss[2 * i], -ss[2 * i + 1]);
     }
   };
-  auto store = [&](const Eight& v, T* y) {
-    float e0[4], e1[4];
-    apart<INTER>(v, e0, e1);
-    Quad<T>::store(y, e0);
-    Quad<T>::store(y + apart_by, e1);
+  auto store = [&](const Pairs<N>& v, T* y) {
+    float e0[N], e1[N];
+    apart<INTER, N>(v, e0, e1);
+    Part<T, N>::store(y, e0);
+    Part<T, N>::store(y + apart_by, e1);
   };
   // y_a = z_a c - z_b s, y_b = z_b c + z_a s, where the pair turns: a rotation may begin or end within the lane
-  auto rotate = [&](Eight& z) {
-    if (turned == 15u) {
+  auto rotate = [&](Pairs<N>& z) {
+    if (turned == kAll) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N / 2; ++i) {
         const float2 u = z.a[i], v = z.b[i];
         z.a[i] = fma2(v, minus_s[i], mul2(u, c[i]));
         z.b[i] = fma2(u, s[i], mul2(v, c[i]));
@@ -334,22 +427,26 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
           v = fmaf(w, sn, v * cs);
         }
       };
-      one(1u, z.a[0].x, z.b[0].x, c[0].x, s[0].x);
-      one(2u, z.a[0].y, z.b[0].y, c[0].y, s[0].y);
-      one(4u, z.a[1].x, z.b[1].x, c[1].x, s[1].x);
-      one(8u, z.a[1].y, z.b[1].y, c[1].y, s[1].y);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        one(1u << 2 * i, z.a[i].x, z.b[i].x, c[i].x, s[i].x);
+        one(2u << 2 * i, z.a[i].y, z.b[i].y, c[i].y, s[i].y);
+      }
     }
   };
-  auto elements = [&](const Quad<T> (&x)[2]) {
-    float e0[4], e1[4];
-    x[0].get(e0);
-    x[1].get(e1);
-    return paired<INTER>(e0, e1);
+  auto two = [&](auto part, uint32_t slot, int apart) {
+    float e0[N], e1[N];
+    part.take(slot);
+    part.get(e0);
+    part.take(slot + apart);
+    part.get(e1);
+    return paired<INTER, N>(e0, e1);
   };
+  auto elements = [&](uint32_t stage, int u) { return two(X{}, x_slot + stage + 2 * u * kX, kX); };
   const bool layer = o.norm == IBWD_NORM_LAYER, normed = o.norm != IBWD_NORM_NONE;
-  // Rows beyond the heads are computed with what the registers hold, and go nowhere. Forward, the sums of all U rows go
-  // through the shuffles together, and the elements are taken apart once more behind them (row after row: 42 us for 40).
-  auto forward = [&](const Rows& r) {
+  // Rows beyond the heads are computed with what the ring holds, and go nowhere. Forward, the sums of all U rows go
+  // through the shuffles together, and the elements are taken apart once more behind them.
+  auto forward = [&](uint32_t stage) {
     float rstd[U], minus[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -359,14 +456,14 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     if (normed) {
       if (layer) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) minus[u] = total(elements(r.x[u]));
+        for (int u = 0; u < U; ++u) minus[u] = total(elements(stage, u));
         group_sums<L>(minus);
 #pragma unroll
         for (int u = 0; u < U; ++u) minus[u] = on ? minus[u] * -inv_d : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        Eight v = elements(r.x[u]);
+        Pairs<N> v = elements(stage, u);
         if (layer) shift(v, minus[u]);
         rstd[u] = product(v, v);
       }
@@ -376,13 +473,26 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      Eight v = elements(r.x[u]);
+      Pairs<N> v = elements(stage, u);
       if (layer) shift(v, minus[u]);
       if (normed) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          v.a[i] = fma2(mul2(v.a[i], both(rstd[u])), g.a[i], bt.a[i]);
-          v.b[i] = fma2(mul2(v.b[i], both(rstd[u])), g.b[i], bt.b[i]);
+        for (int i = 0; i < N / 2; ++i) {
+          v.a[i] = mul2(v.a[i], both(rstd[u]));
+          v.b[i] = mul2(v.b[i], both(rstd[u]));
+        }
+        if (N == 8 && !o.beta) {
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            v.a[i] = mul2(v.a[i], g.a[i]);
+            v.b[i] = mul2(v.b[i], g.b[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            v.a[i] = fma2(v.a[i], g.a[i], N == 8 ? reinterpret_cast<const float2*>(beta)[i] : bt.a[i]);
+            v.b[i] = fma2(v.b[i], g.b[i], N == 8 ? reinterpret_cast<const float2*>(beta)[N / 2 + i] : bt.b[i]);
+          }
         }
       }
       rotate(v);
@@ -390,27 +500,24 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
       out.y += y_step;
     }
   };
-  // Backward, row after row (two at once spill: 82 us for 66 at 8192x40x128 bf16), its sums together: with v = x (layer: x - mean),
+  // Backward, row after row, its sums together: with v = x (layer: x - mean),
   // dx = rstd (d - sum(d)/D) - xh (rstd^2 sum(d v)/D).
-  auto backward = [&](const Rows& r) {
+  auto backward = [&](uint32_t stage) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool live = out.there && out.h0 + u * side + hh < o.heads;
-      float e0[4], e1[4];
-      r.dy[u][0].get(e0);
-      r.dy[u][1].get(e1);
-      Eight d = paired<INTER>(e0, e1);
+      Pairs<N> d = two(DY{}, dy_slot + stage + 2 * u * kDy, kDy);
       rotate(d);
       if (normed) {
-        Eight v = elements(r.x[u]);
+        Pairs<N> v = elements(stage, u);
         if (layer) {
           float m[1] = {total(v)};
           group_sums<L>(m);
           shift(v, on ? m[0] * -inv_d : 0.f);
         }
-        Eight e;  // d gamma
+        Pairs<N> e;  // d gamma
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < N / 2; ++i) {
           e.a[i] = mul2(d.a[i], g.a[i]);
           e.b[i] = mul2(d.b[i], g.b[i]);
         }
@@ -425,7 +532,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
         }
         const float rstd = rsqrtf(fmaf(sums[0], inv_d, a.eps)), k = rstd * (rstd * sums[1] * -inv_d), less = sums[2] * -inv_d;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < N / 2; ++i) {
           const float2 xa = mul2(v.a[i], both(rstd)), xb = mul2(v.b[i], both(rstd));
           if (live) {
             ag.a[i] = fma2(d.a[i], xa, ag.a[i]);
@@ -448,11 +555,11 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     }
   };
   // Whether there are more.
-  auto compute = [&](const Rows& r) {
+  auto compute = [&](uint32_t stage) {
     if constexpr (BWD)
-      backward(r);
+      backward(stage);
     else
-      forward(r);
+      forward(stage);
     out.h0 += U * side;
     if (out.h0 < o.heads) return true;
     out.h0 = 0;
@@ -470,39 +577,42 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
   };
 
   seek_in();
-  load(rows[0]);  // (they come while the angles are computed)
+  // (they come while the angles are computed)
+  for (int i = 0; i < kStages - 1; ++i) load(i * kStage);
   turns.fill(a, out.tile * o.tokens, o.tokens);
   __syncthreads();
   seek_out();
+  uint32_t next = (kStages - 1) * kStage, at = 0;
   while (true) {
-    load(rows[1]);
-    if (!compute(rows[0])) break;
-    load(rows[0]);
-    if (!compute(rows[1])) break;
+    load(next);
+    next = next == (kStages - 1) * kStage ? 0 : next + kStage;
+    cp_async_wait<kStages - 1>();
+    if (!compute(at)) break;
+    at = at == (kStages - 1) * kStage ? 0 : at + kStage;
   }
 
   if (BWD && o.norm != IBWD_NORM_NONE && (o.dgamma || o.dbeta)) {
     // the block's column sums: groups of a warp, then the warps, in a fixed order
     __syncthreads();
     float* red = reinterpret_cast<float*>(smem);  // [warps][2][D]
-    float x[2][8];
+    float x[2][2 * N];
     {
-      float p[4], r[4];
-      apart<INTER>(ag, p, r);
+      float p[N], r[N];
+      apart<INTER, N>(ag, p, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[0][i] = p[i], x[0][4 + i] = r[i];
-      apart<INTER>(ab, p, r);
+      for (int i = 0; i < N; ++i) x[0][i] = p[i], x[0][N + i] = r[i];
+      apart<INTER, N>(ab, p, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[1][i] = p[i], x[1][4 + i] = r[i];
+      for (int i = 0; i < N; ++i) x[1][i] = p[i], x[1][N + i] = r[i];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 2 * N; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int w = L; w < 32; w <<= 1) x[k][i] += __shfl_xor_sync(0xffffffffu, x[k][i], w);
         if (on && (threadIdx.x & 31) < L)
-          red[((threadIdx.x >> 5) * 2 + k) * a.D + (i < 4 ? d0 + i : d1 + i - 4)] = x[k][i];
+          red[((threadIdx.x >> 5) * 2 + k) * a.D + (i < N ? d0 + i : d1 + i - N)] = x[k][i];
       }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.D; i += kHeadThreads) {
@@ -681,10 +791,10 @@ __global__ void __launch_bounds__(kHeadThreads, NE == 4 ? 3 : 1) head_any(const 
 // give a group several heads for one set of the rotation's factors; more of
 // them where that would leave SMs without a tile. All blocks are resident and
 // walk their tiles, shared out between the operands by cost.
-inline void plan_heads(HeadArgs* a, int groups, int per_sm, bool backward) {
+inline void plan_heads(HeadArgs* a, int groups, int per_sm, int side_by, bool backward) {
   const int resident = per_sm * a->num_sms, budget = backward && resident > kHeadBlocks ? kHeadBlocks : resident;
   // what a token costs an operand: its heads, and its angles, as much as about eight heads
-  const int angles = a->pairs ? 8 : 1, first = a->op[0].heads + angles, both = first + a->op[1].heads + angles;
+  const int angles = a->pairs ? 8 : 1;
   for (int w = 0; w < 2; ++w) {
     HeadOp& o = a->op[w];
     o.shift = 0;
@@ -692,7 +802,7 @@ inline void plan_heads(HeadArgs* a, int groups, int per_sm, bool backward) {
     o.blocks = 0;
     o.tiles = 0;
     if (!o.heads || !a->tokens) continue;
-    while ((1 << (o.shift + 1)) <= groups && (16 << (o.shift + 1)) <= o.heads) ++o.shift;
+    while ((1 << (o.shift + 1)) <= groups && (side_by << (o.shift + 1)) <= o.heads) ++o.shift;
     auto tiles = [&](int tokens) { return (a->tokens + tokens - 1) / tokens; };
     while ((1 << o.shift) < groups && (1 << o.shift) < o.heads && tiles(groups >> o.shift) < a->num_sms) ++o.shift;
     o.tokens = groups >> o.shift;
@@ -700,19 +810,32 @@ inline void plan_heads(HeadArgs* a, int groups, int per_sm, bool backward) {
     const int rows = (o.heads + (1 << o.shift) - 1) >> o.shift;
     for (int m = rows; m < 8 && tiles(2 * o.tokens) >= 4 * a->num_sms && 2 * o.tokens * a->pairs <= 2048; m *= 2) o.tokens *= 2;
     o.tiles = tiles(o.tokens);
-    int share = budget;
-    if (a->op[0].heads && a->op[1].heads) {
-      share = (int)((long long)budget * first / both);
-      share = share < 1 ? 1 : share > budget - 1 ? budget - 1 : share;
-      if (w) share = budget - share;
+    o.blocks = (int)(o.tiles < budget ? o.tiles : budget);
+  }
+  HeadOp &q = a->op[0], &k = a->op[1];
+  if (q.tiles + k.tiles <= budget || !q.tiles || !k.tiles) return;
+  // The split whose longest blocks take least: whole tiles, so that one operand's blocks all have as many, or the other's.
+  const long long costs[2] = {q.tokens * (q.heads + angles), k.tokens * (k.heads + angles)};
+  long long least = LLONG_MAX;
+  auto turns = [](long long n, long long by) { return (n + by - 1) / by; };
+  for (int w = 0; w < 2; ++w) {
+    const long long n = a->op[w].tiles, m = a->op[1 - w].tiles;
+    const long long ideal = (n * costs[w] + m * costs[1 - w]) / (budget * costs[w]);
+    for (long long r = ideal > 1 ? ideal : 1; r <= ideal + 2; ++r) {
+      const long long mine = turns(n, r), rest = budget - mine < m ? budget - mine : m;
+      if (rest < 1) continue;
+      const long long t = turns(m, rest) * costs[1 - w], most = r * costs[w] > t ? r * costs[w] : t;
+      if (most >= least) continue;
+      least = most;
+      a->op[w].blocks = (int)mine;
+      a->op[1 - w].blocks = (int)rest;
     }
-    o.blocks = (int)(o.tiles < share ? o.tiles : share);
   }
 }
 
-// Whether every row of an operand is whole quads.
-inline bool heads_aligned(const void* p, long long token, long long head, int size) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && token % 4 == 0 && head % 4 == 0);
+// Whether every row of an operand is whole parts of n elements.
+inline bool heads_aligned(const void* p, long long token, long long head, int size, int n) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (n * size < 16 ? n * size : 16) == 0 && token % n == 0 && head % n == 0);
 }
 
 // [blocks][2][D] column sums of the kernels above to dgamma and dbeta.
@@ -720,29 +843,55 @@ cudaError_t join_heads(const HeadArgs& a, cudaStream_t st);
 
 template <typename T, bool BWD>
 cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
-  bool rows = a.D % 8 == 0 && a.D <= 256 && (a.interleaved ? a.start % 2 == 0 : a.start % 4 == 0 && a.pairs % 4 == 0);
-  for (const HeadOp& o : a.op)
-    if (o.heads)
-      rows = rows && heads_aligned(o.x, o.x_token, o.x_head, sizeof(T)) && heads_aligned(o.y, o.y_token, o.y_head, sizeof(T)) &&
-             (!BWD || heads_aligned(o.dy, o.dy_token, o.dy_head, o.dy_f32 ? 4 : (int)sizeof(T)));
-  int lanes = 8;
-  while (lanes * 8 < a.D) lanes *= 2;
+  auto whole = [&](int n) {
+    bool is = a.D % (2 * n) == 0 && a.D <= 256 && (a.interleaved ? a.start % 2 == 0 : a.start % n == 0 && a.pairs % n == 0);
+    for (const HeadOp& o : a.op)
+      if (o.heads)
+        is = is && heads_aligned(o.x, o.x_token, o.x_head, sizeof(T), n) && heads_aligned(o.y, o.y_token, o.y_head, sizeof(T), n) &&
+             (!BWD || heads_aligned(o.dy, o.dy_token, o.dy_head, o.dy_f32 ? 4 : (int)sizeof(T), n));
+    return is;
+  };
+  // Wide lanes have 16 elements' weights to load first: 320 rows take 3.4 us, with them 3.9; 5120 4.6 and 4.7; 16384
+  // 13.0 and 11.2; 327680 36 and 32.
+  const bool rows = whole(4), wide = !BWD && sizeof(T) == 2 && a.tokens * (a.op[0].heads + a.op[1].heads) >= 8192 && whole(8);
+  int lanes = wide ? 4 : 8;
+  while (lanes * (wide ? 16 : 8) < a.D) lanes *= 2;
   if (!rows) lanes = 32;
-  plan_heads(&a, kHeadThreads / lanes, rows ? 2 : a.D <= 128 ? 3 : 1, BWD);
+  plan_heads(&a, kHeadThreads / lanes, rows ? 2 : a.D <= 128 ? 3 : 1, wide ? 8 : 16, BWD);
   const unsigned grid = a.op[0].blocks + a.op[1].blocks;
   if (grid) {
     const int tokens = a.op[0].tokens > a.op[1].tokens ? a.op[0].tokens : a.op[1].tokens;
-    const size_t table = Turns::bytes(a.pairs, tokens), sums = (size_t)(kHeadThreads / 32) * 2 * a.D * 4;
-    // at most 36 KB, which a launch has without asking: 512 wide rows, and 2048 pairs' factors
+    const size_t table = Turns::bytes(a.pairs, tokens) + (wide ? lanes * 64 : 0), sums = (size_t)(kHeadThreads / 32) * 2 * a.D * 4;
     const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * a.D * 4;
-    const size_t bytes = BWD && sums > used ? sums : used;
+    const size_t base = ((BWD && sums > used ? sums : used) + 15) / 16 * 16;  // at most 36 KB
+    a.ring = (int)base;
     auto launch = [&](const HeadArgs& b, unsigned blocks, bool f32) {
-      auto go = [&](auto kern) { return launch_ex(kern, blocks, kHeadThreads, bytes, st, true, b); };
+      auto go = [&](auto kern) { return launch_ex(kern, blocks, kHeadThreads, base, st, true, b); };
       auto by_lanes = [&](auto dt) {
         using DT = decltype(dt);
-        if (lanes == 8) return a.interleaved ? go(head_rows<T, DT, 8, BWD, true>) : go(head_rows<T, DT, 8, BWD, false>);
-        if (lanes == 16) return a.interleaved ? go(head_rows<T, DT, 16, BWD, true>) : go(head_rows<T, DT, 16, BWD, false>);
-        return a.interleaved ? go(head_rows<T, DT, 32, BWD, true>) : go(head_rows<T, DT, 32, BWD, false>);
+        auto ringed = [&](auto lanes_of, auto n, auto inter) {
+          constexpr int L = decltype(lanes_of)::value, N = decltype(n)::value;
+          constexpr bool INTER = decltype(inter)::value;
+          static std::atomic<size_t> done[64];
+          const auto kern = head_rows<T, DT, L, N, BWD, INTER>;
+          const size_t bytes = base + (size_t)Ring<T, DT, N, BWD>::kStages * Ring<T, DT, N, BWD>::kStage;
+          const cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), bytes, done);
+          return e != cudaSuccess ? e : launch_ex(kern, blocks, kHeadThreads, bytes, st, true, b);
+        };
+        auto by_inter = [&](auto lanes_of, auto n) {
+          return a.interleaved ? ringed(lanes_of, n, std::true_type{}) : ringed(lanes_of, n, std::false_type{});
+        };
+        if constexpr (!BWD && sizeof(T) == 2)
+          if (wide) {
+            constexpr std::integral_constant<int, 8> n{};
+            if (lanes == 4) return by_inter(std::integral_constant<int, 4>{}, n);
+            if (lanes == 8) return by_inter(std::integral_constant<int, 8>{}, n);
+            return by_inter(std::integral_constant<int, 16>{}, n);
+          }
+        constexpr std::integral_constant<int, 4> n{};
+        if (lanes == 8) return by_inter(std::integral_constant<int, 8>{}, n);
+        if (lanes == 16) return by_inter(std::integral_constant<int, 16>{}, n);
+        return by_inter(std::integral_constant<int, 32>{}, n);
       };
       if (!rows) return a.D <= 128 ? go(head_any<T, 4, BWD>) : go(head_any<T, 16, BWD>);
       if constexpr (BWD)

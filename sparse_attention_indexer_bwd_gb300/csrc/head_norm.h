@@ -38,6 +38,7 @@ struct HeadArgs {
   float eps;
   float* part;  // workspace: [blocks][2][D] column sums
   int num_sms;
+  int ring;  // where the ring of rows begins in shared memory
 };
 
 // Blocks of a backward pass at most, which is what its workspace holds.

@@ -96,6 +96,22 @@ def test_many_rows(tokens, heads, kv, dim):
     run(q, k, pos, frequencies(dim // 2), "rms", "layer")
 
 
+@pytest.mark.parametrize("dim", [16, 32, 48, 64, 80, 128, 144, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_many_rows_of_whole_parts(dim, kind):
+    """Enough rows for sixteen elements a lane, in every form that has them, and those next to them."""
+    tokens = 1031
+    for heads, kv in ((8, 1), (3, 5)):
+        q, k = make(tokens, heads, dim, DTYPES[kind], 1, 8, 8), make(tokens, kv, dim, DTYPES[kind], 2)
+        pos = torch.randint(0, 1 << 20, (tokens,), device="cuda", generator=generator(4))
+        for pairs in {dim // 2, dim // 4, 8, dim // 4 * 2 - 4, 1}:
+            for start in {0, 8, 2, dim - 2 * pairs}:
+                if 2 * pairs + start <= dim:
+                    for inter in (False, True):
+                        run(q, k, pos, frequencies(pairs), *(("rms", "layer") if heads == 8 else ("layer", "none")), start=start,
+                            interleaved=inter)
+
+
 @pytest.mark.parametrize("pad,at", [(256, 0), (256, 128), (8, 8), (3, 1), (1, 0)])
 def test_heads_within_a_wider_buffer(pad, at):
     for dim in (64, 128, 20):
