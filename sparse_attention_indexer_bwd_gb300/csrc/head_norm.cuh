@@ -624,19 +624,40 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
   }
 }
 
+// UH rows of a warp, a head every `side`. Every lane loads, places beyond the row or the heads what the last one holds: a
+// load under a condition is waited for before the next.
+template <typename E, int NE, int UH>
+__device__ __forceinline__ void load_any(const void* from, long long token, long long of_head, int h0, int side, int heads, int D,
+                                         float (&to)[UH][NE]) {
+#pragma unroll
+  for (int u = 0; u < UH; ++u) {
+    const E* p = static_cast<const E*>(from) + token + min(h0 + u * side, heads - 1) * of_head;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) to[u][i] = to_f32(p[min((int)(threadIdx.x & 31) + 32 * i, D - 1)]);
+  }
+}
+
 // Any other heads, up to 32 NE wide: a warp a row, lane l has the elements
-// l + 32 i, and a row's rotated pairs meet in shared memory. UH rows are loaded at once.
+// l + 32 i, and a row's rotated pairs meet in shared memory. kRows rows are
+// loaded at once, and their sums and their pairs meet at once: bound by the
+// latency of these steps. 8192x40x127 in bf16 takes 76 us and 127 backward (33
+// and 29 % of the copy rate); row after row in three blocks an SM 140 and 204;
+// loads under a condition 150 and 407.
+template <int NE, bool BWD>
+struct AnyHeads {
+  static constexpr int kRows = NE >= 16 ? 1 : NE == 8 ? 2 - BWD : 4, kBlocks = NE >= 16 ? 1 : NE >= 4 ? 2 : 3;
+};
 template <typename T, int NE, bool BWD>
-__global__ void __launch_bounds__(kHeadThreads, NE == 4 ? 3 : 1) head_any(const __grid_constant__ HeadArgs a) {
-  constexpr int kWarps = kHeadThreads / 32, UH = NE > 4 ? 1 : BWD ? 2 : 4;
+__global__ void __launch_bounds__(kHeadThreads, AnyHeads<NE, BWD>::kBlocks) head_any(const __grid_constant__ HeadArgs a) {
+  constexpr int kWarps = kHeadThreads / 32, UH = AnyHeads<NE, BWD>::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
   chained();
   const int which = blockIdx.x >= (unsigned)a.op[0].blocks;
   const HeadOp& o = a.op[which];
   const int block = blockIdx.x - (which ? a.op[0].blocks : 0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = reinterpret_cast<float*>(smem) + warp * a.D;
-  const Turns turns(smem + (size_t)kWarps * a.D * 4, a, o.tokens);
+  float* row = reinterpret_cast<float*>(smem) + warp * UH * a.D;
+  const Turns turns(smem + (size_t)kWarps * UH * a.D * 4, a, o.tokens);
   const int side = 1 << o.shift;
   const int hh = warp & (side - 1), tt = warp >> o.shift, step = kWarps >> o.shift;
   const float inv_d = 1.f / (float)a.D;
@@ -675,90 +696,114 @@ __global__ void __launch_bounds__(kHeadThreads, NE == 4 ? 3 : 1) head_any(const 
         s[i] = pair[i] >= 0 ? turns.sn[t * a.pairs + pair[i]] : 0.f;
         if ((first_of >> i & 1) != (unsigned)BWD) s[i] = -s[i];
       }
-      auto rotate = [&](float (&z)[NE]) {
+      auto rotate = [&](float (&z)[UH][NE]) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-          if (lane + 32 * i < a.D) row[lane + 32 * i] = z[i];
+        for (int u = 0; u < UH; ++u)
+#pragma unroll
+          for (int i = 0; i < NE; ++i)
+            if (lane + 32 * i < a.D) row[u * a.D + lane + 32 * i] = z[u][i];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-          if (pair[i] >= 0) z[i] = fmaf(z[i], c[i], row[other[i]] * s[i]);
+        for (int u = 0; u < UH; ++u)
+#pragma unroll
+          for (int i = 0; i < NE; ++i)
+            if (pair[i] >= 0) z[u][i] = fmaf(z[u][i], c[i], row[u * a.D + other[i]] * s[i]);
       };
       for (int h0 = hh; h0 < o.heads; h0 += side * UH) {
-        float x[UH][NE], dy[BWD ? UH : 1][NE];
+        float x[UH][NE], dy[UH][NE];
+        if (!BWD || normed) load_any<T, NE, UH>(o.x, token * o.x_token, o.x_head, h0, side, o.heads, a.D, x);
+        if constexpr (BWD) {
+          if (o.dy_f32)
+            load_any<float, NE, UH>(o.dy, token * o.dy_token, o.dy_head, h0, side, o.heads, a.D, dy);
+          else
+            load_any<T, NE, UH>(o.dy, token * o.dy_token, o.dy_head, h0, side, o.heads, a.D, dy);
+        }
 #pragma unroll
-        for (int u = 0; u < UH; ++u) {
-          const int h = h0 + u * side;
-          const T* px = static_cast<const T*>(o.x) + token * o.x_token + h * o.x_head + lane;
-          const long long pd = token * o.dy_token + h * o.dy_head + lane;
+        for (int u = 0; u < UH; ++u)
 #pragma unroll
-          for (int i = 0; i < NE; ++i) {
-            const bool on = h < o.heads && lane + 32 * i < a.D;
-            x[u][i] = 0.f;
-            if (on && (!BWD || normed)) x[u][i] = to_f32(px[32 * i]);
-            if (BWD) {
-              dy[BWD ? u : 0][i] = 0.f;
-              if (on)
-                dy[BWD ? u : 0][i] = o.dy_f32 ? static_cast<const float*>(o.dy)[pd + 32 * i] : to_f32(static_cast<const T*>(o.dy)[pd + 32 * i]);
+          for (int i = 0; i < NE; ++i)
+            if (lane + 32 * i >= a.D) {
+              x[u][i] = 0.f;
+              if (BWD) dy[u][i] = 0.f;
             }
+        float rstd[UH];
+        if (normed) {
+          if (layer) {
+            float m[UH];
+#pragma unroll
+            for (int u = 0; u < UH; ++u) {
+              m[u] = 0.f;
+#pragma unroll
+              for (int i = 0; i < NE; ++i) m[u] += x[u][i];
+            }
+            group_sums<32>(m);
+#pragma unroll
+            for (int u = 0; u < UH; ++u)
+#pragma unroll
+              for (int i = 0; i < NE; ++i) x[u][i] = lane + 32 * i < a.D ? fmaf(m[u], -inv_d, x[u][i]) : 0.f;
+          }
+#pragma unroll
+          for (int u = 0; u < UH; ++u) {
+            rstd[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) rstd[u] = fmaf(x[u][i], x[u][i], rstd[u]);
+          }
+          group_sums<32>(rstd);
+#pragma unroll
+          for (int u = 0; u < UH; ++u) {
+            rstd[u] = rsqrtf(fmaf(rstd[u], inv_d, a.eps));
+#pragma unroll
+            for (int i = 0; i < NE; ++i) x[u][i] *= rstd[u];
+          }
+        }
+        if constexpr (!BWD) {
+          if (normed)
+#pragma unroll
+            for (int u = 0; u < UH; ++u)
+#pragma unroll
+              for (int i = 0; i < NE; ++i) x[u][i] = fmaf(x[u][i], g[i], bt[i]);
+          if (a.pairs) rotate(x);
+        } else {
+          if (a.pairs) rotate(dy);
+          if (!normed) {
+#pragma unroll
+            for (int u = 0; u < UH; ++u)
+#pragma unroll
+              for (int i = 0; i < NE; ++i) x[u][i] = dy[u][i];
+          } else {
+            float s1[UH], s2[UH];
+#pragma unroll
+            for (int u = 0; u < UH; ++u) {
+              s1[u] = s2[u] = 0.f;
+              const bool live = h0 + u * side < o.heads;
+#pragma unroll
+              for (int i = 0; i < NE; ++i) {
+                if (live) {
+                  ag[i] = fmaf(dy[u][i], x[u][i], ag[i]);
+                  ab[i] += dy[u][i];
+                }
+                dy[u][i] *= g[i];
+                s1[u] += dy[u][i];
+                s2[u] = fmaf(dy[u][i], x[u][i], s2[u]);
+              }
+            }
+            if (layer) group_sums<32>(s1);
+            group_sums<32>(s2);
+#pragma unroll
+            for (int u = 0; u < UH; ++u)
+#pragma unroll
+              for (int i = 0; i < NE; ++i)
+                x[u][i] = rstd[u] * (dy[u][i] - (layer ? s1[u] * inv_d : 0.f) - x[u][i] * (s2[u] * inv_d));
           }
         }
 #pragma unroll
         for (int u = 0; u < UH; ++u) {
           const int h = h0 + u * side;
-          if (h >= o.heads) break;  // (alike in the warp)
-          float(&v)[NE] = x[u];
-          float rstd = 1.f;
-          if (normed) {
-            if (layer) {
-              float m = 0.f;
-#pragma unroll
-              for (int i = 0; i < NE; ++i) m += v[i];
-              m = warp_sum(m) * inv_d;
-#pragma unroll
-              for (int i = 0; i < NE; ++i) v[i] = lane + 32 * i < a.D ? v[i] - m : 0.f;
-            }
-            float q = 0.f;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) q = fmaf(v[i], v[i], q);
-            rstd = rsqrtf(fmaf(warp_sum(q), inv_d, a.eps));
-#pragma unroll
-            for (int i = 0; i < NE; ++i) v[i] *= rstd;
-          }
-          if constexpr (!BWD) {
-            if (normed)
-#pragma unroll
-              for (int i = 0; i < NE; ++i) v[i] = fmaf(v[i], g[i], bt[i]);
-            if (a.pairs) rotate(v);
-          } else {
-            float(&d)[NE] = dy[u];
-            if (a.pairs) rotate(d);
-            if (!normed) {
-#pragma unroll
-              for (int i = 0; i < NE; ++i) v[i] = d[i];
-            } else {
-              float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-              for (int i = 0; i < NE; ++i) {
-                if (lane + 32 * i < a.D) {
-                  ag[i] = fmaf(d[i], v[i], ag[i]);
-                  ab[i] += d[i];
-                  d[i] *= g[i];
-                  s1 += d[i];
-                  s2 = fmaf(d[i], v[i], s2);
-                }
-              }
-              s1 = layer ? warp_sum(s1) * inv_d : 0.f;
-              s2 = warp_sum(s2) * inv_d;
-#pragma unroll
-              for (int i = 0; i < NE; ++i) v[i] = rstd * (d[i] - s1 - v[i] * s2);
-            }
-          }
+          T* to = static_cast<T*>(o.y) + token * o.y_token + h * o.y_head;
 #pragma unroll
           for (int i = 0; i < NE; ++i)
-            if (lane + 32 * i < a.D)
-              static_cast<T*>(o.y)[token * o.y_token + h * o.y_head + lane + 32 * i] = from_f32<T>(v[i]);
+            if (h < o.heads && lane + 32 * i < a.D) to[lane + 32 * i] = from_f32<T>(x[u][i]);
         }
       }
     }
@@ -857,12 +902,18 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
   int lanes = wide ? 4 : 8;
   while (lanes * (wide ? 16 : 8) < a.D) lanes *= 2;
   if (!rows) lanes = 32;
-  plan_heads(&a, kHeadThreads / lanes, rows ? 2 : a.D <= 128 ? 3 : 1, wide ? 8 : 16, BWD);
+  struct {
+    int rows, blocks;
+  } any{AnyHeads<16, BWD>::kRows, AnyHeads<16, BWD>::kBlocks};
+  if (a.D <= 256) any = {AnyHeads<8, BWD>::kRows, AnyHeads<8, BWD>::kBlocks};
+  if (a.D <= 128) any = {AnyHeads<4, BWD>::kRows, AnyHeads<4, BWD>::kBlocks};
+  if (a.D <= 64) any = {AnyHeads<2, BWD>::kRows, AnyHeads<2, BWD>::kBlocks};  // (and of one)
+  plan_heads(&a, kHeadThreads / lanes, rows ? 2 : any.blocks, wide ? 8 : 16, BWD);
   const unsigned grid = a.op[0].blocks + a.op[1].blocks;
   if (grid) {
     const int tokens = a.op[0].tokens > a.op[1].tokens ? a.op[0].tokens : a.op[1].tokens;
     const size_t table = Turns::bytes(a.pairs, tokens) + (wide ? lanes * 64 : 0), sums = (size_t)(kHeadThreads / 32) * 2 * a.D * 4;
-    const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * a.D * 4;
+    const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * any.rows * a.D * 4;
     const size_t base = ((BWD && sums > used ? sums : used) + 15) / 16 * 16;  // at most 36 KB
     a.ring = (int)base;
     auto launch = [&](const HeadArgs& b, unsigned blocks, bool f32) {
@@ -893,7 +944,12 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
         if (lanes == 16) return by_inter(std::integral_constant<int, 16>{}, n);
         return by_inter(std::integral_constant<int, 32>{}, n);
       };
-      if (!rows) return a.D <= 128 ? go(head_any<T, 4, BWD>) : go(head_any<T, 16, BWD>);
+      if (!rows) {
+        if (a.D <= 32) return go(head_any<T, 1, BWD>);
+        if (a.D <= 64) return go(head_any<T, 2, BWD>);
+        if (a.D <= 128) return go(head_any<T, 4, BWD>);
+        return a.D <= 256 ? go(head_any<T, 8, BWD>) : go(head_any<T, 16, BWD>);
+      }
       if constexpr (BWD)
         if (f32) return by_lanes(float{});
       return by_lanes(T{});
