@@ -2,6 +2,8 @@
 // the 8-bit cache (cache.py), as train_binding.cpp's.
 #include "heads_binding.h"
 
+#include <ATen/cuda/EmptyTensor.h>
+
 #include <cmath>
 
 #include "binding.h"
@@ -10,6 +12,11 @@
 namespace {
 
 using namespace binding;
+
+// A result of no contents yet, straight from its allocator: through the dispatcher each takes 0.2 us more.
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& of) {
+  return Tensor(at::detail::empty_cuda(shape, type, of.device(), std::nullopt));
+}
 
 // A [..., heads, dim] argument whose tokens step evenly.
 struct Heads {
@@ -71,7 +78,7 @@ struct HeadsOut {
 };
 HeadsOut heads_out(PyObject* o, const char* name, const Heads& of) {
   if (o == Py_None)
-    return {at::empty(of.t->sizes(), of.t->options().requires_grad(false)), of.heads * of.dim, of.dim};
+    return {fresh(of.t->sizes(), of.t->scalar_type(), *of.t), of.heads * of.dim, of.dim};
   const Heads h = heads_like(o, name, of, true);
   if (h.code != of.code) refuse(PyExc_ValueError, name, "expected the type of the input");
   return {*h.t, h.token, h.head, true};
@@ -277,8 +284,8 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       o.dy_token = dy.token;
       o.dy_head = dy.head;
       if (a[16] == Py_True && norm != IBWD_NORM_NONE) {
-        sums[at] = vector_out({h.dim}, at::kFloat, *h.t);
-        if (norm == IBWD_NORM_LAYER) sums[at + 1] = vector_out({h.dim}, at::kFloat, *h.t);
+        sums[at] = fresh({h.dim}, at::kFloat, *h.t);
+        if (norm == IBWD_NORM_LAYER) sums[at + 1] = fresh({h.dim}, at::kFloat, *h.t);
         o.dgamma = data<float>(sums[at]);
         o.dbeta = data<float>(sums[at + 1]);
       }
@@ -290,7 +297,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ws = nullptr;
     size_t bytes = 0;
     if (sums[0].defined() || sums[2].defined()) {
-      work = a[17] == Py_None ? vector_out({(int64_t)ibwd_qk_norm_rope_bwd_workspace_size((int)q.dim)}, at::kByte, *q.t)
+      work = a[17] == Py_None ? fresh({(int64_t)ibwd_qk_norm_rope_bwd_workspace_size((int)q.dim)}, at::kByte, *q.t)
                               : tensor(a[17], "workspace");
       ws = work.data_ptr();
       bytes = work.nbytes();
@@ -352,7 +359,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       like(a[6], "out", shape, -1, type_of(code), c);
       out = tensor(a[6], "out");
     } else {
-      out = vector_out(shape, type_of(code), c);
+      out = fresh(shape, type_of(code), c);
     }
     call("ibwd_cache_read", ibwd_cache_read, &from, &s, out.data_ptr(), code, (int)length, stream_of(c));
     if (given) bump(a[6]);
@@ -383,7 +390,7 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = a[9] == Py_None ? 1.f / std::sqrt((float)q.dim) : number(a[9]);
     Tensor work, out, lse;
     if (a[10] == Py_None) {
-      work = vector_out({(int64_t)ibwd_cache_attention_workspace_size(s.dim)}, at::kByte, kc);
+      work = fresh({(int64_t)ibwd_cache_attention_workspace_size(s.dim)}, at::kByte, kc);
     } else {
       work = tensor(a[10], "workspace");
       if (!work.is_contiguous()) refuse(PyExc_ValueError, "workspace", "expected a contiguous tensor");
@@ -393,11 +400,11 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       like(a[11], "out", q.t->sizes(), -1, q.t->scalar_type(), *q.t);
       out = tensor(a[11], "out");
     } else {
-      out = vector_out(q.t->sizes(), q.t->scalar_type(), *q.t);
+      out = fresh(q.t->sizes(), q.t->scalar_type(), *q.t);
     }
     std::vector<int64_t> rows = q.lead().vec();
     rows.push_back(q.heads);
-    lse = vector_out(rows, at::kFloat, *q.t);
+    lse = fresh(rows, at::kFloat, *q.t);
     call("ibwd_cache_attention", ibwd_cache_attention, q.t->const_data_ptr(), q.token, q.head, q.code,
          (int)(q.heads / s.heads), &ck, &cv, &s, select, kept, scale, out.data_ptr(), data<float>(lse), work.data_ptr(),
          work.nbytes(), stream_of(kc));
