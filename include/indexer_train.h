@@ -196,7 +196,8 @@ typedef struct ibwd_rotation {
   int interleaved;        /* pairs (start + 2i, start + 2i + 1); otherwise (start + i, start + i + pairs) */
 } ibwd_rotation;
 
-/* k or rotation may be NULL. dim <= IBWD_MAX_HEAD_DIM; eps finite, >= 0. */
+/* k or rotation may be NULL. dim <= IBWD_MAX_HEAD_DIM; eps finite, >= 0. Results overlap neither each other nor the
+ * other operand's arguments. */
 IBWD_API int ibwd_qk_norm_rope_fwd(const ibwd_heads* q, const ibwd_heads* k, const ibwd_rotation* rotation, int type,
                                    int w_type, int64_t tokens, int dim, float eps, void* stream);
 

@@ -84,9 +84,10 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu=
     A token sees the positions up to its own; with `select` (int32 [..., kept],
     an indexer's choice, padding outside) those of them that its row lists. A token
     that sees nothing has out 0 and lse -inf; rows behind cu[-1] are left as they
-    were. scale: of the logits, 1 / sqrt(dim) by default. `workspace`: a
-    contiguous tensor of cache_attention_workspace_size bytes (allocated when not
-    given), of one call at a time."""
+    were (undefined where the call allocates the results). scale: of the logits,
+    1 / sqrt(dim) by default. `workspace`: a contiguous tensor of
+    cache_attention_workspace_size bytes (allocated when not given), of one call
+    at a time."""
     if stream is not None:
         return train._on(stream, cache_attention, q, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu, select, scale,
                          workspace, out)

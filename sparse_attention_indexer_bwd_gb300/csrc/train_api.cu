@@ -326,6 +326,16 @@ int heads_common(bool backward, const ibwd_heads* q, const ibwd_heads* k, const 
   int n = 0, rc = head_op(*q, backward, type, w_type, tokens, dim, none, &a.op[0], list, &n);
   if (!rc && k) rc = head_op(*k, backward, type, w_type, tokens, dim, none, &a.op[1], list, &n);
   if (rc) return rc;
+  if (a.op[0].heads && a.op[1].heads && !none) {  // one operand's result is nothing of the other's
+    const HeadOp &o = a.op[0], &p = a.op[1];
+    if (o.y == p.y || o.y == p.x || p.y == o.x || (backward && (o.y == p.dy || p.y == o.dy))) return IBWD_ERR_INVALID_ARG;
+  }
+  if (backward) {
+    const float* const to[4] = {a.op[0].dgamma, a.op[0].dbeta, a.op[1].dgamma, a.op[1].dbeta};
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < i; ++j)
+        if (to[i] && to[i] == to[j]) return IBWD_ERR_INVALID_ARG;
+  }
   if (r && r->positions) {
     if (r->pairs < 0 || r->start < 0 || r->axes < 1 || r->pairs > dim / 2 || r->start > dim - 2 * r->pairs)
       return IBWD_ERR_INVALID_ARG;

@@ -94,6 +94,13 @@ def test_norm_and_rotation(lib):
     assert bwd(lib, q=heads(norm=0, gamma=None)) == INVALID    # sums without a norm
     assert bwd(lib, q=heads(y=16 * P, dy_token=512)) == INVALID
     assert bwd(lib, q=heads(y=16 * P, dy_type=0)) == INVALID
+    # a result that is the other operand's result or argument
+    for q, k in ((dict(), dict()), (dict(), dict(y=P, x=64 * P)), (dict(y=64 * P), dict(x=64 * P)), (dict(x=64 * P), dict(y=64 * P))):
+        for call in (fwd, bwd):
+            assert call(lib, q=heads(**q), k=heads(**{"dgamma": 2 * P, **k})) == INVALID, (q, k)
+    assert bwd(lib, q=heads(y=64 * P), k=heads(dy=64 * P, dgamma=2 * P)) == INVALID
+    assert bwd(lib, q=heads(), k=heads(y=32 * P, dy=64 * P)) == INVALID  # one dgamma for both
+    assert bwd(lib, q=heads(norm=2, dbeta=P)) == INVALID
     assert bwd(lib, ws=None) == WORKSPACE
     assert bwd(lib, ws=P + 8) == WORKSPACE
     assert fwd(lib, tokens=0) == ibwd.IBWD_OK
