@@ -179,7 +179,7 @@ typedef struct ibwd_heads {
   int dy_type;        /* the heads' type or IBWD_F32 */
   int64_t dy_token, dy_head;
   float* dgamma;      /* backward: fp32 [dim], written; NULL when not wanted; NULL without a norm */
-  float* dbeta;
+  float* dbeta;       /* a layer norm's only */
 } ibwd_heads;
 
 /* Which dimensions turn by which angles. */

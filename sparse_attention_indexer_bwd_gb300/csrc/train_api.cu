@@ -288,7 +288,7 @@ int head_op(const ibwd_heads& h, bool backward, int type, int w_type, int64_t to
     if (h.dy_type != type && h.dy_type != IBWD_F32) return type_ok(h.dy_type) ? IBWD_ERR_UNSUPPORTED : IBWD_ERR_INVALID_ARG;
     // (a gradient that several heads or tokens share may have steps of 0)
     if (h.dy_token < 0 || h.dy_head < 0) return IBWD_ERR_INVALID_ARG;
-    if ((h.dgamma || h.dbeta) && h.norm == IBWD_NORM_NONE) return IBWD_ERR_INVALID_ARG;
+    if ((h.dgamma && h.norm == IBWD_NORM_NONE) || (h.dbeta && h.norm != IBWD_NORM_LAYER)) return IBWD_ERR_INVALID_ARG;
     list[(*n)++] = {h.dy, size_of(h.dy_type), none};
     list[(*n)++] = {h.dgamma, 4, true};
     list[(*n)++] = {h.dbeta, 4, true};

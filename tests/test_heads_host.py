@@ -101,6 +101,7 @@ def test_norm_and_rotation(lib):
     assert bwd(lib, q=heads(y=64 * P), k=heads(dy=64 * P, dgamma=2 * P)) == INVALID
     assert bwd(lib, q=heads(), k=heads(y=32 * P, dy=64 * P)) == INVALID  # one dgamma for both
     assert bwd(lib, q=heads(norm=2, dbeta=P)) == INVALID
+    assert bwd(lib, q=heads(dbeta=2 * P)) == INVALID           # a layer norm's only
     assert bwd(lib, ws=None) == WORKSPACE
     assert bwd(lib, ws=P + 8) == WORKSPACE
     assert fwd(lib, tokens=0) == ibwd.IBWD_OK
