@@ -231,25 +231,27 @@ struct Turns {
 // shared memory, each lane's own, so that nobody waits for another; the weights
 // stay in registers. Arithmetic is packed, two fp32 an instruction.
 //
-// What bounds it is instruction issue and latency at 16 warps an SM (58 to 60 %
-// of the issue slots, 19 and 34 million instructions), then HBM. 8192x40x128 in
-// bf16 takes 32 us (78 % of the copy rate) and 54 backward (69 %). One step ahead
-// in registers instead of the ring: 39 and 66. Parts of four elements instead of eight:
-// 36 forward; backward eight spill (62 us). Backward in three blocks an SM: 65; two
-// rows' sums through the shuffles together: 56. Parts side by side in a lane: 53
-// instead of 32 for adjacent pairs (half of each sector an instruction). Single
-// instructions, partners by shuffles: 146 us for 16381x32x128, now 51.
+// What bounds it is instruction issue and latency at 16 warps an SM (about 60 % of
+// the issue slots), then HBM. 8192x40x128 in bf16 takes 32 us (78 % of the copy
+// rate) and 48 backward (78 %). One step ahead in registers instead of the ring:
+// 39 and 66. Parts of four elements instead of eight (N): 36 and 54; a layer norm's
+// backward pass, with dbeta's sums, has registers for no more than four (eight: 62).
+// With four, in three blocks an SM 65 backward, two rows' sums through the shuffles
+// together 56. Parts side by side in a lane: 53 instead of 32 for adjacent pairs
+// (half of each sector an instruction). Single instructions, partners by shuffles:
+// 146 us for 16381x32x128, now 51.
 //
 // Rows that a lane computes at once; kStages times as many are on their way or computed, 48 KB a block (72 KB for 16-bit
 // rows with fp32 gradients, where two stages are 36 us for 34). A fourth stage changes nothing.
 template <typename T, typename DT, int N, bool BWD>
 struct Ring {
-  static constexpr int kRows = !BWD ? 32 / (N * (int)sizeof(T)) : sizeof(T) == 4 ? 1 : 2;
+  static constexpr int kRows = !BWD ? 32 / (N * (int)sizeof(T)) : sizeof(T) == 4 || N == 8 ? 1 : 2;
   static constexpr int kX = Part<T, N>::kStride * Part<T, N>::kChunks, kDy = BWD ? Part<DT, N>::kStride * Part<DT, N>::kChunks : 0;
   static constexpr int kStage = 2 * kRows * (kX + kDy), kStages = 3;  // bytes
 };
 
-template <typename T, typename DT, int L, int N, bool BWD, bool INTER>
+// PLAIN: no layer norm is among the operands.
+template <typename T, typename DT, int L, int N, bool BWD, bool INTER, bool PLAIN>
 __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_constant__ HeadArgs a) {
   using R = Ring<T, DT, N, BWD>;
   constexpr int U = R::kRows;
@@ -301,17 +303,28 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     }
     return paired<INTER, N>(x, y);
   };
-  const Pairs<N> g = weights(o.gamma, 1.f), bt = weights(BWD || N == 8 ? nullptr : o.beta, 0.f);
-  // wide lanes have no registers for beta: it lies behind the table, a lane's elements together
-  float* const beta = reinterpret_cast<float*>(smem) + 2 * o.tokens * a.pairs + li * 2 * N;
-  if (!BWD && N == 8 && o.beta && group == 0) {
-    const Pairs<N> e = weights(o.beta, 0.f);
+  // wide lanes have no registers for beta, or backward for gamma: it lies behind the table
+  constexpr bool kWide = N == 8;
+  const Pairs<N> g = weights(BWD && kWide ? nullptr : o.gamma, 1.f), bt = weights(BWD || kWide ? nullptr : o.beta, 0.f);
+  float4* const beside = reinterpret_cast<float4*>(smem) + (o.tokens * a.pairs + 1) / 2 + li;
+  if (kWide && group == 0 && (BWD || o.beta)) {
+    const Pairs<N> e = weights(BWD ? o.gamma : o.beta, BWD ? 1.f : 0.f);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      reinterpret_cast<float2*>(beta)[i] = e.a[i];
-      reinterpret_cast<float2*>(beta)[N / 2 + i] = e.b[i];
+    for (int i = 0; i < N / 4; ++i) {
+      beside[i * L] = make_float4(e.a[2 * i].x, e.a[2 * i].y, e.a[2 * i + 1].x, e.a[2 * i + 1].y);
+      beside[(N / 4 + i) * L] = make_float4(e.b[2 * i].x, e.b[2 * i].y, e.b[2 * i + 1].x, e.b[2 * i + 1].y);
     }
   }
+  auto from_beside = [&]() {
+    Pairs<N> e;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 x = beside[i * L], y = beside[(N / 4 + i) * L];
+      e.a[2 * i] = make_float2(x.x, x.y), e.a[2 * i + 1] = make_float2(x.z, x.w);
+      e.b[2 * i] = make_float2(y.x, y.y), e.b[2 * i + 1] = make_float2(y.z, y.w);
+    }
+    return e;
+  };
   Pairs<N> ag{}, ab{};
   const float inv_d = 1.f / (float)a.D;
   const long long x_step = side * o.x_head, y_step = side * o.y_head, dy_step = side * o.dy_head;
@@ -443,7 +456,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
     return paired<INTER, N>(e0, e1);
   };
   auto elements = [&](uint32_t stage, int u) { return two(X{}, x_slot + stage + 2 * u * kX, kX); };
-  const bool layer = o.norm == IBWD_NORM_LAYER, normed = o.norm != IBWD_NORM_NONE;
+  const bool layer = !PLAIN && o.norm == IBWD_NORM_LAYER, normed = o.norm != IBWD_NORM_NONE;
   // Rows beyond the heads are computed with what the ring holds, and go nowhere. Forward, the sums of all U rows go
   // through the shuffles together, and the elements are taken apart once more behind them.
   auto forward = [&](uint32_t stage) {
@@ -481,17 +494,18 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
           v.a[i] = mul2(v.a[i], both(rstd[u]));
           v.b[i] = mul2(v.b[i], both(rstd[u]));
         }
-        if (N == 8 && !o.beta) {
+        if (kWide && !o.beta) {
 #pragma unroll
           for (int i = 0; i < N / 2; ++i) {
             v.a[i] = mul2(v.a[i], g.a[i]);
             v.b[i] = mul2(v.b[i], g.b[i]);
           }
         } else {
+          const Pairs<N> e = kWide ? from_beside() : bt;
 #pragma unroll
           for (int i = 0; i < N / 2; ++i) {
-            v.a[i] = fma2(v.a[i], g.a[i], N == 8 ? reinterpret_cast<const float2*>(beta)[i] : bt.a[i]);
-            v.b[i] = fma2(v.b[i], g.b[i], N == 8 ? reinterpret_cast<const float2*>(beta)[N / 2 + i] : bt.b[i]);
+            v.a[i] = fma2(v.a[i], g.a[i], e.a[i]);
+            v.b[i] = fma2(v.b[i], g.b[i], e.b[i]);
           }
         }
       }
@@ -515,12 +529,17 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
           group_sums<L>(m);
           shift(v, on ? m[0] * -inv_d : 0.f);
         }
-        Pairs<N> e;  // d gamma
+        auto times_gamma = [&]() {
+          const Pairs<N> w = kWide ? from_beside() : g;
+          Pairs<N> e;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          e.a[i] = mul2(d.a[i], g.a[i]);
-          e.b[i] = mul2(d.b[i], g.b[i]);
-        }
+          for (int i = 0; i < N / 2; ++i) {
+            e.a[i] = mul2(d.a[i], w.a[i]);
+            e.b[i] = mul2(d.b[i], w.b[i]);
+          }
+          return e;
+        };
+        Pairs<N> e = times_gamma();
         float sums[3] = {product(v, v), on ? product(e, v) : 0.f, layer && on ? total(e) : 0.f};
         if (layer) {
           group_sums<L>(sums);
@@ -531,6 +550,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
           sums[1] = two[1];
         }
         const float rstd = rsqrtf(fmaf(sums[0], inv_d, a.eps)), k = rstd * (rstd * sums[1] * -inv_d), less = sums[2] * -inv_d;
+        if (kWide) e = times_gamma();  // (again: fewer registers over the sums)
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
           const float2 xa = mul2(v.a[i], both(rstd)), xb = mul2(v.b[i], both(rstd));
@@ -898,7 +918,8 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
   };
   // Wide lanes have 16 elements' weights to load first: 320 rows take 3.4 us, with them 3.9; 5120 4.6 and 4.7; 16384
   // 13.0 and 11.2; 327680 36 and 32.
-  const bool rows = whole(4), wide = !BWD && sizeof(T) == 2 && a.tokens * (a.op[0].heads + a.op[1].heads) >= 8192 && whole(8);
+  const bool rows = whole(4), plain = a.op[0].norm != IBWD_NORM_LAYER && a.op[1].norm != IBWD_NORM_LAYER,
+             wide = (!BWD || plain) && sizeof(T) == 2 && a.tokens * (a.op[0].heads + a.op[1].heads) >= 8192 && whole(8);
   int lanes = wide ? 4 : 8;
   while (lanes * (wide ? 16 : 8) < a.D) lanes *= 2;
   if (!rows) lanes = 32;
@@ -912,7 +933,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
   const unsigned grid = a.op[0].blocks + a.op[1].blocks;
   if (grid) {
     const int tokens = a.op[0].tokens > a.op[1].tokens ? a.op[0].tokens : a.op[1].tokens;
-    const size_t table = Turns::bytes(a.pairs, tokens) + (wide ? lanes * 64 : 0), sums = (size_t)(kHeadThreads / 32) * 2 * a.D * 4;
+    const size_t table = (Turns::bytes(a.pairs, tokens) + 15) / 16 * 16 + (wide ? lanes * 64 : 0), sums = (size_t)(kHeadThreads / 32) * 2 * a.D * 4;
     const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * any.rows * a.D * 4;
     const size_t base = ((BWD && sums > used ? sums : used) + 15) / 16 * 16;  // at most 36 KB
     a.ring = (int)base;
@@ -924,7 +945,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
           constexpr int L = decltype(lanes_of)::value, N = decltype(n)::value;
           constexpr bool INTER = decltype(inter)::value;
           static std::atomic<size_t> done[64];
-          const auto kern = head_rows<T, DT, L, N, BWD, INTER>;
+          const auto kern = head_rows<T, DT, L, N, BWD, INTER, BWD && N == 8>;
           const size_t bytes = base + (size_t)Ring<T, DT, N, BWD>::kStages * Ring<T, DT, N, BWD>::kStage;
           const cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), bytes, done);
           return e != cudaSuccess ? e : launch_ex(kern, blocks, kHeadThreads, bytes, st, true, b);
@@ -932,7 +953,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
         auto by_inter = [&](auto lanes_of, auto n) {
           return a.interleaved ? ringed(lanes_of, n, std::true_type{}) : ringed(lanes_of, n, std::false_type{});
         };
-        if constexpr (!BWD && sizeof(T) == 2)
+        if constexpr (sizeof(T) == 2)
           if (wide) {
             constexpr std::integral_constant<int, 8> n{};
             if (lanes == 4) return by_inter(std::integral_constant<int, 4>{}, n);

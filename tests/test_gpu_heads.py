@@ -104,12 +104,16 @@ def test_many_rows_of_whole_parts(dim, kind):
     for heads, kv in ((8, 1), (3, 5)):
         q, k = make(tokens, heads, dim, DTYPES[kind], 1, 8, 8), make(tokens, kv, dim, DTYPES[kind], 2)
         pos = torch.randint(0, 1 << 20, (tokens,), device="cuda", generator=generator(4))
+        run(q, k, None, None, "rms", "rms")
         for pairs in {dim // 2, dim // 4, 8, dim // 4 * 2 - 4, 1}:
             for start in {0, 8, 2, dim - 2 * pairs}:
                 if 2 * pairs + start <= dim:
                     for inter in (False, True):
                         run(q, k, pos, frequencies(pairs), *(("rms", "layer") if heads == 8 else ("layer", "none")), start=start,
                             interleaved=inter)
+                        types = (DTYPES[kind], torch.float32) if start else (torch.float32, torch.float32)
+                        run(q, k, pos, frequencies(pairs), *(("rms", "rms") if heads == 8 else ("none", "rms")), start=start,
+                            interleaved=inter, dy_dtypes=None if inter else types)
 
 
 @pytest.mark.parametrize("pad,at", [(256, 0), (256, 128), (8, 8), (3, 1), (1, 0)])
