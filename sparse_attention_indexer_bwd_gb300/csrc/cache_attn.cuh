@@ -836,114 +836,138 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   }
 }
 
-// Joins the parts of items that lie in several blocks: x the block that ends
-// one, y two of its rows. A thread takes the statistics of a part or two, then
-// the eight warps share out the parts' outputs, eight in flight each, and meet in
-// shared memory in their order: of a single item in all blocks (one sequence of
-// 131072 tokens, one KV head) the parts are 600 KB.
+// Joins the parts of items that lie in several blocks: x `per` of the blocks that
+// may end one, y two of its rows. A thread takes the statistics of a part or two,
+// while the eight warps' first parts of the outputs are on their way, four of
+// each row a warp at once; they meet in shared memory in their order: of a single
+// item in all blocks (one sequence of 131072 tokens, one KV head) the parts are
+// 600 KB. Several blocks' records a block where rows are many, so that the grid
+// is twice what is resident at most: most records end no item (64 selections of 16 rows
+// 20.7 us, a record a block 22.8).
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
-  constexpr int V = D / 32, U = D == 256 ? 4 : 8;
+__global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int per, int grid) {
+  constexpr int V = D / 32, U = D == 256 ? 2 : 4;
   __shared__ float factor[2][kAttnGrid];
   __shared__ float red[2][3][8];
   __shared__ float acc[8][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r0 = blockIdx.y * 2, mine = (int)blockIdx.x * per + lane;
   griddep_wait();
-  const JoinRecord rec = static_cast<const JoinRecord*>(a.work)[blockIdx.x];
-  const int r0 = blockIdx.y * 2;
-  if (!rec.valid || rec.row + r0 >= rec.rows) return;
-  const float* parts = reinterpret_cast<const float*>(static_cast<const JoinRecord*>(a.work) + kAttnGrid);
-  const int n = (int)blockIdx.x - rec.first + 1, rows = min(2, rec.rows - rec.row - r0);
-  auto part = [&](int i, int r) { return parts + ((long long)((rec.first + i) * 2 + (i == 0)) * ROWS + r0 + r) * part_row(D); };
-  constexpr int S = (kAttnGrid + 255) / 256;
-  float4 st[2][S];
-  float m[2], big[2];
+  const JoinRecord* records = static_cast<const JoinRecord*>(a.work);
+  const float* parts = reinterpret_cast<const float*>(records + kAttnGrid);
+  JoinRecord held{};
+  if (lane < per && mine < grid) held = records[mine];
+  unsigned todo = __ballot_sync(0xffffffffu, held.valid && held.row + r0 < held.rows);
+  for (; todo; todo &= todo - 1) {
+    const int from = __ffs(todo) - 1;
+    auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, from); };
+    const int first = of(held.first), token = of(held.token), top = of(held.row) + r0, head = of(held.head);
+    const int n = (int)blockIdx.x * per + from - first + 1, rows = min(2, of(held.rows) - top);
+    auto part = [&](int i, int r) { return parts + ((long long)((first + i) * 2 + (i == 0)) * ROWS + r0 + r) * part_row(D); };
+    // Parts i, i + 8, .. of a warp (a row beyond the item's as the first). At first as many as there are: most items have few.
+    // Then those beyond the last as the last, since a load under a condition is waited for before the next (a single item
+    // of 342 parts 37 us, not 29).
+    float x[2][U][V];
+    auto load = [&](int u, int i) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    m[r] = big[r] = -INFINITY;
+      for (int r = 0; r < 2; ++r) {
+        const float* p = part(i, r < rows ? r : 0) + lane;
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int i = threadIdx.x + 256 * k;
-      st[r][k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-      if (i < n && r < rows) st[r][k] = *reinterpret_cast<const float4*>(part(i, r) + D);
-      m[r] = fmaxf(m[r], st[r][k].x);
-      big[r] = fmaxf(big[r], st[r][k].z);
+        for (int e = 0; e < V; ++e) asm volatile("ld.global.f32 %0, [%1];" : "=f"(x[r][u][e]) : "l"(p + e * 32));
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (warp + 8 * u < n) load(u, warp + 8 * u);
+    constexpr int S = (kAttnGrid + 255) / 256;
+    float4 st[2][S];
+    float m[2], big[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        const int i = threadIdx.x + 256 * k;
+        st[r][k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (i < n && r < rows) st[r][k] = *reinterpret_cast<const float4*>(part(i, r) + D);
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      m[r] = big[r] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        m[r] = fmaxf(m[r], st[r][k].x);
+        big[r] = fmaxf(big[r], st[r][k].z);
+      }
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) {
+        m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], w));
+        big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], w));
+      }
+      if (lane == 0) {
+        red[r][0][warp] = m[r];
+        red[r][1][warp] = big[r];
+      }
     }
+    __syncthreads();
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-      m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], w));
-      big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], w));
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        m[r] = fmaxf(m[r], red[r][0][w]);
+        big[r] = fmaxf(big[r], red[r][1][w]);
+      }
+      float l = 0.f;
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        const int i = threadIdx.x + 256 * k;
+        l = fmaf(st[r][k].y, ex2(st[r][k].x - basis(m[r])), l);
+        if (i < n) factor[r][i] = ex2(st[r][k].z - basis(big[r]));
+      }
+      l = warp_sum(l);
+      if (lane == 0) red[r][2][warp] = l;
     }
-    if (lane == 0) {
-      red[r][0][warp] = m[r];
-      red[r][1][warp] = big[r];
-    }
-  }
-  __syncthreads();
+    __syncthreads();
+    float o[2][V];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      m[r] = fmaxf(m[r], red[r][0][w]);
-      big[r] = fmaxf(big[r], red[r][1][w]);
-    }
-    float l = 0.f;
+      for (int e = 0; e < V; ++e) o[r][e] = 0.f;
+    for (int i = warp; i < n; i += 8 * U) {
+      if (i != warp)
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int i = threadIdx.x + 256 * k;
-      l = fmaf(st[r][k].y, ex2(st[r][k].x - basis(m[r])), l);
-      if (i < n) factor[r][i] = ex2(st[r][k].z - basis(big[r]));
-    }
-    l = warp_sum(l);
-    if (lane == 0) red[r][2][warp] = l;
-  }
-  __syncthreads();
+        for (int u = 0; u < U; ++u) load(u, min(i + 8 * u, n - 1));
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    float o[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-    if (r < rows) {
-      int i = warp;
-      for (; i + 8 * (U - 1) < n; i += 8 * U) {
-        float x[U][V];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float* p = part(i + 8 * u, r) + lane;
-#pragma unroll
-          for (int e = 0; e < V; ++e) asm volatile("ld.global.f32 %0, [%1];" : "=f"(x[u][e]) : "l"(p + e * 32));
-        }
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int u = 0; u < U; ++u)
+          if (i + 8 * u < n) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = fmaf(x[u][e], factor[r][i + 8 * u], o[e]);
-      }
-      for (; i < n; i += 8) {
-        const float* p = part(i, r) + lane;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(p[e * 32], factor[r][i], o[e]);
-      }
+            for (int e = 0; e < V; ++e) o[r][e] = fmaf(x[r][u][e], factor[r][i + 8 * u], o[r][e]);
+          }
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[warp][r][e * 32 + lane] = o[e];
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < rows * D; idx += 256) {
-    const int r = idx / D, d = idx - r * D, R = rec.row + r0 + r, i = R / a.group;
-    const long long row = (long long)(rec.token + i) * a.heads * a.group + rec.head * a.group + R - i * a.group;
-    const float mr = r ? m[1] : m[0], br = r ? big[1] : big[0];
-    float v = 0.f, l = 0.f;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      v += acc[w][r][d];
-      l += red[r][2][w];
+      for (int e = 0; e < V; ++e) acc[warp][r][e * 32 + lane] = o[r][e];
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < rows * D; idx += 256) {
+      const int r = idx / D, d = idx - r * D, R = top + r, i = R / a.group;
+      const long long row = (long long)(token + i) * a.heads * a.group + head * a.group + R - i * a.group;
+      const float mr = r ? m[1] : m[0], br = r ? big[1] : big[0];
+      float v = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        v += acc[w][r][d];
+        l += red[r][2][w];
+      }
+      v *= l == 0.f ? 0.f : ex2(br - kUnit - basis(mr)) / l;
+      if (a.type == IBWD_BF16)
+        static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(v);
+      else
+        static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(v);
+      if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.69314718055994531f;
     }
-    v *= l == 0.f ? 0.f : ex2(br - kUnit - basis(mr)) / l;
-    if (a.type == IBWD_BF16)
-      static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(v);
-    else
-      static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(v);
-    if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
   }
 }
 
@@ -963,7 +987,8 @@ cudaError_t attn_launch(const CacheAttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // rows that an item can have
   const int rows = (a.select || !a.seqs.cu) && a.group < 16 * MT ? a.group : 16 * MT;
-  return launch_ex(attn_join_kernel<D, 16 * MT>, dim3(grid, (rows + 1) / 2), 256, 0, st, true, a);
+  const int pairs = (rows + 1) / 2, most = 8 * a.num_sms, per = (grid * pairs + most - 1) / most;
+  return launch_ex(attn_join_kernel<D, 16 * MT>, dim3((grid + per - 1) / per, pairs), 256, 0, st, true, a, per, grid);
 }
 
 template <int D>
