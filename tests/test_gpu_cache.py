@@ -254,6 +254,18 @@ def test_large_and_ragged_batches():
     attend(lens[:40], counts[:40], 2, 3, 64, 32, INT8, kept=77, seed=3)
 
 
+@pytest.mark.parametrize("dim,group", [(128, 16), (64, 16), (128, 30), (256, 9), (64, 41)])
+def test_many_rows_whose_items_end_in_neighbouring_blocks(dim, group):
+    """Items of two to four tiles, so that nearly every block ends one that another began."""
+    rng = random.Random(dim + group)
+    lens = [rng.choice([129, 200, 300, 390, 500]) for _ in range(330)]
+    attend(lens, None, 1, group, dim, 32, E4M3, seed=4)
+    attend(lens[:170], [rng.choice([1, 2, 3]) for _ in range(170)], 2, group, dim, 16, INT8, seed=5)
+    attend(lens, None, 1, group, dim, 16, INT8, kept=300, seed=6)
+    # and of many parts each
+    attend([9000, 12345, 1, 7000], None, 1, group, dim, 64, E4M3, seed=8)
+
+
 def test_scales_far_apart():
     """Blocks whose scales differ by up to 2^24, and by 2^200."""
     for dim in (64, 128):
