@@ -29,6 +29,10 @@
 namespace ibwd {
 
 constexpr int kHeadThreads = 256;
+constexpr int kHeadAngles = 2048;  // of a block's table at most: a group's tokens times the pairs
+// In front of a ring of rows: the table, and the weights of 16 lanes that are wide. (A backward pass's column sums, 16 KB for
+// heads of 256, take the table's place.)
+constexpr size_t kHeadFront = kHeadAngles * 8 + 16 * 64;
 
 __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
   if (type == IBWD_F32) return static_cast<const float*>(w)[i];
@@ -886,7 +890,7 @@ inline void plan_heads(HeadArgs* a, int groups, int per_sm, int side_by, bool ba
     o.tokens = groups >> o.shift;
     // several tokens a group while there are tiles enough and the table of angles stays at 16 KB
     const int rows = (o.heads + (1 << o.shift) - 1) >> o.shift;
-    for (int m = rows; m < 8 && tiles(2 * o.tokens) >= 4 * a->num_sms && 2 * o.tokens * a->pairs <= 2048; m *= 2) o.tokens *= 2;
+    for (int m = rows; m < 8 && tiles(2 * o.tokens) >= 4 * a->num_sms && 2 * o.tokens * a->pairs <= kHeadAngles; m *= 2) o.tokens *= 2;
     o.tiles = tiles(o.tokens);
     o.blocks = (int)(o.tiles < budget ? o.tiles : budget);
   }
@@ -948,7 +952,7 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
     const int tokens = a.op[0].tokens > a.op[1].tokens ? a.op[0].tokens : a.op[1].tokens;
     const size_t table = (Turns::bytes(a.pairs, tokens) + 15) / 16 * 16 + (wide ? lanes * 64 : 0), sums = (size_t)(kHeadThreads / 32) * 2 * a.D * 4;
     const size_t used = rows ? table : table + (size_t)(kHeadThreads / 32) * any.rows * a.D * 4;
-    const size_t base = ((BWD && sums > used ? sums : used) + 15) / 16 * 16;  // at most 36 KB
+    const size_t base = ((BWD && sums > used ? sums : used) + 15) / 16 * 16;  // at most 32 KB
     a.ring = (int)base;
     auto launch = [&](const HeadArgs& b, unsigned blocks, bool f32) {
       auto go = [&](auto kern) { return launch_ex(kern, blocks, kHeadThreads, base, st, true, b); };
@@ -959,9 +963,11 @@ cudaError_t launch_heads_of(HeadArgs a, cudaStream_t st) {
           constexpr bool INTER = decltype(inter)::value;
           static std::atomic<size_t> done[64];
           const auto kern = head_rows<T, DT, L, N, BWD, INTER, BWD && N == 8>;
-          const size_t bytes = base + (size_t)Ring<T, DT, N, BWD>::kStages * Ring<T, DT, N, BWD>::kStage;
-          const cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), bytes, done);
-          return e != cudaSuccess ? e : launch_ex(kern, blocks, kHeadThreads, bytes, st, true, b);
+          constexpr size_t ring = (size_t)Ring<T, DT, N, BWD>::kStages * Ring<T, DT, N, BWD>::kStage;
+          if (base > kHeadFront) return cudaErrorInvalidValue;  // (never)
+          // The limit is that of the largest front, whatever this launch has: another thread's may have more.
+          const cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), kHeadFront + ring, done);
+          return e != cudaSuccess ? e : launch_ex(kern, blocks, kHeadThreads, base + ring, st, true, b);
         };
         auto by_inter = [&](auto lanes_of, auto n) {
           return a.interleaved ? ringed(lanes_of, n, std::true_type{}) : ringed(lanes_of, n, std::false_type{});
