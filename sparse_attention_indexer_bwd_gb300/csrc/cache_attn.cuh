@@ -24,9 +24,10 @@
 // once more in fp16: with 4 to 32 rows its tiles would be mostly padding.
 //
 // Two running maxima a row: m of the logits (base 2) for the sum l, and M of
-// logit + log2(scale of the value's block), which is what the outputs' unit
+// logit - m + log2(scale of the value's block), which is what the outputs' unit
 // follows, so that a weight has 11 bits relative to the largest contribution
-// whatever the blocks' scales are. Weights are kept in units of 2^-15, at most
+// whatever the blocks' scales are. M counts from m, since log2(scale) beside a
+// large logit would be rounded at that one's size. Weights are kept in units of 2^-15, at most
 // 2^15 in fp16: they lose bits only below 2^-29 of the largest and vanish below 2^-39.
 #pragma once
 #include "cache.h"
@@ -54,7 +55,7 @@ struct JoinRecord {
   int pad[2];
 };
 
-// Floats of one partial result's row: outputs, m, l, M.
+// Floats of one partial result's row: outputs in units of 2^(m + M - 15), m, l, M.
 constexpr int part_row(int D) { return D + 4; }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
@@ -105,6 +106,8 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 // What a maximum is subtracted as: -inf (nothing yet) as 0.
 __device__ __forceinline__ float basis(float m) { return m == -INFINITY ? 0.f : m; }
+// A unit that counts from maximum `m`, as it counts from the larger maximum `to`.
+__device__ __forceinline__ float counted(float unit, float m, float to) { return unit + (m - basis(to)); }
 __device__ __forceinline__ float capped(float e) { return e > 126.f ? 126.f : e; }  // (NaN stays)
 
 // Where 16 bytes of a stage's row lie: ldmatrix takes eight rows at once, and a
@@ -561,8 +564,9 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             mm = fmaxf(mm, p[w * ROWS * 3]);
-            bb = fmaxf(bb, p[w * ROWS * 3 + 2]);
+            bb = fmaxf(bb, p[w * ROWS * 3] + p[w * ROWS * 3 + 2]);
           }
+          bb -= basis(mm);  // (rounded, but any unit near the largest serves in fp32)
           constexpr int V = DC / 32;
           float x[V];
 #pragma unroll
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             ll = fmaf(p[w * ROWS * 3 + 1], ex2(p[w * ROWS * 3] - basis(mm)), ll);
-            const float f = ex2(p[w * ROWS * 3 + 2] - basis(bb));
+            const float f = ex2(counted(p[w * ROWS * 3 + 2], p[w * ROWS * 3], mm) - basis(bb));
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
               const float2 v = *reinterpret_cast<const float2*>(at(w, row, (lane * V + e) / 2));
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           if (whole) {
             const int i = R / a.group;
             const long long out_row = (long long)(c.token + i) * a.heads * a.group + c.head * a.group + R - i * a.group;
-            const float f = ll == 0.f ? 0.f : ex2(bb - kUnit - basis(mm)) / ll;
+            const float f = ll == 0.f ? 0.f : ex2(bb - kUnit) / ll;
             uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out_row * D + d0 + lane * V);
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
@@ -647,6 +651,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     }
     // this lane's positions: 16 u + 4 j + e. The scales of each 16 of them, or (SEL) their own.
     float ks[SUBS][SEL ? 4 : 1], vs[SUBS][SEL ? 4 : 1], lv[SUBS][SEL ? 4 : 1];
+    float most[SUBS];  // of lv
     if (SEL) {
       const float* own = reinterpret_cast<const float*>(st + 2 * kBytes + 32) + 4 * j;
 #pragma unroll
@@ -659,6 +664,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           vs[u][e] = yy[e];
           lv[u][e] = __log2f(yy[e]);
         }
+        most[u] = fmaxf(fmaxf(lv[u][0], lv[u][SEL ? 1 : 0]), fmaxf(lv[u][SEL ? 2 : 0], lv[u][SEL ? 3 : 0]));
       }
     } else {
       const float4 x = *reinterpret_cast<const float4*>(st + 2 * kBytes + 16);
@@ -666,32 +672,29 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       for (int u = 0; u < SUBS; ++u) {
         ks[u][0] = u ? x.z : x.x;
         vs[u][0] = u ? x.w : x.y;
-        lv[u][0] = __log2f(vs[u][0]);
+        most[u] = lv[u][0] = __log2f(vs[u][0]);
       }
     }
     const int here = c.rows - c.rt * ROWS;  // rows of this tile, and on
     constexpr unsigned kAll = SUBS == 2 ? 0xFFFFFFFFu : 0xFFFFu;
     const bool full = mask == kAll && (SEL || first + STEP <= lim_min);
-    uint32_t p[MT][SUBS][4];
+    // Half of a tile may have no rows (KV heads of four, int8: 180 us where it goes through the softmax as well, 172).
+    auto empty = [&](int hf) { return MT == 1 && hf && here <= 8; };
+    // The logit of a row's position e of a lane's four in each 16, then less its row's maximum.
+    auto y = [&](int mt, int hf, int u, int e) -> float& { return sc[mt][2 * u + (e >> 1)][2 * hf + (e & 1)]; };
+    // Whether a contribution may pass its row's unit: by what is there before the step, so that nothing waits for the maxima.
     bool moved = false;
-    float shift[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        if (MT == 1 && hf && here <= 8) {  // half of the tile has no rows (KV heads of four, int8: 180 us without this, 172)
-#pragma unroll
-          for (int u = 0; u < SUBS; ++u) p[mt][u][hf] = p[mt][u][2 + hf] = 0u;
-          shift[mt][hf] = 1.f;
-          continue;
-        }
-        float y[SUBS][4], top = -INFINITY, over = -INFINITY;
+        if (empty(hf)) continue;
+        float top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
           const float unit = qs[mt][hf] * ks[u][0];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[u][e] = sc[mt][2 * u + (e >> 1)][2 * hf + (e & 1)] * (SEL ? qs[mt][hf] * ks[u][SEL ? e : 0] : unit);
+          for (int e = 0; e < 4; ++e) y(mt, hf, u, e) *= SEL ? qs[mt][hf] * ks[u][SEL ? e : 0] : unit;
         }
         if (!full) {
 #pragma unroll
@@ -699,33 +702,70 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int t = 16 * u + 4 * j + e;
-              if (!((mask >> t & 1) && (SEL || first + t < lim[mt][hf]))) y[u][e] = -INFINITY;
+              if (!((mask >> t & 1) && (SEL || first + t < lim[mt][hf]))) y(mt, hf, u, e) = -INFINITY;
             }
         }
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
-          const float t4 = fmaxf(fmaxf(y[u][0], y[u][1]), fmaxf(y[u][2], y[u][3]));
+          const float t4 = fmaxf(fmaxf(y(mt, hf, u, 0), y(mt, hf, u, 1)), fmaxf(y(mt, hf, u, 2), y(mt, hf, u, 3)));
           top = fmaxf(top, t4);
-          if (SEL)
-            over = fmaxf(over, fmaxf(fmaxf(y[u][0] + lv[u][0], y[u][1] + lv[u][SEL ? 1 : 0]),
-                                     fmaxf(y[u][2] + lv[u][SEL ? 2 : 0], y[u][3] + lv[u][SEL ? 3 : 0])));
-          else
-            over = fmaxf(over, t4 + lv[u][0]);
+          moved = moved || t4 - basis(m[mt][hf]) + most[u] > big[mt][hf];
         }
-        const float mn = fmaxf(m[mt][hf], quad_max(top)), bn = fmaxf(big[mt][hf], quad_max(over));
-        const float mb = basis(mn), bb = basis(bn);
-        // A weight is its probability 2^(y - mb) times 2^(mb + log2(scale) - bb), in units of 2^-15. A probability below 2^-126
-        // is 0, whatever its value's scale.
+        const float mn = fmaxf(m[mt][hf], quad_max(top)), mb = basis(mn);
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float2 d = add2(make_float2(y(mt, hf, u, e), y(mt, hf, u, e + 1)), both(-mb));
+            y(mt, hf, u, e) = d.x;
+            y(mt, hf, u, e + 1) = d.y;
+          }
+        sum[mt][hf] *= ex2(m[mt][hf] - mb);
+        big[mt][hf] = counted(big[mt][hf], m[mt][hf], mn);
+        m[mt][hf] = mn;
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (empty(hf)) continue;
+          float over = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) over = fmaxf(over, y(mt, hf, u, e) + lv[u][SEL ? e : 0]);
+          const float bn = fmaxf(big[mt][hf], quad_max(over)), shift = ex2(big[mt][hf] - basis(bn));
+          big[mt][hf] = bn;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[mt][i][2 * hf] *= shift;
+            o[mt][i][2 * hf + 1] *= shift;
+          }
+        }
+    }
+    // A weight is its probability 2^(y - m) times 2^(log2(scale) - M), in units of 2^-15. A probability below 2^-126 is 0,
+    // whatever its value's scale.
+    uint32_t p[MT][SUBS][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (empty(hf)) {
+#pragma unroll
+          for (int u = 0; u < SUBS; ++u) p[mt][u][hf] = p[mt][u][2 + hf] = 0u;
+          continue;
+        }
+        const float bb = basis(big[mt][hf]);
         float2 add = make_float2(0.f, 0.f);
-        const float unit = ex2(capped(mb - bb + kUnit));
+        const float unit = ex2(capped(kUnit - bb));
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
-          const float f = SEL ? 0.f : ex2(capped(mb + lv[u][0] - bb + kUnit));
+          const float f = SEL ? 0.f : ex2(capped(lv[u][0] - bb + kUnit));
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            const float2 d = add2(make_float2(y[u][e], y[u][e + 1]), both(-mb));
-            const float2 pr = make_float2(ex2(d.x), ex2(d.y));
+            const float2 pr = make_float2(ex2(y(mt, hf, u, e)), ex2(y(mt, hf, u, e + 1)));
             add = add2(add, pr);
             const float2 x = mul2(pr, SEL ? mul2(both(unit), make_float2(vs[u][SEL ? e : 0], vs[u][SEL ? e + 1 : 0])) : both(f));
             w[e] = x.x;
@@ -734,25 +774,13 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           if (!full) {  // (an invisible position's scale may be NaN, or its block's factor infinite)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (y[u][e] == -INFINITY) w[e] = 0.f;
+              if (y(mt, hf, u, e) == -INFINITY) w[e] = 0.f;
           }
           p[mt][u][hf] = half_pair(w[0], w[1]);
           p[mt][u][2 + hf] = half_pair(w[2], w[3]);
         }
-        sum[mt][hf] = fmaf(sum[mt][hf], ex2(m[mt][hf] - mb), add.x + add.y);
-        shift[mt][hf] = ex2(big[mt][hf] - bb);
-        moved = moved || bn != big[mt][hf];
-        m[mt][hf] = mn;
-        big[mt][hf] = bn;
+        sum[mt][hf] += add.x + add.y;
       }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][i][e] *= shift[mt][e >> 1];
-    }
     // Values: of 32 dimensions four n-tiles, a lane's four positions side by side.
     const unsigned char* sv = st + kBytes;
     const uint32_t rows = smem_u32(sv) + value_at;
@@ -904,7 +932,7 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant
 #pragma unroll
       for (int k = 0; k < S; ++k) {
         m[r] = fmaxf(m[r], st[r][k].x);
-        big[r] = fmaxf(big[r], st[r][k].z);
+        big[r] = fmaxf(big[r], st[r][k].x + st[r][k].z);
       }
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) {
@@ -924,12 +952,13 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant
         m[r] = fmaxf(m[r], red[r][0][w]);
         big[r] = fmaxf(big[r], red[r][1][w]);
       }
+      big[r] -= basis(m[r]);  // (as where warps meet)
       float l = 0.f;
 #pragma unroll
       for (int k = 0; k < S; ++k) {
         const int i = threadIdx.x + 256 * k;
         l = fmaf(st[r][k].y, ex2(st[r][k].x - basis(m[r])), l);
-        if (i < n) factor[r][i] = ex2(st[r][k].z - basis(big[r]));
+        if (i < n) factor[r][i] = ex2(counted(st[r][k].z, st[r][k].x, m[r]) - basis(big[r]));
       }
       l = warp_sum(l);
       if (lane == 0) red[r][2][warp] = l;
@@ -968,7 +997,7 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant
         v += acc[w][r][d];
         l += red[r][2][w];
       }
-      v *= l == 0.f ? 0.f : ex2(br - kUnit - basis(mr)) / l;
+      v *= l == 0.f ? 0.f : ex2(br - kUnit) / l;
       if (a.type == IBWD_BF16)
         static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(v);
       else
