@@ -29,6 +29,7 @@
 // whatever the blocks' scales are. M counts from m, since log2(scale) beside a
 // large logit would be rounded at that one's size. Weights are kept in units of 2^-15, at most
 // 2^15 in fp16: they lose bits only below 2^-29 of the largest and vanish below 2^-39.
+// A scale below 2^-111 counts as that in M, so that 2^(15 - M) and its inverse are numbers.
 #pragma once
 #include "cache.h"
 #include "elem.cuh"
@@ -45,6 +46,7 @@ namespace ibwd {
 constexpr int kAttnThreads = 128;  // four warps
 constexpr int kAttnGrid = 456;     // blocks at most, which is what the workspace holds
 constexpr float kUnit = 15.f;      // log2 of the largest weight in fp16
+constexpr float kLeast = -111.f;   // log2 of a scale at least, in an outputs' unit
 constexpr int kItemCost = 2;       // what beginning and ending an item costs, in tiles
 
 // What a block leaves for the join: the item that it ends without having begun it.
@@ -108,7 +110,6 @@ __device__ __forceinline__ float quad_sum(float v) {
 __device__ __forceinline__ float basis(float m) { return m == -INFINITY ? 0.f : m; }
 // A unit that counts from maximum `m`, as it counts from the larger maximum `to`.
 __device__ __forceinline__ float counted(float unit, float m, float to) { return unit + (m - basis(to)); }
-__device__ __forceinline__ float capped(float e) { return e > 126.f ? 126.f : e; }  // (NaN stays)
 
 // Where 16 bytes of a stage's row lie: ldmatrix takes eight rows at once, and a
 // lane's quarter of a key two, without a bank conflict. Stages begin on 256
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
             mm = fmaxf(mm, p[w * ROWS * 3]);
             bb = fmaxf(bb, p[w * ROWS * 3] + p[w * ROWS * 3 + 2]);
           }
-          bb -= basis(mm);  // (rounded, but any unit near the largest serves in fp32)
+          bb = fmaxf(bb - basis(mm), kLeast);  // (rounded, but any unit near the largest serves in fp32)
           constexpr int V = DC / 32;
           float x[V];
 #pragma unroll
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             ll = fmaf(p[w * ROWS * 3 + 1], ex2(p[w * ROWS * 3] - basis(mm)), ll);
-            const float f = ex2(counted(p[w * ROWS * 3 + 2], p[w * ROWS * 3], mm) - basis(bb));
+            const float f = ex2(counted(p[w * ROWS * 3 + 2], p[w * ROWS * 3], mm) - bb);
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
               const float2 v = *reinterpret_cast<const float2*>(at(w, row, (lane * V + e) / 2));
@@ -585,11 +586,11 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           if (whole) {
             const int i = R / a.group;
             const long long out_row = (long long)(c.token + i) * a.heads * a.group + c.head * a.group + R - i * a.group;
-            const float f = ll == 0.f ? 0.f : ex2(bb - kUnit) / ll;
+            const float f = ll == 0.f ? 0.f : 1.f / ll, unit = ex2(bb - kUnit);
             uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + out_row * D + d0 + lane * V);
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
-              const float2 v = make_float2(x[e] * f, x[e + 1] * f);
+              const float2 v = make_float2(x[e] * f * unit, x[e + 1] * f * unit);
               to[e / 2] = a.type == IBWD_BF16 ? pack2_of(v, __nv_bfloat16{}) : pack2_of(v, __half{});
             }
             if (a.lse && lane == 0 && d0 == 0) a.lse[out_row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         for (int e = 0; e < (SEL ? 4 : 1); ++e) {
           ks[u][e] = xx[e];
           vs[u][e] = yy[e];
-          lv[u][e] = __log2f(yy[e]);
+          lv[u][e] = fmaxf(__log2f(yy[e]), kLeast);
         }
         most[u] = fmaxf(fmaxf(lv[u][0], lv[u][SEL ? 1 : 0]), fmaxf(lv[u][SEL ? 2 : 0], lv[u][SEL ? 3 : 0]));
       }
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       for (int u = 0; u < SUBS; ++u) {
         ks[u][0] = u ? x.z : x.x;
         vs[u][0] = u ? x.w : x.y;
-        most[u] = lv[u][0] = __log2f(vs[u][0]);
+        most[u] = lv[u][0] = fmaxf(__log2f(vs[u][0]), kLeast);
       }
     }
     const int here = c.rows - c.rt * ROWS;  // rows of this tile, and on
@@ -744,8 +745,8 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           }
         }
     }
-    // A weight is its probability 2^(y - m) times 2^(log2(scale) - M), in units of 2^-15. A probability below 2^-126 is 0,
-    // whatever its value's scale.
+    // A weight is its probability 2^(y - m) times its value's scale, in units of 2^(M - 15): in that order, since the last two
+    // alone may be beyond fp32. A probability below 2^-126 is 0, whatever its value's scale.
     uint32_t p[MT][SUBS][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -758,20 +759,19 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         }
         const float bb = basis(big[mt][hf]);
         float2 add = make_float2(0.f, 0.f);
-        const float unit = ex2(capped(kUnit - bb));
+        const float unit = ex2(kUnit - bb);
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
-          const float f = SEL ? 0.f : ex2(capped(lv[u][0] - bb + kUnit));
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
             const float2 pr = make_float2(ex2(y(mt, hf, u, e)), ex2(y(mt, hf, u, e + 1)));
             add = add2(add, pr);
-            const float2 x = mul2(pr, SEL ? mul2(both(unit), make_float2(vs[u][SEL ? e : 0], vs[u][SEL ? e + 1 : 0])) : both(f));
+            const float2 x = mul2(mul2(pr, both(unit)), make_float2(vs[u][SEL ? e : 0], vs[u][SEL ? e + 1 : 0]));
             w[e] = x.x;
             w[e + 1] = x.y;
           }
-          if (!full) {  // (an invisible position's scale may be NaN, or its block's factor infinite)
+          if (!full) {  // (an invisible position's scale may be anything)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (y(mt, hf, u, e) == -INFINITY) w[e] = 0.f;
@@ -952,13 +952,13 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant
         m[r] = fmaxf(m[r], red[r][0][w]);
         big[r] = fmaxf(big[r], red[r][1][w]);
       }
-      big[r] -= basis(m[r]);  // (as where warps meet)
+      big[r] = fmaxf(big[r] - basis(m[r]), kLeast);  // (as where warps meet)
       float l = 0.f;
 #pragma unroll
       for (int k = 0; k < S; ++k) {
         const int i = threadIdx.x + 256 * k;
         l = fmaf(st[r][k].y, ex2(st[r][k].x - basis(m[r])), l);
-        if (i < n) factor[r][i] = ex2(counted(st[r][k].z, st[r][k].x, m[r]) - basis(big[r]));
+        if (i < n) factor[r][i] = ex2(counted(st[r][k].z, st[r][k].x, m[r]) - big[r]);
       }
       l = warp_sum(l);
       if (lane == 0) red[r][2][warp] = l;
@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant
         v += acc[w][r][d];
         l += red[r][2][w];
       }
-      v *= l == 0.f ? 0.f : ex2(br - kUnit) / l;
+      v = l == 0.f ? 0.f : v * (1.f / l) * ex2(br - kUnit);
       if (a.type == IBWD_BF16)
         static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(v);
       else

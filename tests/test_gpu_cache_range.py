@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import sparse_attention_indexer_bwd_gb300 as ibwd
-from test_gpu_cache import CODES, E4M3, filled, generator, pages_for
+from heads_ref import check_attention
+from test_gpu_cache import CODES, E4M3, filled, generator, offsets, pages_for
 from train_ref import U, half_step, within
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,60 @@ def test_large_logits_with_scales_of_any_value(logit, dim, code):
         alike([7, 300, 64], dim, 16, CODES[code], logit, group, 3, 2)
         alike([400, 300], dim, 32, CODES[code], logit, group, 200, 3)
     alike([9000], dim, 64, CODES[code], logit, 4, 0, 4)  # (one item in all blocks)
+
+
+def of_scales(exponents, logits, dim, code, kept, kind, counts=None, seed=1):
+    """One sequence, a page of 16 positions a block: 2^exponents[i] the scale of page i's values, logits[i] its logits."""
+    n, page = 16 * len(exponents), 16
+    table, pages = pages_for([n], page, 1, seed)
+    at = table[0].long()
+    kc = torch.zeros((pages, 1, page, dim), device="cuda")
+    kc[at, 0, :, 0] = torch.tensor(logits, device="cuda", dtype=torch.float32)[:, None]  # (whole numbers of a few bits)
+    kc, ks = kc.to(code), torch.ones((pages, 1), device="cuda")
+    vc, vs = filled(pages, 1, page, dim, code, seed)
+    vs[at, 0] = torch.exp2(torch.tensor(exponents, device="cuda", dtype=torch.float32))
+    tokens = 1 if counts is None else sum(counts)
+    q = torch.zeros((tokens, 3, dim), device="cuda", dtype=kind)
+    q[..., 0] = 1
+    dl = torch.tensor([n], device="cuda", dtype=torch.int32)
+    select = None
+    if kept:
+        select = torch.randperm(n, device="cuda", generator=generator(seed + 1))[:kept].int().expand(tokens, kept).contiguous()
+    cu = None if counts is None else offsets(counts)
+    got = ibwd.cache_attention(q, kc, vc, ks, vs, table, dl, cu=cu, select=select, scale=1.0)
+    check_attention(got, q, kc, vc, ks, vs, table, [n], None if cu is None else cu.tolist(), select, 1.0, page,
+                    f"scales {exponents}, logits {logits}, kept {kept}")
+    return got
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scales_at_the_ends_of_their_range(dim, code):
+    bf16, code = torch.bfloat16, CODES[code]
+    for kept in (0, 90):
+        # tiny values: they and the outputs are bf16 numbers
+        for e in (-105, -115, -120, -126):
+            got = of_scales([e] * 8, [0, 1, 2, -3, 4, 0, 0, 1], dim, code, kept, bf16)
+            assert (got[0] != 0).any()
+            of_scales([e, e + 3, -126, e + 1, e, -126, e + 4, e], [9, 1, 2, -3, 4, 0, 0, 1], dim, code, kept, bf16)
+        # an improbable block of large values beside a probable one of small values, either of them first
+        for far, large, small in ((80, 100, -20), (84, 119, -2), (60, 110, 20), (80, 60, -60), (72, 115, 100)):
+            of_scales([large, small] * 4, [-far, 0] * 4, dim, code, kept, bf16)
+            of_scales([small, large] * 4, [0, -far] * 4, dim, code, kept, bf16)
+            of_scales([small] * 7 + [large], [0] * 7 + [-far], dim, code, kept, bf16)
+            of_scales([large] + [small] * 7, [-far] + [0] * 7, dim, code, kept, bf16)
+    # a block that some tokens do not see yet, with a scale far above theirs
+    of_scales([-100] * 7 + [120], [0, 1, 2, -3, 4, 0, 0, 1], dim, code, 0, bf16, counts=[20])
+
+
+def test_nothing_but_empty_blocks():
+    """Blocks of zeros have the least scale, or none yet."""
+    for e in (-126.0, -math.inf):
+        for kept in (0, 40):
+            n, page, dim = 64, 16, 64
+            table, pages = pages_for([n], page, 1, 1)
+            c, s = torch.zeros((pages, 1, page, dim), device="cuda").to(E4M3), torch.full((pages, 1), 2.0 ** e, device="cuda")
+            q = torch.randn((1, 4, dim), device="cuda", generator=generator(1)).bfloat16()
+            select = torch.arange(kept, device="cuda", dtype=torch.int32)[None] if kept else None
+            out, lse = ibwd.cache_attention(q, c, c, s, s, table, torch.tensor([n], device="cuda", dtype=torch.int32), select=select)
+            assert (out == 0).all() and torch.allclose(lse, torch.full_like(lse, math.log(kept or n)), rtol=0, atol=2.0 ** -19)
