@@ -156,7 +156,7 @@ struct Cursor {
       token = s.begin(b);
       const int n = max(0, s.begin(b + 1) - token);
       len = n ? s.length(b) : 0;
-      seen = n ? (int)max(-(1ll << 30), min((long long)s.lens[b] - n + 1, 1ll << 30)) : 0;
+      seen = n ? (int)max(-(1ll << 30), (long long)s.lens[b] - n + 1) : 0;  // (n is at most 2^27)
       rows = (int)min((long long)n * a.group, 1ll << 30);
     }
     row_tiles = (rows + ROWS - 1) / ROWS;

@@ -106,3 +106,30 @@ def test_nothing_but_empty_blocks():
             select = torch.arange(kept, device="cuda", dtype=torch.int32)[None] if kept else None
             out, lse = ibwd.cache_attention(q, c, c, s, s, table, torch.tensor([n], device="cuda", dtype=torch.int32), select=select)
             assert (out == 0).all() and torch.allclose(lse, torch.full_like(lse, math.log(kept or n)), rtol=0, atol=2.0 ** -19)
+
+
+@pytest.mark.parametrize("page,length", [(256, (1 << 30) + 700), (256, (1 << 31) - 1)])
+def test_positions_up_to_the_largest(page, length):
+    """A sequence as long as positions are numbers, most of whose pages are none: the others count wherever they lie."""
+    dim, group, width = 64, 3, ((1 << 31) - 1) // page
+    held = min(length, width * page)
+    places = [0, 1, (1 << 29) // page, (1 << 30) // page - 1, (1 << 30) // page, (held - 1) // page - 1, (held - 1) // page]
+    table = torch.full((1, width), -1, device="cuda", dtype=torch.int32)
+    for i, at in enumerate(places):
+        table[0, at] = 6 - i
+    kc, ks = filled(7, 1, page, dim, E4M3, 1)
+    vc, vs = filled(7, 1, page, dim, E4M3, 2)
+    q = torch.randn((2, group, dim), device="cuda", generator=generator(3)).bfloat16()
+    dl, cu = torch.tensor([length], device="cuda", dtype=torch.int32), offsets([2])
+    # the same pages side by side, with as many positions in the last one
+    near, n = torch.arange(6, -1, -1, device="cuda", dtype=torch.int32)[None], 6 * page + held - places[-1] * page
+    # (the tokens see all that is held where the length is beyond it)
+    first = max(0, min(length - 1, held) - places[-1] * page) + 6 * page
+    select = torch.tensor([p * page + 5 for p in places] + [held - 1, 7], device="cuda", dtype=torch.int32).expand(2, 9).contiguous()
+    close = torch.tensor([i * page + 5 for i in range(7)] + [n - 1, 7], device="cuda", dtype=torch.int32).expand(2, 9).contiguous()
+    for ids, ids_near in ((None, None), (select, close)):
+        got = ibwd.cache_attention(q, kc, vc, ks, vs, table, dl, cu=cu, select=ids)
+        for i, seen in enumerate((first, n)):
+            one = lambda t: None if t is None else t[i:i + 1]
+            check_attention([t[i:i + 1] for t in got], q[i:i + 1], kc, vc, ks, vs, near, [seen], None, one(ids_near), dim ** -0.5, page,
+                            f"{length} positions, token {i}")
