@@ -120,6 +120,12 @@ __device__ __forceinline__ uint32_t stage_at(int row, int chunk) {
   return row * D + ((chunk ^ (D == 64 ? row >> 1 & 3 : row & 7)) << 4);
 }
 
+// Tiles of `len` positions, up to the largest int; one where there are none.
+template <int TILE>
+__device__ __forceinline__ int tiles_for(int len) {
+  return (max(len, 1) - 1) / TILE + 1;
+}
+
 // The items in their order, and the tiles of the current one.
 template <int ROWS, int TILE, bool SEL>
 struct Cursor {
@@ -160,7 +166,7 @@ struct Cursor {
       rows = (int)min((long long)n * a.group, 1ll << 30);
     }
     row_tiles = (rows + ROWS - 1) / ROWS;
-    tiles = max(1, (len + TILE - 1) / TILE);
+    tiles = tiles_for<TILE>(len);
   }
   // Moves on by one tile; whether that ends the item.
   __device__ bool step(const CacheAttnArgs& a) {
@@ -185,7 +191,7 @@ __device__ __forceinline__ long long tiles_of(const CacheAttnArgs& a, int b) {
   const CacheSeqs& s = a.seqs;
   const long long n = s.begin(b + 1) - s.begin(b);
   if (n <= 0) return 0;
-  return (n * a.group + ROWS - 1) / ROWS * a.heads * (kItemCost + max(1, (s.length(b) + TILE - 1) / TILE));
+  return (n * a.group + ROWS - 1) / ROWS * a.heads * (kItemCost + tiles_for<TILE>(s.length(b)));
 }
 
 // Groups of 16 positions in a warp's step.
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   c.head = c.rt = c.tile = 0;
   if (SEL) {
     const int tokens = s.cu ? s.begin(s.batch) : (int)s.tokens;
-    const long long each = (long long)((a.group + ROWS - 1) / ROWS) * a.heads * (kItemCost + (a.kept + kTile - 1) / kTile);
+    const long long each = (long long)((a.group + ROWS - 1) / ROWS) * a.heads * (kItemCost + tiles_for<kTile>(a.kept));
     total = each * tokens;
     blocks = min((long long)gridDim.x, total);
     t0 = blockIdx.x < blocks ? total * blockIdx.x / blocks : 0;
@@ -678,7 +684,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     }
     const int here = c.rows - c.rt * ROWS;  // rows of this tile, and on
     constexpr unsigned kAll = SUBS == 2 ? 0xFFFFFFFFu : 0xFFFFu;
-    const bool full = mask == kAll && (SEL || first + STEP <= lim_min);
+    const bool full = mask == kAll && (SEL || first <= lim_min - STEP);
     // Half of a tile may have no rows (KV heads of four, int8: 180 us where it goes through the softmax as well, 172).
     auto empty = [&](int hf) { return MT == 1 && hf && here <= 8; };
     // The logit of a row's position e of a lane's four in each 16, then less its row's maximum.

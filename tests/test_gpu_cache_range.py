@@ -108,7 +108,7 @@ def test_nothing_but_empty_blocks():
             assert (out == 0).all() and torch.allclose(lse, torch.full_like(lse, math.log(kept or n)), rtol=0, atol=2.0 ** -19)
 
 
-@pytest.mark.parametrize("page,length", [(256, (1 << 30) + 700), (256, (1 << 31) - 1)])
+@pytest.mark.parametrize("page,length", [(256, (1 << 30) + 700), (64, (1 << 31) - 1), (16, (1 << 31) - 20), (256, (1 << 31) - 1)])
 def test_positions_up_to_the_largest(page, length):
     """A sequence as long as positions are numbers, most of whose pages are none: the others count wherever they lie."""
     dim, group, width = 64, 3, ((1 << 31) - 1) // page
