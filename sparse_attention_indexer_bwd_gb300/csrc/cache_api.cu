@@ -123,9 +123,11 @@ int ibwd_cache_attention(const void* q, int64_t q_token, int64_t q_head, int typ
   if (!type_ok(type) || group < 1 || !std::isfinite(scale * 1.44269504088896341f) || (select && kept < 1)) return IBWD_ERR_INVALID_ARG;
   if (type == IBWD_F32 || !ibwd_cache_attention_workspace_size(seqs->dim) || group > 65535 || (select && kept > 1 << 30))
     return IBWD_ERR_UNSUPPORTED;
-  // rows of a KV head, and tiles of the whole call, as the kernel counts them
+  // Rows of a KV head, and tiles of the whole call at most: row tiles are of 16 rows at least, tiles of 64 positions, and an
+  // item costs two tiles more. A block counts its share of them, a 304th or less, in an int.
   const double rows = (double)seqs->tokens * group, places = select ? kept : (double)seqs->table_width * seqs->page;
-  if (rows > 1 << 30 || (rows + 16. * seqs->tokens) * seqs->heads * (places / 64 + 2) > 1e15) return IBWD_ERR_UNSUPPORTED;
+  const double ragged = (double)(select || seqs->batch > seqs->tokens ? seqs->tokens : seqs->batch);
+  if (rows > 1 << 30 || (rows / 16 + ragged) * seqs->heads * (places / 64 + 3) > 300. * INT_MAX) return IBWD_ERR_UNSUPPORTED;
   if ((rc = heads_status(q_token, q_head, seqs->tokens, (int64_t)seqs->heads * group))) return rc;
   if (!seqs->cu && seqs->tokens != seqs->batch) return IBWD_ERR_INVALID_ARG;
   if (!seqs->tokens || !seqs->batch) return IBWD_OK;
