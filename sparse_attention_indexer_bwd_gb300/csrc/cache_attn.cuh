@@ -200,7 +200,7 @@ constexpr int attn_subs(int D) { return D == 256 ? 1 : 2; }
 constexpr int attn_stage(int D, bool sel) { return (attn_subs(D) * (32 * D + (sel ? 128 : 0)) + 32 + 255) / 256 * 256; }
 
 template <int D, int MT, bool INT8, bool SEL, int STAGES, int BLOCKS>
-__global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid_constant__ CacheAttnArgs a, bool vec) {
+__global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid_constant__ CacheAttnArgs a, bool vec, long long most_tiles) {
   constexpr int ROWS = 16 * MT, kRowChunks = D / 16;
   constexpr int SUBS = attn_subs(D), STEP = 16 * SUBS, kTile = 4 * STEP;  // positions of a warp's step, of a block's
   constexpr int kBytes = STEP * D, kStage = attn_stage(D, SEL);
@@ -247,6 +247,9 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       if (w < warp) upto += scan[w];
       total += scan[w];
     }
+    // offsets that fall count tokens several times: of such a call, whose results are undefined, there is no more to do than
+    // of any other
+    if (total > most_tiles) total = 0;
     blocks = min((long long)gridDim.x, total);
     t0 = blockIdx.x < blocks ? total * blockIdx.x / blocks : 0;
     t1 = blockIdx.x < blocks ? total * (blockIdx.x + 1) / blocks : 0;
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   if (SEL) __syncthreads();
   long long rest = found_rest;
   c.enter(a);
-  const int units = (int)min(t1 - t0, (long long)INT_MAX);
+  const int units = (int)(t1 - t0);
   int skipped;  // of the first item's own cost
   {
     const long long per_tile = c.tiles + kItemCost, per_head = c.row_tiles * per_tile;
@@ -1024,9 +1027,15 @@ cudaError_t attn_launch(const CacheAttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = a.num_sms * BLOCKS < kAttnGrid ? a.num_sms * BLOCKS : kAttnGrid;
   const bool vec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token % 8 == 0 && a.q_head % 8 == 0;
+  // The tiles of the call at most, with the items' own cost. A block's run of them is an int: the entry point sees to that.
+  const long long items = a.select ? (a.group + 16 * MT - 1) / (16 * MT) * a.seqs.tokens
+                                   : a.seqs.tokens * a.group / (16 * MT) + (a.seqs.batch < a.seqs.tokens ? a.seqs.batch : a.seqs.tokens);
+  const long long places = a.select ? a.kept : (long long)a.seqs.width << a.seqs.page_log;
+  const long long most_tiles = items * a.heads * (kItemCost + (places - 1) / (64 * attn_subs(D)) + 1);
+  if (most_tiles / grid >= INT_MAX) return cudaErrorInvalidValue;
   // Not launched before the kernel in front has ended: its blocks would take
   // places as that one's leave, unevenly (64 ragged sequences 93 us, not 70).
-  e = launch_ex(kern, grid, kAttnThreads, bytes, st, false, a, vec);
+  e = launch_ex(kern, grid, kAttnThreads, bytes, st, false, a, vec, most_tiles);
   if (e != cudaSuccess) return e;
   // rows that an item can have
   const int rows = (a.select || !a.seqs.cu) && a.group < 16 * MT ? a.group : 16 * MT;

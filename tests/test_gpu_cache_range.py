@@ -133,3 +133,25 @@ def test_positions_up_to_the_largest(page, length):
             one = lambda t: None if t is None else t[i:i + 1]
             check_attention([t[i:i + 1] for t in got], q[i:i + 1], kc, vc, ks, vs, near, [seen], None, one(ids_near), dim ** -0.5, page,
                             f"{length} positions, token {i}")
+
+
+def test_offsets_that_fall():
+    """They leave the results undefined, but nothing around them is written, and the call is no longer than others: of 32768
+    times the tokens it would be about 40 ms."""
+    batch, tokens, dim = 1 << 16, 1 << 12, 64
+    kc, ks = filled(4, 1, 16, dim, E4M3, 1)
+    table = torch.zeros((batch, 2), device="cuda", dtype=torch.int32)
+    lens = torch.full((batch,), 30, device="cuda", dtype=torch.int32)
+    cu = torch.zeros(batch + 1, device="cuda", dtype=torch.int32)
+    cu[1::2] = tokens
+    q = torch.randn((tokens, 1, dim), device="cuda", generator=generator(1)).bfloat16()
+    wide = torch.full((tokens + 2, 1, dim), 7.0, device="cuda", dtype=torch.bfloat16)
+    times = []
+    for _ in range(3):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        ibwd.cache_attention(q, kc, kc, ks, ks, table, lens, cu=cu, out=wide[1:-1])
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    assert (wide[0] == 7).all() and (wide[-1] == 7).all() and min(times) < 10.0, times
