@@ -93,8 +93,9 @@ IBWD_API size_t ibwd_cache_attention_workspace_size(int dim);
  *   out     type [tokens, heads * group, dim], contiguous; 16-byte aligned
  *   lse     fp32 [tokens, heads * group], or NULL
  *   select  int32 [tokens, kept], or NULL; dim 64, 128 or 256; scale finite
- *           tokens * group up to 2^30; calls that may have more than 300 * (2^31 - 1) tiles of 16 rows and 64
- *           positions (as the table is wide, or the list long) are unsupported
+ *           tokens * group up to 2^30, heads * group up to 2^31 - 1; calls that may have more than
+ *           300 * (2^31 - 1) tiles of 16 rows and 64 positions (as the table is wide, or the list long)
+ *           are unsupported
  *   workspace  at least ibwd_cache_attention_workspace_size bytes, 16-byte aligned
  */
 IBWD_API int ibwd_cache_attention(const void* q, int64_t q_token, int64_t q_head, int type, int group,

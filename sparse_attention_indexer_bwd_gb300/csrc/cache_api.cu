@@ -121,7 +121,8 @@ int ibwd_cache_attention(const void* q, int64_t q_token, int64_t q_head, int typ
   int rc = seqs_status(seqs, &a.seqs);
   if (rc) return rc;
   if (!type_ok(type) || group < 1 || !std::isfinite(scale * 1.44269504088896341f) || (select && kept < 1)) return IBWD_ERR_INVALID_ARG;
-  if (type == IBWD_F32 || !ibwd_cache_attention_workspace_size(seqs->dim) || group > 65535 || (select && kept > 1 << 30))
+  if (type == IBWD_F32 || !ibwd_cache_attention_workspace_size(seqs->dim) || group > 65535 || (select && kept > 1 << 30) ||
+      (long long)seqs->heads * group > INT_MAX)
     return IBWD_ERR_UNSUPPORTED;
   // Rows of a KV head, and tiles of the whole call at most: row tiles are of 16 rows at least, tiles of 64 positions, and an
   // item costs two tiles more. A block counts its share of them, a 304th or less, in an int.

@@ -14,3 +14,8 @@ def test_more_tiles_than_a_block_counts(lib):  # noqa: F811
     # many sequences under a wide table are no more than their tokens
     assert attend(lib, s=seqs(heads=32, **{**prompt, "batch": 1 << 20}), group=4, q=None) == UNSUPPORTED
     assert attend(lib, s=seqs(heads=32, **{**prompt, "batch": 1 << 10}), group=4, q=None) == INVALID
+
+
+def test_more_query_heads_than_are_counted(lib):  # noqa: F811
+    assert attend(lib, s=seqs(heads=32769, batch=1, tokens=1), group=65535) == UNSUPPORTED
+    assert attend(lib, s=seqs(heads=32768, batch=1, tokens=1), group=65535, q=None) == INVALID
