@@ -47,7 +47,7 @@ typedef struct ibwd_sequences {
   int batch;             /* up to 2^20 */
   const int32_t* lens;   /* [batch] */
   const int32_t* cu;     /* [batch + 1] offsets of the sequences' packed tokens; NULL: one token each */
-  int64_t tokens;        /* rows of the packed tokens, at most 2^27; those from cu[batch] on belong to no sequence */
+  int64_t tokens;        /* rows of the packed tokens, at most 2^27; those before cu[0] and from cu[batch] on are nobody's */
   int64_t pages;
   int heads, page, dim;
   int code;              /* ibwd_code */
@@ -88,7 +88,7 @@ IBWD_API size_t ibwd_cache_attention_workspace_size(int dim);
  * Statistics and sums are fp32; a query is taken in fp16 relative to its
  * largest entry, a probability in fp16 relative to the largest weight (of
  * its own or of the value it weighs), each with 11 bits.
- * Rows of tokens behind the last sequence are left as they were.
+ * Rows of tokens before the first sequence and behind the last are left as they were.
  *   q       type [tokens, heads * group, dim], IBWD_BF16 or IBWD_F16, unit stride along dim
  *   out     type [tokens, heads * group, dim], contiguous; 16-byte aligned
  *   lse     fp32 [tokens, heads * group], or NULL

@@ -7,8 +7,8 @@ int8 with a float32 scale [pages, heads] for each block, one head's tokens of a
 page. page: 16, 32, 64, 128 or 256; dim: a multiple of 16 up to 512. Zeros are an
 empty cache. Sequence b has lens[b] tokens, position t in slot t % page of
 page page_table[b, t // page] (int32). Without `cu` a call has one token a
-sequence; with cu (int32 [sequences + 1], from 0 on) sequence b has the packed tokens
-cu[b] .. cu[b + 1], its last ones. lens counts them: a write and the attention
+sequence; with cu (int32 [sequences + 1]) sequence b has the packed tokens
+cu[b] .. cu[b + 1], its last ones, and those before cu[0] or from cu[-1] on are nobody's. lens counts them: a write and the attention
 behind it take the same lens, cu and page_table.
 
 Page numbers, lengths and offsets are data of the device: what lies outside is
@@ -83,7 +83,7 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu=
 
     A token sees the positions up to its own; with `select` (int32 [..., kept],
     an indexer's choice, padding outside) those of them that its row lists. A token
-    that sees nothing has out 0 and lse -inf; rows behind cu[-1] are left as they
+    that sees nothing has out 0 and lse -inf; rows before cu[0] and from cu[-1] on are left as they
     were (undefined where the call allocates the results). scale: of the logits,
     1 / sqrt(dim) by default. `workspace`: a contiguous tensor of
     cache_attention_workspace_size bytes (allocated when not given), of one call

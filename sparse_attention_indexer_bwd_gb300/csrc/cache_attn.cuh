@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
   long long blocks;  // that have tiles: at least one each, since the join takes a part of each
   c.head = c.rt = c.tile = 0;
   if (SEL) {
-    const int tokens = s.cu ? s.begin(s.batch) : (int)s.tokens;
+    const int from = s.cu ? s.begin(0) : 0;  // (rows before the first sequence are nobody's)
+    const int tokens = max(0, (s.cu ? s.begin(s.batch) : (int)s.tokens) - from);
     const long long each = (long long)((a.group + ROWS - 1) / ROWS) * a.heads * (kItemCost + tiles_for<kTile>(a.kept));
     total = each * tokens;
     blocks = min((long long)gridDim.x, total);
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
     t1 = blockIdx.x < blocks ? total * (blockIdx.x + 1) / blocks : 0;
     c.b = (int)(t0 / each);
     found_rest = t0 - c.b * each;  // (alike in all threads)
+    c.b += from;
   } else {
     const int per = (s.batch + kAttnThreads - 1) / kAttnThreads;
     const int b0 = min((int)threadIdx.x * per, s.batch), b1 = min(b0 + per, s.batch);

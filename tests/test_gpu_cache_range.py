@@ -155,3 +155,27 @@ def test_offsets_that_fall():
         torch.cuda.synchronize()
         times.append(a.elapsed_time(b))
     assert (wide[0] == 7).all() and (wide[-1] == 7).all() and min(times) < 10.0, times
+
+
+def test_rows_before_the_first_sequence():
+    """A part of a batch's offsets with all of its packed tokens: the rows of the others stay as they were."""
+    lens, cu, page, dim = [20, 30, 0], [3, 5, 8, 8], 16, 64
+    table, pages = pages_for(lens, page, 0, 1)
+    kc, ks = filled(pages, 1, page, dim, E4M3, 1)
+    vc, vs = filled(pages, 1, page, dim, E4M3, 2)
+    q = torch.randn((10, 4, dim), device="cuda", generator=generator(3)).bfloat16()
+    dl, offs = (torch.tensor(t, device="cuda", dtype=torch.int32) for t in (lens, cu))
+    for kept in (0, 1, 200):
+        select = torch.randint(-1, 30, (10, kept), device="cuda", generator=generator(4), dtype=torch.int32) if kept else None
+        out = torch.full_like(q, 7)
+        got = ibwd.cache_attention(q, kc, vc, ks, vs, table, dl, cu=offs, select=select, out=out)
+        check_attention(got, q, kc, vc, ks, vs, table, lens, cu, select, dim ** -0.5, page, f"kept {kept}")
+        assert (out[:3] == 7).all() and (out[8:] == 7).all()
+    before = [t.clone() for t in (kc.view(torch.uint8), ks)]
+    k = torch.randn((10, 1, dim), device="cuda", generator=generator(5)).bfloat16()
+    ibwd.cache_write(k, None, kc, None, ks, None, table, dl, cu=offs)
+    a, b = kc.clone(), ks.clone()
+    kc.view(torch.uint8).copy_(before[0])
+    ks.copy_(before[1])
+    ibwd.cache_write(k[3:8].contiguous(), None, kc, None, ks, None, table, dl, cu=offs - 3)
+    assert torch.equal(a.view(torch.uint8), kc.view(torch.uint8)) and torch.equal(b, ks)
