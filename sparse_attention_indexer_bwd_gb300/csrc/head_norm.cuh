@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_rows(const __grid_consta
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         const int at = t * a.pairs + (i < N / 2 ? pair : pair1) + i;
-        *reinterpret_cast<float4*>(cc + i) = *reinterpret_cast<const float4*>(turns.cs + at);
-        *reinterpret_cast<float4*>(ss + i) = *reinterpret_cast<const float4*>(turns.sn + at);
+        const float4 x = *reinterpret_cast<const float4*>(turns.cs + at), y = *reinterpret_cast<const float4*>(turns.sn + at);
+        cc[i] = x.x, cc[i + 1] = x.y, cc[i + 2] = x.z, cc[i + 3] = x.w;
+        ss[i] = y.x, ss[i + 1] = y.y, ss[i + 2] = y.z, ss[i + 3] = y.w;
       }
     } else {
 #pragma unroll
