@@ -59,8 +59,9 @@ typedef struct ibwd_sequences {
  * the block was given (M = 448 or 127), and never falls while the page fills: a
  * token that raises it has the older tokens' codes rounded anew. A page whose
  * slot 0 the call writes begins anew. Codes are rounded to nearest even;
- * infinities become the largest code; NaN is e4m3's NaN, and in int8 makes the
- * block's scale NaN until the page begins anew.
+ * infinities become the largest code, as in int8 do finite values beyond
+ * 127 * 2^120 (1.7e38), which no scale holds; NaN is e4m3's NaN, and in int8
+ * makes the block's scale NaN until the page begins anew.
  *   k, v     type [tokens, heads, dim], unit stride along dim, `token` and `head` elements between
  *            tokens and heads; v, and v_cache with it, NULL for a cache of keys alone
  */

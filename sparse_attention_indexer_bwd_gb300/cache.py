@@ -51,7 +51,8 @@ def cache_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu=N
     A block's scale is the least power of two at which none of its finite values
     is beyond the largest code (448, 127); a token that raises it has the older
     tokens' codes rounded anew, and a page whose slot 0 is written begins anew.
-    Infinities become the largest code; NaN stays NaN, in int8 as the block's scale."""
+    Infinities become the largest code, as do values beyond 127 * 2^120 in int8;
+    NaN stays NaN, in int8 as the block's scale."""
     if stream is not None:
         return train._on(stream, cache_write, k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu)
     (train._n or train._native()).cache_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu)

@@ -72,7 +72,8 @@ struct Chunk {
   }
 };
 
-// The least power of two 2^e, e in [-126, 120], with amax <= M 2^e; amax finite.
+// The least power of two 2^e, e in [-126, 120], with amax <= M 2^e; amax finite. 120 is what the largest float needs in e4m3;
+// whole numbers would need 122, at which their largest codes are no floats: what is beyond 127 * 2^120 gets the largest code.
 template <bool INT8>
 __device__ __forceinline__ float scale_for(float amax) {
   const uint32_t bits = __float_as_uint(amax);
