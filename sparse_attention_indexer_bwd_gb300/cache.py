@@ -86,7 +86,8 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, cu=
     an indexer's choice, padding outside) those of them that its row lists. A token
     that sees nothing has out 0 and lse -inf; rows before cu[0] and from cu[-1] on are left as they
     were (undefined where the call allocates the results). scale: of the logits,
-    1 / sqrt(dim) by default. `workspace`: a contiguous tensor of
+    1 / sqrt(dim) by default. Weights and queries are taken with 11 bits (in float16,
+    relative to the largest), sums and the softmax's statistics in float32. `workspace`: a contiguous tensor of
     cache_attention_workspace_size bytes (allocated when not given), of one call
     at a time."""
     if stream is not None:
