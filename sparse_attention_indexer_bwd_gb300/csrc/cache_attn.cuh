@@ -26,7 +26,7 @@
 // once more in fp16: with 4 to 32 rows its tiles would be mostly padding.
 //
 // Two running maxima a row: m of the logits (base 2) for the sum l, and M of
-// logit - m + log2(scale of the value's block), which is what the outputs' unit
+// logit - m + log2(|scale| of the value's block), which is what the outputs' unit
 // follows, so that a weight has 11 bits relative to the largest contribution
 // whatever the blocks' scales are. M counts from m, since log2(scale) beside a
 // large logit would be rounded at that one's size. Weights are kept in units of 2^-15, at most
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         for (int e = 0; e < (SEL ? 4 : 1); ++e) {
           ks[u][e] = xx[e];
           vs[u][e] = yy[e];
-          lv[u][e] = fmaxf(__log2f(yy[e]), kLeast);
+          lv[u][e] = fmaxf(__log2f(fabsf(yy[e])), kLeast);
         }
         most[u] = fmaxf(fmaxf(lv[u][0], lv[u][SEL ? 1 : 0]), fmaxf(lv[u][SEL ? 2 : 0], lv[u][SEL ? 3 : 0]));
       }
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
       for (int u = 0; u < SUBS; ++u) {
         ks[u][0] = u ? x.z : x.x;
         vs[u][0] = u ? x.w : x.y;
-        most[u] = lv[u][0] = fmaxf(__log2f(vs[u][0]), kLeast);
+        most[u] = lv[u][0] = fmaxf(__log2f(fabsf(vs[u][0])), kLeast);
       }
     }
     const int here = c.rows - c.rt * ROWS;  // rows of this tile, and on

@@ -179,3 +179,24 @@ def test_rows_before_the_first_sequence():
     ks.copy_(before[1])
     ibwd.cache_write(k[3:8].contiguous(), None, kc, None, ks, None, table, dl, cu=offs - 3)
     assert torch.equal(a.view(torch.uint8), kc.view(torch.uint8)) and torch.equal(b, ks)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_negative_scales(dim, code):
+    """A code stands for code * scale whatever the scale's sign: the same numbers as with both turned."""
+    lens, page, code = [300, 17, 1], 16, CODES[code]
+    table, pages = pages_for(lens, page, 1, 1)
+    kc, ks = filled(pages, 2, page, dim, code, 1, spread=2)
+    vc, vs = filled(pages, 2, page, dim, code, 2, spread=2)
+    q = torch.randn((3, 8, dim), device="cuda", generator=generator(3)).bfloat16()
+    dl = torch.tensor(lens, device="cuda", dtype=torch.int32)
+    turned = [torch.where(torch.rand((pages, 2), device="cuda", generator=generator(i)) < 0.5, -1.0, 1.0) for i in (4, 5)]
+    for kept in (0, 40):
+        select = torch.randint(-1, 300, (3, kept), device="cuda", generator=generator(6), dtype=torch.int32) if kept else None
+        want = ibwd.cache_attention(q, kc, vc, ks, vs, table, dl, select=select)
+        codes = [(c.float() * t[:, :, None, None]).to(code) for c, t in ((kc, turned[0]), (vc, turned[1]))]
+        got = ibwd.cache_attention(q, *codes, ks * turned[0], vs * turned[1], table, dl, select=select)
+        # (rounding is the same for both signs)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(ibwd.cache_read(codes[1], vs * turned[1], table, dl, 300), ibwd.cache_read(vc, vs, table, dl, 300))
