@@ -6,7 +6,7 @@
 // queries are few: a row tile is 16 or 32 rows (query tokens x heads of the
 // group) of a KV head, 16 of heads of 256, and each code is read and converted
 // once for a row tile: once where the rows are no more, twice for 64. Of 32x16384
-// positions of 8 heads 4 rows take 164 us (97 % of the copy rate), 32 rows 312.
+// positions of 8 heads 4 rows take 164 us (97 % of the copy rate), 32 rows 310.
 //
 // The work is a list of tiles of 128 positions (64 for heads of 256; sequences, KV heads, row tiles,
 // positions, in that order), cut into equal runs, one a block, wherever that
@@ -108,10 +108,10 @@ __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
-// What a maximum is subtracted as: -inf (nothing yet) as 0.
-__device__ __forceinline__ float basis(float m) { return m == -INFINITY ? 0.f : m; }
+// What m is where nothing is seen yet: a number, so that differences are none of infinities.
+constexpr float kNone = -3.402823466e38f;
 // A unit that counts from maximum `m`, as it counts from the larger maximum `to`.
-__device__ __forceinline__ float counted(float unit, float m, float to) { return unit + (m - basis(to)); }
+__device__ __forceinline__ float counted(float unit, float m, float to) { return unit + (m - to); }
 
 // Where 16 bytes of a stage's row lie: ldmatrix takes eight rows at once, and a
 // lane's quarter of a key two, without a bank conflict. Stages begin on 256
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         down[hf] = none ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
         qs[mt][hf] = (none ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23)) * a.scale_log2;
         if (amax == INFINITY) qs[mt][hf] = __uint_as_float(0x7FC00000u);
-        m[mt][hf] = big[mt][hf] = -INFINITY;
+        m[mt][hf] = kNone;
+        big[mt][hf] = kLeast;
         sum[mt][hf] = 0.f;
       }
 #pragma unroll
@@ -574,20 +575,20 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           const int r = mt * 16 + row, R = c.rt * ROWS + r;
           if (R >= c.rows) break;
           const float* p = stats + r * 3;
-          float mm = -INFINITY, bb = -INFINITY, ll = 0.f;
+          float mm = kNone, bb = kNone, ll = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             mm = fmaxf(mm, p[w * ROWS * 3]);
             bb = fmaxf(bb, p[w * ROWS * 3] + p[w * ROWS * 3 + 2]);
           }
-          bb = fmaxf(bb - basis(mm), kLeast);  // (rounded, but any unit near the largest serves in fp32)
+          bb = fmaxf(bb - mm, kLeast);  // (rounded, but any unit near the largest serves in fp32)
           constexpr int V = DC / 32;
           float x[V];
 #pragma unroll
           for (int e = 0; e < V; ++e) x[e] = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            ll = fmaf(p[w * ROWS * 3 + 1], ex2(p[w * ROWS * 3] - basis(mm)), ll);
+            ll = fmaf(p[w * ROWS * 3 + 1], ex2(p[w * ROWS * 3] - mm), ll);
             const float f = ex2(counted(p[w * ROWS * 3 + 2], p[w * ROWS * 3], mm) - bb);
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
@@ -723,18 +724,18 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
         for (int u = 0; u < SUBS; ++u) {
           const float t4 = fmaxf(fmaxf(y(mt, hf, u, 0), y(mt, hf, u, 1)), fmaxf(y(mt, hf, u, 2), y(mt, hf, u, 3)));
           top = fmaxf(top, t4);
-          moved = moved || t4 - basis(m[mt][hf]) + most[u] > big[mt][hf];
+          moved = moved || t4 - m[mt][hf] + most[u] > big[mt][hf];
         }
-        const float mn = fmaxf(m[mt][hf], quad_max(top)), mb = basis(mn);
+        const float mn = fmaxf(m[mt][hf], quad_max(top));
 #pragma unroll
         for (int u = 0; u < SUBS; ++u)
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            const float2 d = add2(make_float2(y(mt, hf, u, e), y(mt, hf, u, e + 1)), both(-mb));
+            const float2 d = add2(make_float2(y(mt, hf, u, e), y(mt, hf, u, e + 1)), both(-mn));
             y(mt, hf, u, e) = d.x;
             y(mt, hf, u, e + 1) = d.y;
           }
-        sum[mt][hf] *= ex2(m[mt][hf] - mb);
+        sum[mt][hf] *= ex2(m[mt][hf] - mn);
         big[mt][hf] = counted(big[mt][hf], m[mt][hf], mn);
         m[mt][hf] = mn;
       }
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           for (int u = 0; u < SUBS; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) over = fmaxf(over, y(mt, hf, u, e) + lv[u][SEL ? e : 0]);
-          const float bn = fmaxf(big[mt][hf], quad_max(over)), shift = ex2(big[mt][hf] - basis(bn));
+          const float bn = fmaxf(big[mt][hf], quad_max(over)), shift = ex2(big[mt][hf] - bn);
           big[mt][hf] = bn;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
@@ -770,9 +771,8 @@ __global__ void __launch_bounds__(kAttnThreads, BLOCKS) attn_kernel(const __grid
           for (int u = 0; u < SUBS; ++u) p[mt][u][hf] = p[mt][u][2 + hf] = 0u;
           continue;
         }
-        const float bb = basis(big[mt][hf]);
         float2 add = make_float2(0.f, 0.f);
-        const float unit = ex2(kUnit - bb);
+        const float unit = ex2(kUnit - big[mt][hf]);
 #pragma unroll
         for (int u = 0; u < SUBS; ++u) {
           float w[4];
@@ -965,12 +965,12 @@ __global__ void __launch_bounds__(256, 4) attn_join_kernel(const __grid_constant
         m[r] = fmaxf(m[r], red[r][0][w]);
         big[r] = fmaxf(big[r], red[r][1][w]);
       }
-      big[r] = fmaxf(big[r] - basis(m[r]), kLeast);  // (as where warps meet)
+      big[r] = fmaxf(big[r] - m[r], kLeast);  // (as where warps meet)
       float l = 0.f;
 #pragma unroll
       for (int k = 0; k < S; ++k) {
         const int i = threadIdx.x + 256 * k;
-        l = fmaf(st[r][k].y, ex2(st[r][k].x - basis(m[r])), l);
+        l = fmaf(st[r][k].y, ex2(st[r][k].x - m[r]), l);
         if (i < n) factor[r][i] = ex2(counted(st[r][k].z, st[r][k].x, m[r]) - big[r]);
       }
       l = warp_sum(l);
